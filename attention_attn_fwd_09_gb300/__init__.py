@@ -7,12 +7,16 @@ library is missing this module raises at import time; there is no fallback.
 Names match the C ABI in include/attn.h: ``attn_fwd``, ``attn_fwd_kv``,
 ``attn_fwd_varlen`` and ``attn_bwd_varlen`` (packed sequences of different lengths), ``attn_bwd``,
 ``attn_bwd_noalloc``, ``attn_quantize_fp8`` and ``attn_fwd_fp8`` (e4m3 inputs with
-per-block scales), the ``*_workspace_size`` queries, ``attn_last_error`` and the
+per-block scales), ``attn_rope`` and ``attn_rope_bwd`` (rotary positions),
+``attn_kv_append_fp8`` and ``attn_fwd_kv_fp8`` (a paged e4m3 key/value cache and the attention
+over it), the ``*_workspace_size`` queries, ``attn_last_error`` and the
 test/tuning knobs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -75,6 +79,18 @@ _lib.attn_quantize_fp8.argtypes = [_p, _p, _p, _i, _i, _i, _i, _p]
 _lib.attn_quantize_fp8.restype = _i
 _lib.attn_fwd_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p]
 _lib.attn_fwd_fp8.restype = _i
+_lib.attn_rope.argtypes = [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, ctypes.POINTER(_ll), _p]
+_lib.attn_rope.restype = _i
+_lib.attn_rope_bwd.argtypes = _lib.attn_rope.argtypes
+_lib.attn_rope_bwd.restype = _i
+_lib.attn_kv_append_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                                    ctypes.POINTER(_ll), _p]
+_lib.attn_kv_append_fp8.restype = _i
+_lib.attn_fwd_kv_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p,
+                                 _sz, _p]
+_lib.attn_fwd_kv_fp8.restype = _i
+_lib.attn_fwd_kv_fp8_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+_lib.attn_fwd_kv_fp8_workspace_size.restype = _sz
 _lib.attn_exp2_sw.argtypes = [_p, _p, _ll, _i, _p]
 _lib.attn_exp2_sw.restype = _i
 
@@ -394,6 +410,207 @@ def attn_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, causal: bool = False, sc
     return o, lse
 
 
+def _scope(device, stream):
+    """(raw stream, context) of a call on ``device``: in the context that device is current and
+    what is allocated belongs to the stream the call runs on, so that a workspace allocated here
+    is not handed out again before the call has run."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return torch.cuda.current_stream().cuda_stream, _NO_CONTEXT
+        return torch.cuda.current_stream(device).cuda_stream, torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _plain(name, t, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this device, or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+
+
+def attn_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                    trained_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, mscale) for ``attn_rope``: fp64 [rot/2] radians per position, base^(-2j/rot),
+    and the factor on the rotated columns.  ``scaling`` for contexts ``factor`` times longer:
+
+    * ``"none"``;
+    * ``"linear"``: positions compressed, every frequency divided by ``factor``;
+    * ``"ntk"``: the base raised to base * factor^(rot / (rot - 2)), so that the slowest pair is
+      compressed by ``factor`` and the fastest left alone;
+    * ``"yarn"``: by the turns a pair makes over ``trained_length`` positions: from ``beta_fast``
+      turns on left alone, up to ``beta_slow`` turns compressed, blended in between; mscale =
+      0.1 ln(factor) + 1.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot={rot} must be even and at least 2")
+    if not (base > 1.0 and math.isfinite(base)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base must be finite and > 1, factor finite and >= 1")
+    j = torch.arange(0, rot, 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk":
+        if rot == 2:
+            raise ValueError("scaling='ntk' needs rot > 2")
+        base *= factor ** (rot / (rot - 2))
+    f = float(base) ** (-j / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if trained_length < 1 or not beta_fast > beta_slow:
+            raise ValueError("scaling='yarn' needs trained_length >= 1 and beta_fast > beta_slow")
+        turns = trained_length * f / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling={scaling!r} (none, linear, ntk or yarn)")
+    return f.to(device), mscale
+
+
+def _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream):
+    dims = q.dim()
+    if dims not in (3, 4):
+        raise ValueError(f"q: expected [B,H,N,d] or [H,T,d], got {tuple(q.shape)}")
+    dev = q.device
+    raw, context = _scope(dev, stream) if q.is_cuda else (0, _NO_CONTEXT)
+    with context:
+        N, d = q.shape[-2], q.shape[-1]
+        B = q.shape[0] if dims == 4 else 1
+        Hq, Hk = q.shape[-3], (k.shape[-3] if k is not None else 0)
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+        strides = []
+        for name, t, h in (("q", q, Hq), ("k", k, Hk), ("q_out", q_out, Hq), ("k_out", k_out, Hk)):
+            if t is None:
+                strides += (0, 0, 0)
+                continue
+            st = t.stride()
+            if (t.dtype is not torch.bfloat16 or not t.is_cuda or t.device != dev or st[-1] != 1
+                    or t.shape != ((B, h, N, d) if dims == 4 else (h, N, d))):
+                raise ValueError(f"{name}: expected a bf16 tensor of shape {((B, h, N, d) if dims == 4 else (h, N, d))} with "
+                                 f"contiguous columns on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
+            strides += (st[0] if dims == 4 else 0, st[-3], st[-2])
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq: expected a 1-D tensor of rot / 2 values")
+        _plain("inv_freq", inv_freq, torch.float64, inv_freq.shape, dev)
+        if positions is not None:
+            _plain("positions", positions, torch.int32, (B, N) if positions.dim() == 2 or dims == 4 else (N,), dev)
+        _check(call(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(), k_out.data_ptr() if Hk else None,
+                    inv_freq.data_ptr(), positions.data_ptr() if positions is not None else None, B, Hq, Hk, N, d,
+                    2 * inv_freq.numel(), int(bool(interleaved)), float(mscale), (_ll * 12)(*strides), raw))
+    return q_out, k_out
+
+
+def attn_rope(q, k, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None,
+              stream=None):
+    """q and k (or None) with rotary positions: bf16 [B,H,N,d] (or packed [H,T,d]) CUDA tensors of
+    any strides with contiguous columns, such as views of a fused projection.  ``inv_freq``: fp64
+    [rot/2] (``attn_rope_freqs``); ``positions``: int32 [B,N] ([T] when packed), default 0 .. N-1.
+    Pairs are columns (j, j + rot/2), or (2j, 2j+1) with ``interleaved``.  Returns (q_out, k_out),
+    new contiguous tensors unless given; an output may be its own input (in place)."""
+    return _rope(_lib.attn_rope, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream)
+
+
+def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, q_out=None,
+                  k_out=None, stream=None):
+    """Gradients of ``attn_rope``'s inputs from those of its outputs (the transposed rotation;
+    arguments as there)."""
+    return _rope(_lib.attn_rope_bwd, dq, dk, inv_freq, positions, interleaved, mscale, q_out, k_out, stream)
+
+
+def _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu, cu_name, kv_lens, dev):
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: expected [num_pages, Hkv, page_size, d], got {tuple(k_cache.shape)}")
+    shape = k_cache.shape
+    _plain("k_cache", k_cache, torch.uint8, shape, dev)
+    _plain("v_cache", v_cache, torch.uint8, shape, dev)
+    _plain("k_scale", k_scale, torch.float32, shape[:2], dev)
+    _plain("v_scale", v_scale, torch.float32, shape[:2], dev)
+    B = kv_lens.numel()
+    _plain("kv_lens", kv_lens, torch.int32, (B,), dev)
+    _plain(cu_name, cu, torch.int32, (B + 1,), dev)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
+    _plain("page_table", page_table, torch.int32, (B, page_table.shape[1]), dev)
+    return B, shape[0], shape[1], shape[2], shape[3], page_table.shape[1]
+
+
+def attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens, stream=None):
+    """Appends packed rows k, v ([Hkv, total, d] CUDA bf16, contiguous columns, strides multiples
+    of 8) to the paged cache in place: k_cache, v_cache uint8 [num_pages, Hkv, page_size, d] e4m3
+    codes, k_scale, v_scale fp32 [num_pages, Hkv].  ``page_table`` int32 [B, max_pages];
+    ``cu_seqlens`` int32 [B + 1], the new rows of each sequence; ``kv_lens`` int32 [B], its rows
+    after the call.  Each page's scale is a power of two that keeps its rows within +-448 codes;
+    the offsets, lengths and pages are checked on the device (attn_device_status())."""
+    if not k.is_cuda or k.dim() != 3:
+        raise ValueError(f"k: expected a CUDA tensor [Hkv, total, d], got {tuple(k.shape)} on {k.device}")
+    dev = k.device
+    B, pages, Hkv, P, d, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, "cu_seqlens",
+                                                kv_lens, dev)
+    T = k.shape[1]
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype is not torch.bfloat16 or t.device != dev or t.shape != (Hkv, T, d) or t.stride()[2] != 1:
+            raise ValueError(f"{name}: expected a bf16 tensor of shape {(Hkv, T, d)} with contiguous columns on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    raw, context = _scope(dev, stream)
+    sk, sv = k.stride(), v.stride()
+    with context:
+        _check(_lib.attn_kv_append_fp8(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                       k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+                                       cu_seqlens.data_ptr(), kv_lens.data_ptr(), B, Hkv, T, d, pages, P, width,
+                                       (_ll * 4)(sk[0], sk[1], sv[0], sv[1]), raw))
+
+
+def attn_fwd_kv_fp8_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_q: int, d: int) -> int:
+    n = _lib.attn_fwd_kv_fp8_workspace_size(B, Hq, Hkv, total_q, max_q, d)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(-1, attn_last_error())
+    return int(n)
+
+
+def attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, max_q: int,
+                    causal: bool = True, scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """O, LSE of packed queries q [Hq, total_q, d] (CUDA bf16) over a paged e4m3 cache (tensors as
+    ``attn_kv_append_fp8``): sequence b's n = cu_seqlens_q[b+1] - cu_seqlens_q[b] <= ``max_q``
+    queries stand at its last n of kv_lens[b] keys (causal: query i sees keys up to
+    i + kv_lens[b] - n).  ``workspace``: a uint8 CUDA tensor of at least
+    attn_fwd_kv_fp8_workspace_size(...) bytes (allocated when None).  The offsets, lengths and
+    pages are checked on the device (attn_device_status())."""
+    if not q.is_cuda or q.dim() != 3:
+        raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
+    dev = q.device
+    B, pages, Hkv, P, d, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q,
+                                                "cu_seqlens_q", kv_lens, dev)
+    Hq, T = q.shape[0], q.shape[1]
+    _plain("q", q, torch.bfloat16, (Hq, T, d), dev)
+    raw, context = _scope(dev, stream)
+    with context:
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _plain("o", o, torch.bfloat16, (Hq, T, d), dev)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        else:
+            _plain("lse", lse, torch.float32, (Hq, T), dev)
+        if workspace is None:
+            n = attn_fwd_kv_fp8_workspace_size(B, Hq, Hkv, T, int(max_q), d)
+            workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
+        _check(_lib.attn_fwd_kv_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(),
+                                    kv_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, int(max_q), d,
+                                    pages, P, width, int(bool(causal)), float(d ** -0.5 if scale is None else scale),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
+    return o, lse
+
+
 def attn_set_debug_knobs(tau: float = 8.0, poly_per_16: int = 0, wait_limit_ns: int = 2_000_000_000,
                          sync_check: bool = False):
     _check(_lib.attn_set_debug_knobs(float(tau), int(poly_per_16), int(wait_limit_ns), int(bool(sync_check))))
@@ -432,4 +649,5 @@ def attn_exp2_sw(x, variant: int = 0, stream=None):
 
 __all__ = ["attn_fwd", "attn_fwd_fp8", "attn_quantize_fp8", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_workspace_size", "attn_last_error", "attn_version",
            "attn_set_debug_knobs", "attn_get_debug_knobs", "attn_device_status", "attn_rescale_counter",
-           "attn_exp2_sw", "attn_set_test_hooks", "AttnError", "LIB_PATH"]
+           "attn_exp2_sw", "attn_set_test_hooks", "attn_rope", "attn_rope_bwd", "attn_rope_freqs", "attn_kv_append_fp8",
+           "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "AttnError", "LIB_PATH"]

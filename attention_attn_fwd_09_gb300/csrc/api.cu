@@ -158,6 +158,8 @@ int check_shape(int B, int Hq, int Hkv, int N, int d, float scale, bool wide = f
 int status_fail(int v) {
   if (v == DEV_BAD_OFFSETS)
     return fail(ATTN_ERR_INVALID_ARG, "packed-sequence offsets failed the device check (device status %d)", v);
+  if (v == DEV_BAD_PAGE)
+    return fail(ATTN_ERR_INVALID_ARG, "a page table entry in use is outside the cache (device status %d)", v);
   return fail(ATTN_ERR_TIMEOUT, "a kernel gave up on a bounded wait (device status %d)", v);
 }
 
@@ -747,6 +749,187 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
   e = launch_bwd(maps, p, st);
   if (e == cudaErrorNotSupported) return fail(ATTN_ERR_UNSUPPORTED, "backward not available for these arguments");
   if (e != cudaSuccess) return cuda_fail(e, "backward launch");
+  return post_launch(s, st);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+// strides: {q, k, q_out, k_out} x {batch, head, token} in elements, or null for contiguous
+// [B, H, N, d] tensors.
+static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
+                     const int* positions, int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale,
+                     const long long* strides, int backward, void* stream) {
+  if (B < 0 || N < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d and N=%d must be >= 0", B, N);
+  if (Hq <= 0 || Hk < 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d must be >= 1 and Hk=%d >= 0", Hq, Hk);
+  if (d != 64 && d != 128 && d != 192 && d != 256)
+    return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128, 192, 256)", d);
+  if (rot < 2 || rot > d || (rot & 1))
+    return fail(ATTN_ERR_INVALID_ARG, "rot=%d must be even and between 2 and d=%d", rot, d);
+  if (!std::isfinite(mscale)) return fail(ATTN_ERR_INVALID_ARG, "mscale must be finite");
+  if ((long long)Hq + Hk > 65535) return fail(ATTN_ERR_INVALID_ARG, "Hq + Hk too large");
+  if (B == 0 || N == 0) return ATTN_OK;
+  if (!q || !q_out || !inv_freq || (Hk > 0 && (!k || !k_out))) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  RopeParams p{};
+  p.q.in = q; p.q.out = q_out; p.k.in = k; p.k.out = k_out;
+  const long long cq[3] = {(long long)Hq * N * d, (long long)N * d, d}, ck[3] = {(long long)Hk * N * d, (long long)N * d, d};
+  const long long* sq = strides ? strides : cq;
+  const long long* sk = strides ? strides + 3 : ck;
+  const long long* oq = strides ? strides + 6 : cq;
+  const long long* ok = strides ? strides + 9 : ck;
+  p.q.in_b = sq[0]; p.q.in_h = sq[1]; p.q.in_n = sq[2]; p.q.out_b = oq[0]; p.q.out_h = oq[1]; p.q.out_n = oq[2];
+  p.k.in_b = sk[0]; p.k.in_h = sk[1]; p.k.in_n = sk[2]; p.k.out_b = ok[0]; p.k.out_h = ok[1]; p.k.out_n = ok[2];
+  uintptr_t bits = 0;
+  const int ext[2][3] = {{B, Hq, N}, {B, Hk, N}};
+  for (int i = 0; i < (Hk > 0 ? 2 : 1); ++i) {
+    const RopeTensor& t = i ? p.k : p.q;
+    const long long in[3] = {t.in_b, t.in_h, t.in_n}, out[3] = {t.out_b, t.out_h, t.out_n};
+    bits |= reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out);
+    for (int a = 0; a < 3; ++a) {
+      if (ext[i][a] <= 1) continue;                    // the stride is not used
+      bits |= (uintptr_t)(in[a] * 2) | (uintptr_t)(out[a] * 2);
+      if (out[a] < d && out[a] > -d) return fail(ATTN_ERR_INVALID_ARG, "output rows overlap (stride %lld)", out[a]);
+      if (t.in == t.out && in[a] != out[a])
+        return fail(ATTN_ERR_INVALID_ARG, "in place needs equal strides of input and output");
+    }
+  }
+  if (bits & 1) return fail(ATTN_ERR_MISALIGNED, "bf16 tensors must be 2-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(ATTN_ERR_MISALIGNED, "inv_freq must be 8-byte aligned, positions 4-byte aligned");
+  const int vec = (bits & 15) == 0 && rot % 16 == 0 ? 8 : ((bits & 7) == 0 && rot % 8 == 0 ? 4 : 1);
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.B = B; p.N = N; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot;
+  p.mscale = mscale;
+  p.sign = backward ? -1.f : 1.f;
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_rope(p, vec, interleaved ? 1 : 0, std::max(1, s->sms), st);
+  if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+  return post_launch(s, st);
+}
+
+int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const int* positions,
+              int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale, const long long* strides,
+              void* stream) {
+  return rope_impl(q, k, q_out, k_out, inv_freq, positions, B, Hq, Hk, N, d, rot, interleaved, mscale, strides, 0,
+                   stream);
+}
+
+int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const double* inv_freq,
+                  const int* positions, int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale,
+                  const long long* strides, void* stream) {
+  return rope_impl(dq, dk, dq_out, dk_out, inv_freq, positions, B, Hq, Hk, N, d, rot, interleaved, mscale, strides, 1,
+                   stream);
+}
+
+// Sizes common to the paged cache's calls.
+static int check_cache(int B, int Hkv, int total, int d, int num_pages, int page_size, int max_pages) {
+  if (B < 0 || total < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d and the packed length %d must be >= 0", B, total);
+  if (B == 0 && total > 0) return fail(ATTN_ERR_INVALID_ARG, "%d packed rows but no sequence", total);
+  if (Hkv <= 0 || Hkv > 65535) return fail(ATTN_ERR_INVALID_ARG, "Hkv=%d must be between 1 and 65535", Hkv);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim d=%d (the 8-bit cache supports 64, 128)", d);
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return fail(ATTN_ERR_UNSUPPORTED, "page size %d (supported: 16, 32, 64, 128)", page_size);
+  if (num_pages < 0 || max_pages < 0) return fail(ATTN_ERR_INVALID_ARG, "page counts must be >= 0");
+  if ((long long)max_pages * page_size > 0x7fff0000LL)
+    return fail(ATTN_ERR_INVALID_ARG, "max_pages * page_size must stay below 2^31 - 65536");
+  if (total > 0x7fff0000) return fail(ATTN_ERR_INVALID_ARG, "packed length must stay below 2^31 - 65536");
+  if ((long long)num_pages * Hkv > 0x7fffffffLL) return fail(ATTN_ERR_INVALID_ARG, "num_pages * Hkv too large");
+  return ATTN_OK;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// strides: {k head, k token, v head, v token} in elements, or null for contiguous [Hkv, total, d].
+int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hkv, int total,
+                       int d, int num_pages, int page_size, int max_pages, const long long* strides, void* stream) {
+  int rc = check_cache(B, Hkv, total, d, num_pages, page_size, max_pages);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || total == 0) return ATTN_OK;
+  if (num_pages == 0 || max_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d rows to append, but no pages", total);
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens || !kv_lens)
+    return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  const long long contiguous[4] = {(long long)total * d, d, (long long)total * d, d};
+  const long long* st4 = strides ? strides : contiguous;
+  uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
+  for (int i = 0; i < 4; ++i)
+    if ((i & 1 ? total : Hkv) > 1) bits |= (uintptr_t)(st4[i] * 2);
+  if ((bits & 15) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(ATTN_ERR_MISALIGNED, "k, v (their strides too) and the cache must be 16-byte aligned");
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) || !aligned4(cu_seqlens) || !aligned4(kv_lens))
+    return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets and lengths must be 4-byte aligned");
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  AppendParams p{};
+  p.k = k; p.v = v;
+  p.k_h = st4[0]; p.k_t = st4[1]; p.v_h = st4[2]; p.v_t = st4[3];
+  p.k_cache = k_cache; p.v_cache = v_cache; p.k_scale = k_scale; p.v_scale = v_scale;
+  p.table = page_table; p.cu = cu_seqlens; p.kv_lens = kv_lens;
+  p.B = B; p.Hkv = Hkv; p.total = total; p.num_pages = num_pages; p.page = page_size; p.max_pages = max_pages;
+  p.max_len = max_pages * page_size;
+  p.status = s->status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_kv_append(p, d, st);
+  if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+  return post_launch(s, st);
+}
+
+size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total_q < 0 || max_q < 0 || (d != 64 && d != 128)) {
+    set_last_error("attn_fwd_kv_fp8_workspace_size: invalid sizes");
+    return (size_t)-1;
+  }
+  if (B == 0 || total_q == 0) return 0;
+  const DevSyms* s = dev_syms(nullptr);
+  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
+  return cache_workspace_bytes(B, Hq, Hkv, total_q, max_q, d, sms);
+}
+
+int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o,
+                    float* lse, int B, int Hq, int Hkv, int total_q, int max_q, int d, int num_pages, int page_size,
+                    int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache(B, Hkv, total_q, d, num_pages, page_size, max_pages);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_shape(B, Hq, Hkv, total_q, d, scale)) != ATTN_OK) return rc;
+  if (Hq > 65535) return fail(ATTN_ERR_UNSUPPORTED, "Hq=%d: packed sequences support at most 65535 heads", Hq);
+  if (B == 0 || total_q == 0) return ATTN_OK;
+  if (max_q < 1 || max_q > total_q)
+    return fail(ATTN_ERR_INVALID_ARG, "max_q=%d must be between 1 and the %d packed queries", max_q, total_q);
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens_q || !kv_lens || !o || !lse)
+    return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(o) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(ATTN_ERR_MISALIGNED, "q, o and the cache must be 16-byte aligned");
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) || !aligned4(cu_seqlens_q) ||
+      !aligned4(kv_lens) || !aligned4(lse))
+    return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets, lengths and lse must be 4-byte aligned");
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  const int sms = std::max(1, s->sms);
+  const size_t need = cache_workspace_bytes(B, Hq, Hkv, total_q, max_q, d, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  if (need > 0 && !aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  CacheParams p{};
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale; p.v_scale = v_scale;
+  p.table = page_table; p.cu_q = cu_seqlens_q; p.kv_lens = kv_lens;
+  p.o = o; p.lse = lse;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.total_q = total_q; p.max_q = max_q;
+  p.num_pages = num_pages; p.page = page_size; p.max_pages = max_pages; p.max_len = max_pages * page_size;
+  p.causal = causal ? 1 : 0;
+  p.c = scale * 1.4426950408889634f;
+  p.ws = workspace;
+  p.wait_ns = (unsigned long long)g_wait_ns.load();
+  p.status = s->status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_fwd_cache(p, d, sms, st);
+  if (e != cudaSuccess) return cuda_fail(e, "cached attention launch");
   return post_launch(s, st);
 }
 

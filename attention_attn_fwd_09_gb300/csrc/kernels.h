@@ -31,7 +31,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // Device status word codes (see attn_device_status).  Kernels never trap: a kernel that
 // gives up on a bounded wait, or finds its device-side arguments invalid, writes one of
 // these and returns.
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_OFFSETS = 2 };
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_OFFSETS = 2, DEV_BAD_PAGE = 3 };
 
 struct FwdParams {
   int B, Hq, Hkv, N, g;      // N: query length
@@ -171,5 +171,52 @@ void bwd_workspace_carve(void* ws, int B, int Hq, int Hkv, int N, int d, int det
 size_t bwd_wide_workspace_bytes(int B, int Hq, int N, int d, int deterministic);
 void bwd_wide_workspace_carve(void* ws, int B, int Hq, int N, int d, int deterministic, BwdParams* p);
 cudaError_t launch_bwd_wide(const BwdMaps& maps, const BwdParams& p, cudaStream_t stream);
+
+// Rotary positions (rope.cu).  Element strides of batch, head and token; columns contiguous.
+struct RopeTensor {
+  const void* in;
+  void* out;
+  long long in_b, in_h, in_n, out_b, out_h, out_n;
+};
+struct RopeParams {
+  RopeTensor q, k;           // k unused when Hk = 0
+  const double* inv_freq;    // [rot / 2] radians per position (device)
+  const int* positions;      // [B, N] (device) or null: 0 .. N - 1
+  int B, N, Hq, Hk, d, rot;
+  float mscale, sign;        // factor on the rotated part; +1 forward, -1 transposed
+  int tile, tiles, head_group;   // filled in by launch_rope: tokens per CTA, tiles per sequence, heads per CTA
+};
+// vec: elements per access (8, 4 or 1) that every pointer, stride and rot allow.
+cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s);
+
+// Rows into the paged e4m3 cache (kv_append.cu); d = 64 or 128, page = 16, 32, 64 or 128.
+struct AppendParams {
+  const void *k, *v;         // bf16 [Hkv, total, d], strides in elements, columns contiguous
+  long long k_h, k_t, v_h, v_t;
+  void *k_cache, *v_cache;   // [num_pages, Hkv, page, d] e4m3
+  float *k_scale, *v_scale;  // [num_pages, Hkv]
+  const int *table, *cu, *kv_lens;   // [B, max_pages], [B + 1], [B]
+  int B, Hkv, total, num_pages, page, max_pages, max_len;
+  int* status;
+};
+cudaError_t launch_kv_append(const AppendParams& p, int d, cudaStream_t s);
+
+// Packed queries over the paged e4m3 cache (fwd_cache.cu).
+struct CacheParams {
+  const void* q;             // bf16 [Hq, total_q, d]
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int *table, *cu_q, *kv_lens;
+  void* o;                   // bf16 [Hq, total_q, d]
+  float* lse;                // [Hq, total_q], natural log
+  int B, Hq, Hkv, g, total_q, max_q, num_pages, page, max_pages, max_len;   // max_len = max_pages * page
+  int causal;
+  float c;                   // scale * log2(e)
+  void* ws;
+  unsigned long long wait_ns;
+  int* status;
+};
+size_t cache_workspace_bytes(int B, int Hq, int Hkv, int total_q, int max_q, int d, int sms);
+cudaError_t launch_fwd_cache(const CacheParams& p, int d, int sms, cudaStream_t s);
 
 }  // namespace attn

@@ -1,0 +1,180 @@
+// Rotary positions of Q and K, and the transposed rotation of their gradients.
+//
+// A pair (a, b) of a head at position p turns by the angle t = p f_j:
+//     y_a = m (a cos t - b sin t),   y_b = m (b cos t + a sin t)
+// with the pairs (x_j, x_{j + rot/2}) (half-split) or (x_2j, x_2j+1) (interleaved), f_j the
+// pair's frequency and m one factor for the rotated part; columns rot .. d-1 pass through.
+// The gradient takes the transposed rotation: the same with sin t negated.
+//
+// Angles: f_j comes in 64 bits (radians per position).  A CTA turns it once into a
+// fixed-point number F_j = f_j / 2 pi mod 1 in units of 2^-64 turns; p F_j mod 2^64 is then
+// an exact integer product, its upper 32 bits the angle in turns with the whole turns
+// already dropped, so position 10^6 is as exact as position 1 and no argument reduction is
+// needed (sincospif of a number in [-1, 1)).  fp32 p f_j would be wrong by 0.06 rad there.
+//
+// Bound by bytes (2 read and 2 written per element).  A CTA takes a tile of tokens of one
+// sequence and every head of them: the cosines and sines are computed once per token into
+// shared memory and used by all heads of Q and K.
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+// V bf16 values (V = 8, 4, 1) as 32-bit words / one half word.
+template <int V>
+struct BfVec {
+  uint32_t w[V / 2];
+};
+template <>
+struct BfVec<1> {
+  uint16_t w[1];
+};
+template <int V>
+__device__ __forceinline__ BfVec<V> ld_vec(const uint16_t* p) {
+  BfVec<V> r;
+  if constexpr (V == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+  } else if constexpr (V == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = u.x; r.w[1] = u.y;
+  } else {
+    r.w[0] = *p;
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void st_vec(uint16_t* p, const BfVec<V>& r) {
+  if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+  else *p = r.w[0];
+}
+template <int V>
+__device__ __forceinline__ void unpack(const BfVec<V>& r, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = __uint_as_float(uint32_t(r.w[0]) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(r.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ BfVec<V> pack(const float (&f)[V]) {
+  BfVec<V> r;
+  if constexpr (V == 1) {
+    r.w[0] = (uint16_t)(pack_bf16x2(f[0], 0.f) & 0xffffu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  }
+  return r;
+}
+
+// A work item is 2 V elements of one head row: half-split columns j .. j+V-1 with their
+// partners at + rot/2, interleaved columns c .. c+2V-1, or 2 V columns of the part that
+// passes through.  V = 8 needs rot % 16 == 0 and 16-byte rows, V = 4 rot % 8 == 0 and 8-byte
+// rows; V = 1 takes every even rot and alignment.
+template <int V, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  extern __shared__ float2 cs[];                       // [tokens][rot / 2] (m cos, m sin)
+  unsigned long long* turn = reinterpret_cast<unsigned long long*>(cs + p.tile * (p.rot / 2));   // [rot / 2]
+  const int half = p.rot / 2;
+  const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x % p.tiles) * p.tile;
+  const int tn = min(p.tile, p.N - n0);
+  const int h0 = blockIdx.y * p.head_group, hn = min(p.head_group, p.Hq + p.Hk - h0);
+  for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+    const double t = p.inv_freq[j] * 0.15915494309189535;          // turns per position
+    turn[j] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tn * half; i += kRopeThreads) {
+    const int n = i / half, j = i - n * half;
+    const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : n0 + n;
+    const unsigned long long ph = turn[j] * (unsigned long long)pos;
+    float s, c;
+    sincospif(__int2float_rn((int)(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+    cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+  }
+  __syncthreads();
+  const int upr = p.d / (2 * V);                       // items per head row
+  const int items = tn * hn * upr;
+  for (int i = threadIdx.x; i < items; i += kRopeThreads) {
+    const int u = i % upr, r = i / upr;
+    const int n = r % tn, h = h0 + r / tn;
+    const bool is_q = h < p.Hq;
+    const int hh = is_q ? h : h - p.Hq;
+    const RopeTensor& t = is_q ? p.q : p.k;
+    const uint16_t* src = static_cast<const uint16_t*>(t.in) + b * t.in_b + hh * t.in_h + (long long)(n0 + n) * t.in_n;
+    uint16_t* dst = static_cast<uint16_t*>(t.out) + b * t.out_b + hh * t.out_h + (long long)(n0 + n) * t.out_n;
+    const bool rotated = INTER ? u * 2 * V < p.rot : u * V < half;
+    const int ca = (INTER || !rotated) ? u * 2 * V : u * V;
+    const int cb = (INTER || !rotated) ? ca + V : ca + half;
+    const BfVec<V> a = ld_vec<V>(src + ca), bb = ld_vec<V>(src + cb);
+    if (!rotated) {
+      st_vec<V>(dst + ca, a);
+      st_vec<V>(dst + cb, bb);
+      continue;
+    }
+    float x[V], y[V], xo[V], yo[V];
+    unpack<V>(a, x);
+    unpack<V>(bb, y);
+    if constexpr (INTER && V > 1) {
+      const float2* w = cs + n * half + u * V;         // 2 V columns hold V pairs
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const float2 e = w[k], f = w[V / 2 + k];
+        xo[2 * k] = x[2 * k] * e.x - x[2 * k + 1] * e.y;
+        xo[2 * k + 1] = x[2 * k + 1] * e.x + x[2 * k] * e.y;
+        yo[2 * k] = y[2 * k] * f.x - y[2 * k + 1] * f.y;
+        yo[2 * k + 1] = y[2 * k + 1] * f.x + y[2 * k] * f.y;
+      }
+    } else {
+      const float2* w = cs + n * half + u * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        xo[k] = x[k] * w[k].x - y[k] * w[k].y;
+        yo[k] = y[k] * w[k].x + x[k] * w[k].y;
+      }
+    }
+    st_vec<V>(dst + ca, pack<V>(xo));
+    st_vec<V>(dst + cb, pack<V>(yo));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s) {
+  // Tokens per CTA: 8 when that still gives every SM work (the cosines and sines of a token
+  // are then shared by all heads), else one token per CTA and the heads split over CTAs so
+  // that each thread has about one item.
+  const int upr = p.d / (2 * vec), heads = p.Hq + p.Hk;
+  p.tile = (long long)p.B * ((p.N + 7) / 8) >= sms ? 8 : 1;
+  p.tiles = (p.N + p.tile - 1) / p.tile;
+  p.head_group = p.tile > 1 ? heads : (kRopeThreads + upr - 1) / upr;
+  const long long gx = (long long)p.B * p.tiles;
+  const int gy = (heads + p.head_group - 1) / p.head_group;
+  if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidValue;
+  const size_t smem = (size_t)(p.tile + 1) * (p.rot / 2) * sizeof(float2);
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  auto go = [&](auto kern) { kern<<<grid, kRopeThreads, smem, s>>>(p); };
+  if (interleaved) {
+    if (vec == 8) go(rope_kernel<8, true>);
+    else if (vec == 4) go(rope_kernel<4, true>);
+    else go(rope_kernel<1, true>);
+  } else {
+    if (vec == 8) go(rope_kernel<8, false>);
+    else if (vec == 4) go(rope_kernel<4, false>);
+    else go(rope_kernel<1, false>);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace attn

@@ -128,6 +128,92 @@ int attn_fwd_fp8(const void* q8, const void* k8, const void* v8, const float* q_
 size_t attn_fwd_kv_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 
 /*
+ * Rotary positions of Q and K, in the layout the attention calls take or on the way to it.
+ * A pair (a, b) of a head's columns at position p turns by p * inv_freq[j]:
+ *     y_a = mscale (a cos - b sin),  y_b = mscale (b cos + a sin),
+ * where the pairs are columns (j, j + rot/2), or (2j, 2j+1) when interleaved, j < rot/2.
+ * Columns rot .. d-1 are copied.  No counterpart on the pages: they start from rotated Q, K.
+ *
+ *   q, k [B,H,N,d] bf16 in, q_out, k_out bf16 out, rounded once; k and k_out may be NULL with
+ *       Hk = 0.  An output may be its own input (equal strides: in place); otherwise inputs
+ *       and outputs do not overlap.
+ *   strides: NULL for contiguous [B,H,N,d] tensors, or a HOST array of 12 element strides,
+ *       {q, k, q_out, k_out} x {batch, head, token}; the d columns are contiguous.  The views
+ *       of a fused projection [B,N,H,d] need no copy.  Rows that start on 16 bytes are fastest
+ *       (with rot a multiple of 16); any 2-byte aligned ones work.
+ *   inv_freq: DEVICE fp64 [rot/2], radians per position (scaling for long contexts is in these
+ *       values and in mscale).  The angle is exact to 2^-32 turns plus 2^-52 of p * inv_freq.
+ *   positions: DEVICE int32 [B,N], or NULL for 0 .. N-1.
+ *   d: 64, 128, 192 or 256; rot even, 2 .. d; mscale finite.
+ * Packed sequences ([H, total, d]): B = 1, N = total and the positions of each row.
+ */
+int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const int* positions,
+              int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale, const long long* strides,
+              void* stream);
+
+/*
+ * Gradient of attn_rope: dq, dk of the rotated tensors in, gradients of the unrotated ones out
+ * (the transposed rotation, mscale kept).  Arguments as attn_rope.
+ */
+int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const double* inv_freq,
+                  const int* positions, int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale,
+                  const long long* strides, void* stream);
+
+/*
+ * Paged 8-bit key/value cache.  k_cache and v_cache are [num_pages, Hkv, page_size, d] e4m3
+ * codes (one byte each), k_scale and v_scale [num_pages, Hkv] fp32: the value of an element is
+ * decode(code) * scale of its page and head.  Row t of sequence b is row t % page_size of page
+ * page_table[b][t / page_size]; page_table is a DEVICE int32 array [B, max_pages], of which only
+ * the entries that a sequence's length reaches are read.  kv_lens, DEVICE int32 [B]: the rows of
+ * each sequence AFTER the call (appending) or at the call (attention).  d: 64 or 128;
+ * page_size: 16, 32, 64 or 128.
+ *
+ * attn_kv_append_fp8: appends the packed rows k, v [Hkv, total, d] bf16: rows cu_seqlens[b] ..
+ *   cu_seqlens[b+1]-1 (n of them; DEVICE int32, B + 1 offsets) become rows kv_lens[b] - n ..
+ *   kv_lens[b] - 1 of sequence b.  Per page and head touched, with amax the largest finite |x|
+ *   of the new rows: scale = the smallest power of two with amax / scale <= 448 (0 for amax =
+ *   0), code = e4m3(x / scale) rounded to nearest even, infinities saturated to +-448, NaN kept.
+ *   Where earlier rows stay in the page its scale may only grow, and if it does their codes are
+ *   rounded again at the new scale.  Rows behind the last one are left as they were.
+ *   strides: NULL for contiguous rows, or a HOST array {k head, k token, v head, v token} of
+ *   element strides (multiples of 8).  A page that receives rows belongs to one sequence.
+ * Errors as attn_fwd_varlen: the offsets and lengths are checked on the device (offsets as
+ *   there; n <= kv_lens[b] <= max_pages * page_size); if they break a rule nothing is written
+ *   and the device status word reads ATTN_ERR_INVALID_ARG.  It reads the same when an entry of
+ *   the page table in use is outside 0 .. num_pages-1; such a page is neither read nor written.
+ */
+int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hkv, int total,
+                       int d, int num_pages, int page_size, int max_pages, const long long* strides, void* stream);
+
+/*
+ * Forward of packed queries over the paged 8-bit cache: O = softmax(scale Q K~^T [causal]) V~ and
+ * LSE, K~ and V~ the dequantised rows.  Decoding (one query per sequence), drafts of a few tokens
+ * and pieces of prompts, mixed freely.  Query i of sequence b's n stands at key position
+ * i + kv_lens[b] - n (causal: it sees keys up to there; otherwise all kv_lens[b]).
+ *
+ *   q, o [Hq, total_q, d] bf16; lse [Hq, total_q] fp32 (natural log); cu_seqlens_q as
+ *       attn_fwd_varlen; the cache as above.
+ *   max_q: an upper bound on the queries of one sequence (1 when decoding).
+ *   scales finite and >= 0.  Codes of rows behind kv_lens[b] are never used, whatever they are.
+ *   A query that sees no key (kv_lens[b] = 0, not causal) gets O = 0 and LSE = -inf.
+ *   workspace: device memory of attn_fwd_kv_fp8_workspace_size(...) bytes, 16-byte aligned, owned
+ *       by the caller, contents on entry irrelevant.
+ * Errors as attn_kv_append_fp8's (with causal: n <= kv_lens[b]; and n <= max_q), plus
+ *   ATTN_ERR_WORKSPACE; the results of a sequence with a bad page are undefined.
+ */
+int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o,
+                    float* lse, int B, int Hq, int Hkv, int total_q, int max_q, int d, int num_pages, int page_size,
+                    int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_fwd_kv_fp8 needs on the current device: depends on these sizes only,
+ * not on the lengths; (size_t)-1 for invalid sizes.
+ */
+size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d);
+
+/*
  * Forward over B packed sequences of different lengths ("FlashAttention-4 explained"
  * page, section 06: sequences of different lengths, the CTAs with the most work started
  * first).  Each sequence is its own attention problem; sequence b owns query rows
@@ -314,7 +400,7 @@ int attn_set_test_hooks(int skip_first_kv_load);
 /*
  * Synchronises the current device and reads the device status word: ATTN_OK,
  * ATTN_ERR_TIMEOUT if some kernel gave up on a wait since the last clear, or
- * ATTN_ERR_INVALID_ARG if attn_fwd_varlen's offsets failed their device check.
+ * ATTN_ERR_INVALID_ARG if a packed call's offsets, lengths or pages failed their device check.
  * clear = 1 resets the word.
  */
 int attn_device_status(int clear);
