@@ -1,8 +1,31 @@
-// Attention of packed queries over a paged e4m3 cache.
+// Attention of packed queries over a paged e4m3 cache: few query rows per K/V head (decoding,
+// drafts of a few tokens).  Up to 16 rows, the n queries x g heads that share a K/V head, are
+// one row tile (row r: query r / g, head r % g); the work is the cache, read once.
 //
-// O_i = sum_j softmax_j(scale q_i . k_j sk) v_j sv over the keys j <= i + len - n (causal) or
-// j < len; one warp per query row and head, 32 keys at a time with a running maximum and sum.
+// What bounds it: the cache's bytes (2 d per key and K/V head).  So
+//   * Work is cut by keys, not by sequences: all units (sequence, K/V head) laid end to end in
+//     32-key pieces, every CTA takes the same number of consecutive pieces (lengths differ and
+//     are known on the device only: each CTA adds them up itself).  A unit cut between CTAs
+//     leaves partial results that fwd_cache_merge_kernel joins.
+//   * A CTA has 4 warps and an SM two CTAs; each warp is on its own: it takes every fourth
+//     piece, keeps a ring of pieces in flight with TMA (96 KB per CTA) and never waits for the
+//     other warps until a unit ends.
+//   * A piece goes from shared memory to registers in the layout the matrix instruction wants:
+//     S = Q K^T and O += P V with mma.m16n8k16 in f16.  e4m3 widens to f16 exactly.  Both key
+//     and column orders inside a piece are free (a sum does not mind, as long as P and V, or Q
+//     and K, agree), which turns every fragment into whole 16-byte loads: a thread's share of a
+//     K row is 16 neighbouring columns, its share of V 16 neighbouring columns of a key, and
+//     pairs of keys are interleaved by byte permutes.  The key order within 8 (d = 128) or 16
+//     (d = 64) rows is chosen so that under TMA's 128-byte swizzle both kinds of load touch
+//     every bank once.
+//
+// Numbers: q is scaled by a power of two per row (largest |q| in [1, 2)) and held in f16,
+// exact but for components 2^14 below the row's largest.  exp2(s - m + 14) <= 2^14 times the
+// page's V scale over the largest V scale so far is rounded to f16 (11 bits, against 8 of a
+// bf16 weight; the 2^14 keeps weights down to 2^-28 of the largest normal).  Scores, maxima,
+// sums and O are fp32.
 #include <cstdint>
+#include <mutex>
 
 #include "cache.cuh"
 #include "kernels.h"
@@ -11,97 +34,625 @@
 namespace attn {
 namespace {
 
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kPiece = 32;                   // keys per piece
+constexpr float kShift = 14.f;               // weights are held times 2^14
+constexpr float kMinScale = 1.17549435e-38f; // 2^-126: the V scale reference never is 0
+constexpr float kLn2 = 0.6931471805599453f;
+
 template <int D>
-__global__ void __launch_bounds__(128) fwd_cache_simple_kernel(const CacheParams p) {
-  __shared__ float qs[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x;
-  int b = -1;
-  bool bad = false;
-  for (int base = 0; base < p.B; base += 128) {
-    const int i = base + threadIdx.x;
-    bool below = false, wrong = false;
-    if (i < p.B) {
-      const int c0 = p.cu_q[i], c1 = p.cu_q[i + 1], len = p.kv_lens[i];
-      wrong = c1 < c0 || c0 < 0 || c1 - c0 > p.max_q || len < 0 || len > p.max_len || (p.causal && c1 - c0 > len) ||
-              (i == 0 && c0 != 0) || (i == p.B - 1 && c1 != p.total_q);
-      below = c0 <= t;
+struct DecCfg {
+  static constexpr int KB = kPiece * D;            // bytes of a piece of K (and of V)
+  static constexpr int STAGES = D == 128 ? 3 : 6;  // pieces per warp: 24 KB
+  static constexpr int RING = kWarps * STAGES * 2 * KB;
+  static constexpr int NACC = D / 8;               // O column blocks of 8
+  static constexpr int SLOT = 32 * 4 * (NACC * 4); // one warp's O registers
+  static constexpr int OFF_MERGE = RING;
+  static constexpr int OFF_STAT = OFF_MERGE + 2 * SLOT;   // [2][8] float4 (m, m, l, l of rows i, i + 8), then [2] r
+  static constexpr int OFF_BAR = OFF_STAT + 2 * 8 * 16 + 16;
+  static constexpr int OFF_MISC = OFF_BAR + kWarps * STAGES * 8;
+  static constexpr int SMEM = OFF_MISC + 64;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// Workspace: header (256 bytes: [0] 1 when the device checks passed), per unit {first CTA, CTAs},
+// per partial (two per CTA: its first and its last unit) 16 rows of (m, l, r, -), then O rows.
+struct DecWs {
+  size_t rec, stat, part, total;
+};
+__host__ __device__ inline DecWs dec_ws(int B, int Hkv, int rows, int d, int ctas) {
+  DecWs w;
+  w.rec = 256;
+  w.stat = (w.rec + (size_t)B * Hkv * 8 + 255) & ~size_t(255);
+  w.part = w.stat + (size_t)ctas * 2 * rows * 16;
+  w.part = (w.part + 255) & ~size_t(255);
+  w.total = w.part + (size_t)ctas * 2 * rows * d * 4;
+  return w;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {
+  const int n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
+  return n > 0 ? max(1, (__ldg(p.kv_lens + b) + kPiece - 1) / kPiece) : 0;
+}
+
+// Where a warp is in the CTA's run of pieces.
+struct Cursor {
+  int b, h;
+  long long f, ubeg, uend;                   // piece, and the unit's first and last + 1
+  __device__ __forceinline__ void settle(const CacheParams& p, long long end) {   // into the unit that holds f
+    while (f < end && f >= uend) {
+      ubeg = uend;
+      if (++h == p.Hkv) {
+        h = 0;
+        int np;
+        do np = pieces_of(p, ++b);           // f < end: there is another unit
+        while (np == 0);
+        uend = ubeg + np;
+      } else {
+        uend = ubeg + pieces_of(p, b);
+      }
     }
-    bad |= __syncthreads_or(wrong) != 0;
-    b += __syncthreads_count(below);
   }
-  if (bad) {
-    if (threadIdx.x == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
-    return;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    fwd_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const CacheParams p, const int rows_max) {
+  using C = DecCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = lane & 3, rq = lane >> 2;    // fragment column group and row
+  long long* misc = reinterpret_cast<long long*>(smem + C::OFF_MISC);   // [4] warp sums / [0] b, [1] unit start
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 48);
+  const uint32_t bars = smem_u32(smem + C::OFF_BAR) + warp * C::STAGES * 8;
+  const WaitCtl wc{p.wait_ns, p.status, abort_flag};
+  const DecWs W = dec_ws(p.B, p.Hkv, rows_max, D, gridDim.x);
+  char* ws = static_cast<char*>(p.ws);
+  pdl_trigger();
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kWarps * C::STAGES; ++i) mbar_init(smem_u32(smem + C::OFF_BAR) + 8 * i, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  const int n = p.cu_q[b + 1] - p.cu_q[b], len = p.kv_lens[b];
-  const int vis = p.causal ? t - p.cu_q[b] + len - n + 1 : len;
-  for (int h = blockIdx.y * 4 + warp; h < p.Hq; h += gridDim.y * 4) {
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((long long)h * p.total_q + t) * D;
-    for (int c = lane; c < D; c += 32) qs[warp][c] = __uint_as_float(uint32_t(q[c]) << 16);
+
+  // ---- the run of pieces of this CTA; thread t adds up sequences [t per_thread, ...)
+  const int per_thread = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
+  long long mine = 0;
+  bool wrong = false;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b), n = c1 - c0;
+    wrong |= c0 < 0 || c1 < c0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
+             (b == 0 && c0 != 0) || (b == p.B - 1 && c1 != p.total_q);
+    if (n > 0) mine += max(1, (len + kPiece - 1) / kPiece);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) misc[warp] = incl;
+  const bool bad = __syncthreads_or(wrong) != 0;
+  if (blockIdx.x == 0 && tid == 0) {
+    *reinterpret_cast<int*>(ws) = bad ? 0 : 1;
+    if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
+  }
+  if (bad) return;
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += misc[w];
+    total += misc[w];
+  }
+  total *= p.Hkv;
+  before *= p.Hkv;
+  mine *= p.Hkv;
+  // Equal runs, but a piece for every warp at least: a shorter run would only add partial results.
+  const long long run = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
+  const long long rs = run * blockIdx.x, re = min(rs + run, total);
+  if (rs >= total) return;
+  __syncthreads();                           // misc has been read
+  if (before <= rs && rs < before + mine) {
+    int b = b_lo;
+    long long at = before;
+    for (;;) {
+      const long long step = (long long)pieces_of(p, b) * p.Hkv;
+      if (rs < at + step) break;
+      at += step;
+      ++b;
+    }
+    misc[0] = b;
+    misc[1] = at;
+  }
+  __syncthreads();
+  Cursor seg;                                // the unit being worked on
+  seg.b = (int)misc[0];
+  {
+    const int np = pieces_of(p, seg.b);
+    seg.h = (int)((rs - misc[1]) / np);
+    seg.ubeg = misc[1] + (long long)seg.h * np;
+    seg.uend = seg.ubeg + np;
+    seg.f = rs;
+  }
+
+  // ---- this warp's loads, STAGES pieces ahead of its work
+  const int page_shift = 31 - __clz(p.page);
+  const int grp = lane & 1;                  // half of a piece (16 keys) this lane looks after
+  uint8_t* ring = smem + warp * C::STAGES * 2 * C::KB;
+  Cursor ahead = seg;
+  ahead.f = rs + warp;
+  ahead.settle(p, re);
+  // The page of this lane's half of the piece at `ahead`: -1 behind the last key, -2 bad.
+  auto page_at = [&]() -> int {
+    if (ahead.f >= re) return -1;
+    const int key = (int)(ahead.f - ahead.ubeg) * kPiece + grp * 16;
+    if (key >= __ldg(p.kv_lens + ahead.b)) return -1;
+    const int pg = __ldg(p.table + (long long)ahead.b * p.max_pages + (key >> page_shift));
+    if (pg < 0 || pg >= p.num_pages) {
+      atomicExch(p.status, DEV_BAD_PAGE);
+      return -2;
+    }
+    return pg;
+  };
+  // Scale of this lane's half: K for lanes with bit 1 clear, V with it set.
+  auto scale_of = [&](int pg, int h) -> float {
+    return pg >= 0 ? __ldg(((lane & 2) ? p.v_scale : p.k_scale) + (long long)pg * p.Hkv + h) : 0.f;
+  };
+  auto issue = [&](int stage, int pg) {
+    // Pages of 16 rows: two boxes, by lanes 0 and 1; larger ones hold the whole piece.
+    const int p0 = __shfl_sync(0xffffffffu, pg, 0), p1 = __shfl_sync(0xffffffffu, pg, 1);
+    const bool two = p.page == 16;
+    const uint32_t bar = bars + 8 * stage;
+    const uint32_t box = two ? C::KB / 2 : C::KB;
+    if (lane == 0) {
+      const int boxes = (p0 >= 0 ? 1 : 0) + (two && p1 >= 0 ? 1 : 0);
+      mbar_arrive_expect_tx(bar, boxes * 2 * box);
+    }
     __syncwarp();
-    const int hk = h / p.g;
-    float m = -INFINITY, l = 0.f, o[D / 32];
-    for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
-    for (int k0 = 0; k0 < vis; k0 += 32) {
-      const int key = k0 + lane;
-      float s = -INFINITY, sv = 0.f;
-      const uint8_t* vrow = nullptr;
-      if (key < vis) {
-        const int page = p.table[(long long)b * p.max_pages + key / p.page];
-        if (page < 0 || page >= p.num_pages) {
-          atomicExch(p.status, DEV_BAD_PAGE);
-        } else {
-          const long long ph = (long long)page * p.Hkv + hk;
-          const long long row = (ph * p.page + key % p.page) * D;
-          vrow = p.v_cache + row;
-          sv = p.v_scale[ph];
-          float acc = 0.f;
-          for (int c = 0; c < D; c += 4) {
-            float x0, x1, x2, x3;
-            e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(p.k_cache + row + c), x0, x1, x2, x3);
-            acc += qs[warp][c] * x0 + qs[warp][c + 1] * x1 + qs[warp][c + 2] * x2 + qs[warp][c + 3] * x3;
+    if (lane < (two ? 2 : 1) && pg >= 0) {
+      const int key = (int)(ahead.f - ahead.ubeg) * kPiece + lane * 16;
+      const int line = (key & (p.page - 1)) * D / 128;
+      const int z = pg * p.Hkv + ahead.h;
+      const uint32_t dst = smem_u32(ring + stage * 2 * C::KB) + lane * box;
+      tma_load_3d(dst, &tm_k, 0, line, z, bar);
+      tma_load_3d(dst + C::KB, &tm_v, 0, line, z, bar);
+    }
+  };
+  int pages[C::STAGES + 1], heads[C::STAGES + 1];     // of the pieces under way, oldest first; one more looked up
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i <= C::STAGES; ++i) {
+    pages[i] = page_at();
+    heads[i] = ahead.h;
+    if (i < C::STAGES) {
+      if (ahead.f < re) issue(i, pages[i]);
+      ahead.f += kWarps;
+      ahead.settle(p, re);
+    }
+  }
+  // `ahead` now stands at piece number STAGES of this warp, whose page is pages[STAGES].
+  float sc_next = scale_of(pages[0], heads[0]);
+  int stage = 0;
+  uint32_t phase = 0;
+  long long f = rs + warp;                   // this warp's next piece
+
+  // Shared-memory offsets of this thread's fragments within a piece.
+  uint32_t koff[2], voff[2];
+  if constexpr (D == 128) {
+    const int kr = (rq & 1) ? (((rq - 1) ^ 4) + 1) : rq;          // row of fragment column rq: 0 5 2 7 4 1 6 3
+    koff[0] = kr * 128 + ((c ^ kr) << 4);
+    koff[1] = kr * 128 + (((c + 4) ^ kr) << 4);
+    const int v0 = 2 * c, v1 = ((2 * c) ^ 4) + 1;
+    voff[0] = v0 * 128 + ((rq ^ v0) << 4);
+    voff[1] = v1 * 128 + ((rq ^ v1) << 4);
+  } else {
+    // Two rows of 64 bytes share a 128-byte line; within 16 rows fragment columns 2i, 2i+1 of the
+    // first block are rows 4i, 4i+1 and of the second block rows 4i+2, 4i+3.
+    const int line = (rq >> 1) * 2, half = rq & 1;
+    koff[0] = line * 128 + (((half * 4 + c) ^ line) << 4);                    // first block
+    koff[1] = (line + 1) * 128 + (((half * 4 + c) ^ (line + 1)) << 4);        // second block
+    const int vl = 2 * c;
+    voff[0] = vl * 128 + (((rq >> 1) ^ vl) << 4) + (rq & 1) * 8;              // first block, row 4c
+    voff[1] = (vl + 1) * 128 + (((rq >> 1) ^ (vl + 1)) << 4) + (rq & 1) * 8;  // second block, row 4c + 2
+  }
+
+  const int g = p.g;
+  // ---- units
+  while (seg.f < re) {
+    const int q0 = __ldg(p.cu_q + seg.b), n = __ldg(p.cu_q + seg.b + 1) - q0, len = __ldg(p.kv_lens + seg.b);
+    const long long send = min(seg.uend, re);
+    const int rows = n * g;
+    // Visible keys of this thread's two rows.
+    int lim[2];
+    float crow[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rq + 8 * i, qi = r / g;
+      lim[i] = p.causal && r < rows ? len - n + qi + 1 : len;
+      uint4 w[D / 32];
+      float amax = 0.f;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                            ((long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi) * D + c * 16;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {     // 16 columns at 16 c, and for d = 128 at 64 + 16 c
+        w[k] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + (k >> 1) * 64) + (k & 1)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          amax = fmax3(amax, fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const uint32_t e = __float_as_uint(amax) >> 23;              // biased exponent
+      const bool usable = e > 0 && e < 254;                        // else (0, tiny, inf) leave the row as it is
+      const float inv = usable ? __uint_as_float((254u - e) << 23) : 1.f;
+      crow[i] = p.c * (usable ? __uint_as_float(e << 23) : 1.f);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h2 = pack_f16x2(__uint_as_float(u[j] << 16) * inv, __uint_as_float(u[j] & 0xffff0000u) * inv);
+          // columns 16 c + 4 (step & 3) + {0, 1} are fragment columns 2c, 2c + 1, + {2, 3} are 2c + 8, 2c + 9
+          const int word = (k & 1) * 4 + j;
+          qf[(k >> 1) * 4 + (word >> 1)][(word & 1) * 2 + i] = h2;
+        }
+      }
+    }
+    const int min_lim = p.causal ? len - n + 1 : len;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, rref = kMinScale, rinv = 1.f / kMinScale;
+    float o[C::NACC][4];
+#pragma unroll
+    for (int i = 0; i < C::NACC; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    // ---- this warp's pieces of the unit
+    for (; f < send; f += kWarps) {
+      const float sc = sc_next;
+      const int key0 = (int)(f - seg.ubeg) * kPiece;
+      const int pg = pages[0];
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phase, wc))) {
+        // A wait ran out: this warp loads and computes no more.  Its copies under way land first.
+        ok = false;
+        const unsigned long long t0 = globaltimer_ns();
+        for (int k = 0; k < C::STAGES; ++k) {
+          const int st = stage + k < C::STAGES ? stage + k : stage + k - C::STAGES;
+          const uint32_t par = stage + k < C::STAGES ? phase : phase ^ 1u;
+          if (f + (long long)k * kWarps < re)
+            while (!mbar_try_wait(bars + 8 * st, par) && globaltimer_ns() - t0 < p.wait_ns) {
+            }
+        }
+        __syncwarp();
+      }
+      sc_next = scale_of(pages[1], heads[1]);
+      if (ok) {
+        const uint8_t* kt = ring + stage * 2 * C::KB;
+        const uint8_t* vt = kt + C::KB;
+        float s[4][4];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+          s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+          if constexpr (D == 128) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint4 w = *reinterpret_cast<const uint4*>(kt + nb * 1024 + koff[k]);
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_f16(s[nb], qf[k * 4 + j][0], qf[k * 4 + j][1], qf[k * 4 + j][2], qf[k * 4 + j][3], e4m3x2_f16x2(u[j]),
+                        e4m3x2_f16x2_hi(u[j]));
+            }
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(kt + (nb >> 1) * 1024 + koff[nb & 1]);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f16(s[nb], qf[j][0], qf[j][1], qf[j][2], qf[j][3], e4m3x2_f16x2(u[j]), e4m3x2_f16x2_hi(u[j]));
           }
-          s = acc * (p.k_scale[ph] * p.c);
+        }
+        const float ks[2] = {__shfl_sync(0xffffffffu, sc, 0), __shfl_sync(0xffffffffu, sc, 1)};
+        const float vs[2] = {__shfl_sync(0xffffffffu, sc, 2), __shfl_sync(0xffffffffu, sc, 3)};
+        const bool got0 = __shfl_sync(0xffffffffu, pg, 0) >= 0, got1 = __shfl_sync(0xffffffffu, pg, 1) >= 0;
+        const bool partial = key0 + kPiece > min_lim || !got0 || !got1;
+        // Key of fragment column 2c + e of block nb, relative to the piece.
+        auto key_of = [&](int nb, int e) -> int {
+          if constexpr (D == 128) return nb * 8 + (e ? ((2 * c) ^ 4) + 1 : 2 * c);
+          else return (nb >> 1) * 16 + 4 * c + 2 * (nb & 1) + e;
+        };
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nb][i] *= ks[nb >> 1] * crow[i >> 1];
+        if (partial) {
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + key_of(nb, i & 1) >= lim[i >> 1] || !((nb >> 1) ? got1 : got0)) s[nb][i] = -INFINITY;
+        }
+        float mx[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float a = fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]);
+          a = fmax3(a, s[1][2 * i + 1], s[2][2 * i]);
+          a = fmax3(a, s[2][2 * i + 1], s[3][2 * i]);
+          a = fmaxf(a, s[3][2 * i + 1]);
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+          mx[i] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        }
+        const float vmax = fmaxf(vs[0], vs[1]);
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1]) || vmax > rref) {
+          float fac = 1.f;
+          if (vmax > rref) {
+            rinv = 1.f / vmax;
+            fac = rref * rinv;
+            rref = vmax;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[i], mx[i]);
+            const float alpha = mn == -INFINITY ? 1.f : ex2_mufu(m[i] - mn);
+            m[i] = mn;
+            l[i] *= alpha;
+#pragma unroll
+            for (int j = 0; j < C::NACC; ++j) {
+              o[j][2 * i] *= alpha * fac;
+              o[j][2 * i + 1] *= alpha * fac;
+            }
+          }
+        }
+        uint32_t pf[4][2];
+        const float vw[2] = {vs[0] * rinv, vs[1] * rinv};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float off = kShift - (m[i] == -INFINITY ? 0.f : m[i]);
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) {
+            const float a = ex2_mufu(s[nb][2 * i] + off), b = ex2_mufu(s[nb][2 * i + 1] + off);
+            l[i] += a + b;
+            pf[nb][i] = pack_f16x2(a * vw[nb >> 1], b * vw[nb >> 1]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // Rows of V behind the last key may hold any code (NaN too): their weight is 0, their value must be.
+          bool live[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            live[x] = key0 + key_of(2 * t + (x >> 1), x & 1) < len && (t ? got1 : got0);
+          if constexpr (D == 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              v[x] = *reinterpret_cast<const uint4*>(vt + t * 2048 + (x >> 1) * 1024 + voff[x & 1]);
+              if (partial && !live[x]) v[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            const uint32_t u[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                      {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a = __byte_perm(u[0][w], u[1][w], 0x5140), b = __byte_perm(u[0][w], u[1][w], 0x7362);
+              const uint32_t e = __byte_perm(u[2][w], u[3][w], 0x5140), d = __byte_perm(u[2][w], u[3][w], 0x7362);
+              mma_f16(o[4 * w], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2(a), e4m3x2_f16x2(e));
+              mma_f16(o[4 * w + 1], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2_hi(a), e4m3x2_f16x2_hi(e));
+              mma_f16(o[4 * w + 2], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2(b), e4m3x2_f16x2(d));
+              mma_f16(o[4 * w + 3], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2_hi(b), e4m3x2_f16x2_hi(d));
+            }
+          } else {
+            // Rows 4c and 4c + 1 (first block) are the halves of one line, as are 4c + 2, 4c + 3.
+            uint2 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              v[x] = *reinterpret_cast<const uint2*>(vt + t * 1024 + (voff[x >> 1] ^ ((x & 1) << 6)));
+              if (partial && !live[x]) v[x] = make_uint2(0u, 0u);
+            }
+            const uint32_t u[4][2] = {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}};
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t a = __byte_perm(u[0][w], u[1][w], 0x5140), b = __byte_perm(u[0][w], u[1][w], 0x7362);
+              const uint32_t e = __byte_perm(u[2][w], u[3][w], 0x5140), d = __byte_perm(u[2][w], u[3][w], 0x7362);
+              mma_f16(o[4 * w], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2(a), e4m3x2_f16x2(e));
+              mma_f16(o[4 * w + 1], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2_hi(a), e4m3x2_f16x2_hi(e));
+              mma_f16(o[4 * w + 2], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2(b), e4m3x2_f16x2(d));
+              mma_f16(o[4 * w + 3], pf[2 * t][0], pf[2 * t][1], pf[2 * t + 1][0], pf[2 * t + 1][1], e4m3x2_f16x2_hi(b), e4m3x2_f16x2_hi(d));
+            }
+          }
         }
       }
-      float mx = s;
-      for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
-      const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m - mu), e = exp2f(s - mu);
-      float sum = e;
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
-      l = l * alpha + sum;
-      m = mn;
-      for (int c = 0; c < D / 32; ++c) o[c] *= alpha;
-      for (int k = 0; k < 32; ++k) {
-        const float w = __shfl_sync(~0u, e * sv, k);
-        const uint8_t* vr = reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, (unsigned long long)vrow, k));
-        if (vr == nullptr) continue;
-        for (int c = 0; c < D / 32; ++c) {
-          const uint32_t f = e4m3x2_f16x2(vr[c * 32 + lane]);
-          o[c] += w * __low2float(*reinterpret_cast<const __half2*>(&f));
+      // The stage is read: the next piece into it.
+      __syncwarp();
+      if (ok && ahead.f < re) issue(stage, pages[C::STAGES]);
+#pragma unroll
+      for (int i = 0; i < C::STAGES; ++i) {
+        pages[i] = pages[i + 1];
+        heads[i] = heads[i + 1];
+      }
+      ahead.f += kWarps;
+      ahead.settle(p, re);
+      pages[C::STAGES] = page_at();
+      heads[C::STAGES] = ahead.h;
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // ---- the four warps' results of the unit into one (warp 0)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    float4* slots = reinterpret_cast<float4*>(smem + C::OFF_MERGE);
+    float4* stats = reinterpret_cast<float4*>(smem + C::OFF_STAT);
+    float* refs = reinterpret_cast<float*>(smem + C::OFF_STAT + 2 * 8 * 16);
+    auto put = [&](int slot) {
+#pragma unroll
+      for (int j = 0; j < C::NACC; ++j) slots[(slot * C::NACC + j) * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      if (c == 0) stats[slot * 8 + rq] = make_float4(m[0], m[1], l[0], l[1]);
+      if (lane == 0) refs[slot] = rref;
+    };
+    auto take = [&](int slot) {
+      const float4 st = stats[slot * 8 + rq];
+      const float ro = refs[slot], rn = fmaxf(rref, ro), ri = 1.f / rn;
+      const float mo[2] = {st.x, st.y}, lo[2] = {st.z, st.w};
+      float wa[2], wb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], mo[i]), mu = mn == -INFINITY ? 0.f : mn;
+        wa[i] = ex2_mufu(m[i] - mu);
+        wb[i] = ex2_mufu(mo[i] - mu);
+        l[i] = l[i] * wa[i] + lo[i] * wb[i];
+        m[i] = mn;
+        wa[i] *= rref * ri;
+        wb[i] *= ro * ri;
+      }
+      rref = rn;
+#pragma unroll
+      for (int j = 0; j < C::NACC; ++j) {
+        const float4 x = slots[(slot * C::NACC + j) * 32 + lane];
+        o[j][0] = o[j][0] * wa[0] + x.x * wb[0];
+        o[j][1] = o[j][1] * wa[0] + x.y * wb[0];
+        o[j][2] = o[j][2] * wa[1] + x.z * wb[1];
+        o[j][3] = o[j][3] * wa[1] + x.w * wb[1];
+      }
+    };
+    __syncthreads();                         // the slots are free
+    if (warp >= 2) put(warp - 2);
+    __syncthreads();
+    if (warp < 2) take(warp);
+    if (warp == 1) put(1);                   // only warp 1 has read this slot
+    __syncthreads();
+    if (warp == 0) {
+      take(1);
+      const bool whole = seg.ubeg >= rs && seg.uend <= re;
+      const int unit = seg.b * p.Hkv + seg.h;
+      // First unit of the CTA: partial 0, its last one: partial 1.
+      const int part = 2 * blockIdx.x + (seg.ubeg > rs ? 1 : 0);
+      if (seg.ubeg >= rs && lane == 0)
+        reinterpret_cast<int2*>(ws + W.rec)[unit] = make_int2(whole ? -1 : part, whole ? 0 : (int)((seg.uend - 1) / run) - (int)blockIdx.x);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = rq + 8 * i, qi = r / g;
+        if (r >= rows) continue;
+        // Columns of o[j][2i] and o[j][2i + 1]: for d = 128, 32 c + j and 32 c + 16 + j; d = 64, 16 c + j and 16 c + 8 + j.
+        if (whole) {
+          const float inv = l[i] == 0.f ? 0.f : rref / l[i];
+          const long long row = (long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi;
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + c * (D / 4));
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < C::NACC / 8; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = pack_bf16x2(o[8 * k + 2 * x][2 * i + e] * inv, o[8 * k + 2 * x + 1][2 * i + e] * inv);
+              out[e * (C::NACC / 8) + k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          if (c == 0) p.lse[row] = (m[i] - kShift + __log2f(l[i])) * kLn2;
+        } else {
+          float4* out = reinterpret_cast<float4*>(ws + W.part) + ((long long)part * rows_max + r) * (D / 4) + c * (D / 16);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < C::NACC / 4; ++k)
+              out[e * (C::NACC / 4) + k] = make_float4(o[4 * k][2 * i + e], o[4 * k + 1][2 * i + e], o[4 * k + 2][2 * i + e],
+                                                       o[4 * k + 3][2 * i + e]);
+          if (c == 0)
+            reinterpret_cast<float4*>(ws + W.stat)[(long long)part * rows_max + r] = make_float4(m[i], l[i], rref, 0.f);
         }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* out = static_cast<uint16_t*>(p.o) + ((long long)h * p.total_q + t) * D;
-    for (int c = 0; c < D / 32; ++c) out[c * 32 + lane] = (uint16_t)(pack_bf16x2(o[c] * inv, 0.f) & 0xffffu);
-    if (lane == 0) p.lse[(long long)h * p.total_q + t] = (m + log2f(l)) * 0.6931471805599453f;
-    __syncwarp();
+    seg.f = send;
+    seg.settle(p, re);
   }
+}
+
+// Joins the partial results of units that were cut: one CTA per unit and 128 groups of 4 columns.
+template <int D>
+__global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int ctas) {
+  const DecWs W = dec_ws(p.B, p.Hkv, rows_max, D, ctas);
+  const char* ws = static_cast<const char*>(p.ws);
+  const int unit = blockIdx.x, b = unit / p.Hkv, h = unit - b * p.Hkv;
+  const int i = blockIdx.y * 128 + threadIdx.x, r = i / (D / 4), col = i % (D / 4);
+  pdl_wait();
+  if (*reinterpret_cast<const int*>(ws) == 0) return;
+  const int q0 = p.cu_q[b], n = p.cu_q[b + 1] - q0;
+  if (r >= n * p.g) return;
+  const int2 rec = reinterpret_cast<const int2*>(ws + W.rec)[unit];
+  if (rec.x < 0) return;
+  // The unit's partials: its first CTA's, then partial 0 of each CTA behind it.
+  const float4* stat = reinterpret_cast<const float4*>(ws + W.stat);
+  const float4* part = reinterpret_cast<const float4*>(ws + W.part);
+  const int first = rec.x, cta = rec.x >> 1;
+  auto index = [&](int k) -> long long { return (long long)(k == 0 ? first : 2 * (cta + k)) * rows_max + r; };
+  float m = -INFINITY, ref = kMinScale;
+  for (int k = 0; k <= rec.y; ++k) {
+    const float4 s = stat[index(k)];
+    m = fmaxf(m, s.x);
+    ref = fmaxf(ref, s.z);
+  }
+  const float mu = m == -INFINITY ? 0.f : m, rinv = 1.f / ref;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k <= rec.y; ++k) {
+    const float4 s = stat[index(k)];
+    const float4 x = part[index(k) * (D / 4) + col];
+    const float w = ex2_mufu(s.x - mu), v = w * (s.z * rinv);
+    l += w * s.y;
+    o.x += v * x.x;
+    o.y += v * x.y;
+    o.z += v * x.z;
+    o.w += v * x.w;
+  }
+  const int qi = r / p.g;
+  const long long row = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
+  const float inv = l == 0.f ? 0.f : ref / l;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + col;
+  *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (col == 0) p.lse[row] = (m - kShift + __log2f(l)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows, int grid, cudaStream_t s) {
+  using C = DecCfg<D>;
+  static std::once_flag flags[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::call_once(flags[dev & 63], [&] {
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
+  fwd_cache_decode_kernel<D><<<grid, kThreads, C::SMEM, s>>>(maps.k, maps.v, p, rows);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const dim3 mgrid((unsigned)(p.B * p.Hkv), (unsigned)((rows * (D / 4) + 127) / 128));
+  return launch_pdl(fwd_cache_merge_kernel<D>, mgrid, dim3(128), 0, s, p, rows, grid);
 }
 
 }  // namespace
 
-size_t cache_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t cache_decode_workspace_bytes(int B, int Hkv, int rows, int d, int sms) {
+  return dec_ws(B, Hkv, rows, d, 2 * sms).total;
+}
 
-cudaError_t launch_fwd_cache(const CacheParams& p, int d, int sms, cudaStream_t s) {
-  (void)sms;
-  const dim3 grid((unsigned)p.total_q, (unsigned)((p.Hq + 3) / 4));
-  if (d == 64) fwd_cache_simple_kernel<64><<<grid, 128, 0, s>>>(p);
-  else fwd_cache_simple_kernel<128><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
+  const int rows = p.max_q * p.g, grid = 2 * sms;      // dec_ws() of the workspace query has this many CTAs
+  return d == 64 ? launch_decode<64>(maps, p, rows, grid, s) : launch_decode<128>(maps, p, rows, grid, s);
 }
 
 }  // namespace attn

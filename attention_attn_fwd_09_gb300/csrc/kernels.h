@@ -216,7 +216,15 @@ struct CacheParams {
   unsigned long long wait_ns;
   int* status;
 };
-size_t cache_workspace_bytes(int B, int Hq, int Hkv, int total_q, int max_q, int d, int sms);
-cudaError_t launch_fwd_cache(const CacheParams& p, int d, int sms, cudaStream_t s);
+// Tensor maps over the codes as 128-byte lines, [num_pages * Hkv][page * d / 128][128], boxes of
+// 32 keys (a page of 16: 16 keys), 128-byte swizzle.
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+// At most 16 rows (queries x heads of a group) per sequence and K/V head: fwd_cache.cu.
+constexpr int kCacheDecodeRows = 16;
+size_t cache_decode_workspace_bytes(int B, int Hkv, int rows, int d, int sms);
+cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
+cudaError_t launch_fwd_cache_rows(const CacheParams& p, int d, cudaStream_t s);
 
 }  // namespace attn
