@@ -17,7 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 ROOT = os.path.dirname(PKG)
 SOURCES = ["api.cu", "fwd.cu", "fwd_wide.cu", "fwd_persist.cu", "fwd_fp8.cu", "bwd.cu", "bwd_wide.cu", "noalloc.cu", "varlen.cu",
-           "rope.cu", "kv_append.cu", "fwd_cache.cu", "fwd_cache_rows.cu"]
+           "rope.cu", "kv_append.cu", "fwd_cache.cu", "fwd_cache_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-diag-suppress", "177"]

@@ -137,17 +137,18 @@ int make_map_e4m3(CUtensorMap* m, const void* base, int rows, long long bh, cons
   return ATTN_OK;
 }
 
-// Codes of a paged cache as 128-byte lines, boxes of box_lines of them, 128-byte swizzle.
-int make_map_cache(CUtensorMap* m, const void* base, int lines, long long pages, int box_lines, const char* name) {
+// Codes of a paged cache as lines of line bytes (128 or 64), boxes of box_lines of them, swizzled.
+int make_map_cache(CUtensorMap* m, const void* base, int line, int lines, long long pages, int box_lines,
+                   const char* name) {
   EncodeFn enc = get_encode();
   if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(g_encode_err));
-  cuuint64_t dims[3] = {128, (cuuint64_t)lines, (cuuint64_t)pages};
-  cuuint64_t strides[2] = {128, (cuuint64_t)lines * 128};
-  cuuint32_t box[3] = {128, (cuuint32_t)box_lines, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)line, (cuuint64_t)lines, (cuuint64_t)pages};
+  cuuint64_t strides[2] = {(cuuint64_t)line, (cuuint64_t)lines * line};
+  cuuint32_t box[3] = {(cuuint32_t)line, (cuuint32_t)box_lines, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "tensor map for %s: CUresult %d", name, (int)r);
   return ATTN_OK;
 }
@@ -892,9 +893,9 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
   return post_launch(s, st);
 }
 
-static size_t cache_workspace_bytes(int B, int Hq, int Hkv, int max_q, int d, int sms) {
+static size_t cache_workspace_bytes(int Hq, int Hkv, int max_q, int d, int sms) {
   const long long rows = (long long)max_q * (Hq / Hkv);
-  return rows <= kCacheDecodeRows ? cache_decode_workspace_bytes(B, Hkv, (int)rows, d, sms) : 0;
+  return rows <= kCacheDecodeRows ? cache_decode_workspace_bytes((int)rows, d, sms) : cache_tile_workspace_bytes(d, sms);
 }
 
 size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d) {
@@ -905,7 +906,7 @@ size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int m
   if (B == 0 || total_q == 0) return 0;
   const DevSyms* s = dev_syms(nullptr);
   const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
-  return cache_workspace_bytes(B, Hq, Hkv, max_q, d, sms);
+  return cache_workspace_bytes(Hq, Hkv, max_q, d, sms);
 }
 
 int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -916,6 +917,7 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   if (rc != ATTN_OK) return rc;
   if ((rc = check_shape(B, Hq, Hkv, total_q, d, scale)) != ATTN_OK) return rc;
   if (Hq > 65535) return fail(ATTN_ERR_UNSUPPORTED, "Hq=%d: packed sequences support at most 65535 heads", Hq);
+  if (Hq / Hkv > 256) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv = %d (supported: up to 256)", Hq / Hkv);
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
   if (max_q < 1 || max_q > total_q)
@@ -930,7 +932,7 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   const DevSyms* s = dev_syms(nullptr);
   if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   const int sms = std::max(1, s->sms);
-  const size_t need = cache_workspace_bytes(B, Hq, Hkv, max_q, d, sms);
+  const size_t need = cache_workspace_bytes(Hq, Hkv, max_q, d, sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
   if (need > 0 && !aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
@@ -950,16 +952,16 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   p.status = s->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((long long)max_q * p.g <= kCacheDecodeRows) {
-    if ((long long)B * Hkv > 0x7fffffffLL) return fail(ATTN_ERR_INVALID_ARG, "B * Hkv too large");
-    CacheMaps maps;
-    const int lines = page_size * d / 128, box = std::min(page_size, 32) * d / 128;
-    if ((rc = make_map_cache(&maps.k, k_cache, lines, (long long)num_pages * Hkv, box, "k_cache")) != ATTN_OK) return rc;
-    if ((rc = make_map_cache(&maps.v, v_cache, lines, (long long)num_pages * Hkv, box, "v_cache")) != ATTN_OK) return rc;
-    e = launch_fwd_cache_decode(maps, p, d, sms, st);
-  } else {
-    e = launch_fwd_cache_rows(p, d, st);
-  }
+  const bool few = (long long)max_q * p.g <= kCacheDecodeRows;
+  const int box = std::min(page_size, few ? 32 : 128);       // keys per copy
+  const long long slabs = (long long)num_pages * Hkv;
+  const int kline = few ? 128 : d;
+  CacheMaps maps;
+  if ((rc = make_map_cache(&maps.k, k_cache, kline, page_size * d / kline, slabs, box * d / kline, "k_cache")) != ATTN_OK)
+    return rc;
+  if ((rc = make_map_cache(&maps.v, v_cache, 128, page_size * d / 128, slabs, box * d / 128, "v_cache")) != ATTN_OK)
+    return rc;
+  e = few ? launch_fwd_cache_decode(maps, p, d, sms, st) : launch_fwd_cache_tile(maps, p, d, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "cached attention launch");
   return post_launch(s, st);
 }

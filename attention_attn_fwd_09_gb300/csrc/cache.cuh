@@ -1,4 +1,4 @@
-// Shared by the kernels of the paged e4m3 cache: number formats.
+// Shared by the kernels of the paged e4m3 cache: number formats, the workspace of partial results.
 #pragma once
 #include <cstdint>
 
@@ -31,6 +31,27 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   const uint32_t bits = __float_as_uint(amax);
   const int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+
+constexpr float kMinScale = 1.17549435e-38f;   // 2^-126: a reference for V scales that never is 0
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Attention over the cache cuts its work evenly by keys, so a unit (some query rows of one
+// sequence and K/V head) may be worked on by several CTAs, each of which leaves a partial
+// result: per row m (running maximum, log2), l (sum of 2^(s - m)), a reference scale r and
+// O / r.  A CTA has at most two: partial 0 for its first unit, partial 1 for its last.
+// Workspace: per CTA an int4 {b, K/V head, first query, 2 x further CTAs + which partial} for the
+// unit that starts in it and is cut (last field < 2: none); then per partial and row
+// (m, l, r, -); then the O rows.
+struct CacheWs {
+  size_t stat, part, total;
+};
+__host__ __device__ inline CacheWs cache_ws(int ctas, int rows, int d) {
+  CacheWs w;
+  w.stat = ((size_t)ctas * 16 + 255) & ~size_t(255);
+  w.part = w.stat + (((size_t)ctas * 2 * rows * 16 + 255) & ~size_t(255));
+  w.total = w.part + (size_t)ctas * 2 * rows * d * 4;
+  return w;
 }
 
 }  // namespace attn

@@ -37,8 +37,6 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kPiece = 32;                   // keys per piece
 constexpr float kShift = 14.f;               // weights are held times 2^14
-constexpr float kMinScale = 1.17549435e-38f; // 2^-126: the V scale reference never is 0
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct DecCfg {
@@ -54,21 +52,6 @@ struct DecCfg {
   static constexpr int SMEM = OFF_MISC + 64;
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
-
-// Workspace: header (256 bytes: [0] 1 when the device checks passed), per unit {first CTA, CTAs},
-// per partial (two per CTA: its first and its last unit) 16 rows of (m, l, r, -), then O rows.
-struct DecWs {
-  size_t rec, stat, part, total;
-};
-__host__ __device__ inline DecWs dec_ws(int B, int Hkv, int rows, int d, int ctas) {
-  DecWs w;
-  w.rec = 256;
-  w.stat = (w.rec + (size_t)B * Hkv * 8 + 255) & ~size_t(255);
-  w.part = w.stat + (size_t)ctas * 2 * rows * 16;
-  w.part = (w.part + 255) & ~size_t(255);
-  w.total = w.part + (size_t)ctas * 2 * rows * d * 4;
-  return w;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -114,8 +97,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 48);
   const uint32_t bars = smem_u32(smem + C::OFF_BAR) + warp * C::STAGES * 8;
   const WaitCtl wc{p.wait_ns, p.status, abort_flag};
-  const DecWs W = dec_ws(p.B, p.Hkv, rows_max, D, gridDim.x);
+  const CacheWs W = cache_ws(gridDim.x, rows_max, D);
   char* ws = static_cast<char*>(p.ws);
+  int4* rec = reinterpret_cast<int4*>(ws) + blockIdx.x;
   pdl_trigger();
   if (tid == 0) {
     *abort_flag = 0;
@@ -144,8 +128,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (lane == 31) misc[warp] = incl;
   const bool bad = __syncthreads_or(wrong) != 0;
-  if (blockIdx.x == 0 && tid == 0) {
-    *reinterpret_cast<int*>(ws) = bad ? 0 : 1;
+  if (tid == 0) {
+    *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
   }
   if (bad) return;
@@ -537,11 +521,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0) {
       take(1);
       const bool whole = seg.ubeg >= rs && seg.uend <= re;
-      const int unit = seg.b * p.Hkv + seg.h;
       // First unit of the CTA: partial 0, its last one: partial 1.
-      const int part = 2 * blockIdx.x + (seg.ubeg > rs ? 1 : 0);
-      if (seg.ubeg >= rs && lane == 0)
-        reinterpret_cast<int2*>(ws + W.rec)[unit] = make_int2(whole ? -1 : part, whole ? 0 : (int)((seg.uend - 1) / run) - (int)blockIdx.x);
+      const int second = seg.ubeg > rs ? 1 : 0, part = 2 * blockIdx.x + second;
+      if (seg.ubeg >= rs && !whole && lane == 0)
+        *rec = make_int4(seg.b, seg.h, 0, 2 * ((int)((seg.uend - 1) / run) - (int)blockIdx.x) + second);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = rq + 8 * i, qi = r / g;
@@ -571,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               out[e * (C::NACC / 4) + k] = make_float4(o[4 * k][2 * i + e], o[4 * k + 1][2 * i + e], o[4 * k + 2][2 * i + e],
                                                        o[4 * k + 3][2 * i + e]);
           if (c == 0)
-            reinterpret_cast<float4*>(ws + W.stat)[(long long)part * rows_max + r] = make_float4(m[i], l[i], rref, 0.f);
+            reinterpret_cast<float4*>(ws + W.stat)[(long long)part * rows_max + r] = make_float4(m[i] - kShift, l[i], rref, 0.f);
         }
       }
     }
@@ -580,26 +563,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the partial results of units that were cut: one CTA per unit and 128 groups of 4 columns.
+// Joins the partial results of cut units: block x takes the unit that starts in CTA x of the main
+// kernel and goes on in others (at most one), block y 128 groups of 4 columns of it.
 template <int D>
 __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int ctas) {
-  const DecWs W = dec_ws(p.B, p.Hkv, rows_max, D, ctas);
+  const CacheWs W = cache_ws(ctas, rows_max, D);
   const char* ws = static_cast<const char*>(p.ws);
-  const int unit = blockIdx.x, b = unit / p.Hkv, h = unit - b * p.Hkv;
   const int i = blockIdx.y * 128 + threadIdx.x, r = i / (D / 4), col = i % (D / 4);
   pdl_wait();
-  if (*reinterpret_cast<const int*>(ws) == 0) return;
-  const int q0 = p.cu_q[b], n = p.cu_q[b + 1] - q0;
-  if (r >= n * p.g) return;
-  const int2 rec = reinterpret_cast<const int2*>(ws + W.rec)[unit];
-  if (rec.x < 0) return;
-  // The unit's partials: its first CTA's, then partial 0 of each CTA behind it.
+  const int4 rec = reinterpret_cast<const int4*>(ws)[blockIdx.x];   // {b, h, first query, 2 x further CTAs + which partial}
+  if (rec.w < 2) return;
+  const int b = rec.x, h = rec.y, q0 = p.cu_q[b], n = p.cu_q[b + 1] - q0, qi = rec.z + r / p.g;
+  if (r >= rows_max / p.g * p.g || qi >= n) return;           // a unit holds whole queries
+  const int first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
   const float4* stat = reinterpret_cast<const float4*>(ws + W.stat);
   const float4* part = reinterpret_cast<const float4*>(ws + W.part);
-  const int first = rec.x, cta = rec.x >> 1;
-  auto index = [&](int k) -> long long { return (long long)(k == 0 ? first : 2 * (cta + k)) * rows_max + r; };
+  // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
+  auto index = [&](int k) -> long long { return (long long)(k == 0 ? first : 2 * ((int)blockIdx.x + k)) * rows_max + r; };
   float m = -INFINITY, ref = kMinScale;
-  for (int k = 0; k <= rec.y; ++k) {
+  for (int k = 0; k <= more; ++k) {
     const float4 s = stat[index(k)];
     m = fmaxf(m, s.x);
     ref = fmaxf(ref, s.z);
@@ -608,7 +590,7 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = 0; k <= rec.y; ++k) {
+  for (int k = 0; k <= more; ++k) {
     const float4 s = stat[index(k)];
     const float4 x = part[index(k) * (D / 4) + col];
     const float w = ex2_mufu(s.x - mu), v = w * (s.z * rinv);
@@ -618,12 +600,11 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     o.z += v * x.z;
     o.w += v * x.w;
   }
-  const int qi = r / p.g;
-  const long long row = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
+  const long long row = (long long)(h * p.g + r % p.g) * p.total_q + q0 + qi;
   const float inv = l == 0.f ? 0.f : ref / l;
   uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + col;
   *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (col == 0) p.lse[row] = (m - kShift + __log2f(l)) * kLn2;
+  if (col == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -640,18 +621,21 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   fwd_cache_decode_kernel<D><<<grid, kThreads, C::SMEM, s>>>(maps.k, maps.v, p, rows);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 mgrid((unsigned)(p.B * p.Hkv), (unsigned)((rows * (D / 4) + 127) / 128));
-  return launch_pdl(fwd_cache_merge_kernel<D>, mgrid, dim3(128), 0, s, p, rows, grid);
+  return launch_fwd_cache_merge(p, D, rows, grid, s);
 }
 
 }  // namespace
 
-size_t cache_decode_workspace_bytes(int B, int Hkv, int rows, int d, int sms) {
-  return dec_ws(B, Hkv, rows, d, 2 * sms).total;
+cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
+  const dim3 grid((unsigned)ctas, (unsigned)((rows * (d / 4) + 127) / 128));
+  return d == 64 ? launch_pdl(fwd_cache_merge_kernel<64>, grid, dim3(128), 0, s, p, rows, ctas)
+                 : launch_pdl(fwd_cache_merge_kernel<128>, grid, dim3(128), 0, s, p, rows, ctas);
 }
 
+size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }
+
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
-  const int rows = p.max_q * p.g, grid = 2 * sms;      // dec_ws() of the workspace query has this many CTAs
+  const int rows = p.max_q * p.g, grid = 2 * sms;      // as in the workspace's size
   return d == 64 ? launch_decode<64>(maps, p, rows, grid, s) : launch_decode<128>(maps, p, rows, grid, s);
 }
 

@@ -1,0 +1,815 @@
+// Attention of packed queries over a paged e4m3 cache: many query rows per K/V head (pieces of
+// prompts, long drafts).  fwd_cache.cu is the kernel for few rows.
+//
+// A unit is 256 rows of one sequence and K/V head as two 128-row tiles: row r is query r / g,
+// head r % g of the group, so every tile is full whatever g is and the g heads share the K, V
+// they share.  What bounds it is tensor and exponential throughput, so it is the ping-pong of
+// fwd.cu (a TMA producer warp, one thread issuing tcgen05.mma, a softmax warpgroup per tile, a
+// correction warpgroup that rescales O only when a maximum grew by more than tau) with
+//   * S on the 8-bit tensor path, K's codes as they lie in the cache.  Q, scaled by a power of two
+//     per row (largest |q| in [128, 256)), is the sum of two e4m3 tiles, Q1 = e4m3(q) and
+//     Q2 = e4m3(q - Q1): bf16 has 8 significant bits and e4m3 4, so the sum is q itself down to
+//     2^-9 of the row's largest component and off by at most 2^-18 of that below.  Both products
+//     together cost what one 16-bit product costs, and K needs no widening;
+//   * V widened to f16 by the correction warpgroup between its rescales, times its page's scale
+//     over the largest V scale so far, times 2^7 (448 * 2^7 < 65504): a page's codes keep their
+//     bits down to 2^-17 of the largest scale.  When the largest scale grows O is rescaled like
+//     for a maximum.  Weights are held times 2^7 (2^8 at most times tau's 2^8) in f16;
+//   * the work cut evenly: all units' 128-key blocks laid end to end, one persistent CTA per SM
+//     takes an equal run of them.  Units cut between CTAs leave partial results for the merge
+//     kernel.  Each role walks the CTA's units on its own; K, V of the next unit load while this
+//     one ends, and its Q is prepared while O is written out.
+//
+// Shared memory (d = 128): Q1, Q2 2 x 32 KB, K8 ring 2 x 16 KB, V8 ring 3 x 16 KB, V16 2 x 32 KB.
+// TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P_t (f16 pairs) overwrites S_t.
+#include <cstdint>
+#include <mutex>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kTThreads = 512;
+constexpr int kTRows = 256;                  // rows of a unit
+constexpr float kPShift = 7.f;               // weights are held times 2^7
+constexpr float kVShift = 128.f;             // and V times 2^7 over the reference scale
+constexpr float kTau = 8.f;                  // rescale when a maximum grows by more (2^(7 + 8) < 65504)
+constexpr float kMinFactor = 1e-30f;         // keeps -inf * factor = -inf for pages whose scale is 0
+
+template <int D>
+struct TileCfg {
+  static constexpr uint32_t Q8 = 128 * D;          // one e4m3 tile of Q
+  static constexpr uint32_t K8 = 128 * D;          // 128 keys of e4m3 K or V
+  static constexpr uint32_t CH16 = 128 * 128;      // 128 keys x 64 f16 columns (a swizzled box)
+  static constexpr uint32_t V16 = (D / 64) * CH16;
+  static constexpr int NK = 2, NV8 = 3, NV16 = 2;
+  static constexpr uint32_t OFF_Q = 0;             // [tile][Q1, Q2]
+  static constexpr uint32_t OFF_K = OFF_Q + 4 * Q8;
+  static constexpr uint32_t OFF_V8 = OFF_K + NK * K8;
+  static constexpr uint32_t OFF_V16 = OFF_V8 + NV8 * K8;
+  static constexpr uint32_t OFF_CTRL = OFF_V16 + NV16 * V16;
+  static constexpr uint32_t CTRL_BYTES = 256 + (2 * 128 + 4 * 128) * 4 + 64;
+  static constexpr uint32_t SMEM = 1024 + OFF_CTRL + CTRL_BYTES;
+  // K-major rows of D bytes: 128-byte swizzle for d = 128, 64-byte for d = 64.
+  static constexpr uint32_t IDESC_QK = idesc_f32acc(128, 128, FMT_E4M3, FMT_E4M3, false, false);
+  static constexpr uint32_t IDESC_PV = idesc_f32acc(128, D, FMT_F16, FMT_F16, false, true);
+  static constexpr uint32_t QK_HI = D == 128 ? sdesc_sw128_hi(1024) : ((512u >> 4) | (1u << 14) | (4u << 29));
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+enum {
+  T_Q = 0,         // +t: Q_t of the unit written (128)
+  T_SFULL = 2,     // +t: S_t of a block complete
+  T_PFULL = 4,     // +t: P written (softmax, 128) and O rescaled (correction, 128)
+  T_STATS = 6,     // +t: row statistics of a block written (128)
+  T_OFULL = 8,     // +t: the unit's last PV of tile t complete
+  T_OFREE = 10,    // +t: O_t read out of tensor memory (128)
+  T_FIN = 12,      // +t: the unit's final statistics written (128)
+  T_KFULL = 14,    // +slot (2)
+  T_KFREE = 16,    // +slot (2): products that read the slot complete
+  T_V8FULL = 18,   // +slot (3)
+  T_V8FREE = 21,   // +slot (3): widened (128)
+  T_V16FULL = 24,  // +slot (2): widened (128)
+  T_V16FREE = 26,  // +slot (2): products that read the slot complete
+  T_EPI = 28,      // the unit's results written (128)
+  T_DONE = 29,
+  T_COUNT = 30
+};
+static_assert(T_COUNT * 8 <= 256, "barriers fit the control block's first 256 bytes");
+
+// sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0, in O(log) steps.
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// A sequence: its units per K/V head and their blocks of 128 keys.  Unit rt holds queries rt qu ..
+// rt qu + qu - 1, qu = 256 / g.
+struct TileSeq {
+  int q0, n, len;
+  long long units;
+  __device__ __forceinline__ TileSeq(const CacheParams& p, int b, int qu) {
+    q0 = __ldg(p.cu_q + b);
+    n = __ldg(p.cu_q + b + 1) - q0;
+    len = __ldg(p.kv_lens + b);
+    units = (n + qu - 1) / qu;
+  }
+  __device__ __forceinline__ int blocks(const CacheParams& p, int qu, int rt) const {
+    const int lim = p.causal ? len - n + min(n, (rt + 1) * qu) : len;
+    return (max(lim, 1) + 127) / 128;
+  }
+  // Blocks of the units before rt (a unit without keys counts as one block).
+  __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, long long rt) const {
+    const int l = max(len, 1);
+    if (rt <= 0) return 0;
+    if (!p.causal) return rt * ((l + 127) / 128);
+    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127);
+    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128;
+  }
+};
+
+// The unit a role works on, and the CTA's part of it.  Blocks are counted from the CTA's first.
+struct TileUnit {
+  int f, ubeg, uend, re;                     // first block here, the unit's blocks, the CTA's end
+  int b, h, rt;
+  int q0, n, len, rows;                      // rows: in use of 256
+  int kt0;                                   // first key block here
+  int nt[2];                                 // key blocks here, per tile
+  int nmax;
+  __device__ __forceinline__ bool valid() const { return f < re; }
+  __device__ __forceinline__ void fill(const CacheParams& p, int qu) {
+    const TileSeq s(p, b, qu);
+    q0 = s.q0; n = s.n; len = s.len;
+    rows = min(qu, n - rt * qu) * p.g;
+    kt0 = f - ubeg;
+    const int kt1 = min(uend, re) - ubeg;
+    nmax = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r = min(rows, (t + 1) * 128) - t * 128;                 // rows of the tile
+      const int lim = r > 0 ? (p.causal ? len - n + rt * qu + (t * 128 + r - 1) / p.g + 1 : len) : 0;
+      nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
+      nmax = max(nmax, nt[t]);
+    }
+  }
+  __device__ __forceinline__ void next(const CacheParams& p, int qu) {
+    f = uend;
+    if (f >= re) return;
+    TileSeq s(p, b, qu);
+    if (++rt >= s.units) {
+      rt = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do s = TileSeq(p, ++b, qu);          // f < re: there is another unit
+        while (s.units == 0);
+      }
+    }
+    ubeg = uend;
+    uend = ubeg + s.blocks(p, qu, rt);
+    fill(p, qu);
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  const bool ok = mbar_wait(bar, parity, w);
+  return __all_sync(0xffffffffu, ok);
+}
+template <int N>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+// Two fp32 values -> two e4m3 codes (low byte: a), and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// NG: groups of columns of a key block that may have scales of their own (1: a page holds the
+// block; 8: 16 keys each).
+template <int D, int NG>
+__global__ void __launch_bounds__(kTThreads, 1)
+    fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const CacheParams p) {
+  using C = TileCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint8_t* ctrl = smem + C::OFF_CTRL;
+  const uint32_t bar0 = smem_u32(ctrl);
+  auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * i; };
+  float* alpha_buf = reinterpret_cast<float*>(ctrl + 256);   // [2][128]
+  float* fin = alpha_buf + 256;                              // [2][m, l][128]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 512);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  long long* misc = reinterpret_cast<long long*>(tmem_slot + 2);   // [4]: b, h, rt, unit start
+  long long* sums = reinterpret_cast<long long*>(smem + C::OFF_Q); // [16] warp sums, before Q is written
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id(), wg = warp >> 2;
+  const int qu = kTRows / p.g;                               // queries per unit
+  const WaitCtl wc{p.wait_ns, p.status, abort_flag};
+  const CacheWs W = cache_ws(gridDim.x, kTRows, D);
+  char* ws = static_cast<char*>(p.ws);
+  int4* rec = reinterpret_cast<int4*>(ws) + blockIdx.x;
+  pdl_trigger();
+
+  if (tid == 0) {
+    mbar_init(BAR(T_EPI), 128);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(BAR(T_Q + t), 128);
+      mbar_init(BAR(T_SFULL + t), 1);
+      mbar_init(BAR(T_PFULL + t), 256);
+      mbar_init(BAR(T_STATS + t), 128);
+      mbar_init(BAR(T_OFULL + t), 1);
+      mbar_init(BAR(T_OFREE + t), 128);
+      mbar_init(BAR(T_FIN + t), 128);
+      mbar_init(BAR(T_KFULL + t), 1);
+      mbar_init(BAR(T_KFREE + t), 1);
+      mbar_init(BAR(T_V16FULL + t), 128);
+      mbar_init(BAR(T_V16FREE + t), 1);
+    }
+    for (int s = 0; s < C::NV8; ++s) {
+      mbar_init(BAR(T_V8FULL + s), 1);
+      mbar_init(BAR(T_V8FREE + s), 128);
+    }
+    mbar_init(BAR(T_DONE), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+
+  // ---- the run of blocks of this CTA; thread t adds up sequences [t per_thread, ...)
+  const int per_thread = (p.B + kTThreads - 1) / kTThreads;
+  const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
+  long long mine = 0;
+  bool wrong = false;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const TileSeq s(p, b, qu);
+    const int c1 = s.q0 + s.n;
+    const bool w = s.q0 < 0 || s.n < 0 || c1 < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_len ||
+                   (p.causal && s.n > s.len) || (b == 0 && s.q0 != 0) || (b == p.B - 1 && c1 != p.total_q);
+    wrong |= w;
+    if (!w) mine += s.blocks_before(p, qu, s.units);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  const bool bad = __syncthreads_or(wrong) != 0;
+  if (tid == 0) {
+    *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
+    if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
+  }
+  if (bad) return;
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kTThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  total *= p.Hkv;
+  before *= p.Hkv;
+  mine *= p.Hkv;
+  const long long run = max((total + gridDim.x - 1) / gridDim.x, 2LL);
+  const long long rs = run * blockIdx.x, re = min(rs + run, total);
+  if (rs >= total) return;
+  if (before <= rs && rs < before + mine) {
+    int b = b_lo;
+    long long at = before;
+    for (;;) {
+      const TileSeq s(p, b, qu);
+      const long long per_head = s.blocks_before(p, qu, s.units);
+      if (rs < at + per_head * p.Hkv) {
+        const int h = (int)((rs - at) / per_head);
+        at += h * per_head;
+        long long lo = 0, hi = s.units - 1;            // the last rt whose first block is <= rs
+        while (lo < hi) {
+          const long long mid = (lo + hi + 1) / 2;
+          if (at + s.blocks_before(p, qu, mid) <= rs) lo = mid;
+          else hi = mid - 1;
+        }
+        misc[0] = b;
+        misc[1] = h;
+        misc[2] = lo;
+        misc[3] = at + s.blocks_before(p, qu, lo);
+        break;
+      }
+      at += per_head * p.Hkv;
+      ++b;
+    }
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  TileUnit U;
+  U.b = (int)misc[0];
+  U.h = (int)misc[1];
+  U.rt = (int)misc[2];
+  U.ubeg = (int)(misc[3] - rs);
+  U.f = 0;
+  U.re = (int)(re - rs);
+  U.uend = U.ubeg + TileSeq(p, U.b, qu).blocks(p, qu, U.rt);
+  U.fill(p, qu);
+  const int page_shift = 31 - __clz(p.page);
+
+  // Register split against the launch's 128 x 512: producer and MMA 64; softmax 184 each;
+  // correction (and V widening) 80.
+  if (wg == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer
+      // Lane i < 128 / page loads the box of page i of a block (lane 0 alone when a page holds it).
+      const int boxes = max(1, 128 >> page_shift), box_keys = min(p.page, 128);
+      const uint32_t box_bytes = box_keys * D;
+      uint32_t n_k = 0, n_v = 0;             // K, V blocks loaded so far
+      bool ok = true;
+      while (U.valid() && ok) {
+        auto page_of = [&](int j) -> int {
+          const int key = (U.kt0 + j) * 128 + lane * box_keys;
+          if (lane >= boxes || j >= U.nmax || key >= U.len) return -1;
+          const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+          if (pg < 0 || pg >= p.num_pages) {
+            atomicExch(p.status, DEV_BAD_PAGE);
+            return 0;                        // any page of the cache: the sequence's results are undefined
+          }
+          return pg;
+        };
+        int pg_next = page_of(0);
+        for (int j = 0; j < U.nmax; ++j) {
+          const int pg = pg_next;
+          pg_next = page_of(j + 1);
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
+          const int z = pg * p.Hkv + U.h;
+          const int ks = (int)(n_k % C::NK), vs = (int)(n_v % C::NV8);
+          if (n_k >= C::NK && !warp_wait(BAR(T_KFREE + ks), (n_k / C::NK - 1) & 1, wc)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
+          __syncwarp();
+          if (pg >= 0) tma_load_3d(sbase + C::OFF_K + ks * C::K8 + lane * box_bytes, &tm_k, 0, 0, z, BAR(T_KFULL + ks));
+          ++n_k;
+          if (n_v >= C::NV8 && !warp_wait(BAR(T_V8FREE + vs), (n_v / C::NV8 - 1) & 1, wc)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(BAR(T_V8FULL + vs), bytes);
+          __syncwarp();
+          if (pg >= 0) tma_load_3d(sbase + C::OFF_V8 + vs * C::K8 + lane * box_bytes, &tm_v, 0, 0, z, BAR(T_V8FULL + vs));
+          ++n_v;
+        }
+        U.next(p, qu);
+      }
+      // Every copy has landed before the shared memory goes away, also when a wait ran out.
+      if (lane == 0) {
+        const unsigned long long t0 = globaltimer_ns();
+        for (uint32_t i = n_k > C::NK ? n_k - C::NK : 0; i < n_k; ++i)
+          while (!mbar_try_wait(BAR(T_KFULL + (i % C::NK)), (i / C::NK) & 1) && globaltimer_ns() - t0 < p.wait_ns) {
+          }
+        for (uint32_t i = n_v > C::NV8 ? n_v - C::NV8 : 0; i < n_v; ++i)
+          while (!mbar_try_wait(BAR(T_V8FULL + (i % C::NV8)), (i / C::NV8) & 1) && globaltimer_ns() - t0 < p.wait_ns) {
+          }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t nk = 0, nv = 0;             // blocks whose S, PV were issued
+        uint32_t np[2] = {0, 0}, no[2] = {0, 0};   // P phases used; units of tile t whose last PV was issued
+        constexpr uint32_t HI = sdesc_sw128_hi(1024);
+        for (; U.valid() && ok; U.next(p, qu)) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (U.nt[t] > 0 && !mbar_wait(BAR(T_Q + t), no[t] & 1, wc)) ok = false;
+          if (!ok || U.nmax == 0) continue;
+          tc_fence_after();
+          for (int j = 0; j <= U.nmax && ok; ++j) {
+            const uint32_t ks = nk % C::NK, vs = nv % C::NV16;
+            if (j < U.nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
+            if (j >= 1 && !mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
+            const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + vs * C::V16, C::CH16);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok) break;
+              const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
+              if (j >= 1 && j <= U.nt[t]) {
+                // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
+                if (j == 1 && no[t] > 0 && !mbar_wait(BAR(T_OFREE + t), (no[t] - 1) & 1, wc)) { ok = false; break; }
+                if (!mbar_wait(BAR(T_PFULL + t), np[t] & 1, wc)) { ok = false; break; }
+                ++np[t];
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
+                if (j == U.nt[t]) {
+                  mma_commit(BAR(T_OFULL + t));
+                  ++no[t];
+                }
+              }
+              if (j < U.nt[t]) {
+                // S_t = (Q1_t + Q2_t) K8_j^T, K = 32 columns a step
+                const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + 2 * t * C::Q8, 16);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                  for (int kk = 0; kk < D / 32; ++kk)
+                    mma_ss_f8_w(tS, q_lo + ((part * C::Q8 + kk * 32) >> 4), C::QK_HI, k_lo + ((kk * 32) >> 4), C::QK_HI,
+                                C::IDESC_QK, (part > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(BAR(T_SFULL + t));
+              }
+            }
+            if (!ok) break;
+            if (j < U.nmax) {
+              mma_commit(BAR(T_KFREE + ks));
+              ++nk;
+            }
+            if (j >= 1) {
+              mma_commit(BAR(T_V16FREE + vs));
+              ++nv;
+            }
+          }
+        }
+        mma_commit(BAR(T_DONE));
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(BAR(T_DONE), 0) && globaltimer_ns() - t0 < p.wait_ns) {
+        }
+      }
+    }
+  } else if (wg == 1 || wg == 2) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // ------------------------------------------------------------------ softmax
+    const int t = wg - 1;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(t * 128);
+    uint32_t ns = 0, nu = 0;                 // S phases used; units
+    bool ok = true;
+    for (; U.valid() && ok; U.next(p, qu), ++nu) {
+      const int r = t * 128 + row;           // row of the unit
+      const int qi = r / p.g;
+      const bool live = r < U.rows;
+      const int n_t = t ? U.nt[1] : U.nt[0];
+      const int lim = !live ? U.len : (p.causal ? U.len - U.n + U.rt * qu + qi + 1 : U.len);
+      const int min_lim = p.causal ? U.len - U.n + U.rt * qu + t * 128 / p.g + 1 : U.len;   // the tile's first row
+      float c_row = 0.f;
+      if (n_t > 0) {
+        // This tile's Q is free: every S of the unit before has been waited for.
+        uint4 w[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) +
+            ((long long)(U.h * p.g + (r - qi * p.g)) * p.total_q + U.q0 + U.rt * qu + qi) * D);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmax3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
+        }
+        const uint32_t e = __float_as_uint(amax) >> 23;            // biased exponent
+        const bool usable = e >= 8 && e < 255;                     // else 0 or tiny: left as it is; infinite: NaN
+        const float inv = usable ? __uint_as_float((254u + 7u - e) << 23) : 1.f;
+        c_row = p.c * (usable ? __uint_as_float((e - 7u) << 23) : 1.f);
+        const uint32_t poison = e == 255 ? 0x7f7f7f7fu : 0u;
+        uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + row * D;
+        const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ++ch) {                      // 16 columns: one 16-byte piece of Q1 and of Q2
+          uint32_t c1[4], c2[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {                            // 4 columns
+            const uint4 v = w[2 * ch + (k >> 1)];
+            const uint32_t a = (k & 1) ? v.z : v.x, b = (k & 1) ? v.w : v.y;
+            const float x0 = __uint_as_float(a << 16) * inv, x1 = __uint_as_float(a & 0xffff0000u) * inv;
+            const float x2 = __uint_as_float(b << 16) * inv, x3 = __uint_as_float(b & 0xffff0000u) * inv;
+            const uint32_t h = to_e4m3x2(x0, x1) | (to_e4m3x2(x2, x3) << 16);
+            float y0, y1, y2, y3;
+            e4m3x4_to_f32(h, y0, y1, y2, y3);
+            c1[k] = h | poison;
+            c2[k] = to_e4m3x2(x0 - y0, x1 - y1) | (to_e4m3x2(x2 - y2, x3 - y3) << 16);
+          }
+          const int off = (ch ^ sw) << 4;
+          *reinterpret_cast<uint4*>(q1 + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+          *reinterpret_cast<uint4*>(q1 + C::Q8 + off) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+        }
+        fence_proxy_async_smem();            // generic writes -> tensor-core reads
+        mbar_arrive(BAR(T_Q + t));
+      }
+      // K scales: lane & 7 looks after a group of 16 keys (all lanes after the one page when NG = 1);
+      // pages one block further ahead than scales.
+      auto page_of = [&](int j) -> int {
+        const int key = (U.kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        if (j >= n_t || key >= U.len) return -1;
+        const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+        return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
+      };
+      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.k_scale + (long long)pg * p.Hkv + U.h) : 0.f; };
+      float sk_next = scale_of(page_of(0));
+      int pg_next = page_of(1);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n_t; ++j) {
+        const float sk = sk_next;
+        sk_next = scale_of(pg_next);
+        pg_next = page_of(j + 2);
+        float fac[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+          fac[i] = fmaxf(c_row * (NG > 1 ? __shfl_sync(0xffffffffu, sk, i) : sk), kMinFactor);
+        if (!warp_wait(BAR(T_SFULL + t), ns & 1, wc)) { ok = false; break; }
+        ++ns;
+        tc_fence_after();
+        uint32_t u[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[q * 32]));
+        tmem_wait_ld();
+        reg_fence(u);
+        float* s = reinterpret_cast<float*>(u);
+        const int kb = (U.kt0 + j) * 128;
+        if (kb + 128 > min_lim) {
+          const int vis = lim - kb;          // visible columns
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= vis) s[i] = -INFINITY;
+        }
+        float rmax = -INFINITY;
+        if constexpr (NG == 1) {
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < 124; i += 8) {
+            mx[0] = fmax3(mx[0], s[i], s[i + 1]);
+            mx[1] = fmax3(mx[1], s[i + 2], s[i + 3]);
+            mx[2] = fmax3(mx[2], s[i + 4], s[i + 5]);
+            mx[3] = fmax3(mx[3], s[i + 6], s[i + 7]);
+          }
+          mx[0] = fmax3(mx[0], s[124], s[125]);
+          mx[1] = fmax3(mx[1], s[126], s[127]);
+          rmax = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * fac[0];
+        } else {
+#pragma unroll
+          for (int gq = 0; gq < NG; ++gq) {
+            const float* x = s + gq * 16;
+            float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]);
+            a = fmax3(a, x[6], x[7]);
+            b = fmax3(b, x[8], x[9]);
+            a = fmax3(a, x[10], x[11]);
+            b = fmax3(b, x[12], x[13]);
+            rmax = fmaxf(rmax, fmax3(fmaxf(a, b), x[14], x[15]) * fac[gq]);
+          }
+        }
+        const float m_cand = fmaxf(m, rmax);
+        float alpha = 1.f;
+        if (j == 0) {
+          m = m_cand;
+        } else if (m_cand - m > kTau) {
+          alpha = ex2_mufu(m - m_cand);
+          m = m_cand;
+        }
+        alpha_buf[t * 128 + row] = alpha;
+        mbar_arrive(BAR(T_STATS + t));
+        const float off = kPShift - (m == -INFINITY ? 0.f : m);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[64];
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+          float x0, x1;
+          ffma2_bc(x0, x1, s[i], s[i + 1], fac[NG > 1 ? i / 16 : 0], off);
+          const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
+          pk[i >> 1] = pack_f16x2(e0, e1);
+          const int a2 = ((i >> 1) & 1) * 2;
+          fadd2(acc[a2], acc[a2 + 1], acc[a2], acc[a2 + 1], e0, e1);
+        }
+        l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+        tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(T_PFULL + t));
+      }
+      // The statistics of the unit before have been read.  (This also keeps a tile without rows
+      // from running ahead of the other roles.)
+      if (ok && nu > 0 && !warp_wait(BAR(T_EPI), (nu - 1) & 1, wc)) ok = false;
+      if (!ok) break;
+      float* out = fin + t * 256 + row;
+      out[0] = m;
+      out[128] = l;
+      mbar_arrive(BAR(T_FIN + t));
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ------------------------------------------------------------------ correction, V, epilogue
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const int ct = tid - 384, w4 = ct >> 5;
+    uint32_t nv = 0, nst[2] = {0, 0}, nof[2] = {0, 0}, nu = 0;   // V blocks widened; statistics, O phases used; units
+    bool ok = true;
+    for (; U.valid() && ok; U.next(p, qu), ++nu) {
+      float rref = kMinScale, fac = 1.f;     // largest V scale so far; old over new with the newest block
+      float ref_t[2] = {kMinScale, kMinScale};   // what O_t is relative to
+      auto page_of = [&](int j) -> int {
+        const int key = (U.kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        if (j >= U.nmax || key >= U.len) return -1;
+        const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+        return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
+      };
+      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + U.h) : 0.f; };
+      float sv_next = scale_of(page_of(0));
+      int pg_next = page_of(1);
+      // V8 block jj -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle).
+      // Thread pieces of 16 codes; each quarter-warp takes half of two adjacent 128-byte lines, so
+      // that its loads and each of its two rounds of stores fall on eight distinct bank groups.
+      auto widen = [&](int jj) -> bool {
+        const float sv = sv_next;
+        sv_next = scale_of(pg_next);
+        pg_next = page_of(jj + 2);
+        float vmax = sv;
+        if constexpr (NG > 1) {
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+        }
+        fac = 1.f;
+        if (vmax > rref) {
+          fac = rref / vmax;
+          rref = vmax;
+        }
+        const float wgt = sv / rref * kVShift;
+        const uint32_t w_mine = pack_f16x2(wgt, wgt);
+        const uint32_t vs8 = nv % C::NV8, vs16 = nv % C::NV16;
+        if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) return false;
+        if (nv >= C::NV16 && !warp_wait(BAR(T_V16FREE + vs16), (nv / C::NV16 - 1) & 1, wc)) return false;
+        const uint8_t* src = smem + C::OFF_V8 + vs8 * C::K8;
+        uint8_t* dst = smem + C::OFF_V16 + vs16 * C::V16;
+        const int left = U.len - (U.kt0 + jj) * 128;               // keys that exist
+        const int quarter = lane >> 3, half = (lane & 7) >> 2;
+        const int u = (lane & 3) + 4 * (half ^ (quarter & 1));     // 16-byte piece of a line
+        const int r0 = 4 * w4 + 2 * (quarter >> 1) + half, sw = r0 & 7;   // line 16 it + r0
+        const uint8_t* s_base = src + r0 * 128 + ((u ^ sw) << 4);
+#pragma unroll
+        for (int it = 0; it < D / 16; ++it) {
+          uint4 v = *reinterpret_cast<const uint4*>(s_base + it * 2048);
+          // d = 128: a line is a key; d = 64: two keys.
+          const int key = D == 128 ? it * 16 + r0 : 2 * (it * 16 + r0) + (u >> 2);
+          uint32_t wv = w_mine;
+          if constexpr (NG > 1) wv = __shfl_sync(0xffffffffu, w_mine, D == 128 ? it : 2 * it + (w4 >> 1));
+          if (key >= left) v = make_uint4(0u, 0u, 0u, 0u);         // whatever the codes are (NaN too)
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[2 * i] = hmul2(e4m3x2_f16x2(in[i]), wv);
+            h[2 * i + 1] = hmul2(e4m3x2_f16x2_hi(in[i]), wv);
+          }
+          const int q = u & 3;                                     // pieces 2q, 2q + 1 of the f16 row
+          uint8_t* d_row = dst + (D == 128 ? (u >> 2) * C::CH16 : 0u) + key * 128;
+          const int ks = key & 7;
+          *reinterpret_cast<uint4*>(d_row + (((2 * q) ^ ks) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(d_row + (((2 * q + 1) ^ ks) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();            // generic writes -> tensor-core reads
+        mbar_arrive(BAR(T_V16FULL + vs16));
+        mbar_arrive(BAR(T_V8FREE + vs8));
+        ++nv;
+        return true;
+      };
+      if (U.nmax > 0 && !widen(0)) { ok = false; break; }
+      for (int j = 0; j < U.nmax && ok; ++j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= U.nt[t]) continue;
+          if (!warp_wait(BAR(T_STATS + t), nst[t] & 1, wc)) { ok = false; break; }
+          ++nst[t];
+          ref_t[t] = rref;
+          const float alpha = alpha_buf[t * 128 + row] * fac;
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // S_t(j) complete => PV_t(j-1), issued before it, is complete too.
+            if (!warp_wait(BAR(T_SFULL + t), (nst[t] - 1) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
+            uint32_t x[32];
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              tmem_ld32(tO + q * 32, x);
+              tmem_wait_ld();
+              reg_fence(x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+              tmem_st32(tO + q * 32, x);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(BAR(T_PFULL + t));
+        }
+        // The next block's V, needed by the PV products two MMA iterations from now.
+        if (ok && j + 1 < U.nmax && !widen(j + 1)) ok = false;
+      }
+      if (!ok) break;
+      // Epilogue per tile: O / l to its rows, or O and the statistics to the workspace.
+      const bool whole = U.ubeg >= 0 && U.uend <= U.re;
+      const int second = U.ubeg > 0 ? 1 : 0, part = 2 * blockIdx.x + second;
+      if (U.ubeg >= 0 && !whole && ct == 0)      // re is the run here: the unit goes on in the next CTA
+        *rec = make_int4(U.b, U.h, U.rt * qu, 2 * ((U.uend - 1) / U.re) + second);
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int n_t = t ? U.nt[1] : U.nt[0];
+        if (!warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
+        if (n_t > 0) {
+          const uint32_t par = t ? nof[1] : nof[0];
+          if (!warp_wait(BAR(T_OFULL + t), par & 1, wc)) { ok = false; break; }
+          if (t) ++nof[1]; else ++nof[0];
+        }
+        tc_fence_after();
+        const float* st = fin + t * 256 + row;
+        const float m = st[0], l = st[128], ref = (t ? ref_t[1] : ref_t[0]) / kVShift;
+        const int r = t * 128 + row, qi = r / p.g;
+        const bool live = r < U.rows;
+        const long long orow = (long long)(U.h * p.g + (r - qi * p.g)) * p.total_q + U.q0 + U.rt * qu + qi;
+        const long long prow = (long long)part * kTRows + r;
+        const float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f;
+        const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
+        uint32_t x[32];
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          if (n_t > 0) {
+            tmem_ld32(tO + q * 32, x);
+            tmem_wait_ld();
+            reg_fence(x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0u;
+          }
+          if (live && whole) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + q * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv, __uint_as_float(x[8 * i + 2 * k + 1]) * inv);
+              out[i] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (live) {
+            uint4* out = reinterpret_cast<uint4*>(ws + W.part) + prow * (D / 4) + q * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        if (n_t > 0) {
+          tc_fence_before();
+          mbar_arrive(BAR(T_OFREE + t));
+        }
+        if (live) {
+          if (whole) p.lse[orow] = (m - kPShift + __log2f(l)) * kLn2;
+          else reinterpret_cast<float4*>(ws + W.stat)[prow] = make_float4(m - kPShift, l, ref, 0.f);
+        }
+      }
+      if (!ok) break;
+      mbar_arrive(BAR(T_EPI));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int NG>
+cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, cudaStream_t s) {
+  using C = TileCfg<D>;
+  static std::once_flag flags[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::call_once(flags[dev & 63], [&] {
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
+  fwd_cache_tile_kernel<D, NG><<<grid, kTThreads, C::SMEM, s>>>(maps.k, maps.v, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_fwd_cache_merge(p, D, kTRows, grid, s);
+}
+
+}  // namespace
+
+size_t cache_tile_workspace_bytes(int d, int sms) { return cache_ws(sms, kTRows, d).total; }
+
+cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
+  const bool one = p.page == 128;            // a key block has one scale
+  if (d == 64) return one ? launch_tile<64, 1>(maps, p, sms, s) : launch_tile<64, 8>(maps, p, sms, s);
+  return one ? launch_tile<128, 1>(maps, p, sms, s) : launch_tile<128, 8>(maps, p, sms, s);
+}
+
+}  // namespace attn

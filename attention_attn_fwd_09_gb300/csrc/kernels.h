@@ -223,8 +223,13 @@ struct CacheMaps {
 };
 // At most 16 rows (queries x heads of a group) per sequence and K/V head: fwd_cache.cu.
 constexpr int kCacheDecodeRows = 16;
-size_t cache_decode_workspace_bytes(int B, int Hkv, int rows, int d, int sms);
+size_t cache_decode_workspace_bytes(int rows, int d, int sms);
+// Joins what the main kernel's ctas CTAs left of units cut between them, a dependent launch.
+cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s);
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
-cudaError_t launch_fwd_cache_rows(const CacheParams& p, int d, cudaStream_t s);
+// More rows: fwd_cache_tile.cu.  Maps as above, but boxes of 128 keys (a smaller page: its keys), and
+// K's lines are keys (d bytes; 64-byte swizzle for d = 64).  g <= 256.
+size_t cache_tile_workspace_bytes(int d, int sms);
+cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
 
 }  // namespace attn
