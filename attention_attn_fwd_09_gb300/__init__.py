@@ -410,27 +410,35 @@ def attn_fwd_fp8(q8, k8, v8, q_scale, k_scale, v_scale, causal: bool = False, sc
     return o, lse
 
 
-def _scope(device, stream):
-    """(raw stream, context) of a call on ``device``: in the context that device is current and
-    what is allocated belongs to the stream the call runs on, so that a workspace allocated here
-    is not handed out again before the call has run."""
-    if stream is None:
-        if device.index == torch.cuda.current_device():
-            return torch.cuda.current_stream().cuda_stream, _NO_CONTEXT
-        return torch.cuda.current_stream(device).cuda_stream, torch.cuda.device(device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+# The current device's index, and the raw current stream of a device: what torch.cuda.current_device()
+# and current_stream() return, without making a Stream object (3 us of a call's host time).
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+@contextlib.contextmanager
+def _there(device, stream):
+    """``device`` and ``stream`` (a torch stream, a raw one or None) made current, so that what a
+    call allocates belongs to the stream it runs on and is not handed out again before it has run."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _bad(name, t, dtype, shape, device):
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
 
 def _plain(name, t, dtype, shape, device):
     """A contiguous tensor of this type and shape on this device, or ValueError."""
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+        _bad(name, t, dtype, shape, device)
 
 
 def attn_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -471,38 +479,50 @@ def attn_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", fact
     return f.to(device), mscale
 
 
+_Strides12, _Strides4 = _ll * 12, _ll * 4
+_ROW = (0, 0, 0)
+
+
+def _rows(name, t, shape, dev):
+    """(batch, head, token) strides of a bf16 tensor [B,H,N,d] or [H,T,d] with contiguous columns."""
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or st[-1] != 1:
+        raise ValueError(f"{name}: expected a bf16 tensor of shape {tuple(shape)} with contiguous columns on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
+    return st[:3] if len(st) == 4 else (0, st[0], st[1])
+
+
 def _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream):
-    dims = q.dim()
-    if dims not in (3, 4):
-        raise ValueError(f"q: expected [B,H,N,d] or [H,T,d], got {tuple(q.shape)}")
-    dev = q.device
-    raw, context = _scope(dev, stream) if q.is_cuda else (0, _NO_CONTEXT)
-    with context:
-        N, d = q.shape[-2], q.shape[-1]
-        B = q.shape[0] if dims == 4 else 1
-        Hq, Hk = q.shape[-3], (k.shape[-3] if k is not None else 0)
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-        strides = []
-        for name, t, h in (("q", q, Hq), ("k", k, Hk), ("q_out", q_out, Hq), ("k_out", k_out, Hk)):
-            if t is None:
-                strides += (0, 0, 0)
-                continue
-            st = t.stride()
-            if (t.dtype is not torch.bfloat16 or not t.is_cuda or t.device != dev or st[-1] != 1
-                    or t.shape != ((B, h, N, d) if dims == 4 else (h, N, d))):
-                raise ValueError(f"{name}: expected a bf16 tensor of shape {((B, h, N, d) if dims == 4 else (h, N, d))} with "
-                                 f"contiguous columns on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
-            strides += (st[0] if dims == 4 else 0, st[-3], st[-2])
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq: expected a 1-D tensor of rot / 2 values")
-        _plain("inv_freq", inv_freq, torch.float64, inv_freq.shape, dev)
-        if positions is not None:
-            _plain("positions", positions, torch.int32, (B, N) if positions.dim() == 2 or dims == 4 else (N,), dev)
-        _check(call(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(), k_out.data_ptr() if Hk else None,
-                    inv_freq.data_ptr(), positions.data_ptr() if positions is not None else None, B, Hq, Hk, N, d,
-                    2 * inv_freq.numel(), int(bool(interleaved)), float(mscale), (_ll * 12)(*strides), raw))
+    shape, dev = q.shape, q.device
+    dims = len(shape)
+    if dims not in (3, 4) or not q.is_cuda:
+        raise ValueError(f"q: expected a CUDA tensor [B,H,N,d] or [H,T,d], got {tuple(shape)} on {dev}")
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, None)
+    if dims == 4:
+        B, Hq, N, d = shape
+    else:
+        B, (Hq, N, d) = 1, shape
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    sq, oq = _rows("q", q, shape, dev), _rows("q_out", q_out, shape, dev)
+    Hk, sk, ok, pk, pok = 0, _ROW, _ROW, None, None
+    if k is not None:
+        Hk = k.shape[-3] if k.dim() == dims else 0
+        kshape = (B, Hk, N, d) if dims == 4 else (Hk, N, d)
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=torch.bfloat16, device=dev)
+        sk, ok = _rows("k", k, kshape, dev), _rows("k_out", k_out, kshape, dev)
+        pk, pok = k.data_ptr(), k_out.data_ptr()
+    half = inv_freq.numel()
+    _plain("inv_freq", inv_freq, torch.float64, (half,), dev)
+    pos = None
+    if positions is not None:
+        _plain("positions", positions, torch.int32, (N,) if dims == 3 and positions.dim() == 1 else (B, N), dev)
+        pos = positions.data_ptr()
+    _check(call(q.data_ptr(), pk, q_out.data_ptr(), pok, inv_freq.data_ptr(), pos, B, Hq, Hk, N, d, 2 * half,
+                1 if interleaved else 0, mscale, _Strides12(*sq, *sk, *oq, *ok), _current_stream(dev.index)))
     return q_out, k_out
 
 
@@ -524,20 +544,21 @@ def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, m
 
 
 def _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu, cu_name, kv_lens, dev):
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache: expected [num_pages, Hkv, page_size, d], got {tuple(k_cache.shape)}")
-    shape = k_cache.shape
-    _plain("k_cache", k_cache, torch.uint8, shape, dev)
-    _plain("v_cache", v_cache, torch.uint8, shape, dev)
-    _plain("k_scale", k_scale, torch.float32, shape[:2], dev)
-    _plain("v_scale", v_scale, torch.float32, shape[:2], dev)
-    B = kv_lens.numel()
-    _plain("kv_lens", kv_lens, torch.int32, (B,), dev)
-    _plain(cu_name, cu, torch.int32, (B + 1,), dev)
-    if page_table.dim() != 2:
+    """Checks a paged cache and its index tensors; (num_pages, Hkv, page_size, d, B, max_pages)."""
+    shape, (B, width) = k_cache.shape, page_table.shape if page_table.dim() == 2 else (-1, -1)
+    if len(shape) != 4:
+        raise ValueError(f"k_cache: expected [num_pages, Hkv, page_size, d], got {tuple(shape)}")
+    if B < 0:
         raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
-    _plain("page_table", page_table, torch.int32, (B, page_table.shape[1]), dev)
-    return B, shape[0], shape[1], shape[2], shape[3], page_table.shape[1]
+    u8, f32, i32, pairs = torch.uint8, torch.float32, torch.int32, shape[:2]
+    _plain("k_cache", k_cache, u8, shape, dev)
+    _plain("v_cache", v_cache, u8, shape, dev)
+    _plain("k_scale", k_scale, f32, pairs, dev)
+    _plain("v_scale", v_scale, f32, pairs, dev)
+    _plain("page_table", page_table, i32, (B, width), dev)
+    _plain(cu_name, cu, i32, (B + 1,), dev)
+    _plain("kv_lens", kv_lens, i32, (B,), dev)
+    return (*shape, B, width)
 
 
 def attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens, stream=None):
@@ -550,20 +571,18 @@ def attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_
     if not k.is_cuda or k.dim() != 3:
         raise ValueError(f"k: expected a CUDA tensor [Hkv, total, d], got {tuple(k.shape)} on {k.device}")
     dev = k.device
-    B, pages, Hkv, P, d, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, "cu_seqlens",
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens)
+    pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, "cu_seqlens",
                                                 kv_lens, dev)
     T = k.shape[1]
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype is not torch.bfloat16 or t.device != dev or t.shape != (Hkv, T, d) or t.stride()[2] != 1:
-            raise ValueError(f"{name}: expected a bf16 tensor of shape {(Hkv, T, d)} with contiguous columns on {dev}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    raw, context = _scope(dev, stream)
-    sk, sv = k.stride(), v.stride()
-    with context:
-        _check(_lib.attn_kv_append_fp8(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                       k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
-                                       cu_seqlens.data_ptr(), kv_lens.data_ptr(), B, Hkv, T, d, pages, P, width,
-                                       (_ll * 4)(sk[0], sk[1], sv[0], sv[1]), raw))
+    shape = (Hkv, T, d)
+    sk, sv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
+    _check(_lib.attn_kv_append_fp8(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                   k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(),
+                                   kv_lens.data_ptr(), B, Hkv, T, d, pages, P, width,
+                                   _Strides4(sk[1], sk[2], sv[1], sv[2]), _current_stream(dev.index)))
 
 
 def attn_fwd_kv_fp8_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_q: int, d: int) -> int:
@@ -584,30 +603,33 @@ def attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlen
     if not q.is_cuda or q.dim() != 3:
         raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
     dev = q.device
-    B, pages, Hkv, P, d, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q,
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, max_q, causal,
+                                   scale, o, lse, workspace)
+    pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q,
                                                 "cu_seqlens_q", kv_lens, dev)
-    Hq, T = q.shape[0], q.shape[1]
-    _plain("q", q, torch.bfloat16, (Hq, T, d), dev)
-    raw, context = _scope(dev, stream)
-    with context:
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _plain("o", o, torch.bfloat16, (Hq, T, d), dev)
-        if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-        else:
-            _plain("lse", lse, torch.float32, (Hq, T), dev)
-        if workspace is None:
-            n = attn_fwd_kv_fp8_workspace_size(B, Hq, Hkv, T, int(max_q), d)
-            workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
-        _check(_lib.attn_fwd_kv_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                    v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(),
-                                    kv_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, int(max_q), d,
-                                    pages, P, width, int(bool(causal)), float(d ** -0.5 if scale is None else scale),
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
+    Hq, T, _ = q.shape
+    shape = (Hq, T, d)
+    _plain("q", q, torch.bfloat16, shape, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _plain("o", o, torch.bfloat16, shape, dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _plain("lse", lse, torch.float32, (Hq, T), dev)
+    if workspace is None:
+        n = attn_fwd_kv_fp8_workspace_size(B, Hq, Hkv, T, max_q, d)
+        workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
+    _check(_lib.attn_fwd_kv_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+                                o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, max_q, d, pages, P, width,
+                                1 if causal else 0, d ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                                workspace.nbytes, _current_stream(dev.index)))
     return o, lse
 
 

@@ -40,9 +40,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // sequence and K/V head) may be worked on by several CTAs, each of which leaves a partial
 // result: per row m (running maximum, log2), l (sum of 2^(s - m)), a reference scale r and
 // O / r.  A CTA has at most two: partial 0 for its first unit, partial 1 for its last.
-// Workspace: per CTA an int4 {b, K/V head, first query, 2 x further CTAs + which partial} for the
-// unit that starts in it and is cut (last field < 2: none); then per partial and row
-// (m, l, r, -); then the O rows.
+// Workspace: per CTA an int4 {K/V head, first packed query, queries, 2 x further CTAs + which
+// partial} for the unit that starts in it and is cut (last field < 2: none); then per partial and
+// row (m, l, r, -); then the O rows.
 struct CacheWs {
   size_t stat, part, total;
 };

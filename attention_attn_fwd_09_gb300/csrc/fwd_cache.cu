@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // First unit of the CTA: partial 0, its last one: partial 1.
       const int second = seg.ubeg > rs ? 1 : 0, part = 2 * blockIdx.x + second;
       if (seg.ubeg >= rs && !whole && lane == 0)
-        *rec = make_int4(seg.b, seg.h, 0, 2 * ((int)((seg.uend - 1) / run) - (int)blockIdx.x) + second);
+        *rec = make_int4(seg.h, q0, n, 2 * ((int)((seg.uend - 1) / run) - (int)blockIdx.x) + second);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = rq + 8 * i, qi = r / g;
@@ -564,47 +564,62 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the partial results of cut units: block x takes the unit that starts in CTA x of the main
-// kernel and goes on in others (at most one), block y 128 groups of 4 columns of it.
+// kernel and goes on in others (at most one); its threads take 4 columns of a row at a time.  The
+// kernel is short (two dependent reads once the main kernel is done), so it reads statistics and
+// rows of four partials at once and joins them as they come.
 template <int D>
 __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int ctas) {
   const CacheWs W = cache_ws(ctas, rows_max, D);
   const char* ws = static_cast<const char*>(p.ws);
-  const int i = blockIdx.y * 128 + threadIdx.x, r = i / (D / 4), col = i % (D / 4);
-  pdl_wait();
-  const int4 rec = reinterpret_cast<const int4*>(ws)[blockIdx.x];   // {b, h, first query, 2 x further CTAs + which partial}
-  if (rec.w < 2) return;
-  const int b = rec.x, h = rec.y, q0 = p.cu_q[b], n = p.cu_q[b + 1] - q0, qi = rec.z + r / p.g;
-  if (r >= rows_max / p.g * p.g || qi >= n) return;           // a unit holds whole queries
-  const int first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
   const float4* stat = reinterpret_cast<const float4*>(ws + W.stat);
   const float4* part = reinterpret_cast<const float4*>(ws + W.part);
-  // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
-  auto index = [&](int k) -> long long { return (long long)(k == 0 ? first : 2 * ((int)blockIdx.x + k)) * rows_max + r; };
-  float m = -INFINITY, ref = kMinScale;
-  for (int k = 0; k <= more; ++k) {
-    const float4 s = stat[index(k)];
-    m = fmaxf(m, s.x);
-    ref = fmaxf(ref, s.z);
+  pdl_wait();
+  const int4 rec = reinterpret_cast<const int4*>(ws)[blockIdx.x];
+  if (rec.w < 2) return;
+  const int h = rec.x, rows = rec.z * p.g, first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
+  for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (D / 4); i += gridDim.y * 128) {
+    const int r = i / (D / 4), col = i % (D / 4);
+    float m = -INFINITY, ref = kMinScale, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 <= more; k0 += 4) {
+      float4 st[4], x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j;
+        // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
+        const long long at = (long long)(k == 0 ? first : 2 * ((int)blockIdx.x + k)) * rows_max + r;
+        st[j] = k <= more ? stat[at] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        x[j] = k <= more ? part[at * (D / 4) + col] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float mn = m, rn = ref;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mn = fmaxf(mn, st[j].x);
+        rn = fmaxf(rn, st[j].z);
+      }
+      const float mu = mn == -INFINITY ? 0.f : mn, rinv = 1.f / rn;
+      const float w0 = ex2_mufu(m - mu), v0 = w0 * (ref * rinv);
+      l *= w0;
+      o.x *= v0; o.y *= v0; o.z *= v0; o.w *= v0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = ex2_mufu(st[j].x - mu), v = w * (st[j].z * rinv);
+        l += w * st[j].y;
+        o.x += v * x[j].x;
+        o.y += v * x[j].y;
+        o.z += v * x[j].z;
+        o.w += v * x[j].w;
+      }
+      m = mn;
+      ref = rn;
+    }
+    const int qi = r / p.g;
+    const long long row = (long long)(h * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
+    const float inv = l == 0.f ? 0.f : ref / l;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + col;
+    *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (col == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
   }
-  const float mu = m == -INFINITY ? 0.f : m, rinv = 1.f / ref;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k <= more; ++k) {
-    const float4 s = stat[index(k)];
-    const float4 x = part[index(k) * (D / 4) + col];
-    const float w = ex2_mufu(s.x - mu), v = w * (s.z * rinv);
-    l += w * s.y;
-    o.x += v * x.x;
-    o.y += v * x.y;
-    o.z += v * x.z;
-    o.w += v * x.w;
-  }
-  const long long row = (long long)(h * p.g + r % p.g) * p.total_q + q0 + qi;
-  const float inv = l == 0.f ? 0.f : ref / l;
-  uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + col;
-  *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (col == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -627,7 +642,8 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
 }  // namespace
 
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
-  const dim3 grid((unsigned)ctas, (unsigned)((rows * (d / 4) + 127) / 128));
+  // 16 blocks for a unit of 256 rows: all blocks are resident at once, with a few rows a thread.
+  const dim3 grid((unsigned)ctas, (unsigned)min((rows * (d / 4) + 127) / 128, 16));
   return d == 64 ? launch_pdl(fwd_cache_merge_kernel<64>, grid, dim3(128), 0, s, p, rows, ctas)
                  : launch_pdl(fwd_cache_merge_kernel<128>, grid, dim3(128), 0, s, p, rows, ctas);
 }

@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const bool whole = U.ubeg >= 0 && U.uend <= U.re;
       const int second = U.ubeg > 0 ? 1 : 0, part = 2 * blockIdx.x + second;
       if (U.ubeg >= 0 && !whole && ct == 0)      // re is the run here: the unit goes on in the next CTA
-        *rec = make_int4(U.b, U.h, U.rt * qu, 2 * ((U.uend - 1) / U.re) + second);
+        *rec = make_int4(U.h, U.q0 + U.rt * qu, U.rows / p.g, 2 * ((U.uend - 1) / U.re) + second);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int n_t = t ? U.nt[1] : U.nt[0];

@@ -184,7 +184,7 @@ struct RopeParams {
   const int* positions;      // [B, N] (device) or null: 0 .. N - 1
   int B, N, Hq, Hk, d, rot;
   float mscale, sign;        // factor on the rotated part; +1 forward, -1 transposed
-  int tile, tiles, head_group;   // filled in by launch_rope: tokens per CTA, tiles per sequence, heads per CTA
+  int tile_shift, tiles, head_group;   // filled in by launch_rope: log2(tokens per CTA), tiles per sequence, heads per CTA
 };
 // vec: elements per access (8, 4 or 1) that every pointer, stride and rot allow.
 cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s);
@@ -197,9 +197,10 @@ struct AppendParams {
   float *k_scale, *v_scale;  // [num_pages, Hkv]
   const int *table, *cu, *kv_lens;   // [B, max_pages], [B + 1], [B]
   int B, Hkv, total, num_pages, page, max_pages, max_len;
+  int page_shift;            // log2(page), filled in by launch_kv_append
   int* status;
 };
-cudaError_t launch_kv_append(const AppendParams& p, int d, cudaStream_t s);
+cudaError_t launch_kv_append(AppendParams p, int d, cudaStream_t s);
 
 // Packed queries over the paged e4m3 cache (fwd_cache.cu).
 struct CacheParams {

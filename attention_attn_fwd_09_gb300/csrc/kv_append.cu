@@ -8,10 +8,13 @@
 // lose nothing by it: e4m3 is a floating-point format), so a row coded again keeps its value
 // but for results below 2^-6, and rows appended one by one end as rows appended at once.
 //
-// One CTA per page, head and K or V.  Nothing on the host knows the lengths: CTA slots are
-// numbered so that sequence b owns the slots from floor(cu[b] / P) + 2 b on, which leaves it
-// at least floor(n / P) + 2 >= the pages its n rows can touch; spare slots exit.  Bound by
-// bytes (2 read, 1 written per element) for prompts, by latency for single tokens.
+// Nothing on the host knows the lengths: slots are numbered so that sequence b owns the slots
+// from floor(cu[b] / P) + 2 b on, which leaves it at least floor(n / P) + 2 >= the pages its n
+// rows can touch; spare slots exit.  Two kernels:
+//   * prompts (bound by bytes, 2 read and 1 written per element): a CTA per slot, head and K or
+//     V holds the page's new rows in registers between the maximum and the rounding;
+//   * a few rows per sequence (bound by latency): a warp per slot, head and K or V, no barrier
+//     behind the search for the slot.
 #include <cstdint>
 
 #include "cache.cuh"
@@ -55,98 +58,165 @@ struct Divisor {
   __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : (s > 0.f ? __fdiv_rn(x, s) : x); }
 };
 
-// 8 elements (16 bytes in, 8 bytes out) per thread and step; NV steps cover a page.
-template <int D, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendParams p) {
-  __shared__ float red[THREADS / 32];
+// The slot's sequence and page; false: nothing to do (or the offsets are wrong).  Every thread of
+// the CTA calls it with the CTA's slot.
+struct Slot {
+  int kept, rows;            // rows of the page in use before and after
+  int src0;                  // packed row of the page's row 0 (new rows: kept .. rows - 1)
+  int page;
+};
+template <int THREADS>
+__device__ __forceinline__ bool find_slot(const AppendParams& p, int slot, Slot& out) {
   const int tid = threadIdx.x;
-  // The sequence of this slot: the last b with floor(cu[b] / P) + 2 b <= slot.
-  const int slot = blockIdx.x;
+  // The last b with floor(cu[b] / P) + 2 b <= slot.
   int b = -1;
   bool bad = false;
   for (int base = 0; base < p.B; base += THREADS) {
     const int i = base + tid;
     bool below = false, wrong = false;
     if (i < p.B) {
-      const int c0 = p.cu[i], c1 = p.cu[i + 1], len = p.kv_lens[i];
+      const int c0 = __ldg(p.cu + i), c1 = __ldg(p.cu + i + 1), len = __ldg(p.kv_lens + i);
       wrong = c1 < c0 || c0 < 0 || c1 - c0 > len || len > p.max_len || (i == 0 && c0 != 0) ||
               (i == p.B - 1 && c1 != p.total);
-      below = c0 / p.page + 2 * i <= slot;
+      below = (c0 >> p.page_shift) + 2 * i <= slot;
     }
     bad |= __syncthreads_or(wrong) != 0;
     b += __syncthreads_count(below);
   }
   if (bad) {
     if (tid == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
-    return;
+    return false;
   }
-  const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.kv_lens[b], start = len - n;
-  const int blk = start / p.page + slot - (c0 / p.page + 2 * b);
-  const int first = blk * p.page;                      // < max_len + 2 pages
-  if (n == 0 || first >= len) return;
-  const int page = p.table[(long long)b * p.max_pages + blk];
-  if (page < 0 || page >= p.num_pages) {
+  const int c0 = __ldg(p.cu + b), n = __ldg(p.cu + b + 1) - c0, len = __ldg(p.kv_lens + b), start = len - n;
+  const int blk = (start >> p.page_shift) + slot - ((c0 >> p.page_shift) + 2 * b);
+  const int first = blk << p.page_shift;                // < max_len + 2 pages
+  if (n == 0 || first >= len) return false;
+  out.page = __ldg(p.table + (long long)b * p.max_pages + blk);
+  if (out.page < 0 || out.page >= p.num_pages) {
     if (tid == 0) atomicExch(p.status, DEV_BAD_PAGE);
-    return;
+    return false;
   }
-  const int kept = max(start, first) - first;          // earlier rows of the page
-  const int rows = min(len - first, p.page);           // rows in use afterwards
-  const int head = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + head * (is_v ? p.v_h : p.k_h);
-  const long long st = is_v ? p.v_t : p.k_t;
-  const long long ph = (long long)page * p.Hkv + head;
-  uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + ph * p.page * D;
-  float* scale = (is_v ? p.v_scale : p.k_scale) + ph;
+  out.kept = max(start, first) - first;
+  out.rows = min(len - first, 1 << p.page_shift);
+  out.src0 = c0 + first - start;
+  return true;
+}
 
+// One head's K or V of a page.
+struct Target {
+  const uint16_t* src;       // packed row 0 of the head
+  long long st;              // token stride
+  uint8_t* dst;              // the page's codes
+  float* scale;
+  __device__ __forceinline__ Target(const AppendParams& p, const Slot& s, int head, bool is_v, int d)
+      : src(static_cast<const uint16_t*>(is_v ? p.v : p.k) + head * (is_v ? p.v_h : p.k_h)), st(is_v ? p.v_t : p.k_t) {
+    const long long ph = (long long)s.page * p.Hkv + head;
+    dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + (ph << p.page_shift) * d;
+    scale = (is_v ? p.v_scale : p.k_scale) + ph;
+  }
+};
+
+// Largest finite magnitude: infinities saturate and NaN stays NaN, neither sets the scale.
+__device__ __forceinline__ float amax8(const uint4& v, float amax) {
+  float f[8];
+  bf16x8(v, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float a = fabsf(f[k]);
+    amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+  }
+  return amax;
+}
+__device__ __forceinline__ uint2 code8(const uint4& v, const Divisor& div) {
+  float f[8];
+  bf16x8(v, f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = div(f[k]);
+  return e4m3x8(f);
+}
+// Codes of an earlier row at the page's new scale.
+__device__ __forceinline__ uint2 recode8(const uint2& old, float s_old, const Divisor& div) {
+  float f[8];
+  e4m3x4_to_f32(old.x, f[0], f[1], f[2], f[3]);
+  e4m3x4_to_f32(old.y, f[4], f[5], f[6], f[7]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = div(f[k] * s_old);
+  return e4m3x8(f);
+}
+
+// 8 elements (16 bytes in, 8 bytes out) per thread and step; NV steps cover a page.
+template <int D, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_kernel(const AppendParams p) {
+  __shared__ float red[THREADS / 32];
+  const int tid = threadIdx.x;
+  Slot s;
+  if (!find_slot<THREADS>(p, blockIdx.x, s)) return;
+  const Target t(p, s, blockIdx.y, blockIdx.z != 0, D);
   uint4 x[NV];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = (tid + i * THREADS) * 8, r = e / D, c = e % D;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= kept && r < rows) x[i] = *reinterpret_cast<const uint4*>(src + (long long)(c0 + first + r - start) * st + c);
-    float f[8];
-    bf16x8(x[i], f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float a = fabsf(f[k]);
-      amax = fmaxf(amax, a < INFINITY ? a : 0.f);      // infinities saturate, NaN stays NaN: neither sets the scale
-    }
+    x[i] = r >= s.kept && r < s.rows ? __ldcs(reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c))
+                                     : make_uint4(0u, 0u, 0u, 0u);
   }
+  const float s_old = s.kept > 0 ? *t.scale : 0.f;
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) amax = amax8(x[i], amax);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((tid & 31) == 0) red[tid >> 5] = amax;
-  const float s_old = kept > 0 ? *scale : 0.f;
   __syncthreads();
   amax = red[0];
 #pragma unroll
   for (int i = 1; i < THREADS / 32; ++i) amax = fmaxf(amax, red[i]);
-  const float s = fmaxf(s_old, pow2_scale(amax));
-  if (tid == 0 && s != s_old) *scale = s;
-  if (tid == 0 && kept == 0) *scale = s;
-  const Divisor div(s);
-  const bool again = s > s_old && s_old > 0.f;         // the kept rows' codes change
+  const float sc = fmaxf(s_old, pow2_scale(amax));
+  if (tid == 0) *t.scale = sc;
+  const Divisor div(sc);
+  const bool again = sc > s_old && s_old > 0.f;        // the kept rows' codes change
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = (tid + i * THREADS) * 8, r = e / D;
-    float f[8];
-    if (r < kept) {
-      if (!again) continue;
-      const uint2 old = *reinterpret_cast<const uint2*>(dst + e);
-      e4m3x4_to_f32(old.x, f[0], f[1], f[2], f[3]);
-      e4m3x4_to_f32(old.y, f[4], f[5], f[6], f[7]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = div(f[k] * s_old);
-    } else if (r < rows) {
-      bf16x8(x[i], f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = div(f[k]);
-    } else {
-      continue;                                        // rows behind the last one stay as they are
-    }
-    *reinterpret_cast<uint2*>(dst + e) = e4m3x8(f);
+    uint2* out = reinterpret_cast<uint2*>(t.dst + e);
+    if (r >= s.kept && r < s.rows) *out = code8(x[i], div);   // rows behind the last one stay as they are
+    else if (r < s.kept && again) *out = recode8(*out, s_old, div);
   }
+}
+
+constexpr int kStepWarps = 8;
+
+// Warp w of block (x, y): head 8 y + w of slot x / 2, K or V by x & 1.
+template <int D>
+__global__ void __launch_bounds__(kStepWarps * 32) kv_append_step_kernel(const AppendParams p) {
+  const int lane = threadIdx.x & 31, head = blockIdx.y * kStepWarps + (threadIdx.x >> 5);
+  Slot s;
+  if (!find_slot<kStepWarps * 32>(p, blockIdx.x >> 1, s) || head >= p.Hkv) return;
+  const Target t(p, s, head, blockIdx.x & 1, D);
+  constexpr int RPW = 32 / (D / 8);                    // rows a warp reads at once
+  const int r0 = lane / (D / 8), c = lane % (D / 8) * 8;
+  const float s_old = s.kept > 0 ? *t.scale : 0.f;
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  float amax = 0.f;
+  for (int r = s.kept + r0; r < s.rows; r += RPW) {
+    x = *reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c);
+    amax = amax8(x, amax);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float sc = fmaxf(s_old, pow2_scale(amax));
+  const Divisor div(sc);
+  for (int r = s.kept + r0; r < s.rows; r += RPW) {
+    if (s.rows - s.kept > RPW) x = *reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c);
+    *reinterpret_cast<uint2*>(t.dst + r * D + c) = code8(x, div);
+  }
+  if (sc > s_old && s_old > 0.f) {
+    for (int r = r0; r < s.kept; r += RPW) {
+      uint2* out = reinterpret_cast<uint2*>(t.dst + r * D + c);
+      *out = recode8(*out, s_old, div);
+    }
+  }
+  __syncwarp();                                        // every lane has read the old scale
+  if (lane == 0) *t.scale = sc;
 }
 
 template <int D>
@@ -156,16 +226,24 @@ cudaError_t launch_d(const AppendParams& p, dim3 grid, cudaStream_t s) {
   else if (vecs == 256) kv_append_kernel<D, 1, 256><<<grid, 256, 0, s>>>(p);
   else if (vecs == 512) kv_append_kernel<D, 2, 256><<<grid, 256, 0, s>>>(p);
   else if (vecs == 1024) kv_append_kernel<D, 4, 256><<<grid, 256, 0, s>>>(p);
-  else if (vecs == 2048) kv_append_kernel<D, 8, 256><<<grid, 256, 0, s>>>(p);
+  else if (vecs == 2048) kv_append_kernel<D, 4, 512><<<grid, 512, 0, s>>>(p);
   else return cudaErrorInvalidValue;
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_append(const AppendParams& p, int d, cudaStream_t s) {
+cudaError_t launch_kv_append(AppendParams p, int d, cudaStream_t s) {
+  p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
   const long long slots = (long long)p.total / p.page + 2LL * p.B;
-  if (slots > 0x7fffffffLL || p.Hkv > 65535) return cudaErrorInvalidValue;
+  if (slots > 0x3fffffffLL || p.Hkv > 65535) return cudaErrorInvalidValue;
+  // Up to 4 rows per sequence on average: a warp per page and head.
+  if (p.total <= 4LL * p.B) {
+    const dim3 grid((unsigned)(2 * slots), (unsigned)((p.Hkv + kStepWarps - 1) / kStepWarps));
+    if (d == 64) kv_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
+    else kv_append_step_kernel<128><<<grid, kStepWarps * 32, 0, s>>>(p);
+    return cudaGetLastError();
+  }
   const dim3 grid((unsigned)slots, (unsigned)p.Hkv, 2);
   return d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);
 }

@@ -82,71 +82,98 @@ __device__ __forceinline__ BfVec<V> pack(const float (&f)[V]) {
 // partners at + rot/2, interleaved columns c .. c+2V-1, or 2 V columns of the part that
 // passes through.  V = 8 needs rot % 16 == 0 and 16-byte rows, V = 4 rot % 8 == 0 and 8-byte
 // rows; V = 1 takes every even rot and alignment.
-template <int V, bool INTER>
+template <int V, bool INTER, int D>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   extern __shared__ float2 cs[];                       // [tokens][rot / 2] (m cos, m sin)
-  unsigned long long* turn = reinterpret_cast<unsigned long long*>(cs + p.tile * (p.rot / 2));   // [rot / 2]
+  constexpr int UPR = D / (2 * V);                     // items per head row
+  constexpr int BATCH = V == 8 ? 4 : 2;                // items a thread has in flight
   const int half = p.rot / 2;
-  const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x % p.tiles) * p.tile;
-  const int tn = min(p.tile, p.N - n0);
+  unsigned long long* turn = reinterpret_cast<unsigned long long*>(cs + (half << p.tile_shift));   // [rot / 2]
+  const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x - b * p.tiles) << p.tile_shift;
+  const int tile = 1 << p.tile_shift, tn = min(tile, p.N - n0);
   const int h0 = blockIdx.y * p.head_group, hn = min(p.head_group, p.Hq + p.Hk - h0);
-  for (int j = threadIdx.x; j < half; j += kRopeThreads) {
-    const double t = p.inv_freq[j] * 0.15915494309189535;          // turns per position
-    turn[j] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tn * half; i += kRopeThreads) {
-    const int n = i / half, j = i - n * half;
-    const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : n0 + n;
-    const unsigned long long ph = turn[j] * (unsigned long long)pos;
-    float s, c;
-    sincospif(__int2float_rn((int)(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-    cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
-  }
-  __syncthreads();
-  const int upr = p.d / (2 * V);                       // items per head row
-  const int items = tn * hn * upr;
-  for (int i = threadIdx.x; i < items; i += kRopeThreads) {
-    const int u = i % upr, r = i / upr;
-    const int n = r % tn, h = h0 + r / tn;
-    const bool is_q = h < p.Hq;
-    const int hh = is_q ? h : h - p.Hq;
-    const RopeTensor& t = is_q ? p.q : p.k;
-    const uint16_t* src = static_cast<const uint16_t*>(t.in) + b * t.in_b + hh * t.in_h + (long long)(n0 + n) * t.in_n;
-    uint16_t* dst = static_cast<uint16_t*>(t.out) + b * t.out_b + hh * t.out_h + (long long)(n0 + n) * t.out_n;
-    const bool rotated = INTER ? u * 2 * V < p.rot : u * V < half;
-    const int ca = (INTER || !rotated) ? u * 2 * V : u * V;
-    const int cb = (INTER || !rotated) ? ca + V : ca + half;
-    const BfVec<V> a = ld_vec<V>(src + ca), bb = ld_vec<V>(src + cb);
-    if (!rotated) {
-      st_vec<V>(dst + ca, a);
-      st_vec<V>(dst + cb, bb);
-      continue;
-    }
-    float x[V], y[V], xo[V], yo[V];
-    unpack<V>(a, x);
-    unpack<V>(bb, y);
-    if constexpr (INTER && V > 1) {
-      const float2* w = cs + n * half + u * V;         // 2 V columns hold V pairs
+  const int items = (hn << p.tile_shift) * UPR;
+  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += BATCH * kRopeThreads) {
+    BfVec<V> a[BATCH], bb[BATCH];
 #pragma unroll
-      for (int k = 0; k < V / 2; ++k) {
-        const float2 e = w[k], f = w[V / 2 + k];
-        xo[2 * k] = x[2 * k] * e.x - x[2 * k + 1] * e.y;
-        xo[2 * k + 1] = x[2 * k + 1] * e.x + x[2 * k] * e.y;
-        yo[2 * k] = y[2 * k] * f.x - y[2 * k + 1] * f.y;
-        yo[2 * k + 1] = y[2 * k + 1] * f.x + y[2 * k] * f.y;
-      }
-    } else {
-      const float2* w = cs + n * half + u * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        xo[k] = x[k] * w[k].x - y[k] * w[k].y;
-        yo[k] = y[k] * w[k].x + x[k] * w[k].y;
-      }
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * kRopeThreads, u = i % UPR, r = i / UPR;
+      const int n = r & (tile - 1), h = h0 + (r >> p.tile_shift);
+      if (i >= items || n >= tn) continue;
+      const bool is_q = h < p.Hq;
+      const RopeTensor& t = is_q ? p.q : p.k;
+      const uint16_t* src = static_cast<const uint16_t*>(t.in) + b * t.in_b + (is_q ? h : h - p.Hq) * t.in_h + (n0 + n) * t.in_n;
+      const bool rotated = INTER ? u * 2 * V < p.rot : u * V < half;
+      const int ca = (INTER || !rotated) ? u * 2 * V : u * V;
+      a[k] = ld_vec<V>(src + ca);
+      bb[k] = ld_vec<V>(src + ((INTER || !rotated) ? ca + V : ca + half));
     }
-    st_vec<V>(dst + ca, pack<V>(xo));
-    st_vec<V>(dst + cb, pack<V>(yo));
+    if (i0 == (int)threadIdx.x) {
+      // The angles, while the first rows are under way.
+      for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+        const double t = p.inv_freq[j] * 0.15915494309189535;          // turns per position
+        turn[j] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < tn * half; i += kRopeThreads) {
+        const int n = i / half, j = i - n * half;
+        const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : n0 + n;
+        const unsigned long long ph = turn[j] * (unsigned long long)pos;
+        float s, c;
+        sincospif(__int2float_rn((int)(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * kRopeThreads, u = i % UPR, r = i / UPR;
+      const int n = r & (tile - 1), h = h0 + (r >> p.tile_shift);
+      if (i >= items || n >= tn) continue;
+      const bool is_q = h < p.Hq;
+      const RopeTensor& t = is_q ? p.q : p.k;
+      uint16_t* dst = static_cast<uint16_t*>(t.out) + b * t.out_b + (is_q ? h : h - p.Hq) * t.out_h + (n0 + n) * t.out_n;
+      const bool rotated = INTER ? u * 2 * V < p.rot : u * V < half;
+      const int ca = (INTER || !rotated) ? u * 2 * V : u * V;
+      uint16_t* dst_b = dst + ((INTER || !rotated) ? ca + V : ca + half);
+      if (!rotated) {
+        st_vec<V>(dst + ca, a[k]);
+        st_vec<V>(dst_b, bb[k]);
+        continue;
+      }
+      float x[V], y[V], xo[V], yo[V];
+      unpack<V>(a[k], x);
+      unpack<V>(bb[k], y);
+      const float2* w = cs + n * half + u * V;         // V pairs
+      if constexpr (INTER && V > 1) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 e = w[j], f = w[V / 2 + j];
+          xo[2 * j] = x[2 * j] * e.x - x[2 * j + 1] * e.y;
+          xo[2 * j + 1] = x[2 * j + 1] * e.x + x[2 * j] * e.y;
+          yo[2 * j] = y[2 * j] * f.x - y[2 * j + 1] * f.y;
+          yo[2 * j + 1] = y[2 * j + 1] * f.x + y[2 * j] * f.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          xo[j] = x[j] * w[j].x - y[j] * w[j].y;
+          yo[j] = y[j] * w[j].x + x[j] * w[j].y;
+        }
+      }
+      st_vec<V>(dst + ca, pack<V>(xo));
+      st_vec<V>(dst_b, pack<V>(yo));
+    }
   }
+}
+
+template <int V, bool INTER>
+cudaError_t launch_v(const RopeParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  if (p.d == 64) rope_kernel<V, INTER, 64><<<grid, kRopeThreads, smem, s>>>(p);
+  else if (p.d == 128) rope_kernel<V, INTER, 128><<<grid, kRopeThreads, smem, s>>>(p);
+  else if (p.d == 192) rope_kernel<V, INTER, 192><<<grid, kRopeThreads, smem, s>>>(p);
+  else rope_kernel<V, INTER, 256><<<grid, kRopeThreads, smem, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -156,25 +183,17 @@ cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStr
   // are then shared by all heads), else one token per CTA and the heads split over CTAs so
   // that each thread has about one item.
   const int upr = p.d / (2 * vec), heads = p.Hq + p.Hk;
-  p.tile = (long long)p.B * ((p.N + 7) / 8) >= sms ? 8 : 1;
-  p.tiles = (p.N + p.tile - 1) / p.tile;
-  p.head_group = p.tile > 1 ? heads : (kRopeThreads + upr - 1) / upr;
+  p.tile_shift = (long long)p.B * ((p.N + 7) / 8) >= sms ? 3 : 0;
+  p.tiles = (p.N + (1 << p.tile_shift) - 1) >> p.tile_shift;
+  p.head_group = p.tile_shift > 0 ? heads : (kRopeThreads + upr - 1) / upr;
   const long long gx = (long long)p.B * p.tiles;
   const int gy = (heads + p.head_group - 1) / p.head_group;
   if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)(p.tile + 1) * (p.rot / 2) * sizeof(float2);
+  const size_t smem = ((size_t)(1 << p.tile_shift) + 1) * (p.rot / 2) * sizeof(float2);
   const dim3 grid((unsigned)gx, (unsigned)gy);
-  auto go = [&](auto kern) { kern<<<grid, kRopeThreads, smem, s>>>(p); };
-  if (interleaved) {
-    if (vec == 8) go(rope_kernel<8, true>);
-    else if (vec == 4) go(rope_kernel<4, true>);
-    else go(rope_kernel<1, true>);
-  } else {
-    if (vec == 8) go(rope_kernel<8, false>);
-    else if (vec == 4) go(rope_kernel<4, false>);
-    else go(rope_kernel<1, false>);
-  }
-  return cudaGetLastError();
+  if (vec == 8) return interleaved ? launch_v<8, true>(p, grid, smem, s) : launch_v<8, false>(p, grid, smem, s);
+  if (vec == 4) return interleaved ? launch_v<4, true>(p, grid, smem, s) : launch_v<4, false>(p, grid, smem, s);
+  return interleaved ? launch_v<1, true>(p, grid, smem, s) : launch_v<1, false>(p, grid, smem, s);
 }
 
 }  // namespace attn
