@@ -51,7 +51,7 @@ struct TileCfg {
   static constexpr uint32_t OFF_V8 = OFF_K + NK * K8;
   static constexpr uint32_t OFF_V16 = OFF_V8 + NV8 * K8;
   static constexpr uint32_t OFF_CTRL = OFF_V16 + NV16 * V16;
-  static constexpr uint32_t CTRL_BYTES = 256 + (2 * 128 + 4 * 128) * 4 + 64;
+  static constexpr uint32_t CTRL_BYTES = 512 + (2 * 128 + 4 * 128) * 4 + 64 + 256;
   static constexpr uint32_t SMEM = 1024 + OFF_CTRL + CTRL_BYTES;
   // K-major rows of D bytes: 128-byte swizzle for d = 128, 64-byte for d = 64.
   static constexpr uint32_t IDESC_QK = idesc_f32acc(128, 128, FMT_E4M3, FMT_E4M3, false, false);
@@ -75,10 +75,13 @@ enum {
   T_V16FULL = 24,  // +slot (2): widened (128)
   T_V16FREE = 26,  // +slot (2): products that read the slot complete
   T_EPI = 28,      // the unit's results written (128)
-  T_DONE = 29,
-  T_COUNT = 30
+  T_UFULL = 29,    // +slot (4): unit descriptor written
+  T_UFREE = 33,    // +slot (4): every role is through with the unit (14 warps)
+  T_DONE = 37,
+  T_COUNT = 38
 };
-static_assert(T_COUNT * 8 <= 256, "barriers fit the control block's first 256 bytes");
+static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
+constexpr int kUnitSlots = 4, kUnitReaders = 14;   // producer, MMA issuer, 8 softmax and 4 correction warps
 
 // sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0, in O(log) steps.
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -123,46 +126,20 @@ struct TileSeq {
   }
 };
 
-// The unit a role works on, and the CTA's part of it.  Blocks are counted from the CTA's first.
-struct TileUnit {
-  int f, ubeg, uend, re;                     // first block here, the unit's blocks, the CTA's end
-  int b, h, rt;
-  int q0, n, len, rows;                      // rows: in use of 256
+// A unit as the roles see it (shared memory, written by the scheduler warp).
+struct __align__(16) UnitDesc {
+  int nmax;                                  // key blocks here: of the longer tile (-1: no more units)
+  int nt[2];                                 // and of each tile
   int kt0;                                   // first key block here
-  int nt[2];                                 // key blocks here, per tile
-  int nmax;
-  __device__ __forceinline__ bool valid() const { return f < re; }
-  __device__ __forceinline__ void fill(const CacheParams& p, int qu) {
-    const TileSeq s(p, b, qu);
-    q0 = s.q0; n = s.n; len = s.len;
-    rows = min(qu, n - rt * qu) * p.g;
-    kt0 = f - ubeg;
-    const int kt1 = min(uend, re) - ubeg;
-    nmax = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r = min(rows, (t + 1) * 128) - t * 128;                 // rows of the tile
-      const int lim = r > 0 ? (p.causal ? len - n + rt * qu + (t * 128 + r - 1) / p.g + 1 : len) : 0;
-      nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
-      nmax = max(nmax, nt[t]);
-    }
-  }
-  __device__ __forceinline__ void next(const CacheParams& p, int qu) {
-    f = uend;
-    if (f >= re) return;
-    TileSeq s(p, b, qu);
-    if (++rt >= s.units) {
-      rt = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do s = TileSeq(p, ++b, qu);          // f < re: there is another unit
-        while (s.units == 0);
-      }
-    }
-    ubeg = uend;
-    uend = ubeg + s.blocks(p, qu, rt);
-    fill(p, qu);
-  }
+  int len;                                   // the sequence's keys
+  int b, h;
+  int rows;                                  // in use of 256
+  int q0;                                    // first packed query
+  int lim0;                                  // visible keys of the first query (not causal: of all)
+  int whole;                                 // the unit is this CTA's alone
+  int second;                                // partial 1 of the CTA, else partial 0
+  int more;                                  // CTAs behind this one that go on with it, if it starts here (else -1)
+  int pad[3];
 };
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
@@ -201,7 +178,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint8_t* ctrl = smem + C::OFF_CTRL;
   const uint32_t bar0 = smem_u32(ctrl);
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * i; };
-  float* alpha_buf = reinterpret_cast<float*>(ctrl + 256);   // [2][128]
+  UnitDesc* desc = reinterpret_cast<UnitDesc*>(ctrl + 512);  // [4]
+  float* alpha_buf = reinterpret_cast<float*>(ctrl + 768);   // [2][128]
   float* fin = alpha_buf + 256;                              // [2][m, l][128]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 512);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -218,6 +196,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   if (tid == 0) {
     mbar_init(BAR(T_EPI), 128);
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(BAR(T_UFULL + i), 1);
+      mbar_init(BAR(T_UFREE + i), kUnitReaders);
+    }
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(T_Q + t), 128);
       mbar_init(BAR(T_SFULL + t), 1);
@@ -313,16 +295,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  TileUnit U;
-  U.b = (int)misc[0];
-  U.h = (int)misc[1];
-  U.rt = (int)misc[2];
-  U.ubeg = (int)(misc[3] - rs);
-  U.f = 0;
-  U.re = (int)(re - rs);
-  U.uend = U.ubeg + TileSeq(p, U.b, qu).blocks(p, qu, U.rt);
-  U.fill(p, qu);
   const int page_shift = 31 - __clz(p.page);
+  // The roles' view of unit u: wait for its descriptor, and hand it back (one lane per warp).
+  auto unit_ready = [&](uint32_t u) -> bool { return mbar_wait(BAR(T_UFULL + u % kUnitSlots), (u / kUnitSlots) & 1, wc); };
+  auto unit_done = [&](uint32_t u) { mbar_arrive(BAR(T_UFREE + u % kUnitSlots)); };
 
   // Register split against the launch's 128 x 512: producer and MMA 64; softmax 184 each;
   // correction (and V widening) 80.
@@ -335,11 +311,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint32_t box_bytes = box_keys * D;
       uint32_t n_k = 0, n_v = 0;             // K, V blocks loaded so far
       bool ok = true;
-      while (U.valid() && ok) {
+      for (uint32_t nu = 0; ok; ++nu) {
+        if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
+        const UnitDesc& U = desc[nu % kUnitSlots];
+        const int nmax = U.nmax, key0 = U.kt0 * 128 + lane * box_keys, len = U.len, h = U.h;
+        const int* table = p.table + (long long)U.b * p.max_pages;
+        __syncwarp();
+        if (lane == 0) unit_done(nu);
+        if (nmax < 0) break;
         auto page_of = [&](int j) -> int {
-          const int key = (U.kt0 + j) * 128 + lane * box_keys;
-          if (lane >= boxes || j >= U.nmax || key >= U.len) return -1;
-          const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+          const int key = key0 + j * 128;
+          if (lane >= boxes || j >= nmax || key >= len) return -1;
+          const int pg = __ldg(table + (key >> page_shift));
           if (pg < 0 || pg >= p.num_pages) {
             atomicExch(p.status, DEV_BAD_PAGE);
             return 0;                        // any page of the cache: the sequence's results are undefined
@@ -347,11 +330,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
           return pg;
         };
         int pg_next = page_of(0);
-        for (int j = 0; j < U.nmax; ++j) {
+        for (int j = 0; j < nmax; ++j) {
           const int pg = pg_next;
           pg_next = page_of(j + 1);
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
-          const int z = pg * p.Hkv + U.h;
+          const int z = pg * p.Hkv + h;
           const int ks = (int)(n_k % C::NK), vs = (int)(n_v % C::NV8);
           if (n_k >= C::NK && !warp_wait(BAR(T_KFREE + ks), (n_k / C::NK - 1) & 1, wc)) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
@@ -364,7 +347,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (pg >= 0) tma_load_3d(sbase + C::OFF_V8 + vs * C::K8 + lane * box_bytes, &tm_v, 0, 0, z, BAR(T_V8FULL + vs));
           ++n_v;
         }
-        U.next(p, qu);
       }
       // Every copy has landed before the shared memory goes away, also when a wait ran out.
       if (lane == 0) {
@@ -383,15 +365,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t nk = 0, nv = 0;             // blocks whose S, PV were issued
         uint32_t np[2] = {0, 0}, no[2] = {0, 0};   // P phases used; units of tile t whose last PV was issued
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
-        for (; U.valid() && ok; U.next(p, qu)) {
+        for (uint32_t nu = 0; ok; ++nu) {
+          if (!unit_ready(nu)) { ok = false; break; }
+          const UnitDesc& U = desc[nu % kUnitSlots];
+          const int nmax = U.nmax, nt[2] = {U.nt[0], U.nt[1]};
+          unit_done(nu);
+          if (nmax < 0) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (U.nt[t] > 0 && !mbar_wait(BAR(T_Q + t), no[t] & 1, wc)) ok = false;
-          if (!ok || U.nmax == 0) continue;
+            if (nt[t] > 0 && !mbar_wait(BAR(T_Q + t), no[t] & 1, wc)) ok = false;
+          if (!ok || nmax == 0) continue;
           tc_fence_after();
-          for (int j = 0; j <= U.nmax && ok; ++j) {
+          for (int j = 0; j <= nmax && ok; ++j) {
             const uint32_t ks = nk % C::NK, vs = nv % C::NV16;
-            if (j < U.nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
+            if (j < nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
             if (j >= 1 && !mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
             tc_fence_after();
             const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
@@ -400,7 +387,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             for (int t = 0; t < 2; ++t) {
               if (!ok) break;
               const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
-              if (j >= 1 && j <= U.nt[t]) {
+              if (j >= 1 && j <= nt[t]) {
                 // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
                 if (j == 1 && no[t] > 0 && !mbar_wait(BAR(T_OFREE + t), (no[t] - 1) & 1, wc)) { ok = false; break; }
                 if (!mbar_wait(BAR(T_PFULL + t), np[t] & 1, wc)) { ok = false; break; }
@@ -409,12 +396,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
-                if (j == U.nt[t]) {
+                if (j == nt[t]) {
                   mma_commit(BAR(T_OFULL + t));
                   ++no[t];
                 }
               }
-              if (j < U.nt[t]) {
+              if (j < nt[t]) {
                 // S_t = (Q1_t + Q2_t) K8_j^T, K = 32 columns a step
                 const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + 2 * t * C::Q8, 16);
 #pragma unroll
@@ -427,7 +414,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               }
             }
             if (!ok) break;
-            if (j < U.nmax) {
+            if (j < nmax) {
               mma_commit(BAR(T_KFREE + ks));
               ++nk;
             }
@@ -442,6 +429,58 @@ __global__ void __launch_bounds__(kTThreads, 1)
         while (!mbar_try_wait(BAR(T_DONE), 0) && globaltimer_ns() - t0 < p.wait_ns) {
         }
       }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- scheduler
+      // Walks the CTA's units; blocks are counted from the CTA's first.
+      if (lane == 0) {
+        int b = (int)misc[0], h = (int)misc[1], rt = (int)misc[2], f = 0, ubeg = (int)(misc[3] - rs);
+        const int end = (int)(re - rs);
+        TileSeq sq(p, b, qu);
+        int uend = ubeg + sq.blocks(p, qu, rt);
+        for (uint32_t nu = 0;; ++nu) {
+          if (nu >= kUnitSlots && !mbar_wait(BAR(T_UFREE + nu % kUnitSlots), (nu / kUnitSlots - 1) & 1, wc)) break;
+          UnitDesc& U = desc[nu % kUnitSlots];
+          if (f >= end) {
+            U.nmax = -1;
+            mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
+            break;
+          }
+          const int rows = min(qu, sq.n - rt * qu) * p.g, kt0 = f - ubeg, kt1 = min(uend, end) - ubeg;
+          int nt[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int r = min(rows, (t + 1) * 128) - t * 128;           // rows of the tile
+            const int lim = r > 0 ? (p.causal ? sq.len - sq.n + rt * qu + (t * 128 + r - 1) / p.g + 1 : sq.len) : 0;
+            nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
+          }
+          U.nmax = max(nt[0], nt[1]);
+          U.nt[0] = nt[0];
+          U.nt[1] = nt[1];
+          U.kt0 = kt0;
+          U.len = sq.len;
+          U.b = b;
+          U.h = h;
+          U.rows = rows;
+          U.q0 = sq.q0 + rt * qu;
+          U.lim0 = p.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
+          U.whole = ubeg >= 0 && uend <= end ? 1 : 0;
+          U.second = ubeg > 0 ? 1 : 0;
+          U.more = ubeg >= 0 ? (uend - 1) / end : -1;  // cut: end is the run here, and the unit goes on behind it
+          mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
+          f = uend;
+          if (f >= end) continue;
+          if (++rt >= sq.units) {
+            rt = 0;
+            if (++h == p.Hkv) {
+              h = 0;
+              do sq = TileSeq(p, ++b, qu);   // f < end: there is another unit
+              while (sq.units == 0);
+            }
+          }
+          ubeg = uend;
+          uend = ubeg + sq.blocks(p, qu, rt);
+        }
+      }
     }
   } else if (wg == 1 || wg == 2) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -449,22 +488,27 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int t = wg - 1;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(t * 128);
-    uint32_t ns = 0, nu = 0;                 // S phases used; units
+    const int r = t * 128 + row, qi = r / p.g;         // row of the unit, its query
+    uint32_t ns = 0;                         // S phases used
     bool ok = true;
-    for (; U.valid() && ok; U.next(p, qu), ++nu) {
-      const int r = t * 128 + row;           // row of the unit
-      const int qi = r / p.g;
-      const bool live = r < U.rows;
-      const int n_t = t ? U.nt[1] : U.nt[0];
-      const int lim = !live ? U.len : (p.causal ? U.len - U.n + U.rt * qu + qi + 1 : U.len);
-      const int min_lim = p.causal ? U.len - U.n + U.rt * qu + t * 128 / p.g + 1 : U.len;   // the tile's first row
+    for (uint32_t nu = 0; ok; ++nu) {
+      if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
+      const UnitDesc& U = desc[nu % kUnitSlots];
+      const int n_t = U.nt[t], kt0 = U.kt0, len = U.len, h = U.h, q0 = U.q0;
+      const bool more = U.nmax >= 0, live = r < U.rows;
+      const int* table = p.table + (long long)U.b * p.max_pages;
+      const int lim = (p.causal && live ? U.lim0 + qi : len) - kt0 * 128;                       // visible keys of this row,
+      const int min_lim = (p.causal ? U.lim0 + t * 128 / p.g : len) - kt0 * 128;                // of the tile's first row
+      __syncwarp();
+      if (lane == 0) unit_done(nu);
+      if (!more) break;
       float c_row = 0.f;
       if (n_t > 0) {
         // This tile's Q is free: every S of the unit before has been waited for.
         uint4 w[D / 8];
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(p.q) +
-            ((long long)(U.h * p.g + (r - qi * p.g)) * p.total_q + U.q0 + U.rt * qu + qi) * D);
+            ((long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi) * D);
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) w[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -507,12 +551,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // K scales: lane & 7 looks after a group of 16 keys (all lanes after the one page when NG = 1);
       // pages one block further ahead than scales.
       auto page_of = [&](int j) -> int {
-        const int key = (U.kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
-        if (j >= n_t || key >= U.len) return -1;
-        const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+        const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        if (j >= n_t || key >= len) return -1;
+        const int pg = __ldg(table + (key >> page_shift));
         return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
       };
-      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.k_scale + (long long)pg * p.Hkv + U.h) : 0.f; };
+      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.k_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sk_next = scale_of(page_of(0));
       int pg_next = page_of(1);
       float m = -INFINITY, l = 0.f;
@@ -533,9 +577,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tmem_wait_ld();
         reg_fence(u);
         float* s = reinterpret_cast<float*>(u);
-        const int kb = (U.kt0 + j) * 128;
-        if (kb + 128 > min_lim) {
-          const int vis = lim - kb;          // visible columns
+        if (j * 128 + 128 > min_lim) {
+          const int vis = lim - j * 128;     // visible columns
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i >= vis) s[i] = -INFINITY;
@@ -609,18 +652,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const int ct = tid - 384, w4 = ct >> 5;
-    uint32_t nv = 0, nst[2] = {0, 0}, nof[2] = {0, 0}, nu = 0;   // V blocks widened; statistics, O phases used; units
+    uint32_t nv = 0, nst[2] = {0, 0}, nof[2] = {0, 0};   // V blocks widened; statistics, O phases used
     bool ok = true;
-    for (; U.valid() && ok; U.next(p, qu), ++nu) {
+    for (uint32_t nu = 0; ok; ++nu) {
+      if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
+      const UnitDesc& U = desc[nu % kUnitSlots];
+      const int nmax = U.nmax, nt[2] = {U.nt[0], U.nt[1]}, kt0 = U.kt0, len = U.len, h = U.h;
+      const int* table = p.table + (long long)U.b * p.max_pages;
+      if (nmax < 0) break;                   // the last descriptor is not reused
       float rref = kMinScale, fac = 1.f;     // largest V scale so far; old over new with the newest block
       float ref_t[2] = {kMinScale, kMinScale};   // what O_t is relative to
       auto page_of = [&](int j) -> int {
-        const int key = (U.kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
-        if (j >= U.nmax || key >= U.len) return -1;
-        const int pg = __ldg(p.table + (long long)U.b * p.max_pages + (key >> page_shift));
+        const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        if (j >= nmax || key >= len) return -1;
+        const int pg = __ldg(table + (key >> page_shift));
         return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
       };
-      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + U.h) : 0.f; };
+      auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sv_next = scale_of(page_of(0));
       int pg_next = page_of(1);
       // V8 block jj -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle).
@@ -647,7 +695,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nv >= C::NV16 && !warp_wait(BAR(T_V16FREE + vs16), (nv / C::NV16 - 1) & 1, wc)) return false;
         const uint8_t* src = smem + C::OFF_V8 + vs8 * C::K8;
         uint8_t* dst = smem + C::OFF_V16 + vs16 * C::V16;
-        const int left = U.len - (U.kt0 + jj) * 128;               // keys that exist
+        const int left = len - (kt0 + jj) * 128;               // keys that exist
         const int quarter = lane >> 3, half = (lane & 7) >> 2;
         const int u = (lane & 3) + 4 * (half ^ (quarter & 1));     // 16-byte piece of a line
         const int r0 = 4 * w4 + 2 * (quarter >> 1) + half, sw = r0 & 7;   // line 16 it + r0
@@ -679,11 +727,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ++nv;
         return true;
       };
-      if (U.nmax > 0 && !widen(0)) { ok = false; break; }
-      for (int j = 0; j < U.nmax && ok; ++j) {
+      if (nmax > 0 && !widen(0)) { ok = false; break; }
+      for (int j = 0; j < nmax && ok; ++j) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= U.nt[t]) continue;
+          if (!ok || j >= nt[t]) continue;
           if (!warp_wait(BAR(T_STATS + t), nst[t] & 1, wc)) { ok = false; break; }
           ++nst[t];
           ref_t[t] = rref;
@@ -709,17 +757,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
           mbar_arrive(BAR(T_PFULL + t));
         }
         // The next block's V, needed by the PV products two MMA iterations from now.
-        if (ok && j + 1 < U.nmax && !widen(j + 1)) ok = false;
+        if (ok && j + 1 < nmax && !widen(j + 1)) ok = false;
       }
       if (!ok) break;
       // Epilogue per tile: O / l to its rows, or O and the statistics to the workspace.
-      const bool whole = U.ubeg >= 0 && U.uend <= U.re;
-      const int second = U.ubeg > 0 ? 1 : 0, part = 2 * blockIdx.x + second;
-      if (U.ubeg >= 0 && !whole && ct == 0)      // re is the run here: the unit goes on in the next CTA
-        *rec = make_int4(U.h, U.q0 + U.rt * qu, U.rows / p.g, 2 * ((U.uend - 1) / U.re) + second);
+      const bool whole = U.whole != 0;
+      const int part = 2 * blockIdx.x + U.second, rows = U.rows, q0 = U.q0;
+      if (U.more > 0 && !whole && ct == 0) *rec = make_int4(h, q0, rows / p.g, 2 * U.more + U.second);
+      __syncwarp();
+      if (lane == 0) unit_done(nu);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        const int n_t = t ? U.nt[1] : U.nt[0];
+        const int n_t = t ? nt[1] : nt[0];
         if (!warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
         if (n_t > 0) {
           const uint32_t par = t ? nof[1] : nof[0];
@@ -730,8 +779,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float* st = fin + t * 256 + row;
         const float m = st[0], l = st[128], ref = (t ? ref_t[1] : ref_t[0]) / kVShift;
         const int r = t * 128 + row, qi = r / p.g;
-        const bool live = r < U.rows;
-        const long long orow = (long long)(U.h * p.g + (r - qi * p.g)) * p.total_q + U.q0 + U.rt * qu + qi;
+        const bool live = r < rows;
+        const long long orow = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
         const long long prow = (long long)part * kTRows + r;
         const float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f;
         const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
