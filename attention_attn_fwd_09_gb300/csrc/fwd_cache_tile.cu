@@ -63,25 +63,23 @@ struct TileCfg {
 enum {
   T_Q = 0,         // +t: Q_t of the unit written (128)
   T_SFULL = 2,     // +t: S_t of a block complete
-  T_PFULL = 4,     // +t: P written (softmax, 128) and O rescaled (correction, 128)
+  T_PFULL = 4,     // +t: P written (softmax, 128); O rescaled and the block's V widened (correction, 128)
   T_STATS = 6,     // +t: row statistics of a block written (128)
   T_OFULL = 8,     // +t: the unit's last PV of tile t complete
   T_OFREE = 10,    // +t: O_t read out of tensor memory (128)
   T_FIN = 12,      // +t: the unit's final statistics written (128)
   T_KFULL = 14,    // +slot (2)
-  T_KFREE = 16,    // +slot (2): products that read the slot complete
-  T_V8FULL = 18,   // +slot (3)
-  T_V8FREE = 21,   // +slot (3): widened (128)
-  T_V16FULL = 24,  // +slot (2): widened (128)
-  T_V16FREE = 26,  // +slot (2): products that read the slot complete
-  T_EPI = 28,      // the unit's results written (128)
-  T_UFULL = 29,    // +slot (4): unit descriptor written
-  T_UFREE = 33,    // +slot (4): every role is through with the unit (14 warps)
-  T_DONE = 37,
-  T_COUNT = 38
+  T_V8FULL = 16,   // +slot (3)
+  T_V8FREE = 19,   // +slot (3): widened (128)
+  T_REL = 22,      // +(group & 7): both issuers' products of a group (S of block j, PV of block j - 1) complete
+  T_EPI = 30,      // the unit's results written (128)
+  T_UFULL = 31,    // +slot (4): unit descriptor written
+  T_UFREE = 35,    // +slot (4): every role is through with the unit (15 warps)
+  T_DONE = 39,     // +t
+  T_COUNT = 41
 };
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
-constexpr int kUnitSlots = 4, kUnitReaders = 14;   // producer, MMA issuer, 8 softmax and 4 correction warps
+constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 correction warps
 
 // sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0, in O(log) steps.
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -209,15 +207,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(BAR(T_OFREE + t), 128);
       mbar_init(BAR(T_FIN + t), 128);
       mbar_init(BAR(T_KFULL + t), 1);
-      mbar_init(BAR(T_KFREE + t), 1);
-      mbar_init(BAR(T_V16FULL + t), 128);
-      mbar_init(BAR(T_V16FREE + t), 1);
+      mbar_init(BAR(T_DONE + t), 1);
     }
     for (int s = 0; s < C::NV8; ++s) {
       mbar_init(BAR(T_V8FULL + s), 1);
       mbar_init(BAR(T_V8FREE + s), 128);
     }
-    mbar_init(BAR(T_DONE), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(BAR(T_REL + i), 2);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -310,6 +306,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int boxes = max(1, 128 >> page_shift), box_keys = min(p.page, 128);
       const uint32_t box_bytes = box_keys * D;
       uint32_t n_k = 0, n_v = 0;             // K, V blocks loaded so far
+      uint32_t group = 0, g1 = 0, g2 = 0;    // product group of the next block; of the last two blocks
       bool ok = true;
       for (uint32_t nu = 0; ok; ++nu) {
         if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
@@ -336,7 +333,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
           const int z = pg * p.Hkv + h;
           const int ks = (int)(n_k % C::NK), vs = (int)(n_v % C::NV8);
-          if (n_k >= C::NK && !warp_wait(BAR(T_KFREE + ks), (n_k / C::NK - 1) & 1, wc)) { ok = false; break; }
+          // The slot's block, two before this one, was read by the products of group g2.
+          if (n_k >= C::NK && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) { ok = false; break; }
+          g2 = g1;
+          g1 = group++;
           if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
           __syncwarp();
           if (pg >= 0) tma_load_3d(sbase + C::OFF_K + ks * C::K8 + lane * box_bytes, &tm_k, 0, 0, z, BAR(T_KFULL + ks));
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (pg >= 0) tma_load_3d(sbase + C::OFF_V8 + vs * C::K8 + lane * box_bytes, &tm_v, 0, 0, z, BAR(T_V8FULL + vs));
           ++n_v;
         }
+        if (nmax > 0) ++group;               // the last PV is a group of its own
       }
       // Every copy has landed before the shared memory goes away, also when a wait ran out.
       if (lane == 0) {
@@ -358,75 +359,67 @@ __global__ void __launch_bounds__(kTThreads, 1)
           while (!mbar_try_wait(BAR(T_V8FULL + (i % C::NV8)), (i / C::NV8) & 1) && globaltimer_ns() - t0 < p.wait_ns) {
           }
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------------- MMA issuer
+    } else if (warp <= 2) {
+      // ---------------------------------------------------------------- MMA issuers, one per tile
+      // (one thread for both tiles lost 1000 cycles per block in its waits and commits).  Group j of a
+      // unit: PV of block j - 1 and S of block j.
       if (lane == 0) {
+        const int t = warp - 1;
         bool ok = true;
-        uint32_t nk = 0, nv = 0;             // blocks whose S, PV were issued
-        uint32_t np[2] = {0, 0}, no[2] = {0, 0};   // P phases used; units of tile t whose last PV was issued
+        uint32_t nk = 0, nv = 0, np = 0, no = 0, group = 0;   // blocks, V blocks, P phases used; units with a PV
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
+        const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
+        const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + 2 * t * C::Q8, 16);
         for (uint32_t nu = 0; ok; ++nu) {
           if (!unit_ready(nu)) { ok = false; break; }
           const UnitDesc& U = desc[nu % kUnitSlots];
-          const int nmax = U.nmax, nt[2] = {U.nt[0], U.nt[1]};
+          const int nmax = U.nmax, n_t = U.nt[t];
           unit_done(nu);
           if (nmax < 0) break;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (nt[t] > 0 && !mbar_wait(BAR(T_Q + t), no[t] & 1, wc)) ok = false;
-          if (!ok || nmax == 0) continue;
-          tc_fence_after();
-          for (int j = 0; j <= nmax && ok; ++j) {
-            const uint32_t ks = nk % C::NK, vs = nv % C::NV16;
-            if (j < nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
-            if (j >= 1 && !mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
-            const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + vs * C::V16, C::CH16);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!ok) break;
-              const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
-              if (j >= 1 && j <= nt[t]) {
+          if (nmax == 0) continue;
+          for (int j = 0; j <= nmax; ++j) {
+            if (j >= 1) {
+              if (j <= n_t) {
                 // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
-                if (j == 1 && no[t] > 0 && !mbar_wait(BAR(T_OFREE + t), (no[t] - 1) & 1, wc)) { ok = false; break; }
-                if (!mbar_wait(BAR(T_PFULL + t), np[t] & 1, wc)) { ok = false; break; }
-                ++np[t];
+                if (j == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
+                if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
+                ++np;
                 tc_fence_after();
+                const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + (nv % C::NV16) * C::V16, C::CH16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
-                if (j == nt[t]) {
+                if (j == n_t) {
                   mma_commit(BAR(T_OFULL + t));
-                  ++no[t];
+                  ++no;
                 }
               }
-              if (j < nt[t]) {
+              ++nv;
+            }
+            if (j < nmax) {
+              const uint32_t ks = nk % C::NK;
+              if (j == 0 && j < n_t && !mbar_wait(BAR(T_Q + t), no & 1, wc)) { ok = false; break; }
+              // Also for a tile through with its blocks: it must not run ahead of the other.
+              if (!mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
+              ++nk;
+              if (j < n_t) {
                 // S_t = (Q1_t + Q2_t) K8_j^T, K = 32 columns a step
-                const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + 2 * t * C::Q8, 16);
+                tc_fence_after();
+                const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                  for (int kk = 0; kk < D / 32; ++kk)
-                    mma_ss_f8_w(tS, q_lo + ((part * C::Q8 + kk * 32) >> 4), C::QK_HI, k_lo + ((kk * 32) >> 4), C::QK_HI,
-                                C::IDESC_QK, (part > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 2 * (D / 32); ++kk)
+                  mma_ss_f8_w(tS, q_lo + (((kk / (D / 32)) * C::Q8 + (kk % (D / 32)) * 32) >> 4), C::QK_HI,
+                              k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, C::IDESC_QK, kk > 0 ? 1u : 0u);
                 mma_commit(BAR(T_SFULL + t));
               }
             }
-            if (!ok) break;
-            if (j < nmax) {
-              mma_commit(BAR(T_KFREE + ks));
-              ++nk;
-            }
-            if (j >= 1) {
-              mma_commit(BAR(T_V16FREE + vs));
-              ++nv;
-            }
+            mma_commit(BAR(T_REL + (group & 7)));
+            ++group;
           }
         }
-        mma_commit(BAR(T_DONE));
+        mma_commit(BAR(T_DONE + t));
         const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_try_wait(BAR(T_DONE), 0) && globaltimer_ns() - t0 < p.wait_ns) {
+        while (!mbar_try_wait(BAR(T_DONE + t), 0) && globaltimer_ns() - t0 < p.wait_ns) {
         }
       }
     } else if (warp == 3) {
@@ -505,16 +498,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       float c_row = 0.f;
       if (n_t > 0) {
         // This tile's Q is free: every S of the unit before has been waited for.
-        uint4 w[D / 8];
         const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) +
-            ((long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi) * D);
+            static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi) * D);
         float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint4 w = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             amax = fmax3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
@@ -526,19 +516,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const uint32_t poison = e == 255 ? 0x7f7f7f7fu : 0u;
         uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + row * D;
         const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < D / 16; ++ch) {                      // 16 columns: one 16-byte piece of Q1 and of Q2
+          const uint4 va = live ? __ldg(src + 2 * ch) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 vb = live ? __ldg(src + 2 * ch + 1) : make_uint4(0u, 0u, 0u, 0u);
           uint32_t c1[4], c2[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {                            // 4 columns
-            const uint4 v = w[2 * ch + (k >> 1)];
+            const uint4 v = k < 2 ? va : vb;
             const uint32_t a = (k & 1) ? v.z : v.x, b = (k & 1) ? v.w : v.y;
             const float x0 = __uint_as_float(a << 16) * inv, x1 = __uint_as_float(a & 0xffff0000u) * inv;
             const float x2 = __uint_as_float(b << 16) * inv, x3 = __uint_as_float(b & 0xffff0000u) * inv;
-            const uint32_t h = to_e4m3x2(x0, x1) | (to_e4m3x2(x2, x3) << 16);
+            const uint32_t hq = to_e4m3x2(x0, x1) | (to_e4m3x2(x2, x3) << 16);
             float y0, y1, y2, y3;
-            e4m3x4_to_f32(h, y0, y1, y2, y3);
-            c1[k] = h | poison;
+            e4m3x4_to_f32(hq, y0, y1, y2, y3);
+            c1[k] = hq | poison;
             c2[k] = to_e4m3x2(x0 - y0, x1 - y1) | (to_e4m3x2(x2 - y2, x3 - y3) << 16);
           }
           const int off = (ch ^ sw) << 4;
@@ -652,16 +644,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const int ct = tid - 384, w4 = ct >> 5;
-    uint32_t nv = 0, nst[2] = {0, 0}, nof[2] = {0, 0};   // V blocks widened; statistics, O phases used
+    uint32_t group = 0, g1 = 0, g2 = 0;      // product group of the next block's S; of the last two blocks' PV
+    uint32_t nv = 0, nst0 = 0, nst1 = 0, nof0 = 0, nof1 = 0;   // V blocks widened; per tile statistics, O phases used
     bool ok = true;
     for (uint32_t nu = 0; ok; ++nu) {
       if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
       const UnitDesc& U = desc[nu % kUnitSlots];
-      const int nmax = U.nmax, nt[2] = {U.nt[0], U.nt[1]}, kt0 = U.kt0, len = U.len, h = U.h;
+      const int nmax = U.nmax, nt0 = U.nt[0], nt1 = U.nt[1], kt0 = U.kt0, len = U.len, h = U.h;
       const int* table = p.table + (long long)U.b * p.max_pages;
       if (nmax < 0) break;                   // the last descriptor is not reused
       float rref = kMinScale, fac = 1.f;     // largest V scale so far; old over new with the newest block
-      float ref_t[2] = {kMinScale, kMinScale};   // what O_t is relative to
+      float ref0 = kMinScale, ref1 = kMinScale;  // what O_0, O_1 are relative to
       auto page_of = [&](int j) -> int {
         const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
         if (j >= nmax || key >= len) return -1;
@@ -671,37 +664,41 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sv_next = scale_of(page_of(0));
       int pg_next = page_of(1);
-      // V8 block jj -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle).
-      // Thread pieces of 16 codes; each quarter-warp takes half of two adjacent 128-byte lines, so
-      // that its loads and each of its two rounds of stores fall on eight distinct bank groups.
-      auto widen = [&](int jj) -> bool {
-        const float sv = sv_next;
-        sv_next = scale_of(pg_next);
-        pg_next = page_of(jj + 2);
-        float vmax = sv;
-        if constexpr (NG > 1) {
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-        }
-        fac = 1.f;
-        if (vmax > rref) {
-          fac = rref / vmax;
-          rref = vmax;
-        }
-        const float wgt = sv / rref * kVShift;
-        const uint32_t w_mine = pack_f16x2(wgt, wgt);
+      // V8 block jj -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle), half a
+      // block at a time, so that neither tile's statistics wait for long.  Thread pieces of 16 codes;
+      // each quarter-warp takes half of two adjacent 128-byte lines, so that its loads and each of its
+      // two rounds of stores fall on eight distinct bank groups.
+      uint32_t w_mine = 0;                   // this lane's group's factor, two f16
+      float rnext = kMinScale;
+      auto widen = [&](int jj, int part) -> bool {
         const uint32_t vs8 = nv % C::NV8, vs16 = nv % C::NV16;
-        if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) return false;
-        if (nv >= C::NV16 && !warp_wait(BAR(T_V16FREE + vs16), (nv / C::NV16 - 1) & 1, wc)) return false;
+        if (part == 0) {
+          const float sv = sv_next;
+          sv_next = scale_of(pg_next);
+          pg_next = page_of(jj + 2);
+          float vmax = sv;
+          if constexpr (NG > 1) {
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+          }
+          rnext = fmaxf(rref, vmax);
+          const float wgt = sv / rnext * kVShift;
+          w_mine = pack_f16x2(wgt, wgt);
+          if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) return false;
+          // The slot's block, two before this one, was read by the products of group g2.
+          if (nv >= C::NV16 && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) return false;
+          g2 = g1;
+          g1 = ++group;                      // PV of block jj is in the group behind its S
+        }
         const uint8_t* src = smem + C::OFF_V8 + vs8 * C::K8;
         uint8_t* dst = smem + C::OFF_V16 + vs16 * C::V16;
-        const int left = len - (kt0 + jj) * 128;               // keys that exist
+        const int left = len - (kt0 + jj) * 128;                   // keys that exist
         const int quarter = lane >> 3, half = (lane & 7) >> 2;
         const int u = (lane & 3) + 4 * (half ^ (quarter & 1));     // 16-byte piece of a line
         const int r0 = 4 * w4 + 2 * (quarter >> 1) + half, sw = r0 & 7;   // line 16 it + r0
         const uint8_t* s_base = src + r0 * 128 + ((u ^ sw) << 4);
-#pragma unroll
-        for (int it = 0; it < D / 16; ++it) {
+#pragma unroll 2
+        for (int it = part * (D / 32); it < (part + 1) * (D / 32); ++it) {
           uint4 v = *reinterpret_cast<const uint4*>(s_base + it * 2048);
           // d = 128: a line is a key; d = 64: two keys.
           const int key = D == 128 ? it * 16 + r0 : 2 * (it * 16 + r0) + (u >> 2);
@@ -709,57 +706,65 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if constexpr (NG > 1) wv = __shfl_sync(0xffffffffu, w_mine, D == 128 ? it : 2 * it + (w4 >> 1));
           if (key >= left) v = make_uint4(0u, 0u, 0u, 0u);         // whatever the codes are (NaN too)
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h[8];
+          uint32_t hh[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            h[2 * i] = hmul2(e4m3x2_f16x2(in[i]), wv);
-            h[2 * i + 1] = hmul2(e4m3x2_f16x2_hi(in[i]), wv);
+            hh[2 * i] = hmul2(e4m3x2_f16x2(in[i]), wv);
+            hh[2 * i + 1] = hmul2(e4m3x2_f16x2_hi(in[i]), wv);
           }
           const int q = u & 3;                                     // pieces 2q, 2q + 1 of the f16 row
           uint8_t* d_row = dst + (D == 128 ? (u >> 2) * C::CH16 : 0u) + key * 128;
           const int ks = key & 7;
-          *reinterpret_cast<uint4*>(d_row + (((2 * q) ^ ks) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(d_row + (((2 * q + 1) ^ ks) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(d_row + (((2 * q) ^ ks) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+          *reinterpret_cast<uint4*>(d_row + (((2 * q + 1) ^ ks) << 4)) = make_uint4(hh[4], hh[5], hh[6], hh[7]);
         }
-        fence_proxy_async_smem();            // generic writes -> tensor-core reads
-        mbar_arrive(BAR(T_V16FULL + vs16));
-        mbar_arrive(BAR(T_V8FREE + vs8));
-        ++nv;
+        fence_proxy_async_smem();            // generic writes -> tensor-core reads (ordered by T_PFULL)
+        if (part == 1) {
+          mbar_arrive(BAR(T_V8FREE + vs8));
+          ++nv;
+        }
         return true;
       };
-      if (nmax > 0 && !widen(0)) { ok = false; break; }
+      if (nmax > 0) {
+        if (!widen(0, 0) || !widen(0, 1)) { ok = false; break; }
+        rref = rnext;
+      }
       for (int j = 0; j < nmax && ok; ++j) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= nt[t]) continue;
-          if (!warp_wait(BAR(T_STATS + t), nst[t] & 1, wc)) { ok = false; break; }
-          ++nst[t];
-          ref_t[t] = rref;
-          const float alpha = alpha_buf[t * 128 + row] * fac;
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // S_t(j) complete => PV_t(j-1), issued before it, is complete too.
-            if (!warp_wait(BAR(T_SFULL + t), (nst[t] - 1) & 1, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
-            uint32_t x[32];
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              tmem_ld32(tO + q * 32, x);
-              tmem_wait_ld();
-              reg_fence(x);
+        for (int t = 0; t < 2; ++t) {
+          if (j < (t ? nt1 : nt0)) {
+            const uint32_t done = t ? nst1 : nst0;                 // statistics phases used
+            if (!warp_wait(BAR(T_STATS + t), done & 1, wc)) { ok = false; break; }
+            if (t) { ++nst1; ref1 = rref; } else { ++nst0; ref0 = rref; }
+            const float alpha = alpha_buf[t * 128 + row] * fac;
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // S_t(j) complete => PV_t(j-1), issued before it, is complete too.
+              if (!warp_wait(BAR(T_SFULL + t), done & 1, wc)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
+              uint32_t x[32];
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                tmem_ld32(tO + q * 32, x);
+                tmem_wait_ld();
+                reg_fence(x);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-              tmem_st32(tO + q * 32, x);
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+                tmem_st32(tO + q * 32, x);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(BAR(T_PFULL + t));
           }
-          tc_fence_before();
-          mbar_arrive(BAR(T_PFULL + t));
+          // Half of the next block's V, which the next P waits for.
+          if (j + 1 < nmax && !widen(j + 1, t)) { ok = false; break; }
         }
-        // The next block's V, needed by the PV products two MMA iterations from now.
-        if (ok && j + 1 < nmax && !widen(j + 1)) ok = false;
+        fac = rref / rnext;
+        rref = rnext;
       }
       if (!ok) break;
+      if (nmax > 0) ++group;                 // the group of the unit's last PV
       // Epilogue per tile: O / l to its rows, or O and the statistics to the workspace.
       const bool whole = U.whole != 0;
       const int part = 2 * blockIdx.x + U.second, rows = U.rows, q0 = U.q0;
@@ -768,16 +773,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (lane == 0) unit_done(nu);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        const int n_t = t ? nt[1] : nt[0];
+        const int n_t = t ? nt1 : nt0;
         if (!warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
         if (n_t > 0) {
-          const uint32_t par = t ? nof[1] : nof[0];
-          if (!warp_wait(BAR(T_OFULL + t), par & 1, wc)) { ok = false; break; }
-          if (t) ++nof[1]; else ++nof[0];
+          if (!warp_wait(BAR(T_OFULL + t), (t ? nof1 : nof0) & 1, wc)) { ok = false; break; }
+          if (t) ++nof1; else ++nof0;
         }
         tc_fence_after();
         const float* st = fin + t * 256 + row;
-        const float m = st[0], l = st[128], ref = (t ? ref_t[1] : ref_t[0]) / kVShift;
+        const float m = st[0], l = st[128], ref = (t ? ref1 : ref0) / kVShift;
         const int r = t * 128 + row, qi = r / p.g;
         const bool live = r < rows;
         const long long orow = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
