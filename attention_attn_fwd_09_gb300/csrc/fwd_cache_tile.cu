@@ -51,7 +51,7 @@ struct TileCfg {
   static constexpr uint32_t OFF_V8 = OFF_K + NK * K8;
   static constexpr uint32_t OFF_V16 = OFF_V8 + NV8 * K8;
   static constexpr uint32_t OFF_CTRL = OFF_V16 + NV16 * V16;
-  static constexpr uint32_t CTRL_BYTES = 512 + (2 * 128 + 4 * 128) * 4 + 64 + 256;
+  static constexpr uint32_t CTRL_BYTES = 512 + 6 * 128 * 4 + 64 + 256;
   static constexpr uint32_t SMEM = 1024 + OFF_CTRL + CTRL_BYTES;
   // K-major rows of D bytes: 128-byte swizzle for d = 128, 64-byte for d = 64.
   static constexpr uint32_t IDESC_QK = idesc_f32acc(128, 128, FMT_E4M3, FMT_E4M3, false, false);
@@ -63,23 +63,24 @@ struct TileCfg {
 enum {
   T_Q = 0,         // +t: Q_t of the unit written (128)
   T_SFULL = 2,     // +t: S_t of a block complete
-  T_PFULL = 4,     // +t: P written (softmax, 128); O rescaled and the block's V widened (correction, 128)
-  T_STATS = 6,     // +t: row statistics of a block written (128)
-  T_OFULL = 8,     // +t: the unit's last PV of tile t complete
-  T_OFREE = 10,    // +t: O_t read out of tensor memory (128)
-  T_FIN = 12,      // +t: the unit's final statistics written (128)
-  T_KFULL = 14,    // +slot (2)
-  T_V8FULL = 16,   // +slot (3)
-  T_V8FREE = 19,   // +slot (3): widened (128)
+  T_PFULL = 4,     // +t: P written and O rescaled (128)
+  T_OFULL = 6,     // +t: the unit's last PV of tile t complete
+  T_OFREE = 8,     // +t: O_t read out of tensor memory (128)
+  T_FIN = 10,      // +t: the unit's final statistics written (128)
+  T_KFULL = 12,    // +slot (2)
+  T_V8FULL = 14,   // +slot (3)
+  T_V8FREE = 17,   // +slot (3): widened (128)
+  T_V16FULL = 20,  // +slot (2): widened (128)
   T_REL = 22,      // +(group & 7): both issuers' products of a group (S of block j, PV of block j - 1) complete
   T_EPI = 30,      // the unit's results written (128)
   T_UFULL = 31,    // +slot (4): unit descriptor written
   T_UFREE = 35,    // +slot (4): every role is through with the unit (15 warps)
   T_DONE = 39,     // +t
-  T_COUNT = 41
+  T_TURN = 41,     // +t: the other tile's products of a group have been issued
+  T_COUNT = 43
 };
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
-constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 correction warps
+constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 widening warps
 
 // sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0, in O(log) steps.
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -157,6 +158,15 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return r;
 }
 
+// 32 lanes x 16 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -177,9 +187,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const uint32_t bar0 = smem_u32(ctrl);
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * i; };
   UnitDesc* desc = reinterpret_cast<UnitDesc*>(ctrl + 512);  // [4]
-  float* alpha_buf = reinterpret_cast<float*>(ctrl + 768);   // [2][128]
-  float* fin = alpha_buf + 256;                              // [2][m, l][128]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 512);
+  float* fin = reinterpret_cast<float*>(ctrl + 768);         // [2][m, l, reference scale][128]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 768);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   long long* misc = reinterpret_cast<long long*>(tmem_slot + 2);   // [4]: b, h, rt, unit start
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_Q); // [16] warp sums, before Q is written
@@ -201,13 +210,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(T_Q + t), 128);
       mbar_init(BAR(T_SFULL + t), 1);
-      mbar_init(BAR(T_PFULL + t), 256);
-      mbar_init(BAR(T_STATS + t), 128);
+      mbar_init(BAR(T_PFULL + t), 128);
+      mbar_init(BAR(T_V16FULL + t), 128);
       mbar_init(BAR(T_OFULL + t), 1);
       mbar_init(BAR(T_OFREE + t), 128);
       mbar_init(BAR(T_FIN + t), 128);
       mbar_init(BAR(T_KFULL + t), 1);
       mbar_init(BAR(T_DONE + t), 1);
+      mbar_init(BAR(T_TURN + t), 1);
     }
     for (int s = 0; s < C::NV8; ++s) {
       mbar_init(BAR(T_V8FULL + s), 1);
@@ -377,44 +387,46 @@ __global__ void __launch_bounds__(kTThreads, 1)
           unit_done(nu);
           if (nmax < 0) break;
           if (nmax == 0) continue;
-          for (int j = 0; j <= nmax; ++j) {
-            if (j >= 1) {
-              if (j <= n_t) {
-                // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
-                if (j == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
-                if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
-                ++np;
-                tc_fence_after();
-                const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + (nv % C::NV16) * C::V16, C::CH16);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
-                if (j == n_t) {
-                  mma_commit(BAR(T_OFULL + t));
-                  ++no;
-                }
-              }
-              ++nv;
+          for (int j = 0; j <= nmax; ++j, ++group) {
+            const bool pv = j >= 1 && j <= n_t, sp = j < n_t;
+            const uint32_t vs = nv % C::NV16, ks = nk % C::NK;
+            // P is the last to come.  (K also for a tile through with its blocks: it must not run ahead of the other.)
+            if (j < nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
+            if (j == 0 && sp && !mbar_wait(BAR(T_Q + t), no & 1, wc)) { ok = false; break; }
+            if (pv) {
+              if (j == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
+              if (!mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
+              if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
+              ++np;
             }
-            if (j < nmax) {
-              const uint32_t ks = nk % C::NK;
-              if (j == 0 && j < n_t && !mbar_wait(BAR(T_Q + t), no & 1, wc)) { ok = false; break; }
-              // Also for a tile through with its blocks: it must not run ahead of the other.
-              if (!mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
-              ++nk;
-              if (j < n_t) {
-                // S_t = (Q1_t + Q2_t) K8_j^T, K = 32 columns a step
-                tc_fence_after();
-                const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
+            // Tile 0's products of a group go before tile 1's: left alone, the tiles fall into step and
+            // tensor cores and exponentials take turns instead of overlapping.
+            if (!mbar_wait(BAR(T_TURN + t), (group + 1 - t) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            if (pv) {
+              // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
+              const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + vs * C::V16, C::CH16);
 #pragma unroll
-                for (int kk = 0; kk < 2 * (D / 32); ++kk)
-                  mma_ss_f8_w(tS, q_lo + (((kk / (D / 32)) * C::Q8 + (kk % (D / 32)) * 32) >> 4), C::QK_HI,
-                              k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, C::IDESC_QK, kk > 0 ? 1u : 0u);
-                mma_commit(BAR(T_SFULL + t));
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
+              if (j == n_t) {
+                mma_commit(BAR(T_OFULL + t));
+                ++no;
               }
             }
+            if (sp) {
+              // S_t = (Q1_t + Q2_t) K8_j^T, K = 32 columns a step
+              const uint32_t k_lo = sdesc_sw128_lo(sbase + C::OFF_K + ks * C::K8, 16);
+#pragma unroll
+              for (int kk = 0; kk < 2 * (D / 32); ++kk)
+                mma_ss_f8_w(tS, q_lo + (((kk / (D / 32)) * C::Q8 + (kk % (D / 32)) * 32) >> 4), C::QK_HI,
+                            k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, C::IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            mbar_arrive(BAR(T_TURN + 1 - t));
+            if (sp) mma_commit(BAR(T_SFULL + t));
             mma_commit(BAR(T_REL + (group & 7)));
-            ++group;
+            if (j >= 1) ++nv;
+            if (j < nmax) ++nk;
           }
         }
         mma_commit(BAR(T_DONE + t));
@@ -551,11 +563,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.k_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sk_next = scale_of(page_of(0));
       int pg_next = page_of(1);
-      float m = -INFINITY, l = 0.f;
+      // The V scales too: when the largest so far grows, O is rescaled like for a maximum.
+      auto v_scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + h) : 0.f; };
+      float sv_next = v_scale_of(page_of(0));
+      float m = -INFINITY, l = 0.f, rref = kMinScale;
       for (int j = 0; j < n_t; ++j) {
         const float sk = sk_next;
+        float vmax = sv_next;
         sk_next = scale_of(pg_next);
+        sv_next = v_scale_of(pg_next);
         pg_next = page_of(j + 2);
+        if constexpr (NG > 1) {
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+        }
         float fac[NG];
 #pragma unroll
         for (int i = 0; i < NG; ++i)
@@ -608,8 +629,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
           alpha = ex2_mufu(m - m_cand);
           m = m_cand;
         }
-        alpha_buf[t * 128 + row] = alpha;
-        mbar_arrive(BAR(T_STATS + t));
+        // Rare after the first blocks.  S_t(j) complete: PV_t(j - 1), issued before it, is too.
+        const float scale_o = vmax > rref ? alpha * (rref / vmax) : alpha;
+        rref = fmaxf(rref, vmax);
+        if (j > 0 && __any_sync(0xffffffffu, scale_o != 1.f)) {
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t x[16];
+            tmem_ld16(tS + 256u + q * 16, x);   // O_t lies 256 columns behind S_t
+            tmem_wait_ld();
+            reg_fence(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * scale_o);
+            tmem_st16(tS + 256u + q * 16, x);
+          }
+        }
         const float off = kPShift - (m == -INFINITY ? 0.f : m);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[64];
@@ -633,19 +667,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // from running ahead of the other roles.)
       if (ok && nu > 0 && !warp_wait(BAR(T_EPI), (nu - 1) & 1, wc)) ok = false;
       if (!ok) break;
-      float* out = fin + t * 256 + row;
+      float* out = fin + t * 384 + row;
       out[0] = m;
       out[128] = l;
+      out[256] = rref;
       mbar_arrive(BAR(T_FIN + t));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // ------------------------------------------------------------------ correction, V, epilogue
+    // ------------------------------------------------------------------ V, epilogue
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const int ct = tid - 384, w4 = ct >> 5;
     uint32_t group = 0, g1 = 0, g2 = 0;      // product group of the next block's S; of the last two blocks' PV
-    uint32_t nv = 0, nst0 = 0, nst1 = 0, nof0 = 0, nof1 = 0;   // V blocks widened; per tile statistics, O phases used
+    uint32_t nv = 0, nof0 = 0, nof1 = 0;     // V blocks widened; per tile O phases used
     bool ok = true;
     for (uint32_t nu = 0; ok; ++nu) {
       if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
@@ -653,8 +688,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int nmax = U.nmax, nt0 = U.nt[0], nt1 = U.nt[1], kt0 = U.kt0, len = U.len, h = U.h;
       const int* table = p.table + (long long)U.b * p.max_pages;
       if (nmax < 0) break;                   // the last descriptor is not reused
-      float rref = kMinScale, fac = 1.f;     // largest V scale so far; old over new with the newest block
-      float ref0 = kMinScale, ref1 = kMinScale;  // what O_0, O_1 are relative to
+      float rref = kMinScale;                // largest V scale so far
       auto page_of = [&](int j) -> int {
         const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
         if (j >= nmax || key >= len) return -1;
@@ -664,41 +698,36 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sv_next = scale_of(page_of(0));
       int pg_next = page_of(1);
-      // V8 block jj -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle), half a
-      // block at a time, so that neither tile's statistics wait for long.  Thread pieces of 16 codes;
-      // each quarter-warp takes half of two adjacent 128-byte lines, so that its loads and each of its
-      // two rounds of stores fall on eight distinct bank groups.
-      uint32_t w_mine = 0;                   // this lane's group's factor, two f16
-      float rnext = kMinScale;
-      auto widen = [&](int jj, int part) -> bool {
-        const uint32_t vs8 = nv % C::NV8, vs16 = nv % C::NV16;
-        if (part == 0) {
-          const float sv = sv_next;
-          sv_next = scale_of(pg_next);
-          pg_next = page_of(jj + 2);
-          float vmax = sv;
-          if constexpr (NG > 1) {
+      // V8 block -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle).  Thread
+      // pieces of 16 codes; each quarter-warp takes half of two adjacent 128-byte lines, so that its
+      // loads and each of its two rounds of stores fall on eight distinct bank groups.
+      for (int j = 0; j < nmax; ++j) {
+        const float sv = sv_next;
+        sv_next = scale_of(pg_next);
+        pg_next = page_of(j + 2);
+        float vmax = sv;
+        if constexpr (NG > 1) {
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-          }
-          rnext = fmaxf(rref, vmax);
-          const float wgt = sv / rnext * kVShift;
-          w_mine = pack_f16x2(wgt, wgt);
-          if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) return false;
-          // The slot's block, two before this one, was read by the products of group g2.
-          if (nv >= C::NV16 && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) return false;
-          g2 = g1;
-          g1 = ++group;                      // PV of block jj is in the group behind its S
+          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
         }
+        rref = fmaxf(rref, vmax);
+        const float wgt = sv / rref * kVShift;
+        const uint32_t w_mine = pack_f16x2(wgt, wgt);  // this lane's group's factor
+        const uint32_t vs8 = nv % C::NV8, vs16 = nv % C::NV16;
+        if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) { ok = false; break; }
+        // The slot's block, two before this one, was read by the products of group g2.
+        if (nv >= C::NV16 && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) { ok = false; break; }
+        g2 = g1;
+        g1 = ++group;                        // PV of block j is in the group behind its S
         const uint8_t* src = smem + C::OFF_V8 + vs8 * C::K8;
         uint8_t* dst = smem + C::OFF_V16 + vs16 * C::V16;
-        const int left = len - (kt0 + jj) * 128;                   // keys that exist
+        const int left = len - (kt0 + j) * 128;                    // keys that exist
         const int quarter = lane >> 3, half = (lane & 7) >> 2;
         const int u = (lane & 3) + 4 * (half ^ (quarter & 1));     // 16-byte piece of a line
         const int r0 = 4 * w4 + 2 * (quarter >> 1) + half, sw = r0 & 7;   // line 16 it + r0
         const uint8_t* s_base = src + r0 * 128 + ((u ^ sw) << 4);
-#pragma unroll 2
-        for (int it = part * (D / 32); it < (part + 1) * (D / 32); ++it) {
+#pragma unroll 4
+        for (int it = 0; it < D / 16; ++it) {
           uint4 v = *reinterpret_cast<const uint4*>(s_base + it * 2048);
           // d = 128: a line is a key; d = 64: two keys.
           const int key = D == 128 ? it * 16 + r0 : 2 * (it * 16 + r0) + (u >> 2);
@@ -718,50 +747,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
           *reinterpret_cast<uint4*>(d_row + (((2 * q) ^ ks) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
           *reinterpret_cast<uint4*>(d_row + (((2 * q + 1) ^ ks) << 4)) = make_uint4(hh[4], hh[5], hh[6], hh[7]);
         }
-        fence_proxy_async_smem();            // generic writes -> tensor-core reads (ordered by T_PFULL)
-        if (part == 1) {
-          mbar_arrive(BAR(T_V8FREE + vs8));
-          ++nv;
-        }
-        return true;
-      };
-      if (nmax > 0) {
-        if (!widen(0, 0) || !widen(0, 1)) { ok = false; break; }
-        rref = rnext;
-      }
-      for (int j = 0; j < nmax && ok; ++j) {
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          if (j < (t ? nt1 : nt0)) {
-            const uint32_t done = t ? nst1 : nst0;                 // statistics phases used
-            if (!warp_wait(BAR(T_STATS + t), done & 1, wc)) { ok = false; break; }
-            if (t) { ++nst1; ref1 = rref; } else { ++nst0; ref0 = rref; }
-            const float alpha = alpha_buf[t * 128 + row] * fac;
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-              // S_t(j) complete => PV_t(j-1), issued before it, is complete too.
-              if (!warp_wait(BAR(T_SFULL + t), done & 1, wc)) { ok = false; break; }
-              tc_fence_after();
-              const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
-              uint32_t x[32];
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                tmem_ld32(tO + q * 32, x);
-                tmem_wait_ld();
-                reg_fence(x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-                tmem_st32(tO + q * 32, x);
-              }
-              tmem_wait_st();
-            }
-            tc_fence_before();
-            mbar_arrive(BAR(T_PFULL + t));
-          }
-          // Half of the next block's V, which the next P waits for.
-          if (j + 1 < nmax && !widen(j + 1, t)) { ok = false; break; }
-        }
-        fac = rref / rnext;
-        rref = rnext;
+        fence_proxy_async_smem();            // generic writes -> tensor-core reads
+        mbar_arrive(BAR(T_V16FULL + vs16));
+        mbar_arrive(BAR(T_V8FREE + vs8));
+        ++nv;
       }
       if (!ok) break;
       if (nmax > 0) ++group;                 // the group of the unit's last PV
@@ -780,8 +769,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (t) ++nof1; else ++nof0;
         }
         tc_fence_after();
-        const float* st = fin + t * 256 + row;
-        const float m = st[0], l = st[128], ref = (t ? ref1 : ref0) / kVShift;
+        const float* st = fin + t * 384 + row;
+        const float m = st[0], l = st[128], ref = st[256] / kVShift;
         const int r = t * 128 + row, qi = r / p.g;
         const bool live = r < rows;
         const long long orow = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
