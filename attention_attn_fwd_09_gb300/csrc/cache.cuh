@@ -42,7 +42,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // O / r.  A CTA has at most two: partial 0 for its first unit, partial 1 for its last.
 // Workspace: per CTA an int4 {K/V head, first packed query, queries, 2 x further CTAs + which
 // partial} for the unit that starts in it and is cut (last field < 2: none); then per partial and
-// row (m, l, r, -); then the O rows.
+// row (m, l, r, -); then per partial the O rows as [d / 4][rows] pieces of 4 columns.
 struct CacheWs {
   size_t stat, part, total;
 };

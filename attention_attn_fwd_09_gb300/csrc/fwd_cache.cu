@@ -546,12 +546,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           if (c == 0) p.lse[row] = (m[i] - kShift + __log2f(l[i])) * kLn2;
         } else {
-          float4* out = reinterpret_cast<float4*>(ws + W.part) + ((long long)part * rows_max + r) * (D / 4) + c * (D / 16);
+          float4* out = reinterpret_cast<float4*>(ws + W.part) + ((long long)part * (D / 4) + c * (D / 16)) * rows_max + r;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int k = 0; k < C::NACC / 4; ++k)
-              out[e * (C::NACC / 4) + k] = make_float4(o[4 * k][2 * i + e], o[4 * k + 1][2 * i + e], o[4 * k + 2][2 * i + e],
+              out[(e * (C::NACC / 4) + k) * rows_max] = make_float4(o[4 * k][2 * i + e], o[4 * k + 1][2 * i + e], o[4 * k + 2][2 * i + e],
                                                        o[4 * k + 3][2 * i + e]);
           if (c == 0)
             reinterpret_cast<float4*>(ws + W.stat)[(long long)part * rows_max + r] = make_float4(m[i] - kShift, l[i], rref, 0.f);
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
   if (rec.w < 2) return;
   const int h = rec.x, rows = rec.z * p.g, first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
   for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (D / 4); i += gridDim.y * 128) {
-    const int r = i / (D / 4), col = i % (D / 4);
+    const int col = i / rows, r = i - col * rows;      // neighbouring threads read neighbouring rows
     float m = -INFINITY, ref = kMinScale, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 <= more; k0 += 4) {
@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
       for (int j = 0; j < 4; ++j) {
         const int k = k0 + j;
         // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
-        const long long at = (long long)(k == 0 ? first : 2 * ((int)blockIdx.x + k)) * rows_max + r;
-        st[j] = k <= more ? stat[at] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        x[j] = k <= more ? part[at * (D / 4) + col] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long which = k == 0 ? first : 2 * ((int)blockIdx.x + k);
+        st[j] = k <= more ? stat[which * rows_max + r] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        x[j] = k <= more ? part[(which * (D / 4) + col) * rows_max + r] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float mn = m, rn = ref;
 #pragma unroll

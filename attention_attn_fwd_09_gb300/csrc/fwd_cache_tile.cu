@@ -63,7 +63,7 @@ struct TileCfg {
 enum {
   T_Q = 0,         // +t: Q_t of the unit written (128)
   T_SFULL = 2,     // +t: S_t of a block complete
-  T_PFULL = 4,     // +t: P written and O rescaled (128)
+  T_PFULL = 4,     // +t: P written (128)
   T_OFULL = 6,     // +t: the unit's last PV of tile t complete
   T_OFREE = 8,     // +t: O_t read out of tensor memory (128)
   T_FIN = 10,      // +t: the unit's final statistics written (128)
@@ -77,7 +77,8 @@ enum {
   T_UFREE = 35,    // +slot (4): every role is through with the unit (15 warps)
   T_DONE = 39,     // +t
   T_TURN = 41,     // +t: the other tile's products of a group have been issued
-  T_COUNT = 43
+  T_PHALF = 43,    // +t: P of the block's first 64 keys written and O rescaled (128)
+  T_COUNT = 45
 };
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
 constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 widening warps
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(BAR(T_Q + t), 128);
       mbar_init(BAR(T_SFULL + t), 1);
       mbar_init(BAR(T_PFULL + t), 128);
+      mbar_init(BAR(T_PHALF + t), 128);
       mbar_init(BAR(T_V16FULL + t), 128);
       mbar_init(BAR(T_OFULL + t), 1);
       mbar_init(BAR(T_OFREE + t), 128);
@@ -396,8 +398,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (pv) {
               if (j == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
               if (!mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
-              if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
-              ++np;
+              if (!mbar_wait(BAR(T_PHALF + t), np & 1, wc)) { ok = false; break; }
             }
             // Tile 0's products of a group go before tile 1's: left alone, the tiles fall into step and
             // tensor cores and exponentials take turns instead of overlapping.
@@ -406,9 +407,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (pv) {
               // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
               const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + vs * C::V16, C::CH16);
+              // The first half of the keys while the softmax works on the second.
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
+              for (int kk = 0; kk < 4; ++kk)
                 mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
+              if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
+              ++np;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk) mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, 1u);
               if (j == n_t) {
                 mma_commit(BAR(T_OFULL + t));
                 ++no;
@@ -509,46 +516,54 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (!more) break;
       float c_row = 0.f;
       if (n_t > 0) {
-        // This tile's Q is free: every S of the unit before has been waited for.
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi) * D);
-        float amax = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmax3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
-        }
-        const uint32_t e = __float_as_uint(amax) >> 23;            // biased exponent
-        const bool usable = e >= 8 && e < 255;                     // else 0 or tiny: left as it is; infinite: NaN
-        const float inv = usable ? __uint_as_float((254u + 7u - e) << 23) : 1.f;
-        c_row = p.c * (usable ? __uint_as_float((e - 7u) << 23) : 1.f);
-        const uint32_t poison = e == 255 ? 0x7f7f7f7fu : 0u;
-        uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + row * D;
-        const int sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+        // This tile's Q is free: every S of the unit before has been waited for.  Each warp brings its
+        // 32 rows, whole rows at a time (D / 8 lanes of 16 bytes each), QB steps' loads under way at once.
+        constexpr int LPR = D / 8, RPS = 32 / LPR, QB = 8;          // lanes per row, rows per step
+        const long long at = live ? ((long long)(r - qi * p.g) * p.total_q + qi) * D : -1;   // this lane's own row
+        const uint16_t* base = static_cast<const uint16_t*>(p.q) + ((long long)h * p.g * p.total_q + q0) * D + lane % LPR * 8;
+        uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + (warp & 3) * 32 * D;
+        uint32_t e_own = 0;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 16; ++ch) {                      // 16 columns: one 16-byte piece of Q1 and of Q2
-          const uint4 va = live ? __ldg(src + 2 * ch) : make_uint4(0u, 0u, 0u, 0u);
-          const uint4 vb = live ? __ldg(src + 2 * ch + 1) : make_uint4(0u, 0u, 0u, 0u);
-          uint32_t c1[4], c2[4];
+        for (int i0 = 0; i0 < 32 / RPS; i0 += QB) {
+          uint4 w[QB];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {                            // 4 columns
-            const uint4 v = k < 2 ? va : vb;
-            const uint32_t a = (k & 1) ? v.z : v.x, b = (k & 1) ? v.w : v.y;
-            const float x0 = __uint_as_float(a << 16) * inv, x1 = __uint_as_float(a & 0xffff0000u) * inv;
-            const float x2 = __uint_as_float(b << 16) * inv, x3 = __uint_as_float(b & 0xffff0000u) * inv;
-            const uint32_t hq = to_e4m3x2(x0, x1) | (to_e4m3x2(x2, x3) << 16);
-            float y0, y1, y2, y3;
-            e4m3x4_to_f32(hq, y0, y1, y2, y3);
-            c1[k] = hq | poison;
-            c2[k] = to_e4m3x2(x0 - y0, x1 - y1) | (to_e4m3x2(x2 - y2, x3 - y3) << 16);
+          for (int k = 0; k < QB; ++k) {
+            const long long a = __shfl_sync(0xffffffffu, at, (i0 + k) * RPS + lane / LPR);
+            w[k] = a >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + a)) : make_uint4(0u, 0u, 0u, 0u);
           }
-          const int off = (ch ^ sw) << 4;
-          *reinterpret_cast<uint4*>(q1 + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-          *reinterpret_cast<uint4*>(q1 + C::Q8 + off) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+#pragma unroll
+          for (int k = 0; k < QB; ++k) {
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            float amax = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              amax = fmax3(amax, fabsf(__uint_as_float(u[x] << 16)), fabsf(__uint_as_float(u[x] & 0xffff0000u)));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const uint32_t e = __float_as_uint(amax) >> 23;        // biased exponent
+            const uint32_t e_row = __shfl_sync(0xffffffffu, e, lane % RPS * LPR);
+            if (lane / RPS == i0 + k) e_own = e_row;
+            const bool usable = e >= 8 && e < 255;                 // else 0 or tiny: left as it is; infinite: NaN
+            const float inv = usable ? __uint_as_float((254u + 7u - e) << 23) : 1.f;
+            const uint32_t poison = e == 255 ? 0x7f7f7f7fu : 0u;
+            uint32_t c1[2], c2[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float x0 = __uint_as_float(u[2 * x] << 16) * inv, x1 = __uint_as_float(u[2 * x] & 0xffff0000u) * inv;
+              const float x2 = __uint_as_float(u[2 * x + 1] << 16) * inv, x3 = __uint_as_float(u[2 * x + 1] & 0xffff0000u) * inv;
+              const uint32_t hq = to_e4m3x2(x0, x1) | (to_e4m3x2(x2, x3) << 16);
+              float y0, y1, y2, y3;
+              e4m3x4_to_f32(hq, y0, y1, y2, y3);
+              c1[x] = hq | poison;
+              c2[x] = to_e4m3x2(x0 - y0, x1 - y1) | (to_e4m3x2(x2 - y2, x3 - y3) << 16);
+            }
+            const int rw = (i0 + k) * RPS + lane / LPR, ch = lane % LPR;   // row of the warp's 32, 8-byte piece
+            const int off = rw * D + (((ch >> 1) ^ (D == 128 ? (rw & 7) : ((rw >> 1) & 3))) << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(q1 + off) = make_uint2(c1[0], c1[1]);
+            *reinterpret_cast<uint2*>(q1 + C::Q8 + off) = make_uint2(c2[0], c2[1]);
+          }
         }
+        c_row = p.c * (e_own >= 8 && e_own < 255 ? __uint_as_float((e_own - 7u) << 23) : 1.f);
         fence_proxy_async_smem();            // generic writes -> tensor-core reads
         mbar_arrive(BAR(T_Q + t));
       }
@@ -646,22 +661,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         const float off = kPShift - (m == -INFINITY ? 0.f : m);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[64];
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          float x0, x1;
-          ffma2_bc(x0, x1, s[i], s[i + 1], fac[NG > 1 ? i / 16 : 0], off);
-          const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
-          pk[i >> 1] = pack_f16x2(e0, e1);
-          const int a2 = ((i >> 1) & 1) * 2;
-          fadd2(acc[a2], acc[a2 + 1], acc[a2], acc[a2 + 1], e0, e1);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 64 * hf; i < 64 * hf + 64; i += 2) {
+            float x0, x1;
+            ffma2_bc(x0, x1, s[i], s[i + 1], fac[NG > 1 ? i / 16 : 0], off);
+            const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
+            pk[(i >> 1) & 31] = pack_f16x2(e0, e1);
+            const int a2 = ((i >> 1) & 1) * 2;
+            fadd2(acc[a2], acc[a2 + 1], acc[a2], acc[a2 + 1], e0, e1);
+          }
+          tmem_st32(tS + hf * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(BAR((hf ? T_PFULL : T_PHALF) + t));
         }
         l = l * alpha + ((acc[0] + acc[1]) + (acc[2] + acc[3]));
-        tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(BAR(T_PFULL + t));
       }
       // The statistics of the unit before have been read.  (This also keeps a tile without rows
       // from running ahead of the other roles.)
@@ -760,14 +777,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (U.more > 0 && !whole && ct == 0) *rec = make_int4(h, q0, rows / p.g, 2 * U.more + U.second);
       __syncwarp();
       if (lane == 0) unit_done(nu);
+      // Every product of both tiles is complete: O is final and V16 is free.
+      if (nt0 > 0 && !warp_wait(BAR(T_OFULL), nof0++ & 1, wc)) { ok = false; break; }
+      if (nt1 > 0 && !warp_wait(BAR(T_OFULL + 1), nof1++ & 1, wc)) { ok = false; break; }
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int n_t = t ? nt1 : nt0;
         if (!warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
-        if (n_t > 0) {
-          if (!warp_wait(BAR(T_OFULL + t), (t ? nof1 : nof0) & 1, wc)) { ok = false; break; }
-          if (t) ++nof1; else ++nof0;
-        }
         tc_fence_after();
         const float* st = fin + t * 384 + row;
         const float m = st[0], l = st[128], ref = st[256] / kVShift;
@@ -777,6 +793,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const long long prow = (long long)part * kTRows + r;
         const float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f;
         const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
+        // Whole units go through shared memory (V16 slot t: no product reads it any more), so that rows
+        // leave in whole lines; a warp stages its own 32 rows.
+        uint8_t* stage = smem + C::OFF_V16 + t * C::V16 + (warp & 3) * 32 * (2 * D);
         uint32_t x[32];
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -788,20 +807,31 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0u;
           }
-          if (live && whole) {
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * D + q * 32);
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv, __uint_as_float(x[8 * i + 2 * k + 1]) * inv);
-              out[i] = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((q * 4 + i) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else if (live) {
-            uint4* out = reinterpret_cast<uint4*>(ws + W.part) + prow * (D / 4) + q * 8;
+            uint4* out = reinterpret_cast<uint4*>(ws + W.part) + ((long long)part * (D / 4) + q * 8) * kTRows + r;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) out[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) out[i * kTRows] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        if (whole) {
+          constexpr int LPR = D / 8, RPS = 32 / LPR;
+          const long long mine = live ? orow : -1;
+#pragma unroll 4
+          for (int i = 0; i < 32 / RPS; ++i) {
+            const int rw = i * RPS + lane / LPR;
+            const long long a = __shfl_sync(0xffffffffu, mine, rw);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * (2 * D) + (((lane % LPR) ^ (rw & 7)) << 4));
+            if (a >= 0) *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + a * D) + lane % LPR) = v;
           }
           __syncwarp();
         }
