@@ -37,6 +37,7 @@ constexpr int kTRows = 256;                  // rows of a unit
 constexpr float kPShift = 7.f;               // weights are held times 2^7
 constexpr float kVShift = 128.f;             // and V times 2^7 over the reference scale
 constexpr float kTau = 8.f;                  // rescale when a maximum grows by more (2^(7 + 8) < 65504)
+constexpr int kUnitCost = 5;                 // what starting and ending a unit costs, in key blocks
 constexpr float kMinFactor = 1e-30f;         // keeps -inf * factor = -inf for pages whose scale is 0
 
 template <int D>
@@ -102,7 +103,8 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 }
 
 // A sequence: its units per K/V head and their blocks of 128 keys.  Unit rt holds queries rt qu ..
-// rt qu + qu - 1, qu = 256 / g.
+// rt qu + qu - 1, qu = 256 / g.  Work is counted in steps: a unit's blocks and kUnitCost steps before
+// them (CTAs with many short units took 1.4 times as long when blocks alone were counted).
 struct TileSeq {
   int q0, n, len;
   long long units;
@@ -116,13 +118,13 @@ struct TileSeq {
     const int lim = p.causal ? len - n + min(n, (rt + 1) * qu) : len;
     return (max(lim, 1) + 127) / 128;
   }
-  // Blocks of the units before rt (a unit without keys counts as one block).
-  __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, long long rt) const {
+  // Steps of the units before rt (a unit without keys counts as one block).
+  __device__ __forceinline__ long long steps_before(const CacheParams& p, int qu, long long rt) const {
     const int l = max(len, 1);
     if (rt <= 0) return 0;
-    if (!p.causal) return rt * ((l + 127) / 128);
-    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127);
-    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128;
+    if (!p.causal) return rt * ((l + 127) / 128 + kUnitCost);
+    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127) + rt * kUnitCost;
+    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128 + rt * kUnitCost;
   }
 };
 
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
 
-  // ---- the run of blocks of this CTA; thread t adds up sequences [t per_thread, ...)
+  // ---- the run of steps of this CTA; thread t adds up sequences [t per_thread, ...)
   const int per_thread = (p.B + kTThreads - 1) / kTThreads;
   const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
   long long mine = 0;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const bool w = s.q0 < 0 || s.n < 0 || c1 < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_len ||
                    (p.causal && s.n > s.len) || (b == 0 && s.q0 != 0) || (b == p.B - 1 && c1 != p.total_q);
     wrong |= w;
-    if (!w) mine += s.blocks_before(p, qu, s.units);
+    if (!w) mine += s.steps_before(p, qu, s.units);
   }
   long long incl = mine;
 #pragma unroll
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   total *= p.Hkv;
   before *= p.Hkv;
   mine *= p.Hkv;
-  const long long run = max((total + gridDim.x - 1) / gridDim.x, 2LL);
+  const long long run = max((total + gridDim.x - 1) / gridDim.x, (long long)kUnitCost + 2);
   const long long rs = run * blockIdx.x, re = min(rs + run, total);
   if (rs >= total) return;
   if (before <= rs && rs < before + mine) {
@@ -275,20 +277,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
     long long at = before;
     for (;;) {
       const TileSeq s(p, b, qu);
-      const long long per_head = s.blocks_before(p, qu, s.units);
+      const long long per_head = s.steps_before(p, qu, s.units);
       if (rs < at + per_head * p.Hkv) {
         const int h = (int)((rs - at) / per_head);
         at += h * per_head;
         long long lo = 0, hi = s.units - 1;            // the last rt whose first block is <= rs
         while (lo < hi) {
           const long long mid = (lo + hi + 1) / 2;
-          if (at + s.blocks_before(p, qu, mid) <= rs) lo = mid;
+          if (at + s.steps_before(p, qu, mid) <= rs) lo = mid;
           else hi = mid - 1;
         }
         misc[0] = b;
         misc[1] = h;
         misc[2] = lo;
-        misc[3] = at + s.blocks_before(p, qu, lo);
+        misc[3] = at + s.steps_before(p, qu, lo);
         break;
       }
       at += per_head * p.Hkv;
@@ -443,21 +445,26 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- scheduler
-      // Walks the CTA's units; blocks are counted from the CTA's first.
+      // Walks the CTA's units; steps are counted from the CTA's first.
       if (lane == 0) {
-        int b = (int)misc[0], h = (int)misc[1], rt = (int)misc[2], f = 0, ubeg = (int)(misc[3] - rs);
-        const int end = (int)(re - rs);
+        int b = (int)misc[0], h = (int)misc[1], rt = (int)misc[2], ubeg = (int)(misc[3] - rs);
+        const int end = (int)(re - rs), step_run = (int)run;
         TileSeq sq(p, b, qu);
-        int uend = ubeg + sq.blocks(p, qu, rt);
-        for (uint32_t nu = 0;; ++nu) {
+        bool first = true;
+        for (uint32_t nu = 0;;) {
+          const int uend = ubeg + kUnitCost + sq.blocks(p, qu, rt);
+          // The unit's blocks here; none where the run ends in a unit's first steps, or starts behind its last.
+          const int kt0 = max(0, -ubeg - kUnitCost), kt1 = min(uend, end) - ubeg - kUnitCost;
+          const bool over = ubeg >= end;
+          if (over || kt1 > kt0) {
           if (nu >= kUnitSlots && !mbar_wait(BAR(T_UFREE + nu % kUnitSlots), (nu / kUnitSlots - 1) & 1, wc)) break;
           UnitDesc& U = desc[nu % kUnitSlots];
-          if (f >= end) {
+          if (over) {
             U.nmax = -1;
             mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
             break;
           }
-          const int rows = min(qu, sq.n - rt * qu) * p.g, kt0 = f - ubeg, kt1 = min(uend, end) - ubeg;
+          const int rows = min(qu, sq.n - rt * qu) * p.g;
           int nt[2];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -475,22 +482,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
           U.rows = rows;
           U.q0 = sq.q0 + rt * qu;
           U.lim0 = p.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
-          U.whole = ubeg >= 0 && uend <= end ? 1 : 0;
-          U.second = ubeg > 0 ? 1 : 0;
-          U.more = ubeg >= 0 ? (uend - 1) / end : -1;  // cut: end is the run here, and the unit goes on behind it
+          U.whole = kt0 == 0 && uend <= end ? 1 : 0;
+          U.second = first ? 0 : 1;
+          U.more = kt0 == 0 ? (uend - 1) / step_run : -1;   // cut: the CTAs behind this one that go on with it
+          first = false;
           mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
-          f = uend;
-          if (f >= end) continue;
+          ++nu;
+          }
+          ubeg = uend;
+          if (ubeg >= end) continue;
           if (++rt >= sq.units) {
             rt = 0;
             if (++h == p.Hkv) {
               h = 0;
-              do sq = TileSeq(p, ++b, qu);   // f < end: there is another unit
+              do sq = TileSeq(p, ++b, qu);   // steps are left: there is another unit
               while (sq.units == 0);
             }
           }
-          ubeg = uend;
-          uend = ubeg + sq.blocks(p, qu, rt);
         }
       }
     }
@@ -518,8 +526,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (n_t > 0) {
         // This tile's Q is free: every S of the unit before has been waited for.  Each warp brings its
         // 32 rows, whole rows at a time (D / 8 lanes of 16 bytes each), QB steps' loads under way at once.
-        constexpr int LPR = D / 8, RPS = 32 / LPR, QB = 8;          // lanes per row, rows per step
-        const long long at = live ? ((long long)(r - qi * p.g) * p.total_q + qi) * D : -1;   // this lane's own row
+        constexpr int LPR = D / 8, RPS = 32 / LPR, QB = 4;          // lanes per row, rows per step
+        // (rows that are not in use take the unit's first: loads without conditions).
+        const long long at = live ? ((long long)(r - qi * p.g) * p.total_q + qi) * D : 0;    // this lane's own row
         const uint16_t* base = static_cast<const uint16_t*>(p.q) + ((long long)h * p.g * p.total_q + q0) * D + lane % LPR * 8;
         uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + (warp & 3) * 32 * D;
         uint32_t e_own = 0;
@@ -528,8 +537,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           uint4 w[QB];
 #pragma unroll
           for (int k = 0; k < QB; ++k) {
-            const long long a = __shfl_sync(0xffffffffu, at, (i0 + k) * RPS + lane / LPR);
-            w[k] = a >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + a)) : make_uint4(0u, 0u, 0u, 0u);
+            w[k] = __ldg(reinterpret_cast<const uint4*>(base + __shfl_sync(0xffffffffu, at, (i0 + k) * RPS + lane / LPR)));
           }
 #pragma unroll
           for (int k = 0; k < QB; ++k) {
