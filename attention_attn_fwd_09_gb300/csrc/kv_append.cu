@@ -45,18 +45,14 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8]) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// x / s: a multiplication when s is a power of two (exact), else the IEEE division.
-struct Divisor {
-  float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Divisor(float scale) {
-    const uint32_t b = __float_as_uint(scale);
-    s = scale;
-    pow2 = (b & 0x7fffffu) == 0 && b != 0;             // s >= 2^-126, so 1 / s is normal
-    inv = __uint_as_float((254u << 23) - b);
-  }
-  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : (s > 0.f ? __fdiv_rn(x, s) : x); }
-};
+// 1 / s where that is exact (s a power of two, at least 2^-126, or 0 for rows of zeros), else 0: the
+// caller then divides.  Scales that this kernel wrote are powers of two; a cache filled by other
+// means may hold others.
+__device__ __forceinline__ float exact_inverse(float s) {
+  const uint32_t b = __float_as_uint(s);
+  if (b == 0) return 1.f;
+  return (b & 0x7fffffu) == 0 ? __uint_as_float((254u << 23) - b) : 0.f;
+}
 
 // The slot's sequence and page; false: nothing to do (or the offsets are wrong).  Every thread of
 // the CTA calls it with the CTA's slot.
@@ -116,70 +112,104 @@ struct Target {
   }
 };
 
-// Largest finite magnitude: infinities saturate and NaN stays NaN, neither sets the scale.
-__device__ __forceinline__ float amax8(const uint4& v, float amax) {
-  float f[8];
-  bf16x8(v, f);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float a = fabsf(f[k]);
-    amax = fmaxf(amax, a < INFINITY ? a : 0.f);
+// Largest finite magnitude of bf16 values, as bf16 bits: infinities saturate and NaN stays NaN when
+// coded, neither sets the scale.  Two values at a time; bits of infinities and NaN are the largest
+// and are looked at again only if they occur.
+struct Largest {
+  uint32_t two = 0;
+  __device__ __forceinline__ void add(const uint4& v) {
+    two = __vmaxu2(two, v.x & 0x7fff7fffu);
+    two = __vmaxu2(two, v.y & 0x7fff7fffu);
+    two = __vmaxu2(two, v.z & 0x7fff7fffu);
+    two = __vmaxu2(two, v.w & 0x7fff7fffu);
   }
-  return amax;
+  __device__ __forceinline__ uint32_t bits() const { return max(two & 0xffffu, two >> 16); }
+};
+__device__ __noinline__ uint32_t largest_finite(uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  const uint32_t u[4] = {x, y, z, w};
+  uint32_t m = 0;
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = u[i >> 1] >> (i & 1) * 16 & 0x7fffu;
+    if (a < 0x7f80u) m = max(m, a);
+  }
+  return m;
 }
-__device__ __forceinline__ uint2 code8(const uint4& v, const Divisor& div) {
+__device__ __forceinline__ uint2 code8(const uint4& v, float inv) {
   float f[8];
   bf16x8(v, f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = div(f[k]);
+  for (int k = 0; k < 8; ++k) f[k] *= inv;
   return e4m3x8(f);
 }
-// Codes of an earlier row at the page's new scale.
-__device__ __forceinline__ uint2 recode8(const uint2& old, float s_old, const Divisor& div) {
+// The same by division.
+__device__ __noinline__ uint2 code8_div(uint4 v, float s) {
+  float f[8];
+  bf16x8(v, f);
+  for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], s);
+  return e4m3x8(f);
+}
+// Codes of an earlier row at the page's new scale, which is a power of two (it grew).
+__device__ __forceinline__ uint2 recode8(const uint2& old, float s_old, float inv) {
   float f[8];
   e4m3x4_to_f32(old.x, f[0], f[1], f[2], f[3]);
   e4m3x4_to_f32(old.y, f[4], f[5], f[6], f[7]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = div(f[k] * s_old);
+  for (int k = 0; k < 8; ++k) f[k] = f[k] * s_old * inv;
   return e4m3x8(f);
 }
 
-// 8 elements (16 bytes in, 8 bytes out) per thread and step; NV steps cover a page.
-template <int D, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_kernel(const AppendParams p) {
-  __shared__ float red[THREADS / 32];
+// 8 elements (16 bytes in, 8 bytes out) per thread and step; NV steps cover a page of one head.
+template <int D, int NV, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) kv_append_kernel(const AppendParams p) {
+  __shared__ uint32_t red[THREADS / 32];
+  constexpr int RPS = THREADS * 8 / D;                 // rows per step
   const int tid = threadIdx.x;
   Slot s;
   if (!find_slot<THREADS>(p, blockIdx.x, s)) return;
   const Target t(p, s, blockIdx.y, blockIdx.z != 0, D);
+  const int r0 = tid / (D / 8), c = tid % (D / 8) * 8;
+  const float s_old = s.kept > 0 ? *t.scale : 0.f;
   uint4 x[NV];
+  const uint16_t* src = t.src + (s.src0 + r0) * t.st + c;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (tid + i * THREADS) * 8, r = e / D, c = e % D;
-    x[i] = r >= s.kept && r < s.rows ? __ldcs(reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c))
-                                     : make_uint4(0u, 0u, 0u, 0u);
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + i * RPS >= s.kept && r0 + i * RPS < s.rows) x[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+    src += RPS * t.st;
   }
-  const float s_old = s.kept > 0 ? *t.scale : 0.f;
-  float amax = 0.f;
+  Largest big;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) amax = amax8(x[i], amax);
+  for (int i = 0; i < NV; ++i) big.add(x[i]);
+  uint32_t amax = big.bits();
+  if (amax >= 0x7f80u) {
+    amax = 0;
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i) {
+      uint4 v = x[0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int k = 1; k < NV; ++k)
+        if (i == k) v = x[k];
+      amax = max(amax, largest_finite(v.x, v.y, v.z, v.w));
+    }
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
   if ((tid & 31) == 0) red[tid >> 5] = amax;
   __syncthreads();
   amax = red[0];
 #pragma unroll
-  for (int i = 1; i < THREADS / 32; ++i) amax = fmaxf(amax, red[i]);
-  const float sc = fmaxf(s_old, pow2_scale(amax));
+  for (int i = 1; i < THREADS / 32; ++i) amax = max(amax, red[i]);
+  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax << 16)));
   if (tid == 0) *t.scale = sc;
-  const Divisor div(sc);
-  const bool again = sc > s_old && s_old > 0.f;        // the kept rows' codes change
+  const float inv = exact_inverse(sc);
+  uint2* out = reinterpret_cast<uint2*>(t.dst + tid * 8);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (tid + i * THREADS) * 8, r = e / D;
-    uint2* out = reinterpret_cast<uint2*>(t.dst + e);
-    if (r >= s.kept && r < s.rows) *out = code8(x[i], div);   // rows behind the last one stay as they are
-    else if (r < s.kept && again) *out = recode8(*out, s_old, div);
+    const int r = r0 + i * RPS;                        // rows behind the last one stay as they are
+    if (r >= s.kept && r < s.rows) out[i * THREADS] = inv != 0.f ? code8(x[i], inv) : code8_div(x[i], sc);
+  }
+  if (sc > s_old && s_old > 0.f) {                     // the kept rows' codes change
+#pragma unroll 1
+    for (int i = 0; i < NV && r0 + i * RPS < s.kept; ++i) out[i * THREADS] = recode8(out[i * THREADS], s_old, inv);
   }
 }
 
@@ -196,23 +226,24 @@ __global__ void __launch_bounds__(kStepWarps * 32) kv_append_step_kernel(const A
   const int r0 = lane / (D / 8), c = lane % (D / 8) * 8;
   const float s_old = s.kept > 0 ? *t.scale : 0.f;
   uint4 x = make_uint4(0u, 0u, 0u, 0u);
-  float amax = 0.f;
+  uint32_t amax = 0;
   for (int r = s.kept + r0; r < s.rows; r += RPW) {
     x = *reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c);
-    amax = amax8(x, amax);
+    Largest big;
+    big.add(x);
+    amax = max(amax, big.bits() < 0x7f80u ? big.bits() : largest_finite(x.x, x.y, x.z, x.w));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float sc = fmaxf(s_old, pow2_scale(amax));
-  const Divisor div(sc);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax << 16)));
+  const float inv = exact_inverse(sc);
   for (int r = s.kept + r0; r < s.rows; r += RPW) {
     if (s.rows - s.kept > RPW) x = *reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c);
-    *reinterpret_cast<uint2*>(t.dst + r * D + c) = code8(x, div);
+    *reinterpret_cast<uint2*>(t.dst + r * D + c) = inv != 0.f ? code8(x, inv) : code8_div(x, sc);
   }
   if (sc > s_old && s_old > 0.f) {
     for (int r = r0; r < s.kept; r += RPW) {
       uint2* out = reinterpret_cast<uint2*>(t.dst + r * D + c);
-      *out = recode8(*out, s_old, div);
+      *out = recode8(*out, s_old, inv);
     }
   }
   __syncwarp();                                        // every lane has read the old scale
@@ -222,11 +253,11 @@ __global__ void __launch_bounds__(kStepWarps * 32) kv_append_step_kernel(const A
 template <int D>
 cudaError_t launch_d(const AppendParams& p, dim3 grid, cudaStream_t s) {
   const int vecs = p.page * D / 8;                     // 16-byte pieces of a page
-  if (vecs == 128) kv_append_kernel<D, 1, 128><<<grid, 128, 0, s>>>(p);
-  else if (vecs == 256) kv_append_kernel<D, 1, 256><<<grid, 256, 0, s>>>(p);
-  else if (vecs == 512) kv_append_kernel<D, 2, 256><<<grid, 256, 0, s>>>(p);
-  else if (vecs == 1024) kv_append_kernel<D, 4, 256><<<grid, 256, 0, s>>>(p);
-  else if (vecs == 2048) kv_append_kernel<D, 4, 512><<<grid, 512, 0, s>>>(p);
+  if (vecs == 128) kv_append_kernel<D, 1, 128, 12><<<grid, 128, 0, s>>>(p);
+  else if (vecs == 256) kv_append_kernel<D, 1, 256, 6><<<grid, 256, 0, s>>>(p);
+  else if (vecs == 512) kv_append_kernel<D, 2, 256, 6><<<grid, 256, 0, s>>>(p);
+  else if (vecs == 1024) kv_append_kernel<D, 4, 256, 5><<<grid, 256, 0, s>>>(p);
+  else if (vecs == 2048) kv_append_kernel<D, 8, 256, 4><<<grid, 256, 0, s>>>(p);
   else return cudaErrorInvalidValue;
   return cudaGetLastError();
 }

@@ -84,9 +84,9 @@ __device__ __forceinline__ BfVec<V> pack(const float (&f)[V]) {
 // rows; V = 1 takes every even rot and alignment.
 template <int V, bool INTER, int D>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  extern __shared__ float2 cs[];                       // [tokens][rot / 2] (m cos, m sin)
+  extern __shared__ __align__(16) float2 cs[];                       // [tokens][rot / 2] (m cos, m sin)
   constexpr int UPR = D / (2 * V);                     // items per head row
-  constexpr int BATCH = V == 8 ? 4 : 2;                // items a thread has in flight
+  constexpr int BATCH = 2;                             // items a thread has in flight
   const int half = p.rot / 2;
   unsigned long long* turn = reinterpret_cast<unsigned long long*>(cs + (half << p.tile_shift));   // [rot / 2]
   const int b = blockIdx.x / p.tiles, n0 = (blockIdx.x - b * p.tiles) << p.tile_shift;
@@ -121,7 +121,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         const unsigned long long ph = turn[j] * (unsigned long long)pos;
         float s, c;
         sincospif(__int2float_rn((int)(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-        cs[i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+        // Pairs 2k, 2k + 1 of all items of a row lie side by side: neighbouring threads' 16-byte reads then
+        // touch all banks (pair after pair they met in a quarter of them).
+        const int slot = V == 1 ? j : (j % V / 2) * (half / V) * 2 + j / V * 2 + (j & 1);
+        cs[n * half + slot] = make_float2(c * p.mscale, s * p.mscale * p.sign);
       }
       __syncthreads();
     }
@@ -144,21 +147,35 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       float x[V], y[V], xo[V], yo[V];
       unpack<V>(a[k], x);
       unpack<V>(bb[k], y);
-      const float2* w = cs + n * half + u * V;         // V pairs
+      float cw[V], sw[V];                              // of the item's V pairs
+      if constexpr (V == 1) {
+        const float2 w = cs[n * half + u];
+        cw[0] = w.x;
+        sw[0] = w.y;
+      } else {
+        const float4* w = reinterpret_cast<const float4*>(cs + n * half) + u;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float4 e = w[j * (half / V)];
+          cw[2 * j] = e.x;
+          sw[2 * j] = e.y;
+          cw[2 * j + 1] = e.z;
+          sw[2 * j + 1] = e.w;
+        }
+      }
       if constexpr (INTER && V > 1) {
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-          const float2 e = w[j], f = w[V / 2 + j];
-          xo[2 * j] = x[2 * j] * e.x - x[2 * j + 1] * e.y;
-          xo[2 * j + 1] = x[2 * j + 1] * e.x + x[2 * j] * e.y;
-          yo[2 * j] = y[2 * j] * f.x - y[2 * j + 1] * f.y;
-          yo[2 * j + 1] = y[2 * j + 1] * f.x + y[2 * j] * f.y;
+          xo[2 * j] = x[2 * j] * cw[j] - x[2 * j + 1] * sw[j];
+          xo[2 * j + 1] = x[2 * j + 1] * cw[j] + x[2 * j] * sw[j];
+          yo[2 * j] = y[2 * j] * cw[V / 2 + j] - y[2 * j + 1] * sw[V / 2 + j];
+          yo[2 * j + 1] = y[2 * j + 1] * cw[V / 2 + j] + y[2 * j] * sw[V / 2 + j];
         }
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          xo[j] = x[j] * w[j].x - y[j] * w[j].y;
-          yo[j] = y[j] * w[j].x + x[j] * w[j].y;
+          xo[j] = x[j] * cw[j] - y[j] * sw[j];
+          yo[j] = y[j] * cw[j] + x[j] * sw[j];
         }
       }
       st_vec<V>(dst + ca, pack<V>(xo));
@@ -179,11 +196,11 @@ cudaError_t launch_v(const RopeParams& p, dim3 grid, size_t smem, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s) {
-  // Tokens per CTA: 8 when that still gives every SM work (the cosines and sines of a token
+  // Tokens per CTA: 4 when that still gives every SM work (the cosines and sines of a token
   // are then shared by all heads), else one token per CTA and the heads split over CTAs so
   // that each thread has about one item.
   const int upr = p.d / (2 * vec), heads = p.Hq + p.Hk;
-  p.tile_shift = (long long)p.B * ((p.N + 7) / 8) >= sms ? 3 : 0;
+  p.tile_shift = (long long)p.B * ((p.N + 3) / 4) >= sms ? 2 : 0;
   p.tiles = (p.N + (1 << p.tile_shift) - 1) >> p.tile_shift;
   p.head_group = p.tile_shift > 0 ? heads : (kRopeThreads + upr - 1) / upr;
   const long long gx = (long long)p.B * p.tiles;
