@@ -545,19 +545,27 @@ def attn_rope_bwd(dq, dk, inv_freq, positions=None, interleaved: bool = False, m
 
 def _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu, cu_name, kv_lens, dev):
     """Checks a paged cache and its index tensors; (num_pages, Hkv, page_size, d, B, max_pages)."""
-    shape, (B, width) = k_cache.shape, page_table.shape if page_table.dim() == 2 else (-1, -1)
-    if len(shape) != 4:
-        raise ValueError(f"k_cache: expected [num_pages, Hkv, page_size, d], got {tuple(shape)}")
-    if B < 0:
-        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
-    u8, f32, i32, pairs = torch.uint8, torch.float32, torch.int32, shape[:2]
-    _plain("k_cache", k_cache, u8, shape, dev)
-    _plain("v_cache", v_cache, u8, shape, dev)
-    _plain("k_scale", k_scale, f32, pairs, dev)
-    _plain("v_scale", v_scale, f32, pairs, dev)
-    _plain("page_table", page_table, i32, (B, width), dev)
-    _plain(cu_name, cu, i32, (B + 1,), dev)
-    _plain("kv_lens", kv_lens, i32, (B,), dev)
+    shape = k_cache.shape
+    if len(shape) != 4 or page_table.dim() != 2:
+        raise ValueError(f"expected k_cache [num_pages, Hkv, page_size, d] and page_table [B, max_pages], got {tuple(shape)} "
+                         f"and {tuple(page_table.shape)}")
+    B, width = page_table.shape
+    pairs, u8, f32, i32 = shape[:2], torch.uint8, torch.float32, torch.int32
+    # One condition for all, since the checks are most of a call's host time; then the one that failed.
+    if not (k_cache.dtype is u8 and v_cache.dtype is u8 and k_scale.dtype is f32 and v_scale.dtype is f32
+            and page_table.dtype is i32 and cu.dtype is i32 and kv_lens.dtype is i32
+            and v_cache.shape == shape and k_scale.shape == pairs and v_scale.shape == pairs and cu.shape == (B + 1,)
+            and kv_lens.shape == (B,)
+            and k_cache.device == dev and v_cache.device == dev and k_scale.device == dev and v_scale.device == dev
+            and page_table.device == dev and cu.device == dev and kv_lens.device == dev
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and page_table.is_contiguous() and cu.is_contiguous()
+            and kv_lens.is_contiguous()):
+        for name, t, dtype, want in (("k_cache", k_cache, u8, shape), ("v_cache", v_cache, u8, shape),
+                                     ("k_scale", k_scale, f32, pairs), ("v_scale", v_scale, f32, pairs),
+                                     ("page_table", page_table, i32, (B, width)), (cu_name, cu, i32, (B + 1,)),
+                                     ("kv_lens", kv_lens, i32, (B,))):
+            _plain(name, t, dtype, want, dev)
     return (*shape, B, width)
 
 

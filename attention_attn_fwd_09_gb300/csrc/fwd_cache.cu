@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const CacheWs W = cache_ws(gridDim.x, rows_max, D);
   char* ws = static_cast<char*>(p.ws);
   int4* rec = reinterpret_cast<int4*>(ws) + blockIdx.x;
-  pdl_trigger();
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kWarps * C::STAGES; ++i) mbar_init(smem_u32(smem + C::OFF_BAR) + 8 * i, 1);
@@ -109,6 +108,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tm_v);
   }
 
+  pdl_wait();                                // nothing of global memory before this
+  pdl_trigger();
   // ---- the run of pieces of this CTA; thread t adds up sequences [t per_thread, ...)
   const int per_thread = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
@@ -563,63 +564,75 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the partial results of cut units: block x takes the unit that starts in CTA x of the main
-// kernel and goes on in others (at most one); its threads take 4 columns of a row at a time.  The
-// kernel is short (two dependent reads once the main kernel is done), so it reads statistics and
-// rows of four partials at once and joins them as they come.
-template <int D>
-__global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int ctas) {
+// Joins the partial results of cut units: blocks x take the unit that starts in CTA x of the main
+// kernel and goes on in others (at most one).  A thread has one row and CPT pieces of 4 columns of it,
+// and reads JOIN partials' statistics and pieces at once, joining them as they come.  CPT = 4 when a
+// unit has many rows (bytes bound it: with one piece per thread and turn, 18 us for 152 units of 256
+// rows cut in two), 1 for decoding (latency does).
+template <int D, int CPT, int JOIN>
+__global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int row_shift,
+                                                              const int ctas) {
+  constexpr int GROUPS = D / 4 / CPT;
   const CacheWs W = cache_ws(ctas, rows_max, D);
   const char* ws = static_cast<const char*>(p.ws);
-  const float4* stat = reinterpret_cast<const float4*>(ws + W.stat);
-  const float4* part = reinterpret_cast<const float4*>(ws + W.part);
+  const int t = blockIdx.y * 128 + threadIdx.x, r = t & ((1 << row_shift) - 1), cg = t >> row_shift;
+  const int qi = r / p.g;
+  const float4* stat = reinterpret_cast<const float4*>(ws + W.stat) + r;
+  const float4* part = reinterpret_cast<const float4*>(ws + W.part) + (long long)cg * rows_max + r;
   pdl_wait();
+  pdl_trigger();
   const int4 rec = reinterpret_cast<const int4*>(ws)[blockIdx.x];
-  if (rec.w < 2) return;
-  const int h = rec.x, rows = rec.z * p.g, first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
-  for (int i = blockIdx.y * 128 + threadIdx.x; i < rows * (D / 4); i += gridDim.y * 128) {
-    const int col = i / rows, r = i - col * rows;      // neighbouring threads read neighbouring rows
-    float m = -INFINITY, ref = kMinScale, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 <= more; k0 += 4) {
-      float4 st[4], x[4];
+  if (rec.w < 2 || qi >= rec.z || cg >= GROUPS) return;
+  const int first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
+  // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
+  auto which = [&](int k) -> long long { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
+  float m = -INFINITY, ref = kMinScale, l = 0.f;
+  float4 o[CPT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + j;
-        // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
-        const long long which = k == 0 ? first : 2 * ((int)blockIdx.x + k);
-        st[j] = k <= more ? stat[which * rows_max + r] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        x[j] = k <= more ? part[(which * (D / 4) + col) * rows_max + r] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float mn = m, rn = ref;
+  for (int c = 0; c < CPT; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 <= more; k0 += JOIN) {
+    float4 x[JOIN][CPT], st[JOIN];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mn = fmaxf(mn, st[j].x);
-        rn = fmaxf(rn, st[j].z);
-      }
-      const float mu = mn == -INFINITY ? 0.f : mn, rinv = 1.f / rn;
-      const float w0 = ex2_mufu(m - mu), v0 = w0 * (ref * rinv);
-      l *= w0;
-      o.x *= v0; o.y *= v0; o.z *= v0; o.w *= v0;
+    for (int j = 0; j < JOIN; ++j) {
+      const long long w = which(min(k0 + j, more));     // (the last one again: loads without conditions)
+      st[j] = stat[w * rows_max];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float w = ex2_mufu(st[j].x - mu), v = w * (st[j].z * rinv);
-        l += w * st[j].y;
-        o.x += v * x[j].x;
-        o.y += v * x[j].y;
-        o.z += v * x[j].z;
-        o.w += v * x[j].w;
-      }
-      m = mn;
-      ref = rn;
+      for (int c = 0; c < CPT; ++c) x[j][c] = part[(w * (D / 4) + c * GROUPS) * rows_max];
     }
-    const int qi = r / p.g;
-    const long long row = (long long)(h * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
-    const float inv = l == 0.f ? 0.f : ref / l;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + col;
-    *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (col == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
+    float mn = m, rn = ref;
+#pragma unroll
+    for (int j = 0; j < JOIN; ++j) {
+      mn = fmaxf(mn, st[j].x);
+      rn = fmaxf(rn, st[j].z);
+    }
+    const float mu = mn == -INFINITY ? 0.f : mn, rinv = 1.f / rn;
+    const float w0 = ex2_mufu(m - mu), v0 = w0 * (ref * rinv);
+    l *= w0;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) { o[c].x *= v0; o[c].y *= v0; o[c].z *= v0; o[c].w *= v0; }
+#pragma unroll
+    for (int j = 0; j < JOIN; ++j) {
+      if (k0 + j > more) break;
+      const float w = ex2_mufu(st[j].x - mu), v = w * (st[j].z * rinv);
+      l += w * st[j].y;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        o[c].x += v * x[j][c].x;
+        o[c].y += v * x[j][c].y;
+        o[c].z += v * x[j][c].z;
+        o[c].w += v * x[j][c].w;
+      }
+    }
+    m = mn;
+    ref = rn;
   }
+  const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
+  const float inv = l == 0.f ? 0.f : ref / l;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + cg;
+#pragma unroll
+  for (int c = 0; c < CPT; ++c)
+    out[c * GROUPS] = make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
+  if (cg == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -634,18 +647,24 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
     attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-  fwd_cache_decode_kernel<D><<<grid, kThreads, C::SMEM, s>>>(maps.k, maps.v, p, rows);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
+  e = launch_pdl(fwd_cache_decode_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, s, maps.k, maps.v, p, rows);
+  if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, rows, grid, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
-  // 16 blocks for a unit of 256 rows: all blocks are resident at once, with a few rows a thread.
-  const dim3 grid((unsigned)ctas, (unsigned)min((rows * (d / 4) + 127) / 128, 16));
-  return d == 64 ? launch_pdl(fwd_cache_merge_kernel<64>, grid, dim3(128), 0, s, p, rows, ctas)
-                 : launch_pdl(fwd_cache_merge_kernel<128>, grid, dim3(128), 0, s, p, rows, ctas);
+  int shift = 0;
+  while ((1 << shift) < rows) ++shift;
+  auto go = [&](auto kernel, int cpt) {
+    const dim3 grid((unsigned)ctas, (unsigned)((((d / 4 / cpt) << shift) + 127) / 128));
+    return launch_pdl(kernel, grid, dim3(128), 0, s, p, rows, shift, ctas);
+  };
+  if (rows <= kCacheDecodeRows)
+    return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8>, 1) : go(fwd_cache_merge_kernel<128, 1, 8>, 1);
+  return d == 64 ? go(fwd_cache_merge_kernel<64, 4, 2>, 4) : go(fwd_cache_merge_kernel<128, 4, 2>, 4);
 }
 
 size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }

@@ -202,7 +202,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const CacheWs W = cache_ws(gridDim.x, kTRows, D);
   char* ws = static_cast<char*>(p.ws);
   int4* rec = reinterpret_cast<int4*>(ws) + blockIdx.x;
-  pdl_trigger();
 
   if (tid == 0) {
     mbar_init(BAR(T_EPI), 128);
@@ -234,6 +233,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
 
+  pdl_wait();                                // nothing of global memory before this
+  pdl_trigger();
   // ---- the run of steps of this CTA; thread t adds up sequences [t per_thread, ...)
   const int per_thread = (p.B + kTThreads - 1) / kTThreads;
   const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
@@ -877,8 +878,9 @@ cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, c
     attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-  fwd_cache_tile_kernel<D, NG><<<grid, kTThreads, C::SMEM, s>>>(maps.k, maps.v, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
+  e = launch_pdl(fwd_cache_tile_kernel<D, NG>, dim3(grid), dim3(kTThreads), C::SMEM, s, maps.k, maps.v, p);
+  if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, kTRows, grid, s);
 }
 
