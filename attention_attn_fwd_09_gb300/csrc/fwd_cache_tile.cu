@@ -37,7 +37,7 @@ constexpr int kTRows = 256;                  // rows of a unit
 constexpr float kPShift = 7.f;               // weights are held times 2^7
 constexpr float kVShift = 128.f;             // and V times 2^7 over the reference scale
 constexpr float kTau = 8.f;                  // rescale when a maximum grows by more (2^(7 + 8) < 65504)
-constexpr int kUnitCost = 5;                 // what starting and ending a unit costs, in key blocks
+constexpr int kUnitCost = 5;                 // at most what starting and ending a unit counts for, in key blocks
 constexpr float kMinFactor = 1e-30f;         // keeps -inf * factor = -inf for pages whose scale is 0
 
 template <int D>
@@ -103,7 +103,7 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 }
 
 // A sequence: its units per K/V head and their blocks of 128 keys.  Unit rt holds queries rt qu ..
-// rt qu + qu - 1, qu = 256 / g.  Work is counted in steps: a unit's blocks and kUnitCost steps before
+// rt qu + qu - 1, qu = 256 / g.  Work is counted in steps: a unit's blocks and `cost` steps before
 // them (CTAs with many short units took 1.4 times as long when blocks alone were counted).
 struct TileSeq {
   int q0, n, len;
@@ -118,13 +118,12 @@ struct TileSeq {
     const int lim = p.causal ? len - n + min(n, (rt + 1) * qu) : len;
     return (max(lim, 1) + 127) / 128;
   }
-  // Steps of the units before rt (a unit without keys counts as one block).
-  __device__ __forceinline__ long long steps_before(const CacheParams& p, int qu, long long rt) const {
-    const int l = max(len, 1);
+  // Blocks of the units before rt (a unit without keys counts as one).
+  __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, long long rt) const {
     if (rt <= 0) return 0;
-    if (!p.causal) return rt * ((l + 127) / 128 + kUnitCost);
-    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127) + rt * kUnitCost;
-    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128 + rt * kUnitCost;
+    if (!p.causal) return rt * ((max(len, 1) + 127) / 128);
+    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127);
+    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128;
   }
 };
 
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 768);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   long long* misc = reinterpret_cast<long long*>(tmem_slot + 2);   // [4]: b, h, rt, unit start
-  long long* sums = reinterpret_cast<long long*>(smem + C::OFF_Q); // [16] warp sums, before Q is written
+  long long* sums = reinterpret_cast<long long*>(smem + C::OFF_Q); // [16][2] warp sums, before Q is written
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id(), wg = warp >> 2;
   const int qu = kTRows / p.g;                               // queries per unit
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   // ---- the run of steps of this CTA; thread t adds up sequences [t per_thread, ...)
   const int per_thread = (p.B + kTThreads - 1) / kTThreads;
   const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
-  long long mine = 0;
+  long long blocks = 0, units = 0;
   bool wrong = false;
   for (int b = b_lo; b < b_hi; ++b) {
     const TileSeq s(p, b, qu);
@@ -246,31 +245,47 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const bool w = s.q0 < 0 || s.n < 0 || c1 < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_len ||
                    (p.causal && s.n > s.len) || (b == 0 && s.q0 != 0) || (b == p.B - 1 && c1 != p.total_q);
     wrong |= w;
-    if (!w) mine += s.steps_before(p, qu, s.units);
+    if (!w) {
+      blocks += s.blocks_before(p, qu, s.units);
+      units += s.units;
+    }
   }
-  long long incl = mine;
+  long long blocks_to = blocks, units_to = units;      // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const long long v = __shfl_up_sync(0xffffffffu, blocks_to, o), w = __shfl_up_sync(0xffffffffu, units_to, o);
+    if (lane >= o) {
+      blocks_to += v;
+      units_to += w;
+    }
   }
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) {
+    sums[2 * warp] = blocks_to;
+    sums[2 * warp + 1] = units_to;
+  }
   const bool bad = __syncthreads_or(wrong) != 0;
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
   }
   if (bad) return;
-  long long before = incl - mine, total = 0;
+  blocks_to -= blocks;
+  units_to -= units;
+  long long all_blocks = 0, all_units = 0;
 #pragma unroll
   for (int w = 0; w < kTThreads / 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
+    if (w < warp) {
+      blocks_to += sums[2 * w];
+      units_to += sums[2 * w + 1];
+    }
+    all_blocks += sums[2 * w];
+    all_units += sums[2 * w + 1];
   }
-  total *= p.Hkv;
-  before *= p.Hkv;
-  mine *= p.Hkv;
-  const long long run = max((total + gridDim.x - 1) / gridDim.x, (long long)kUnitCost + 2);
+  // Few blocks per CTA: what counts is the longest run of blocks, not the sum of the work.
+  const int cost = (int)min((long long)kUnitCost, all_blocks * p.Hkv / gridDim.x / 4);
+  const long long total = (all_blocks + cost * all_units) * p.Hkv;
+  const long long before = (blocks_to + cost * units_to) * p.Hkv, mine = (blocks + cost * units) * p.Hkv;
+  const long long run = max((total + gridDim.x - 1) / gridDim.x, 2LL);
   const long long rs = run * blockIdx.x, re = min(rs + run, total);
   if (rs >= total) return;
   if (before <= rs && rs < before + mine) {
@@ -278,20 +293,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
     long long at = before;
     for (;;) {
       const TileSeq s(p, b, qu);
-      const long long per_head = s.steps_before(p, qu, s.units);
+      auto steps_before = [&](long long rt) -> long long { return s.blocks_before(p, qu, rt) + rt * cost; };
+      const long long per_head = steps_before(s.units);
       if (rs < at + per_head * p.Hkv) {
         const int h = (int)((rs - at) / per_head);
         at += h * per_head;
-        long long lo = 0, hi = s.units - 1;            // the last rt whose first block is <= rs
+        long long lo = 0, hi = s.units - 1;            // the last rt whose first step is <= rs
         while (lo < hi) {
           const long long mid = (lo + hi + 1) / 2;
-          if (at + s.steps_before(p, qu, mid) <= rs) lo = mid;
+          if (at + steps_before(mid) <= rs) lo = mid;
           else hi = mid - 1;
         }
         misc[0] = b;
         misc[1] = h;
         misc[2] = lo;
-        misc[3] = at + s.steps_before(p, qu, lo);
+        misc[3] = at + steps_before(lo);
         break;
       }
       at += per_head * p.Hkv;
@@ -453,9 +469,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         TileSeq sq(p, b, qu);
         bool first = true;
         for (uint32_t nu = 0;;) {
-          const int uend = ubeg + kUnitCost + sq.blocks(p, qu, rt);
+          const int uend = ubeg + cost + sq.blocks(p, qu, rt);
           // The unit's blocks here; none where the run ends in a unit's first steps, or starts behind its last.
-          const int kt0 = max(0, -ubeg - kUnitCost), kt1 = min(uend, end) - ubeg - kUnitCost;
+          const int kt0 = max(0, -ubeg - cost), kt1 = min(uend, end) - ubeg - cost;
           const bool over = ubeg >= end;
           if (over || kt1 > kt0) {
           if (nu >= kUnitSlots && !mbar_wait(BAR(T_UFREE + nu % kUnitSlots), (nu / kUnitSlots - 1) & 1, wc)) break;
