@@ -480,20 +480,19 @@ def attn_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", fact
 
 
 _Strides12, _Strides4 = _ll * 12, _ll * 4
-_ROW = (0, 0, 0)
 
 
-def _rows(name, t, shape, dev):
-    """(batch, head, token) strides of a bf16 tensor [B,H,N,d] or [H,T,d] with contiguous columns."""
-    st = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or st[-1] != 1:
-        raise ValueError(f"{name}: expected a bf16 tensor of shape {tuple(shape)} with contiguous columns on {dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {st}")
-    return st[:3] if len(st) == 4 else (0, st[0], st[1])
+def _bad_rows(dev, *rows):
+    """ValueError for the first (name, tensor, shape) that is not a bf16 tensor of that shape with
+    contiguous columns on the device."""
+    for name, t, shape in rows:
+        if t is not None and (t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or t.stride()[-1] != 1):
+            raise ValueError(f"{name}: expected a bf16 tensor of shape {tuple(shape)} with contiguous columns on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
 def _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, stream):
-    shape, dev = q.shape, q.device
+    shape, dev, bf16 = q.shape, q.device, torch.bfloat16
     dims = len(shape)
     if dims not in (3, 4) or not q.is_cuda:
         raise ValueError(f"q: expected a CUDA tensor [B,H,N,d] or [H,T,d], got {tuple(shape)} on {dev}")
@@ -505,24 +504,37 @@ def _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
     else:
         B, (Hq, N, d) = 1, shape
     if q_out is None:
-        q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    sq, oq = _rows("q", q, shape, dev), _rows("q_out", q_out, shape, dev)
-    Hk, sk, ok, pk, pok = 0, _ROW, _ROW, None, None
+        q_out = torch.empty(shape, dtype=bf16, device=dev)
+    sq, oq = q.stride(), q_out.stride()
+    ok = (q.dtype is bf16 and q_out.dtype is bf16 and q_out.shape == shape and q_out.device == dev and sq[-1] == 1
+          and oq[-1] == 1)
+    kshape, Hk, sk, pk, pok = None, 0, sq, None, None
+    so = sk
     if k is not None:
-        Hk = k.shape[-3] if k.dim() == dims else 0
-        kshape = (B, Hk, N, d) if dims == 4 else (Hk, N, d)
+        kshape = (B, k.shape[1], N, d) if dims == 4 and k.dim() == 4 else (k.shape[0], N, d)
+        Hk = kshape[-3]
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=torch.bfloat16, device=dev)
-        sk, ok = _rows("k", k, kshape, dev), _rows("k_out", k_out, kshape, dev)
+            k_out = torch.empty(kshape, dtype=bf16, device=dev)
+        sk, so = k.stride(), k_out.stride()
+        ok = (ok and k.dtype is bf16 and k_out.dtype is bf16 and k.shape == kshape and k_out.shape == kshape
+              and len(kshape) == dims and k.device == dev and k_out.device == dev and sk[-1] == 1 and so[-1] == 1)
         pk, pok = k.data_ptr(), k_out.data_ptr()
+    if not ok:
+        if kshape is not None and len(kshape) != dims:
+            raise ValueError(f"k: expected as many dimensions as q, got {tuple(k.shape)}")
+        _bad_rows(dev, ("q", q, shape), ("q_out", q_out, shape), ("k", k, kshape), ("k_out", k_out, kshape))
     half = inv_freq.numel()
     _plain("inv_freq", inv_freq, torch.float64, (half,), dev)
     pos = None
     if positions is not None:
         _plain("positions", positions, torch.int32, (N,) if dims == 3 and positions.dim() == 1 else (B, N), dev)
         pos = positions.data_ptr()
+    if dims == 4:
+        strides = _Strides12(sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], oq[0], oq[1], oq[2], so[0], so[1], so[2])
+    else:
+        strides = _Strides12(0, sq[0], sq[1], 0, sk[0], sk[1], 0, oq[0], oq[1], 0, so[0], so[1])
     _check(call(q.data_ptr(), pk, q_out.data_ptr(), pok, inv_freq.data_ptr(), pos, B, Hq, Hk, N, d, 2 * half,
-                1 if interleaved else 0, mscale, _Strides12(*sq, *sk, *oq, *ok), _current_stream(dev.index)))
+                1 if interleaved else 0, mscale, strides, _current_stream(dev.index)))
     return q_out, k_out
 
 
@@ -585,12 +597,15 @@ def attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_
     pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, "cu_seqlens",
                                                 kv_lens, dev)
     T = k.shape[1]
-    shape = (Hkv, T, d)
-    sk, sv = _rows("k", k, shape, dev), _rows("v", v, shape, dev)
+    shape, bf16 = (Hkv, T, d), torch.bfloat16
+    sk, sv = k.stride(), v.stride()
+    if not (k.dtype is bf16 and v.dtype is bf16 and k.shape == shape and v.shape == shape and v.device == dev
+            and sk[2] == 1 and sv[2] == 1):
+        _bad_rows(dev, ("k", k, shape), ("v", v, shape))
     _check(_lib.attn_kv_append_fp8(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                    k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(),
                                    kv_lens.data_ptr(), B, Hkv, T, d, pages, P, width,
-                                   _Strides4(sk[1], sk[2], sv[1], sv[2]), _current_stream(dev.index)))
+                                   _Strides4(sk[0], sk[1], sv[0], sv[1]), _current_stream(dev.index)))
 
 
 def attn_fwd_kv_fp8_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_q: int, d: int) -> int:
@@ -619,14 +634,15 @@ def attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlen
                                                 "cu_seqlens_q", kv_lens, dev)
     Hq, T, _ = q.shape
     shape = (Hq, T, d)
-    _plain("q", q, torch.bfloat16, shape, dev)
     if o is None:
-        o = torch.empty_like(q)
-    else:
-        _plain("o", o, torch.bfloat16, shape, dev)
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-    else:
+    if not (q.dtype is torch.bfloat16 and o.dtype is torch.bfloat16 and lse.dtype is torch.float32 and q.shape == shape
+            and o.shape == shape and lse.shape == (Hq, T) and o.device == dev and lse.device == dev
+            and q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
+        _plain("q", q, torch.bfloat16, shape, dev)
+        _plain("o", o, torch.bfloat16, shape, dev)
         _plain("lse", lse, torch.float32, (Hq, T), dev)
     if workspace is None:
         n = attn_fwd_kv_fp8_workspace_size(B, Hq, Hkv, T, max_q, d)

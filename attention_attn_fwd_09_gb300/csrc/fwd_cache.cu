@@ -664,7 +664,7 @@ cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ct
   };
   if (rows <= kCacheDecodeRows)
     return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8>, 1) : go(fwd_cache_merge_kernel<128, 1, 8>, 1);
-  return d == 64 ? go(fwd_cache_merge_kernel<64, 4, 2>, 4) : go(fwd_cache_merge_kernel<128, 4, 2>, 4);
+  return d == 64 ? go(fwd_cache_merge_kernel<64, 4, 4>, 4) : go(fwd_cache_merge_kernel<128, 4, 4>, 4);
 }
 
 size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }

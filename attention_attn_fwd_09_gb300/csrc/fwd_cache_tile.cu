@@ -84,18 +84,19 @@ enum {
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
 constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 widening warps
 
-// sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0, in O(log) steps.
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum_{i=0}^{n-1} floor((a i + b) / m) in O(log) steps, for a n + b < 2^32 (64-bit divisions made a
+// CTA's start 4 us longer).
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long s = 0;
   while (n > 0) {
-    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    s += (long long)(n - 1) * n / 2 * (a / m) + (long long)n * (b / m);
     a %= m;
     b %= m;
-    const long long y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -106,24 +107,23 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
 // rt qu + qu - 1, qu = 256 / g.  Work is counted in steps: a unit's blocks and `cost` steps before
 // them (CTAs with many short units took 1.4 times as long when blocks alone were counted).
 struct TileSeq {
-  int q0, n, len;
-  long long units;
+  int q0, n, len, units;
   __device__ __forceinline__ TileSeq(const CacheParams& p, int b, int qu) {
     q0 = __ldg(p.cu_q + b);
     n = __ldg(p.cu_q + b + 1) - q0;
     len = __ldg(p.kv_lens + b);
-    units = (n + qu - 1) / qu;
+    units = (int)(((unsigned)max(n, 0) + qu - 1) / qu);
   }
   __device__ __forceinline__ int blocks(const CacheParams& p, int qu, int rt) const {
     const int lim = p.causal ? len - n + min(n, (rt + 1) * qu) : len;
     return (max(lim, 1) + 127) / 128;
   }
   // Blocks of the units before rt (a unit without keys counts as one).
-  __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, long long rt) const {
+  __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, int rt) const {
     if (rt <= 0) return 0;
-    if (!p.causal) return rt * ((max(len, 1) + 127) / 128);
-    if (rt < units) return floor_sum(rt, 128, qu, (long long)(len - n) + qu + 127);
-    return floor_sum(units - 1, 128, qu, (long long)(len - n) + qu + 127) + (len + 127) / 128;
+    if (!p.causal) return (long long)rt * ((max(len, 1) + 127) / 128);
+    if (rt < units) return floor_sum(rt, 128, qu, (uint32_t)(len - n) + qu + 127);
+    return floor_sum(units - 1, 128, qu, (uint32_t)(len - n) + qu + 127) + (len + 127) / 128;
   }
 };
 
@@ -293,14 +293,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
     long long at = before;
     for (;;) {
       const TileSeq s(p, b, qu);
-      auto steps_before = [&](long long rt) -> long long { return s.blocks_before(p, qu, rt) + rt * cost; };
+      auto steps_before = [&](int rt) -> long long { return s.blocks_before(p, qu, rt) + (long long)rt * cost; };
       const long long per_head = steps_before(s.units);
       if (rs < at + per_head * p.Hkv) {
         const int h = (int)((rs - at) / per_head);
         at += h * per_head;
-        long long lo = 0, hi = s.units - 1;            // the last rt whose first step is <= rs
+        int lo = 0, hi = s.units - 1;                  // the last rt whose first step is <= rs
         while (lo < hi) {
-          const long long mid = (lo + hi + 1) / 2;
+          const int mid = lo + (hi - lo + 1) / 2;
           if (at + steps_before(mid) <= rs) lo = mid;
           else hi = mid - 1;
         }
