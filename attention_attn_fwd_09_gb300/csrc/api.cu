@@ -930,12 +930,12 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
       !aligned4(kv_lens) || !aligned4(lse))
     return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets, lengths and lse must be 4-byte aligned");
   const DevSyms* s = dev_syms(nullptr);
-  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
-  const int sms = std::max(1, s->sms);
+  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
   const size_t need = cache_workspace_bytes(Hq, Hkv, max_q, d, sms);
-  if (need > 0 && (!workspace || workspace_bytes < need))
+  if (!workspace || workspace_bytes < need)
     return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
-  if (need > 0 && !aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  if (!aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   CacheParams p{};
   p.q = q;
   p.k_cache = static_cast<const uint8_t*>(k_cache);

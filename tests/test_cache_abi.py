@@ -75,6 +75,8 @@ def test_attend_refusals(A):
         assert attend(A, **bad) == -1, bad
     assert attend(A, q=ctypes.c_void_p(0x10008)) == -3 and attend(A, o=ctypes.c_void_p(0x10008)) == -3
     assert attend(A, Hq=65536, H=2) == -2
+    assert attend(A, Hq=514, H=2) == -2                         # more than 256 query heads per K/V head
+    assert attend(A, ws=None) == -4 and attend(A, wsn=64) == -4 and attend(A, ws=ctypes.c_void_p(0x10008)) == -3
 
 
 def test_workspace_size_refusals(A):

@@ -299,6 +299,46 @@ def test_shared_pages_and_loose_bound(A):
     run_check(A, c, max_q=3)
 
 
+@pytest.mark.parametrize("heads,n", [((17, 1), 1), ((130, 1), 2), ((256, 1), 1), ((256, 1), 3), ((384, 2), 1), ((85, 1), 4)])
+def test_wide_groups(A, heads, n):
+    """Groups wider than a 128-row tile, and sizes that leave rows of a 256-row unit unused."""
+    run_check(A, filled([n, 129, 300], [n] * 3, *heads, 32, 64, seed=heads[0]))
+
+
+@pytest.mark.parametrize("n,B", [(1, 900), (6, 150)])
+def test_many_sequences(A, n, B):
+    """More sequences than threads, with and without queries."""
+    rng = np.random.RandomState(B)
+    lens = rng.randint(n, 60, B)
+    ns = np.where(rng.rand(B) < 0.3, 0, rng.randint(1, n + 1, B))
+    run_check(A, filled(lens.tolist(), ns.tolist(), 4, 1, 16, 64, seed=B))
+
+
+def test_nothing_to_do(A):
+    c = filled([40, 7], [2, 0], 4, 2, 16, 64)
+    empty = dict(c, q=c["q"][:, :0], cu=np.zeros(3, np.int32))
+    o, lse = attend(A, empty, max_q=1)
+    assert o.shape == (4, 0, 64) and lse.shape == (4, 0)
+
+
+def test_debug_synchronisation_reports_bad_offsets(A):
+    """sync_check: the call itself raises what the device check found."""
+    c = filled([40, 50], [20, 3], 4, 2, 16, 64, seed=1)
+    A.attn_set_debug_knobs(sync_check=True)
+    try:
+        attend(A, c)
+        with pytest.raises(A.AttnError) as e:
+            attend(A, dict(c, lens=np.array([10, 50], np.int32)))            # fewer keys than queries
+        assert e.value.code == INVALID
+        A.attn_device_status(True)
+        with pytest.raises(A.AttnError) as e:
+            attend(A, dict(c, table=c["table"] + 1000))
+        assert e.value.code == INVALID and "page table" in str(e.value)
+    finally:
+        A.attn_set_debug_knobs()
+        A.attn_device_status(True)
+
+
 def test_bad_offsets_and_pages(A):
     c = filled([40, 50], [2, 3], 4, 2, 16, 64, seed=1)
     for key, val in (("cu", [0, 2, 4]), ("cu", [1, 2, 5]), ("cu", [0, 6, 5]), ("lens", [1, 50]), ("lens", [40, 65 + 16]),
@@ -369,9 +409,36 @@ def test_streams(A):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-def test_two_calls_at_once(A):
+@pytest.mark.parametrize("n", [1, 70])
+def test_graph_with_growing_lengths(A, n):
+    """Captured once with its buffers, replayed on other queries and longer sequences: what eager
+    calls give, bit for bit, for both kernels."""
+    c = filled([900, 300, 1500], [n] * 3, 8, 2, 64, 128, seed=31)
+    q, lens = c["q"].to(DEV), dev(c["lens"] - 200)
+    cache = [dev(c[k]) for k in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "cu")]
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(A.attn_fwd_kv_fp8_workspace_size(3, 8, 2, 3 * n, n, 128), dtype=torch.uint8, device=DEV)
+    call = lambda **kw: A.attn_fwd_kv_fp8(q, *cache, lens, n, **kw)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(o=o, lse=lse, workspace=ws)
+        call(o=o, lse=lse, workspace=ws)                   # a workspace serves one call after another
+    for step in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        want = call()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        check(o, lse, reference(dict(c, q=q.cpu(), lens=lens.cpu().numpy())), 128)
+        q.copy_(torch.randn(q.shape).to(torch.bfloat16))
+        lens += 100
+        ws.fill_(0xFF)
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_two_calls_at_once(A, n):
     """Two streams, each with its own workspace."""
-    cs = [filled([4000, 2000], [1, 1], 8, 2, 64, 128, seed=20 + i) for i in range(2)]
+    cs = [filled([4000, 2000], [n, n], 8, 2, 64, 128, seed=20 + i) for i in range(2)]
     want = [attend(A, c) for c in cs]
     args = [[c["q"].to(DEV)] + [dev(c[k]) for k in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "cu", "lens")] for c in cs]
     streams = [torch.cuda.Stream() for _ in cs]
@@ -379,7 +446,7 @@ def test_two_calls_at_once(A):
     got = [None, None]
     for _ in range(20):
         for i, s in enumerate(streams):
-            got[i] = A.attn_fwd_kv_fp8(*args[i], 1, stream=s)
+            got[i] = A.attn_fwd_kv_fp8(*args[i], n, stream=s)
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
