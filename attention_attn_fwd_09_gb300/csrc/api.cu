@@ -950,6 +950,7 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   p.ws = workspace;
   p.wait_ns = (unsigned long long)g_wait_ns.load();
   p.status = s->status;
+  p.test_skip_first_kv = g_test_skip_kv.load();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool few = (long long)max_q * p.g <= kCacheDecodeRows;

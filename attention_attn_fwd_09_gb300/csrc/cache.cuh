@@ -4,6 +4,8 @@
 
 #include <cuda_fp16.h>
 
+#include "kernels.h"
+
 namespace attn {
 
 // Two e4m3 codes (low byte -> low half) as f16, exact.
@@ -53,5 +55,9 @@ __host__ __device__ inline CacheWs cache_ws(int ctas, int rows, int d) {
   w.total = w.part + (size_t)ctas * 2 * rows * d * 4;
   return w;
 }
+
+// How long a CTA that gives up waits for its own copies and products in flight: not less than 10 ms,
+// however short a wait may be.
+__device__ __forceinline__ unsigned long long drain_ns(const CacheParams& p) { return max(p.wait_ns, 10000000ull); }
 
 }  // namespace attn

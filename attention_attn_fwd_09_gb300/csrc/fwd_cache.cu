@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     pages[i] = page_at();
     heads[i] = ahead.h;
     if (i < C::STAGES) {
-      if (ahead.f < re) issue(i, pages[i]);
+      if (ahead.f < re && !(p.test_skip_first_kv && i == 0)) issue(i, pages[i]);
       ahead.f += kWarps;
       ahead.settle(p, re);
     }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int st = stage + k < C::STAGES ? stage + k : stage + k - C::STAGES;
           const uint32_t par = stage + k < C::STAGES ? phase : phase ^ 1u;
           if (f + (long long)k * kWarps < re)
-            while (!mbar_try_wait(bars + 8 * st, par) && globaltimer_ns() - t0 < p.wait_ns) {
+            while (!mbar_try_wait(bars + 8 * st, par) && globaltimer_ns() - t0 < drain_ns(p)) {
             }
         }
         __syncwarp();

@@ -368,9 +368,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (n_k >= C::NK && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) { ok = false; break; }
           g2 = g1;
           g1 = group++;
-          if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
-          __syncwarp();
-          if (pg >= 0) tma_load_3d(sbase + C::OFF_K + ks * C::K8 + lane * box_bytes, &tm_k, 0, 0, z, BAR(T_KFULL + ks));
+          if (n_k > 0 || !p.test_skip_first_kv) {
+            if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
+            __syncwarp();
+            if (pg >= 0) tma_load_3d(sbase + C::OFF_K + ks * C::K8 + lane * box_bytes, &tm_k, 0, 0, z, BAR(T_KFULL + ks));
+          }
           ++n_k;
           if (n_v >= C::NV8 && !warp_wait(BAR(T_V8FREE + vs), (n_v / C::NV8 - 1) & 1, wc)) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(BAR(T_V8FULL + vs), bytes);
@@ -384,10 +386,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (lane == 0) {
         const unsigned long long t0 = globaltimer_ns();
         for (uint32_t i = n_k > C::NK ? n_k - C::NK : 0; i < n_k; ++i)
-          while (!mbar_try_wait(BAR(T_KFULL + (i % C::NK)), (i / C::NK) & 1) && globaltimer_ns() - t0 < p.wait_ns) {
+          while (!mbar_try_wait(BAR(T_KFULL + (i % C::NK)), (i / C::NK) & 1) && globaltimer_ns() - t0 < drain_ns(p)) {
           }
         for (uint32_t i = n_v > C::NV8 ? n_v - C::NV8 : 0; i < n_v; ++i)
-          while (!mbar_try_wait(BAR(T_V8FULL + (i % C::NV8)), (i / C::NV8) & 1) && globaltimer_ns() - t0 < p.wait_ns) {
+          while (!mbar_try_wait(BAR(T_V8FULL + (i % C::NV8)), (i / C::NV8) & 1) && globaltimer_ns() - t0 < drain_ns(p)) {
           }
       }
     } else if (warp <= 2) {
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         mma_commit(BAR(T_DONE + t));
         const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_try_wait(BAR(T_DONE + t), 0) && globaltimer_ns() - t0 < p.wait_ns) {
+        while (!mbar_try_wait(BAR(T_DONE + t), 0) && globaltimer_ns() - t0 < drain_ns(p)) {
         }
       }
     } else if (warp == 3) {

@@ -216,6 +216,7 @@ struct CacheParams {
   void* ws;
   unsigned long long wait_ns;
   int* status;
+  int test_skip_first_kv;    // test hook: each CTA never issues its first K copy
 };
 // Tensor maps over the codes as 128-byte lines, [num_pages * Hkv][page * d / 128][128], boxes of
 // 32 keys (a page of 16: 16 keys), 128-byte swizzle.

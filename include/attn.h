@@ -390,7 +390,7 @@ int attn_set_debug_knobs(float tau, int poly_per_16, long long wait_limit_ns, in
 int attn_get_debug_knobs(float* tau, int* poly_per_16, long long* wait_limit_ns, int* sync_check);
 
 /*
- * Test hook (off by default): skip_first_kv_load = 1 makes the forward's load warp never
+ * Test hook (off by default): skip_first_kv_load = 1 makes the forward (attn_fwd_kv_fp8 too) never
  * issue the first K tile of each CTA, so the consumer's bounded wait runs out, the CTA
  * gives up cleanly and the device status word reads ATTN_ERR_TIMEOUT.  Used to test the
  * timeout path without faulting anything.  No counterpart on the pages.

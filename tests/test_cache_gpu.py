@@ -10,7 +10,7 @@ from cache_cases import bf16, check, empty_cache, filled, offsets, page_tables
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-INVALID = -1
+INVALID, TIMEOUT = -1, -6
 
 
 @pytest.fixture(scope="module")
@@ -319,6 +319,25 @@ def test_nothing_to_do(A):
     empty = dict(c, q=c["q"][:, :0], cu=np.zeros(3, np.int32))
     o, lse = attend(A, empty, max_q=1)
     assert o.shape == (4, 0, 64) and lse.shape == (4, 0)
+
+
+@pytest.mark.parametrize("n", [1, 80])
+def test_a_wait_that_runs_out(A, n):
+    """The first K copy of every CTA is never issued: the waits end, the status says so, and the
+    next call is right."""
+    c = filled([700, 300], [n, n], 8, 2, 64, 128, seed=17)
+    want = attend(A, c)
+    torch.cuda.synchronize()
+    A.attn_set_debug_knobs(wait_limit_ns=20_000_000)
+    A.attn_set_test_hooks(True)
+    try:
+        attend(A, c)
+        assert A.attn_device_status(True) == TIMEOUT
+    finally:
+        A.attn_set_test_hooks(False)
+        A.attn_set_debug_knobs()
+    got = attend(A, c)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_debug_synchronisation_reports_bad_offsets(A):
