@@ -742,6 +742,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto scale_of = [&](int pg) -> float { return pg >= 0 ? __ldg(p.v_scale + (long long)pg * p.Hkv + h) : 0.f; };
       float sv_next = scale_of(page_of(0));
       int pg_next = page_of(1);
+      // Results of the unit before were staged in the V16 slots, each warp's on its own: all have left.
+      if (nu > 0 && !warp_wait(BAR(T_EPI), (nu - 1) & 1, wc)) { ok = false; break; }
       // V8 block -> f16 in the layout the PV product reads (64-column boxes, 128-byte swizzle).  Thread
       // pieces of 16 codes; each quarter-warp takes half of two adjacent 128-byte lines, so that its
       // loads and each of its two rounds of stores fall on eight distinct bank groups.

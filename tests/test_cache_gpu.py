@@ -385,6 +385,24 @@ def test_repeatable(A):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_units(A, d):
+    """Units of one to three key blocks behind one another in a CTA, over and over: no result of one
+    unit meets the values of the next."""
+    rng = np.random.RandomState(d)
+    lens = rng.randint(30, 380, 500)
+    c = filled(lens.tolist(), np.minimum(lens, rng.randint(17, 65, 500)).tolist(), 8, 2, 128, d, seed=d)
+    g = {k: dev(c[k]) for k in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "cu", "lens")}
+    q = c["q"].to(DEV)
+    call = lambda: A.attn_fwd_kv_fp8(q, g["k_cache"], g["v_cache"], g["k_scale"], g["v_scale"], g["table"], g["cu"],
+                                     g["lens"], 64)
+    o, lse = call()
+    check(o, lse, reference(c), d)
+    for _ in range(40):
+        o2, lse2 = call()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_pages_past_32_bits(A):
     """Pages whose byte offset passes 2^32 (and element offset 2^31)."""
     P, H, d = 128, 8, 128                                  # 128 KiB a page
