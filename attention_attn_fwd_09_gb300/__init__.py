@@ -519,6 +519,8 @@ def _rope(call, q, k, inv_freq, positions, interleaved, mscale, q_out, k_out, st
         ok = (ok and k.dtype is bf16 and k_out.dtype is bf16 and k.shape == kshape and k_out.shape == kshape
               and len(kshape) == dims and k.device == dev and k_out.device == dev and sk[-1] == 1 and so[-1] == 1)
         pk, pok = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if not ok:
         if kshape is not None and len(kshape) != dims:
             raise ValueError(f"k: expected as many dimensions as q, got {tuple(k.shape)}")

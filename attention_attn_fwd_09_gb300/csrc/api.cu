@@ -784,6 +784,7 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
   if (rot < 2 || rot > d || (rot & 1))
     return fail(ATTN_ERR_INVALID_ARG, "rot=%d must be even and between 2 and d=%d", rot, d);
   if (!std::isfinite(mscale)) return fail(ATTN_ERR_INVALID_ARG, "mscale must be finite");
+  if (N > 0x7fff0000) return fail(ATTN_ERR_INVALID_ARG, "N must stay below 2^31 - 65536");
   if ((long long)Hq + Hk > 65535) return fail(ATTN_ERR_INVALID_ARG, "Hq + Hk too large");
   if (B == 0 || N == 0) return ATTN_OK;
   if (!q || !q_out || !inv_freq || (Hk > 0 && (!k || !k_out))) return fail(ATTN_ERR_INVALID_ARG, "null pointer");

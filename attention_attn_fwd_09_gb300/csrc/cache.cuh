@@ -56,6 +56,27 @@ __host__ __device__ inline CacheWs cache_ws(int ctas, int rows, int d) {
   return w;
 }
 
+// NaN codes of V.  A weight of 0 does not silence them (0 NaN = NaN), so a key that only some of a
+// tile's queries see must not hold any: its NaN codes are set to 0 where they lie in shared memory,
+// and per column the first such key is noted.  A query sees the keys up to its own limit, so exactly
+// the queries whose limit lies behind the noted key are NaN in that column.
+__device__ __forceinline__ bool any_nan_code(const uint4& v) {
+  const uint32_t a = (v.x & 0x7f7f7f7fu) + 0x01010101u, b = (v.y & 0x7f7f7f7fu) + 0x01010101u;
+  const uint32_t c = (v.z & 0x7f7f7f7fu) + 0x01010101u, d = (v.w & 0x7f7f7f7fu) + 0x01010101u;
+  return ((a | b | c | d) & 0x80808080u) != 0;
+}
+// first[0 .. 15]: of the piece's 16 columns.
+__device__ __forceinline__ void take_nan_codes(uint8_t* piece, int key, int* first, int* any) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    if ((piece[i] & 0x7f) != 0x7f) continue;
+    piece[i] = 0;
+    atomicMin(first + i, key);
+    *any = 1;
+  }
+}
+constexpr int kNoKey = 0x7fffffff;
+
 // How long a CTA that gives up waits for its own copies and products in flight: not less than 10 ms,
 // however short a wait may be.
 __device__ __forceinline__ unsigned long long drain_ns(const CacheParams& p) { return max(p.wait_ns, 10000000ull); }

@@ -49,7 +49,8 @@ struct DecCfg {
   static constexpr int OFF_STAT = OFF_MERGE + 2 * SLOT;   // [2][8] float4 (m, m, l, l of rows i, i + 8), then [2] r
   static constexpr int OFF_BAR = OFF_STAT + 2 * 8 * 16 + 16;
   static constexpr int OFF_MISC = OFF_BAR + kWarps * STAGES * 8;
-  static constexpr int SMEM = OFF_MISC + 64;
+  static constexpr int OFF_NAN = OFF_MISC + 64;           // [D] first hidden key with a NaN value
+  static constexpr int SMEM = OFF_NAN + 4 * D;
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -95,13 +96,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int c = lane & 3, rq = lane >> 2;    // fragment column group and row
   long long* misc = reinterpret_cast<long long*>(smem + C::OFF_MISC);   // [4] warp sums / [0] b, [1] unit start
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 48);
+  int* first_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
+  int* any_nan = reinterpret_cast<int*>(smem + C::OFF_MISC + 52);
   const uint32_t bars = smem_u32(smem + C::OFF_BAR) + warp * C::STAGES * 8;
   const WaitCtl wc{p.wait_ns, p.status, abort_flag};
   const CacheWs W = cache_ws(gridDim.x, rows_max, D);
   char* ws = static_cast<char*>(p.ws);
   int4* rec = reinterpret_cast<int4*>(ws) + blockIdx.x;
+  if (tid < D) first_nan[tid] = kNoKey;
   if (tid == 0) {
     *abort_flag = 0;
+    *any_nan = 0;
     for (int i = 0; i < kWarps * C::STAGES; ++i) mbar_init(smem_u32(smem + C::OFF_BAR) + 8 * i, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -360,6 +365,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nb][i] *= ks[nb >> 1] * crow[i >> 1];
         if (partial) {
+          // V of a key that some queries do not see (its row: D / 16 pieces, for d = 64 half a line).
+          const int key = key0 + lane;
+          if (key >= min_lim && key < len && (lane < 16 ? got0 : got1)) {
+            const int line = D == 128 ? lane : lane >> 1, at = D == 128 ? 0 : (lane & 1) * 4;
+            uint8_t* row = ring + stage * 2 * C::KB + C::KB + line * 128;
+#pragma unroll 1
+            for (int x = 0; x < D / 16; ++x) {
+              uint8_t* piece = row + (((at + x) ^ (line & 7)) << 4);
+              if (any_nan_code(*reinterpret_cast<const uint4*>(piece))) {
+                take_nan_codes(piece, key, first_nan + x * 16, any_nan);
+                fence_proxy_async_smem();    // a copy into this stage comes next
+              }
+            }
+          }
+          __syncwarp();
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
@@ -514,10 +534,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
     __syncthreads();                         // the slots are free
+    const bool nan = *any_nan != 0;
+    if (nan && warp == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)            // o[j][i]: row i / 2, column see below
+#pragma unroll
+        for (int j = 0; j < C::NACC; ++j)
+          if (first_nan[c * (D / 4) + (i & 1) * (D / 8) + j] < lim[i >> 1]) o[j][i] = __int_as_float(0x7fffffff);
+    }
     if (warp >= 2) put(warp - 2);
     __syncthreads();
     if (warp < 2) take(warp);
     if (warp == 1) put(1);                   // only warp 1 has read this slot
+    if (nan && warp == 3) {
+      for (int i = lane; i < D; i += 32) first_nan[i] = kNoKey;
+      if (lane == 0) *any_nan = 0;
+    }
     __syncthreads();
     if (warp == 0) {
       take(1);

@@ -195,7 +195,10 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  *   q, o [Hq, total_q, d] bf16; lse [Hq, total_q] fp32 (natural log); cu_seqlens_q as
  *       attn_fwd_varlen; the cache as above.
  *   max_q: an upper bound on the queries of one sequence (1 when decoding).
- *   scales finite and >= 0.  Codes of rows behind kv_lens[b] are never used, whatever they are.
+ *   scales finite and >= 0 (of pages in use; V scales best within 2^20 of each other).
+ *   Codes of rows behind kv_lens[b] are never used, whatever they are, and a NaN in the cache
+ *   reaches the queries that see its row, no others.
+ *   Hq / Hkv up to 256.
  *   A query that sees no key (kv_lens[b] = 0, not causal) gets O = 0 and LSE = -inf.
  *   workspace: device memory of attn_fwd_kv_fp8_workspace_size(...) bytes, 16-byte aligned, owned
  *       by the caller, contents on entry irrelevant.

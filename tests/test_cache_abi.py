@@ -32,6 +32,7 @@ def test_rope_refusals(A, fn):
                 dict(qo=FAKE, strides=[0, 64, 128, 0, 64, 64, 0, 256, 64, 0, 64, 64])):   # in place, other strides
         assert rope(A, fn=fn, **bad) == -1, bad
         assert A.attn_last_error()
+    assert rope(A, fn=fn, N=0x7fffffff, Hq=1, Hk=0) == -1
     assert rope(A, fn=fn, q=HALF) == -3
     assert rope(A, fn=fn, f=ctypes.c_void_p(0x10004)) == -3
     assert rope(A, fn=fn, pos=ODD) == -3

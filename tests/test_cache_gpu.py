@@ -269,6 +269,52 @@ def test_nonfinite_keys_and_queries(A, n):
     assert torch.equal(o[ok], o2[ok]) and torch.equal(lse[ok], lse2[ok])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("n,heads,lens", [
+    (5, (6, 2), [9, 40, 129, 600]),        # few rows
+    (16, (1, 1), [16, 47, 3000, 31]),
+    (40, (6, 2), [40, 90, 600, 130]),      # tiles
+    (300, (2, 2), [300, 513, 2700, 300]),  # several units of queries, cut between CTAs
+])
+def test_nan_keys_and_values_that_some_queries_do_not_see(A, n, heads, lens, P, d):
+    """NaN in keys and values: the queries that see the row are NaN (a value: in its column), the
+    others' results are the ones without it, bit for bit."""
+    Hq, H = heads
+    g = Hq // H
+    clean = filled(lens, [n] * len(lens), Hq, H, P, d, seed=n)
+    c = dict(clean, k_cache=clean["k_cache"].copy(), v_cache=clean["v_cache"].copy())
+    clean["v_cache"] = clean["v_cache"].copy()
+    want = torch.zeros(Hq, n * len(lens), d, dtype=torch.bool)
+    want_lse = torch.zeros(Hq, n * len(lens), dtype=torch.bool)
+    rng = np.random.RandomState(n + P)
+    # (sequence, key from the end, K/V head, column, in K)
+    spots = [(0, 0, 0, 3, False), (0, 2, H - 1, d - 1, False), (0, n - 1, 0, 17, False), (1, n // 2, 0, 0, False),
+             (1, n // 2, 0, 1, False), (2, 1, 0, 5, True), (2, n // 2, H - 1, 40, False), (2, lens[2] - 1, H - 1, 31, False),
+             (2, lens[2] // 2, 0, 32, False)] + [(2, int(rng.randint(n)), 0, int(rng.randint(d)), False) for _ in range(4)]
+    for b, back, h, col, in_k in spots:
+        key = lens[b] - 1 - back
+        page, row = c["table"][b, key // P], key % P
+        c["k_cache" if in_k else "v_cache"][page, h, row, col] = 0x7F if col & 1 else 0xFF
+        if not in_k:
+            clean["v_cache"][page, h, row, col] = 0
+        sees = np.arange(n) + lens[b] - n >= key
+        for hq in range(h * g, (h + 1) * g):
+            rows = torch.arange(b * n, (b + 1) * n)[torch.from_numpy(sees)]
+            if in_k:
+                want[hq, rows] = True
+                want_lse[hq, rows] = True
+            else:
+                want[hq, rows, col] = True
+    o, lse = attend(A, c)
+    o0, lse0 = attend(A, clean)
+    assert not torch.isnan(o0).any()
+    assert torch.equal(torch.isnan(o).cpu(), want) and torch.equal(torch.isnan(lse).cpu(), want_lse)
+    assert torch.equal(o[~want.to(DEV)], o0[~want.to(DEV)]) and torch.equal(lse[~want_lse.to(DEV)], lse0[~want_lse.to(DEV)])
+    again, _ = attend(A, clean)            # nothing of it stays
+    assert torch.equal(again, o0)
+
+
 def test_rows_behind_the_last_key_do_not_matter(A):
     """Stale codes, NaN codes and scales in the cache where no sequence reads: the same bits."""
     for n, lens in ((1, [1, 17, 130]), (50, [50, 77, 200])):

@@ -229,3 +229,12 @@ def test_rows_past_32_bits(A):
     check(y[None], x[None], f, np.arange(n)[None], False, 1.0, False)
     z, _ = A.attn_rope(y, None, f, q_out=buf.as_strided((1, n, 64), (64, step, 1), 128))
     check(z[None], y[None], f, np.arange(n)[None], False, 1.0, False)
+
+
+def test_an_output_for_no_k_is_refused(A):
+    q = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    f, _ = A.attn_rope_freqs(64)
+    with pytest.raises(ValueError, match="k_out"):
+        A.attn_rope(q, None, f, k_out=torch.empty_like(q))
+    q_out, none = A.attn_rope(q, None, f)
+    assert none is None and torch.equal(q_out, q)
