@@ -689,12 +689,14 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
 
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
   int shift = 0;
-  while ((1 << shift) < rows) ++shift;
+  while ((1 << shift) < rows && (1 << shift) < (long long)p.max_q * p.g) ++shift;     // rows in use
   auto go = [&](auto kernel, int cpt) {
     const dim3 grid((unsigned)ctas, (unsigned)((((d / 4 / cpt) << shift) + 127) / 128));
     return launch_pdl(kernel, grid, dim3(128), 0, s, p, rows, shift, ctas);
   };
-  if (rows <= kCacheDecodeRows)
+  // Few units of many partials each: latency again.
+  const long long units = (long long)p.B * p.Hkv * (((long long)p.max_q * p.g + rows - 1) / rows);
+  if (rows <= kCacheDecodeRows || units * 4 <= ctas)
     return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8>, 1) : go(fwd_cache_merge_kernel<128, 1, 8>, 1);
   return d == 64 ? go(fwd_cache_merge_kernel<64, 4, 4>, 4) : go(fwd_cache_merge_kernel<128, 4, 4>, 4);
 }

@@ -41,15 +41,16 @@ constexpr float kTau = 8.f;                  // rescale when a maximum grows by 
 constexpr int kUnitCost = 5;                 // at most what starting and ending a unit counts for, in key blocks
 constexpr float kMinFactor = 1e-30f;         // keeps -inf * factor = -inf for pages whose scale is 0
 
-template <int D>
+template <int D, bool SPLIT>
 struct TileCfg {
   static constexpr uint32_t Q8 = 128 * D;          // one e4m3 tile of Q
   static constexpr uint32_t K8 = 128 * D;          // 128 keys of e4m3 K or V
   static constexpr uint32_t CH16 = 128 * 128;      // 128 keys x 64 f16 columns (a swizzled box)
   static constexpr uint32_t V16 = (D / 64) * CH16;
-  static constexpr int NK = 2, NV8 = 3, NV16 = 2;
-  static constexpr uint32_t OFF_Q = 0;             // [tile][Q1, Q2]
-  static constexpr uint32_t OFF_K = OFF_Q + 4 * Q8;
+  static constexpr int NK = SPLIT ? 4 : 2, NV8 = 3, NV16 = 2;   // ring slots
+  static constexpr uint32_t OFF_Q = 0;             // [tile][Q1, Q2] (SPLIT: one tile's)
+  static constexpr uint32_t OFF_K = OFF_Q + (SPLIT ? 2 : 4) * Q8;
+  static constexpr int RELS = SPLIT ? 16 : 8;      // release barriers: more than the groups that K's ring spans
   static constexpr uint32_t OFF_V8 = OFF_K + NK * K8;
   static constexpr uint32_t OFF_V16 = OFF_V8 + NV8 * K8;
   static constexpr uint32_t OFF_CTRL = OFF_V16 + NV16 * V16;
@@ -69,18 +70,18 @@ enum {
   T_OFULL = 6,     // +t: the unit's last PV of tile t complete
   T_OFREE = 8,     // +t: O_t read out of tensor memory (128)
   T_FIN = 10,      // +t: the unit's final statistics written (128)
-  T_KFULL = 12,    // +slot (2)
-  T_V8FULL = 14,   // +slot (3)
-  T_V8FREE = 17,   // +slot (3): widened (128)
-  T_V16FULL = 20,  // +slot (2): widened (128)
-  T_REL = 22,      // +(group & 7): both issuers' products of a group (S of block j, PV of block j - 1) complete
-  T_EPI = 30,      // the unit's results written (128)
-  T_UFULL = 31,    // +slot (4): unit descriptor written
-  T_UFREE = 35,    // +slot (4): every role is through with the unit (15 warps)
-  T_DONE = 39,     // +t
-  T_TURN = 41,     // +t: the other tile's products of a group have been issued
-  T_PHALF = 43,    // +t: P of the block's first 64 keys written and O rescaled (128)
-  T_COUNT = 45
+  T_KFULL = 12,    // +slot (up to 4)
+  T_V8FULL = 16,   // +slot (3)
+  T_V8FREE = 19,   // +slot (3): widened (128)
+  T_V16FULL = 22,  // +slot (2): widened (128)
+  T_EPI = 24,      // the unit's results written (128)
+  T_UFULL = 25,    // +slot (4): unit descriptor written
+  T_UFREE = 29,    // +slot (4): every role is through with the unit (15 warps)
+  T_DONE = 33,     // +t
+  T_TURN = 35,     // +t: the other tile's products of a group have been issued
+  T_PHALF = 37,    // +t: P of the block's first 64 keys written and O rescaled (128)
+  T_REL = 39,      // +(group mod 8 or 16): both issuers' products of the group complete
+  T_COUNT = 55
 };
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
 constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 widening warps
@@ -131,7 +132,7 @@ struct TileSeq {
 // A unit as the roles see it (shared memory, written by the scheduler warp).
 struct __align__(16) UnitDesc {
   int nmax;                                  // key blocks here: of the longer tile (-1: no more units)
-  int nt[2];                                 // and of each tile
+  int nt[2];                                 // and of each tile (SPLIT: its share of them)
   int kt0;                                   // first key block here
   int len;                                   // the sequence's keys
   int b, h;
@@ -178,11 +179,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 
 // NG: groups of columns of a key block that may have scales of their own (1: a page holds the
 // block; 8: 16 keys each).
-template <int D, int NG>
+template <int D, int NG, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const CacheParams p) {
-  using C = TileCfg<D>;
+  using C = TileCfg<D, SPLIT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id(), wg = warp >> 2;
   const int qu = kTRows / p.g;                               // queries per unit
+  constexpr int LAG = SPLIT ? 2 : 1;                         // groups from a block's S to its PV
   const WaitCtl wc{p.wait_ns, p.status, abort_flag};
   const CacheWs W = cache_ws(gridDim.x, kTRows, D);
   char* ws = static_cast<char*>(p.ws);
@@ -221,7 +223,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(BAR(T_OFULL + t), 1);
       mbar_init(BAR(T_OFREE + t), 128);
       mbar_init(BAR(T_FIN + t), 128);
-      mbar_init(BAR(T_KFULL + t), 1);
       mbar_init(BAR(T_DONE + t), 1);
       mbar_init(BAR(T_TURN + t), 1);
     }
@@ -229,7 +230,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(BAR(T_V8FULL + s), 1);
       mbar_init(BAR(T_V8FREE + s), 128);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(BAR(T_REL + i), 2);
+    for (int i = 0; i < C::NK; ++i) mbar_init(BAR(T_KFULL + i), 1);
+    for (int i = 0; i < C::RELS; ++i) mbar_init(BAR(T_REL + i), 2);
     *abort_flag = 0;
     any_nan[0] = any_nan[1] = 0;
     fence_mbar_init();
@@ -330,6 +332,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int page_shift = 31 - __clz(p.page);
   // The roles' view of unit u: wait for its descriptor, and hand it back (one lane per warp).
   auto unit_ready = [&](uint32_t u) -> bool { return mbar_wait(BAR(T_UFULL + u % kUnitSlots), (u / kUnitSlots) & 1, wc); };
+  // Release barrier of a product group, and its phase.
+  auto rel = [&](uint32_t group) -> uint32_t { return BAR(T_REL + group % C::RELS); };
+  auto rel_phase = [&](uint32_t group) -> uint32_t { return group / C::RELS & 1; };
   auto unit_done = [&](uint32_t u) { mbar_arrive(BAR(T_UFREE + u % kUnitSlots)); };
 
   // Register split against the launch's 128 x 512: producer and MMA 64; softmax 184 each;
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int boxes = max(1, 128 >> page_shift), box_keys = min(p.page, 128);
       const uint32_t box_bytes = box_keys * D;
       uint32_t n_k = 0, n_v = 0;             // K, V blocks loaded so far
-      uint32_t group = 0, g1 = 0, g2 = 0;    // product group of the next block; of the last two blocks
+      uint32_t group = 0, g[C::NK] = {};     // product group of the next block's S; of the last blocks'
       bool ok = true;
       for (uint32_t nu = 0; ok; ++nu) {
         if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
@@ -369,10 +374,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pg >= 0)) * box_bytes;
           const int z = pg * p.Hkv + h;
           const int ks = (int)(n_k % C::NK), vs = (int)(n_v % C::NV8);
-          // The slot's block, two before this one, was read by the products of group g2.
-          if (n_k >= C::NK && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) { ok = false; break; }
-          g2 = g1;
-          g1 = group++;
+          // The slot's block, NK before this one, was read by the products of group g[NK - 1].
+          if (n_k >= C::NK && !warp_wait(rel(g[C::NK - 1]), rel_phase(g[C::NK - 1]), wc)) { ok = false; break; }
+#pragma unroll
+          for (int i = C::NK - 1; i > 0; --i) g[i] = g[i - 1];
+          g[0] = group++;
           if (n_k > 0 || !p.test_skip_first_kv) {
             if (lane == 0) mbar_arrive_expect_tx(BAR(T_KFULL + ks), bytes);
             __syncwarp();
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (pg >= 0) tma_load_3d(sbase + C::OFF_V8 + vs * C::K8 + lane * box_bytes, &tm_v, 0, 0, z, BAR(T_V8FULL + vs));
           ++n_v;
         }
-        if (nmax > 0) ++group;               // the last PV is a group of its own
+        if (nmax > 0) group += LAG;          // the last PVs are groups of their own
       }
       // Every copy has landed before the shared memory goes away, also when a wait ran out.
       if (lane == 0) {
@@ -405,9 +411,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int t = warp - 1;
         bool ok = true;
         uint32_t nk = 0, nv = 0, np = 0, no = 0, group = 0;   // blocks, V blocks, P phases used; units with a PV
+        uint32_t nq = 0;                     // SPLIT: units with keys (tile 1 may have none of them)
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
         const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
-        const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + 2 * t * C::Q8, 16);
+        const uint32_t q_lo = sdesc_sw128_lo(sbase + C::OFF_Q + (SPLIT ? 0 : 2 * t * C::Q8), 16);
         for (uint32_t nu = 0; ok; ++nu) {
           if (!unit_ready(nu)) { ok = false; break; }
           const UnitDesc& U = desc[nu % kUnitSlots];
@@ -415,14 +422,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
           unit_done(nu);
           if (nmax < 0) break;
           if (nmax == 0) continue;
-          for (int j = 0; j <= nmax; ++j, ++group) {
-            const bool pv = j >= 1 && j <= n_t, sp = j < n_t;
+          const uint32_t q_phase = SPLIT ? nq++ : no;
+          for (int j = 0; j < nmax + LAG; ++j, ++group) {
+            const bool pv = SPLIT ? j >= 2 && (j & 1) == t : j >= 1 && j <= n_t;
+            const bool sp = SPLIT ? j < nmax && (j & 1) == t : j < n_t;
+            const int j_own = SPLIT ? j >> 1 : j;      // step of this tile
             const uint32_t vs = nv % C::NV16, ks = nk % C::NK;
             // P is the last to come.  (K also for a tile through with its blocks: it must not run ahead of the other.)
             if (j < nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
-            if (j == 0 && sp && !mbar_wait(BAR(T_Q + t), no & 1, wc)) { ok = false; break; }
+            if (j_own == 0 && sp && !mbar_wait(BAR(T_Q + (SPLIT ? 0 : t)), q_phase & 1, wc)) { ok = false; break; }
             if (pv) {
-              if (j == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
+              if (j_own == 1 && no > 0 && !mbar_wait(BAR(T_OFREE + t), (no - 1) & 1, wc)) { ok = false; break; }
               if (!mbar_wait(BAR(T_V16FULL + vs), (nv / C::NV16) & 1, wc)) { ok = false; break; }
               if (!mbar_wait(BAR(T_PHALF + t), np & 1, wc)) { ok = false; break; }
             }
@@ -436,13 +446,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
               // The first half of the keys while the softmax works on the second.
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j > 1 || kk > 0) ? 1u : 0u);
+                mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, (j_own > 1 || kk > 0) ? 1u : 0u);
               if (!mbar_wait(BAR(T_PFULL + t), np & 1, wc)) { ok = false; break; }
               ++np;
               tc_fence_after();
 #pragma unroll
               for (int kk = 4; kk < 8; ++kk) mma_ts_w(tO, tS + kk * 8, v_lo + kk * (2048 >> 4), HI, C::IDESC_PV, 1u);
-              if (j == n_t) {
+              if (j_own == n_t) {
                 mma_commit(BAR(T_OFULL + t));
                 ++no;
               }
@@ -457,8 +467,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             mbar_arrive(BAR(T_TURN + 1 - t));
             if (sp) mma_commit(BAR(T_SFULL + t));
-            mma_commit(BAR(T_REL + (group & 7)));
-            if (j >= 1) ++nv;
+            mma_commit(rel(group));
+            if (j >= LAG) ++nv;
             if (j < nmax) ++nk;
           }
         }
@@ -497,8 +507,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
           }
           U.nmax = max(nt[0], nt[1]);
-          U.nt[0] = nt[0];
-          U.nt[1] = nt[1];
+          U.nt[0] = SPLIT ? (nt[0] + 1) / 2 : nt[0];
+          U.nt[1] = SPLIT ? nt[0] / 2 : nt[1];
           U.kt0 = kt0;
           U.len = sq.len;
           U.b = b;
@@ -532,29 +542,34 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int t = wg - 1;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(t * 128);
-    const int r = t * 128 + row, qi = r / p.g;         // row of the unit, its query
-    uint32_t ns = 0;                         // S phases used
+    const int row0 = SPLIT ? 0 : t * 128, r = row0 + row, qi = r / p.g;      // row of the unit, its query
+    constexpr int STRIDE = SPLIT ? 256 : 128;          // keys from one of a tile's blocks to the next
+    uint32_t ns = 0, ns_other = 0;           // S phases used; SPLIT: by tile 1
     bool ok = true;
     for (uint32_t nu = 0; ok; ++nu) {
       if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
       const UnitDesc& U = desc[nu % kUnitSlots];
-      const int n_t = U.nt[t], kt0 = U.kt0, len = U.len, h = U.h, q0 = U.q0;
+      const int n_t = U.nt[t], kt0 = U.kt0 + (SPLIT ? t : 0), len = U.len, h = U.h, q0 = U.q0;
+      const int n_other = SPLIT ? U.nt[1] : 0;
       const bool more = U.nmax >= 0, live = r < U.rows;
       const int* table = p.table + (long long)U.b * p.max_pages;
       const int lim = (p.causal && live ? U.lim0 + qi : len) - kt0 * 128;                       // visible keys of this row,
-      const int min_lim = (p.causal ? U.lim0 + t * 128 / p.g : len) - kt0 * 128;                // of the tile's first row
+      const int min_lim = (p.causal ? U.lim0 + row0 / p.g : len) - kt0 * 128;                // of the tile's first row
       __syncwarp();
       if (lane == 0) unit_done(nu);
       if (!more) break;
       float c_row = 0.f;
       if (n_t > 0) {
-        // This tile's Q is free: every S of the unit before has been waited for.  Each warp brings its
+        // Q is free: every S of the unit before has been waited for (SPLIT: tile 1's too).  Each warp brings its
         // 32 rows, whole rows at a time (D / 8 lanes of 16 bytes each), QB steps' loads under way at once.
         constexpr int LPR = D / 8, RPS = 32 / LPR, QB = 4;          // lanes per row, rows per step
         // (rows that are not in use take the unit's first: loads without conditions).
         const long long at = live ? ((long long)(r - qi * p.g) * p.total_q + qi) * D : 0;    // this lane's own row
         const uint16_t* base = static_cast<const uint16_t*>(p.q) + ((long long)h * p.g * p.total_q + q0) * D + lane % LPR * 8;
-        uint8_t* q1 = smem + C::OFF_Q + 2 * t * C::Q8 + (warp & 3) * 32 * D;
+        uint8_t* q1 = smem + C::OFF_Q + (SPLIT ? 0 : 2 * t * C::Q8) + (warp & 3) * 32 * D;
+        if constexpr (SPLIT) {
+          if (t == 0 && ns_other > 0 && !warp_wait(BAR(T_SFULL + 1), (ns_other - 1) & 1, wc)) { ok = false; break; }
+        }
         uint32_t e_own = 0;
 #pragma unroll 1
         for (int i0 = 0; i0 < 32 / RPS; i0 += QB) {
@@ -591,18 +606,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             const int rw = (i0 + k) * RPS + lane / LPR, ch = lane % LPR;   // row of the warp's 32, 8-byte piece
             const int off = rw * D + (((ch >> 1) ^ (D == 128 ? (rw & 7) : ((rw >> 1) & 3))) << 4) + (ch & 1) * 8;
+            if (SPLIT && t > 0) continue;    // tile 1 wants the rows' factors only
             *reinterpret_cast<uint2*>(q1 + off) = make_uint2(c1[0], c1[1]);
             *reinterpret_cast<uint2*>(q1 + C::Q8 + off) = make_uint2(c2[0], c2[1]);
           }
         }
         c_row = p.c * (e_own >= 8 && e_own < 255 ? __uint_as_float((e_own - 7u) << 23) : 1.f);
         fence_proxy_async_smem();            // generic writes -> tensor-core reads
-        mbar_arrive(BAR(T_Q + t));
+        if (!SPLIT || t == 0) mbar_arrive(BAR(T_Q + t));
       }
+      if constexpr (SPLIT) ns_other += n_other;
       // K scales: lane & 7 looks after a group of 16 keys (all lanes after the one page when NG = 1);
       // pages one block further ahead than scales.
       auto page_of = [&](int j) -> int {
-        const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        const int key = kt0 * 128 + j * STRIDE + (NG > 1 ? (lane & 7) * 16 : 0);
         if (j >= n_t || key >= len) return -1;
         const int pg = __ldg(table + (key >> page_shift));
         return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
@@ -637,8 +654,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tmem_wait_ld();
         reg_fence(u);
         float* s = reinterpret_cast<float*>(u);
-        if (j * 128 + 128 > min_lim) {
-          const int vis = lim - j * 128;     // visible columns
+        if (j * STRIDE + 128 > min_lim) {
+          const int vis = lim - j * STRIDE;     // visible columns
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i >= vis) s[i] = -INFINITY;
@@ -738,6 +755,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int* table = p.table + (long long)U.b * p.max_pages;
       if (nmax < 0) break;                   // the last descriptor is not reused
       float rref = kMinScale;                // largest V scale so far
+      float rref_other = kMinScale;          // SPLIT: of the other tile's blocks (they take turns)
       auto page_of = [&](int j) -> int {
         const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
         if (j >= nmax || key >= len) return -1;
@@ -765,15 +783,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
         }
+        if constexpr (SPLIT) {
+          const float x = rref;
+          rref = rref_other;
+          rref_other = x;
+        }
         rref = fmaxf(rref, vmax);
         const float wgt = sv / rref * kVShift;
         const uint32_t w_mine = pack_f16x2(wgt, wgt);  // this lane's group's factor
         const uint32_t vs8 = nv % C::NV8, vs16 = nv % C::NV16;
         if (!warp_wait(BAR(T_V8FULL + vs8), (nv / C::NV8) & 1, wc)) return false;
         // The slot's block, two before this one, was read by the products of group g2.
-        if (nv >= C::NV16 && !warp_wait(BAR(T_REL + (g2 & 7)), (g2 >> 3) & 1, wc)) return false;
+        if (nv >= C::NV16 && !warp_wait(rel(g2), rel_phase(g2), wc)) return false;
         g2 = g1;
-        g1 = ++group;                        // PV of block j is in the group behind its S
+        g1 = group + LAG;                    // PV of block j
+        ++group;
         const uint8_t* src = smem + C::OFF_V8 + vs8 * C::K8;
         uint8_t* dst = smem + C::OFF_V16 + vs16 * C::V16;
         const int left = len - (kt0 + j) * 128;                    // keys that exist
@@ -824,7 +848,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (const int j_end = min(j_hid, nmax); ok && j < j_end; ++j) ok = widen(j, std::false_type());
       for (; ok && j < nmax; ++j) ok = widen(j, std::true_type());
       if (!ok) break;
-      if (nmax > 0) ++group;                 // the group of the unit's last PV
+      if (nmax > 0) group += LAG;            // the groups of the unit's last PVs
       // Epilogue per tile: O / l to its rows, or O and the statistics to the workspace.
       const bool whole = U.whole != 0;
       const int part = 2 * blockIdx.x + U.second, rows = U.rows, q0 = U.q0;
@@ -832,10 +856,39 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // Every product of both tiles is complete: O is final and V16 is free.
       if (nt0 > 0 && !warp_wait(BAR(T_OFULL), nof0++ & 1, wc)) { ok = false; break; }
       if (nt1 > 0 && !warp_wait(BAR(T_OFULL + 1), nof1++ & 1, wc)) { ok = false; break; }
+      if constexpr (SPLIT) {                 // tile 1's share of the keys into tile 0
+        if (!warp_wait(BAR(T_FIN), nu & 1, wc) || !warp_wait(BAR(T_FIN + 1), nu & 1, wc)) { ok = false; break; }
+        if (nt1 > 0) {
+          tc_fence_after();
+          float* st = fin + row;
+          const float m = fmaxf(st[0], st[384]), mu = m == -INFINITY ? 0.f : m, ref = fmaxf(st[256], st[640]);
+          const float w0 = ex2_mufu(st[0] - mu), w1 = ex2_mufu(st[384] - mu);
+          const float f0 = w0 * (st[256] / ref), f1 = w1 * (st[640] / ref);
+          st[128] = st[128] * w0 + st[512] * w1;
+          st[0] = m;
+          st[256] = ref;
+          const uint32_t tO = tmem + lane_off + 256u;
 #pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t x[16], y[16];
+            tmem_ld16(tO + q * 16, x);
+            tmem_ld16(tO + 128u + q * 16, y);
+            tmem_wait_ld();
+            reg_fence(x);
+            reg_fence(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+            tmem_st16(tO + q * 16, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(BAR(T_OFREE + 1));
+        }
+      }
+#pragma unroll 1
+      for (int t = 0; t < (SPLIT ? 1 : 2); ++t) {
         const int n_t = t ? nt1 : nt0;
-        if (!warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
+        if (!SPLIT && !warp_wait(BAR(T_FIN + t), nu & 1, wc)) { ok = false; break; }
         tc_fence_after();
         const float* st = fin + t * 384 + row;
         const float m = st[0], l = st[128], ref = st[256] / kVShift;
@@ -919,20 +972,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 }
 
-template <int D, int NG>
+template <int D, int NG, bool SPLIT>
 cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, cudaStream_t s) {
-  using C = TileCfg<D>;
+  using C = TileCfg<D, SPLIT>;
   static std::once_flag flags[64];
   static cudaError_t attr_err[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::call_once(flags[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
-  e = launch_pdl(fwd_cache_tile_kernel<D, NG>, dim3(grid), dim3(kTThreads), C::SMEM, s, maps.k, maps.v, p);
+  e = launch_pdl(fwd_cache_tile_kernel<D, NG, SPLIT>, dim3(grid), dim3(kTThreads), C::SMEM, s, maps.k, maps.v, p);
   if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, kTRows, grid, s);
 }
@@ -943,8 +996,16 @@ size_t cache_tile_workspace_bytes(int d, int sms) { return cache_ws(sms, kTRows,
 
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
   const bool one = p.page == 128;            // a key block has one scale
-  if (d == 64) return one ? launch_tile<64, 1>(maps, p, sms, s) : launch_tile<64, 8>(maps, p, sms, s);
-  return one ? launch_tile<128, 1>(maps, p, sms, s) : launch_tile<128, 8>(maps, p, sms, s);
+  const bool split = (long long)p.max_q * p.g <= 128;
+  auto go = [&](auto dim, auto groups) {
+    return split ? launch_tile<dim, groups, true>(maps, p, sms, s) : launch_tile<dim, groups, false>(maps, p, sms, s);
+  };
+  using I1 = std::integral_constant<int, 1>;
+  using I8 = std::integral_constant<int, 8>;
+  using I64 = std::integral_constant<int, 64>;
+  using I128 = std::integral_constant<int, 128>;
+  if (d == 64) return one ? go(I64(), I1()) : go(I64(), I8());
+  return one ? go(I128(), I1()) : go(I128(), I8());
 }
 
 }  // namespace attn

@@ -218,6 +218,19 @@ def test_long_and_many(A, case):
     run_check(A, filled(case["lens"], case["ns"], *case["heads"], 64, 128, seed=9))
 
 
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 32), (128, 128)])
+@pytest.mark.parametrize("heads,n", [((4, 1), 5), ((8, 1), 16), ((2, 1), 40), ((12, 1), 10)])
+def test_units_of_one_tile(A, heads, n, d, P):
+    """Up to 128 rows per sequence and K/V head: two tiles share a unit's key blocks, odd and even
+    numbers of them, cut between CTAs or not, alone and beside units of two tiles."""
+    lens = [n, 128, 129, 256, 257, 300, 640, 641, 5000]
+    run_check(A, filled(lens, [n] * len(lens), *heads, P, d, seed=n + P))
+    ns = [n, 128, 1, 200, 2, 0, n, 500, n]
+    run_check(A, filled(lens, ns, *heads, P, d, seed=n + P + 1))
+    run_check(A, filled([3, 130, 700, 0, 1500], [n] * 5, *heads, P, d, seed=n), causal=False)
+    run_check(A, filled([9001], [n], *heads, P, d, seed=n))
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_no_visible_key(A, n):
     """Sequences without keys (not causal): O = 0 and LSE = -inf; without queries: nothing."""
