@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(BAR(T_V8FREE + s), 128);
     }
     for (int i = 0; i < C::NK; ++i) mbar_init(BAR(T_KFULL + i), 1);
-    for (int i = 0; i < C::RELS; ++i) mbar_init(BAR(T_REL + i), 2);
+    for (int i = 0; i < C::RELS; ++i) mbar_init(BAR(T_REL + i), SPLIT ? 1 : 2);
     *abort_flag = 0;
     any_nan[0] = any_nan[1] = 0;
     fence_mbar_init();
@@ -411,6 +411,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int t = warp - 1;
         bool ok = true;
         uint32_t nk = 0, nv = 0, np = 0, no = 0, group = 0;   // blocks, V blocks, P phases used; units with a PV
+        uint32_t n_turn = 0;                 // SPLIT: turns taken
+        bool turn = false;                   // SPLIT, tile 0: the last group was tile 1's
         uint32_t nq = 0;                     // SPLIT: units with keys (tile 1 may have none of them)
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
         const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * 128);
@@ -427,6 +429,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool pv = SPLIT ? j >= 2 && (j & 1) == t : j >= 1 && j <= n_t;
             const bool sp = SPLIT ? j < nmax && (j & 1) == t : j < n_t;
             const int j_own = SPLIT ? j >> 1 : j;      // step of this tile
+            if (SPLIT && (j & 1) != t) {               // the other tile's group
+              if (j >= LAG) ++nv;
+              if (j < nmax) ++nk;
+              continue;
+            }
             const uint32_t vs = nv % C::NV16, ks = nk % C::NK;
             // P is the last to come.  (K also for a tile through with its blocks: it must not run ahead of the other.)
             if (j < nmax && !mbar_wait(BAR(T_KFULL + ks), (nk / C::NK) & 1, wc)) { ok = false; break; }
@@ -438,7 +445,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             // Tile 0's products of a group go before tile 1's: left alone, the tiles fall into step and
             // tensor cores and exponentials take turns instead of overlapping.
-            if (!mbar_wait(BAR(T_TURN + t), (group + 1 - t) & 1, wc)) { ok = false; break; }
+            // SPLIT: a group belongs to one tile; the unit's first is tile 0's, whoever had the last one.
+            if constexpr (SPLIT) {
+              if (j > 0 || turn) {
+                if (!mbar_wait(BAR(T_TURN + t), n_turn & 1, wc)) { ok = false; break; }
+                ++n_turn;
+              }
+            } else {
+              if (!mbar_wait(BAR(T_TURN + t), (group + 1 - t) & 1, wc)) { ok = false; break; }
+            }
             tc_fence_after();
             if (pv) {
               // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
@@ -465,7 +480,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 mma_ss_f8_w(tS, q_lo + (((kk / (D / 32)) * C::Q8 + (kk % (D / 32)) * 32) >> 4), C::QK_HI,
                             k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, C::IDESC_QK, kk > 0 ? 1u : 0u);
             }
-            mbar_arrive(BAR(T_TURN + 1 - t));
+            if (SPLIT) turn = j + 1 < nmax + LAG || t > 0;
+            if (!SPLIT || turn) mbar_arrive(BAR(T_TURN + 1 - t));
             if (sp) mma_commit(BAR(T_SFULL + t));
             mma_commit(rel(group));
             if (j >= LAG) ++nv;
