@@ -19,6 +19,10 @@
 //     (d = 64) rows is chosen so that under TMA's 128-byte swizzle both kinds of load touch
 //     every bank once.
 //
+// Measured (d = 128, 32 heads on 8, one query): 32 sequences of up to 32000 keys 355 us, 6.2 TB/s of
+// cache, 91 % of a copy's rate; 8 of 8192 keys 32.9 us in a graph, 4.1 TB/s (15 us of it are the
+// start, the first pieces' way from memory and the merge); one of 1024 keys 8.5 us in a graph.
+//
 // Numbers: q is scaled by a power of two per row (largest |q| in [1, 2)) and held in f16,
 // exact but for components 2^14 below the row's largest.  exp2(s - m + 14) <= 2^14 times the
 // page's V scale over the largest V scale so far is rounded to f16 (11 bits, against 8 of a

@@ -1,24 +1,42 @@
 // Attention of packed queries over a paged e4m3 cache: many query rows per K/V head (pieces of
-// prompts, long drafts).  fwd_cache.cu is the kernel for few rows.
+// prompts, drafts).  fwd_cache.cu is the kernel for up to 16 rows.
 //
-// A unit is 256 rows of one sequence and K/V head as two 128-row tiles: row r is query r / g,
+// A unit is up to 256 rows of one sequence and K/V head as two 128-row tiles: row r is query r / g,
 // head r % g of the group, so every tile is full whatever g is and the g heads share the K, V
-// they share.  What bounds it is tensor and exponential throughput, so it is the ping-pong of
-// fwd.cu (a TMA producer warp, one thread issuing tcgen05.mma, a softmax warpgroup per tile, a
-// correction warpgroup that rescales O only when a maximum grew by more than tau) with
+// they share.  What bounds it is the tensor cores and, behind them, each tile's own chain S ->
+// softmax -> P -> PV, so two tiles run half a turn apart and one's products cover the other's
+// softmax.  16 warps, a persistent CTA per SM:
+//   * producer: K, V codes by TMA, a box per page;
+//   * two MMA issuers, one per tile, that take turns (one thread for both lost 1000 cycles per block
+//     in its waits; two without turns fall into step).  A group of products is PV of one block and S
+//     of the next; its completion frees the slots that it read;
+//   * scheduler: walks the CTA's units and describes each in shared memory, four ahead (each role
+//     finding its own units by division cost 2 us per unit);
+//   * two softmax warpgroups, a row per thread.  They prepare Q, rescale O themselves when a maximum
+//     grew by more than tau or a larger V scale came (rare after the first blocks), and hand P over
+//     in two halves, so that PV begins before the second half's exponentials;
+//   * a warpgroup that widens V and writes the results.
+// Numbers:
 //   * S on the 8-bit tensor path, K's codes as they lie in the cache.  Q, scaled by a power of two
 //     per row (largest |q| in [128, 256)), is the sum of two e4m3 tiles, Q1 = e4m3(q) and
 //     Q2 = e4m3(q - Q1): bf16 has 8 significant bits and e4m3 4, so the sum is q itself down to
 //     2^-9 of the row's largest component and off by at most 2^-18 of that below.  Both products
 //     together cost what one 16-bit product costs, and K needs no widening;
-//   * V widened to f16 by the correction warpgroup between its rescales, times its page's scale
-//     over the largest V scale so far, times 2^7 (448 * 2^7 < 65504): a page's codes keep their
-//     bits down to 2^-17 of the largest scale.  When the largest scale grows O is rescaled like
-//     for a maximum.  Weights are held times 2^7 (2^8 at most times tau's 2^8) in f16;
-//   * the work cut evenly: all units' 128-key blocks laid end to end, one persistent CTA per SM
-//     takes an equal run of them.  Units cut between CTAs leave partial results for the merge
-//     kernel.  Each role walks the CTA's units on its own; K, V of the next unit load while this
-//     one ends, and its Q is prepared while O is written out.
+//   * V widened to f16, times its page's scale over the largest V scale so far, times 2^7 (448 * 2^7
+//     < 65504): a page's codes keep their bits down to 2^-17 of the largest scale.  Weights are held
+//     times 2^7 (2^8 at most times tau's 2^8) in f16.
+// The work is cut evenly: all units' 128-key blocks laid end to end, with a cost for starting and
+// ending a unit, and every CTA takes an equal run.  Units cut between CTAs leave partial results for
+// the merge kernel.
+//
+// SPLIT (no sequence has more than 128 rows per K/V head): both tiles hold the same rows and take
+// the unit's blocks in turn, joined in tensor memory at the end.  With one tile idle a block took
+// its whole chain, 3850 cycles; taken in turn 2100.  One Q instead of two leaves room for four K slots.
+//
+// Measured: two prompts of 4096 over 8192 keys, 32 heads on 8, d = 128: 684 us, 1206 TFLOP/s (a
+// two-tile step of 128 keys takes 3900 cycles, of which the tensor cores need 2050 and shared memory
+// 2180); four pieces of up to 512 over up to 16000 keys: 238 us, 1075 TFLOP/s.  SPLIT: 16 sequences
+// of 16000 keys, 8 K/V heads of 32 rows: 141 us, 3.7 TB/s of cache (198 us without).
 //
 // Shared memory (d = 128): Q1, Q2 2 x 32 KB, K8 ring 2 x 16 KB, V8 ring 3 x 16 KB, V16 2 x 32 KB.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P_t (f16 pairs) overwrites S_t.
@@ -178,7 +196,7 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // NG: groups of columns of a key block that may have scales of their own (1: a page holds the
-// block; 8: 16 keys each).
+// block; 8: 16 keys each).  Prompts of 4096 over pages of 64 take 4 % longer than over pages of 128.
 template <int D, int NG, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -337,8 +355,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   auto rel_phase = [&](uint32_t group) -> uint32_t { return group / C::RELS & 1; };
   auto unit_done = [&](uint32_t u) { mbar_arrive(BAR(T_UFREE + u % kUnitSlots)); };
 
-  // Register split against the launch's 128 x 512: producer and MMA 64; softmax 184 each;
-  // correction (and V widening) 80.
+  // Register split against the launch's 128 x 512: producer, MMA, scheduler 64; softmax 184 each;
+  // V and epilogue 80.
   if (wg == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
@@ -405,8 +423,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
     } else if (warp <= 2) {
       // ---------------------------------------------------------------- MMA issuers, one per tile
-      // (one thread for both tiles lost 1000 cycles per block in its waits and commits).  Group j of a
-      // unit: PV of block j - 1 and S of block j.
+      // Group j of a unit: PV of block j - 1 (SPLIT: j - 2) and S of block j.
       if (lane == 0) {
         const int t = warp - 1;
         bool ok = true;
@@ -456,7 +473,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             tc_fence_after();
             if (pv) {
-              // O_t += P_t V16_(j-1), A = P from tensor memory (f16 pairs)
+              // O_t += P_t V16, A = P from tensor memory (f16 pairs)
               const uint32_t v_lo = sdesc_sw128_lo(sbase + C::OFF_V16 + vs * C::V16, C::CH16);
               // The first half of the keys while the softmax works on the second.
 #pragma unroll
