@@ -19,7 +19,7 @@
 //     (d = 64) rows is chosen so that under TMA's 128-byte swizzle both kinds of load touch
 //     every bank once.
 //
-// Measured (d = 128, 32 heads on 8, one query): 32 sequences of up to 32000 keys 355 us, 6.2 TB/s of
+// Measured (d = 128, 32 heads on 8, one query): 64 sequences of up to 32768 keys 355 us, 6.2 TB/s of
 // cache, 91 % of a copy's rate; 8 of 8192 keys 32.9 us in a graph, 4.1 TB/s (15 us of it are the
 // start, the first pieces' way from memory and the merge); one of 1024 keys 8.5 us in a graph.
 //

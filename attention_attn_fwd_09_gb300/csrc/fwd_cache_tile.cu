@@ -10,8 +10,7 @@
 //   * two MMA issuers, one per tile, that take turns (one thread for both lost 1000 cycles per block
 //     in its waits; two without turns fall into step).  A group of products is PV of one block and S
 //     of the next; its completion frees the slots that it read;
-//   * scheduler: walks the CTA's units and describes each in shared memory, four ahead (each role
-//     finding its own units by division cost 2 us per unit);
+//   * scheduler: walks the CTA's units and describes each in shared memory, up to four ahead;
 //   * two softmax warpgroups, a row per thread.  They prepare Q, rescale O themselves when a maximum
 //     grew by more than tau or a larger V scale came (rare after the first blocks), and hand P over
 //     in two halves, so that PV begins before the second half's exponentials;
@@ -196,7 +195,7 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // NG: groups of columns of a key block that may have scales of their own (1: a page holds the
-// block; 8: 16 keys each).  Prompts of 4096 over pages of 64 take 4 % longer than over pages of 128.
+// block; 8: 16 keys each). 
 template <int D, int NG, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -1028,7 +1027,8 @@ cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, c
 size_t cache_tile_workspace_bytes(int d, int sms) { return cache_ws(sms, kTRows, d).total; }
 
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
-  const bool one = p.page == 128;            // a key block has one scale
+  const bool one = p.page == 128;            // a key block has one scale (two prompts of 4096: 671 us, of eight 743)
+  // 16 sequences of 16000 keys, 128 rows per K/V head: 145 us against 203; 32 rows 141 against 198.
   const bool split = (long long)p.max_q * p.g <= 128;
   auto go = [&](auto dim, auto groups) {
     return split ? launch_tile<dim, groups, true>(maps, p, sms, s) : launch_tile<dim, groups, false>(maps, p, sms, s);
