@@ -194,12 +194,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// NG: groups of columns of a key block that may have scales of their own (1: a page holds the
-// block; 8: 16 keys each). 
+// NG: groups of columns of a key block that may have scales of their own, one per page of it. 
 template <int D, int NG, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const CacheParams p) {
+  constexpr int KG = 128 / NG;               // keys of a group
   using C = TileCfg<D, SPLIT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -648,10 +648,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!SPLIT || t == 0) mbar_arrive(BAR(T_Q + t));
       }
       if constexpr (SPLIT) ns_other += n_other;
-      // K scales: lane & 7 looks after a group of 16 keys (all lanes after the one page when NG = 1);
+      // K scales: lane % NG looks after a group of KG keys (all lanes after the one page when NG = 1);
       // pages one block further ahead than scales.
       auto page_of = [&](int j) -> int {
-        const int key = kt0 * 128 + j * STRIDE + (NG > 1 ? (lane & 7) * 16 : 0);
+        const int key = kt0 * 128 + j * STRIDE + (NG > 1 ? lane % NG * KG : 0);
         if (j >= n_t || key >= len) return -1;
         const int pg = __ldg(table + (key >> page_shift));
         return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         pg_next = page_of(j + 2);
         if constexpr (NG > 1) {
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+          for (int o = NG / 2; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
         }
         float fac[NG];
 #pragma unroll
@@ -708,13 +708,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
         } else {
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {
-            const float* x = s + gq * 16;
+            const float* x = s + gq * KG;
             float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]);
-            a = fmax3(a, x[6], x[7]);
-            b = fmax3(b, x[8], x[9]);
-            a = fmax3(a, x[10], x[11]);
-            b = fmax3(b, x[12], x[13]);
-            rmax = fmaxf(rmax, fmax3(fmaxf(a, b), x[14], x[15]) * fac[gq]);
+#pragma unroll
+            for (int i = 6; i < KG - 2; i += 4) {
+              a = fmax3(a, x[i], x[i + 1]);
+              b = fmax3(b, x[i + 2], x[i + 3]);
+            }
+            rmax = fmaxf(rmax, fmax3(fmaxf(a, b), x[KG - 2], x[KG - 1]) * fac[gq]);
           }
         }
         const float m_cand = fmaxf(m, rmax);
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
           for (int i = 64 * hf; i < 64 * hf + 64; i += 2) {
             float x0, x1;
-            ffma2_bc(x0, x1, s[i], s[i + 1], fac[NG > 1 ? i / 16 : 0], off);
+            ffma2_bc(x0, x1, s[i], s[i + 1], fac[i / KG], off);
             const float e0 = ex2_mufu(x0), e1 = ex2_mufu(x1);
             pk[(i >> 1) & 31] = pack_f16x2(e0, e1);
             const int a2 = ((i >> 1) & 1) * 2;
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       float rref = kMinScale;                // largest V scale so far
       float rref_other = kMinScale;          // SPLIT: of the other tile's blocks (they take turns)
       auto page_of = [&](int j) -> int {
-        const int key = (kt0 + j) * 128 + (NG > 1 ? (lane & 7) * 16 : 0);
+        const int key = (kt0 + j) * 128 + (NG > 1 ? lane % NG * KG : 0);
         if (j >= nmax || key >= len) return -1;
         const int pg = __ldg(table + (key >> page_shift));
         return (unsigned)pg < (unsigned)p.num_pages ? pg : 0;
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         float vmax = sv;
         if constexpr (NG > 1) {
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+          for (int o = NG / 2; o > 0; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
         }
         if constexpr (SPLIT) {
           const float x = rref;
@@ -853,7 +854,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           uint4 v = *reinterpret_cast<const uint4*>(s_base + it * 2048);
           const int key = key_of(it);
           uint32_t wv = w_mine;
-          if constexpr (NG > 1) wv = __shfl_sync(0xffffffffu, w_mine, D == 128 ? it : 2 * it + (w4 >> 1));
+          if constexpr (NG > 1) wv = __shfl_sync(0xffffffffu, w_mine, (D == 128 ? it : 2 * it + (w4 >> 1)) * 16 / KG);
           if (key >= left) v = make_uint4(0u, 0u, 0u, 0u);         // whatever the codes are (NaN too)
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t hh[8];
@@ -1027,7 +1028,6 @@ cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, c
 size_t cache_tile_workspace_bytes(int d, int sms) { return cache_ws(sms, kTRows, d).total; }
 
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
-  const bool one = p.page == 128;            // a key block has one scale (two prompts of 4096: 671 us, of eight 743)
   // 16 sequences of 16000 keys, 128 rows per K/V head: 145 us against 203; 32 rows 141 against 198.
   const bool split = (long long)p.max_q * p.g <= 128;
   auto go = [&](auto dim, auto groups) {
@@ -1037,8 +1037,13 @@ cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, i
   using I8 = std::integral_constant<int, 8>;
   using I64 = std::integral_constant<int, 64>;
   using I128 = std::integral_constant<int, 128>;
-  if (d == 64) return one ? go(I64(), I1()) : go(I64(), I8());
-  return one ? go(I128(), I1()) : go(I128(), I8());
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  // Two prompts of 4096 over pages of 128 / 64 / 32 / 16: 670 / 677 / 702 / 746 us (the middle two with eight groups: 741, 743).
+  if (p.page == 128) return d == 64 ? go(I64(), I1()) : go(I128(), I1());
+  if (p.page == 64) return d == 64 ? go(I64(), I2()) : go(I128(), I2());
+  if (p.page == 32) return d == 64 ? go(I64(), I4()) : go(I128(), I4());
+  return d == 64 ? go(I64(), I8()) : go(I128(), I8());
 }
 
 }  // namespace attn
