@@ -889,7 +889,7 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
   p.max_len = max_pages * page_size;
   p.status = s->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_kv_append(p, d, st);
+  cudaError_t e = launch_kv_append(p, d, std::max(1, s->sms), st);
   if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
   return post_launch(s, st);
 }

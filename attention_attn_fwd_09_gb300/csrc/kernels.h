@@ -200,7 +200,7 @@ struct AppendParams {
   int page_shift;            // log2(page), filled in by launch_kv_append
   int* status;
 };
-cudaError_t launch_kv_append(AppendParams p, int d, cudaStream_t s);
+cudaError_t launch_kv_append(AppendParams p, int d, int sms, cudaStream_t s);
 
 // Packed queries over the paged e4m3 cache (fwd_cache.cu).
 struct CacheParams {

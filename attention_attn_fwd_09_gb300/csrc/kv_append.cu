@@ -14,8 +14,8 @@
 //   * prompts (bound by bytes, 2 read and 1 written per element): a CTA per slot, head and K or
 //     V holds the page's new rows in registers between the maximum and the rounding, one pass
 //     over the data.  8192 rows of 8 heads twice, d = 128: 20.6 us (4.9 TB/s);
-//   * a few rows per sequence (bound by latency): a warp per slot, head and K or V, no barrier
-//     behind the search for the slot.  One row of 64 sequences: 2.5 us in a graph.
+//   * a few rows per sequence (bound by latency), or many small pages: a warp per slot, head and
+//     K or V, no barrier behind the search for the slot.  One row of 64 sequences: 2.5 us in a graph.
 #include <cstdint>
 
 #include "cache.cuh"
@@ -278,14 +278,18 @@ cudaError_t launch_d(const AppendParams& p, dim3 grid, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(AppendParams p, int d, cudaStream_t s) {
+cudaError_t launch_kv_append(AppendParams p, int d, int sms, cudaStream_t s) {
   p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
   const long long slots = (long long)p.total / p.page + 2LL * p.B;
   if (slots > 0x3fffffffLL || p.Hkv > 65535) return cudaErrorInvalidValue;
   // Up to 4 rows per sequence on average: a warp per page and head (64 sequences, 8 heads, pages of 128:
   // 1 row each 2.8 us against 7.0 with a CTA each, 4 rows 3.2 against 7.1; a piece of 128 rows among 63
   // single ones, which the host cannot tell from 3 rows each, 9.8 against 7.2).
-  if (p.total <= 4LL * p.B) {
+  // So too many small pages, a CTA each of which comes and goes for little: 2 x 4096 rows of 8 heads,
+  // d = 128, over pages of 16: 9.7 us against 18.2, of 32: 9.5 against 11.9.  Fewer would leave SMs
+  // idle (of 2 heads, 14 CTAs per SM, 6.2 against 6.1; 1 head, 5.6 against 3.8).
+  const bool small = p.page <= 32 && 2 * slots * p.Hkv >= 16LL * sms;
+  if (p.total <= 4LL * p.B || small) {
     const dim3 grid((unsigned)(2 * slots), (unsigned)((p.Hkv + kStepWarps - 1) / kStepWarps));
     if (d == 64) kv_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
     else kv_append_step_kernel<128><<<grid, kStepWarps * 32, 0, s>>>(p);

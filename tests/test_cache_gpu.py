@@ -84,6 +84,25 @@ def test_append_prompts_then_tokens(A, P, d):
     c.same()
 
 
+@pytest.mark.parametrize("P,H,d,ns", [
+    (16, 8, 64, [2600, 17, 1]), (32, 9, 128, [3000, 1500, 0, 33]), (16, 33, 128, [520, 100]),     # many small pages
+    (128, 9, 128, [1] * 40 + [97]), (64, 3, 64, [1, 0, 1] * 20 + [70]),                          # a piece among single rows
+])
+def test_append_many_rows_in_one_page_of_a_warp(A, P, H, d, ns):
+    rng = np.random.RandomState(P + H)
+    had = rng.randint(0, 2 * P, len(ns))
+    lens = [int(h) + n for h, n in zip(had, ns)]
+    table, pages = page_tables(lens, P, 3)
+    c = Cache(A, table, pages, H, P, d)
+    c.append(*kv(rng, H, int(had.sum()), d, gain=0.25), had.tolist(), had.tolist())
+    c.same()
+    k, v = kv(rng, H, sum(ns), d)
+    k[0, :, 5] = float("inf")
+    v[H - 1, ::3, d - 1] = float("nan")
+    c.append(k, v, ns, lens)
+    c.same()
+
+
 def test_append_strided_projection(A):
     """K, V as views of a fused projection, [tokens, heads, d]."""
     rng = np.random.RandomState(1)
