@@ -399,7 +399,7 @@ def test_nothing_to_do(A):
     assert o.shape == (4, 0, 64) and lse.shape == (4, 0)
 
 
-@pytest.mark.parametrize("n", [1, 80])
+@pytest.mark.parametrize("n", [1, 8, 80])
 def test_a_wait_that_runs_out(A, n):
     """The first K copy of every CTA is never issued: the waits end, the status says so, and the
     next call is right."""
