@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kPiece = 32;                   // keys per piece
+constexpr int kSMs = 152;                  // blocks of the merge kernel are a multiple of these
 constexpr float kShift = 14.f;               // weights are held times 2^14
 
 template <int D>
@@ -600,75 +601,110 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the partial results of cut units: blocks x take the unit that starts in CTA x of the main
-// kernel and goes on in others (at most one).  A thread has one row and CPT pieces of 4 columns of it,
-// and reads JOIN partials' statistics and pieces at once, joining them as they come.  CPT = 4 when a
-// unit has many rows (bytes bound it: with one piece per thread and turn, 18 us for 152 units of 256
-// rows cut in two), 1 for decoding (latency does).
-template <int D, int CPT, int JOIN>
+// Joins the partial results of cut units.  An item is 128 threads' share of a unit that starts in one
+// CTA of the main kernel and goes on in others (at most one per CTA): a thread has one row and CPT
+// neighbouring pieces of 4 columns of it, and reads JOIN partials' statistics and pieces at once, joining
+// them as they come.  CPT = JOIN = 2 when there are many units (bytes and the blocks in flight bound it:
+// of two prompts of 4096, 152 units of 256 rows, 11 us of 680; CPT = JOIN = 4 took 2 us longer), CPT = 1
+// and JOIN = 8 for decoding and for few units (latency does; JOIN = 4 or 16 is slower).
+// COMPACT: the blocks first look which CTAs left a unit and share these units' items; otherwise block i
+// takes item i of all CTAs, which is one look-up shorter but comes to several waves of blocks that find
+// nothing when few CTAs leave a unit of many items (4 drafted tokens, 8 units: 25.1 us against 26.1;
+// 16 sequences of 16 rows in 1216 blocks 99.6 against 97.6, with many units 3 us more).
+template <int D, int CPT, int JOIN, bool COMPACT>
 __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int row_shift,
                                                               const int ctas) {
   constexpr int GROUPS = D / 4 / CPT;
+  static_assert(CPT <= 2, "one store per row and thread");
+  __shared__ uint32_t cut[32];               // bit i: CTA i left a unit (COMPACT: at most 1024 CTAs)
   const CacheWs W = cache_ws(ctas, rows_max, D);
   const char* ws = static_cast<const char*>(p.ws);
-  const int t = blockIdx.y * 128 + threadIdx.x, r = t & ((1 << row_shift) - 1), cg = t >> row_shift;
-  const int qi = r / p.g;
-  const float4* stat = reinterpret_cast<const float4*>(ws + W.stat) + r;
-  const float4* part = reinterpret_cast<const float4*>(ws + W.part) + (long long)cg * rows_max + r;
+  const int4* recs = reinterpret_cast<const int4*>(ws);
   pdl_wait();
   pdl_trigger();
-  const int4 rec = reinterpret_cast<const int4*>(ws)[blockIdx.x];
-  if (rec.w < 2 || qi >= rec.z || cg >= GROUPS) return;
-  const int first = 2 * blockIdx.x + (rec.w & 1), more = rec.w >> 1;
-  // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
-  auto which = [&](int k) -> long long { return k == 0 ? first : 2 * ((int)blockIdx.x + k); };
-  float m = -INFINITY, ref = kMinScale, l = 0.f;
-  float4 o[CPT];
-#pragma unroll
-  for (int c = 0; c < CPT; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 <= more; k0 += JOIN) {
-    float4 x[JOIN][CPT], st[JOIN];
-#pragma unroll
-    for (int j = 0; j < JOIN; ++j) {
-      const long long w = which(min(k0 + j, more));     // (the last one again: loads without conditions)
-      st[j] = stat[w * rows_max];
-#pragma unroll
-      for (int c = 0; c < CPT; ++c) x[j][c] = part[(w * (D / 4) + c * GROUPS) * rows_max];
+  int units = ctas;
+  if constexpr (COMPACT) {
+    for (int i = threadIdx.x; i < (ctas + 31) / 32 * 32; i += 128) {
+      const uint32_t b = __ballot_sync(0xffffffffu, i < ctas && recs[min(i, ctas - 1)].w >= 2);
+      if ((i & 31) == 0) cut[i >> 5] = b;
     }
-    float mn = m, rn = ref;
-#pragma unroll
-    for (int j = 0; j < JOIN; ++j) {
-      mn = fmaxf(mn, st[j].x);
-      rn = fmaxf(rn, st[j].z);
-    }
-    const float mu = mn == -INFINITY ? 0.f : mn, rinv = 1.f / rn;
-    const float w0 = ex2_mufu(m - mu), v0 = w0 * (ref * rinv);
-    l *= w0;
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) { o[c].x *= v0; o[c].y *= v0; o[c].z *= v0; o[c].w *= v0; }
-#pragma unroll
-    for (int j = 0; j < JOIN; ++j) {
-      if (k0 + j > more) break;
-      const float w = ex2_mufu(st[j].x - mu), v = w * (st[j].z * rinv);
-      l += w * st[j].y;
-#pragma unroll
-      for (int c = 0; c < CPT; ++c) {
-        o[c].x += v * x[j][c].x;
-        o[c].y += v * x[j][c].y;
-        o[c].z += v * x[j][c].z;
-        o[c].w += v * x[j][c].w;
-      }
-    }
-    m = mn;
-    ref = rn;
+    __syncthreads();
+    units = 0;
+    for (int i = 0; i < (ctas + 31) / 32; ++i) units += __popc(cut[i]);
   }
-  const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
-  const float inv = l == 0.f ? 0.f : ref / l;
-  uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D) + cg;
+  const int shares = ((GROUPS << row_shift) + 127) / 128;
+  for (int item = blockIdx.x; item < units * shares; item += gridDim.x) {
+    const int share = item / units;
+    int cta = item - share * units;
+    if constexpr (COMPACT) {                 // the cta-th bit set
+      int w = 0;
+      while (cta >= __popc(cut[w])) cta -= __popc(cut[w++]);
+      uint32_t bits = cut[w];
+      for (; cta > 0; --cta) bits &= bits - 1;
+      cta = w * 32 + __ffs(bits) - 1;
+    }
+    const int t = share * 128 + threadIdx.x, r = t & ((1 << row_shift) - 1), cg = t >> row_shift;
+    const int qi = r / p.g;
+    const float4* stat = reinterpret_cast<const float4*>(ws + W.stat) + r;
+    const float4* part = reinterpret_cast<const float4*>(ws + W.part) + (long long)cg * CPT * rows_max + r;
+    const int4 rec = recs[cta];
+    if (rec.w < 2 || qi >= rec.z || cg >= GROUPS) continue;
+    const int first = 2 * cta + (rec.w & 1), more = rec.w >> 1;
+    // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
+    auto which = [&](int k) -> long long { return k == 0 ? first : 2 * (cta + k); };
+    float m = -INFINITY, ref = kMinScale, l = 0.f;
+    float4 o[CPT];
 #pragma unroll
-  for (int c = 0; c < CPT; ++c)
-    out[c * GROUPS] = make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
-  if (cg == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
+    for (int c = 0; c < CPT; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 <= more; k0 += JOIN) {
+      float4 x[JOIN][CPT], st[JOIN];
+#pragma unroll
+      for (int j = 0; j < JOIN; ++j) {
+        const long long w = which(min(k0 + j, more));     // (the last one again: loads without conditions)
+        st[j] = stat[w * rows_max];
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) x[j][c] = part[(w * (D / 4) + c) * rows_max];
+      }
+      float mn = m, rn = ref;
+#pragma unroll
+      for (int j = 0; j < JOIN; ++j) {
+        mn = fmaxf(mn, st[j].x);
+        rn = fmaxf(rn, st[j].z);
+      }
+      const float mu = mn == -INFINITY ? 0.f : mn, rinv = 1.f / rn;
+      const float w0 = ex2_mufu(m - mu), v0 = w0 * (ref * rinv);
+      l *= w0;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) { o[c].x *= v0; o[c].y *= v0; o[c].z *= v0; o[c].w *= v0; }
+#pragma unroll
+      for (int j = 0; j < JOIN; ++j) {
+        if (k0 + j > more) break;
+        const float w = ex2_mufu(st[j].x - mu), v = w * (st[j].z * rinv);
+        l += w * st[j].y;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+          o[c].x += v * x[j][c].x;
+          o[c].y += v * x[j][c].y;
+          o[c].z += v * x[j][c].z;
+          o[c].w += v * x[j][c].w;
+        }
+      }
+      m = mn;
+      ref = rn;
+    }
+    const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
+    const float inv = l == 0.f ? 0.f : ref / l;
+    uint32_t y[2 * CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      y[2 * c] = pack_bf16x2(o[c].x * inv, o[c].y * inv);
+      y[2 * c + 1] = pack_bf16x2(o[c].z * inv, o[c].w * inv);
+    }
+    uint16_t* out = static_cast<uint16_t*>(p.o) + row * D + cg * CPT * 4;
+    if constexpr (CPT == 1) *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+    else *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (cg == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
+  }
 }
 
 template <int D>
@@ -694,15 +730,19 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
   int shift = 0;
   while ((1 << shift) < rows && (1 << shift) < (long long)p.max_q * p.g) ++shift;     // rows in use
-  auto go = [&](auto kernel, int cpt) {
-    const dim3 grid((unsigned)ctas, (unsigned)((((d / 4 / cpt) << shift) + 127) / 128));
-    return launch_pdl(kernel, grid, dim3(128), 0, s, p, rows, shift, ctas);
+  auto go = [&](auto kernel, int cpt, bool compact) {
+    const int shares = (((d / 4 / cpt) << shift) + 127) / 128;
+    const int blocks = compact ? 4 * kSMs : ctas * shares;
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(128), 0, s, p, rows, shift, ctas);
   };
-  // Few units of many partials each: latency again.
+  // Few units of many partials each: latency again (a sequence of 30000 keys, 32 rows: 33 us against 35).
   const long long units = (long long)p.B * p.Hkv * (((long long)p.max_q * p.g + rows - 1) / rows);
-  if (rows <= kCacheDecodeRows || units * 4 <= ctas)
-    return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8>, 1) : go(fwd_cache_merge_kernel<128, 1, 8>, 1);
-  return d == 64 ? go(fwd_cache_merge_kernel<64, 4, 4>, 4) : go(fwd_cache_merge_kernel<128, 4, 4>, 4);
+  if (rows <= kCacheDecodeRows || units * 4 <= ctas) {
+    if (((d / 4) << shift) / 128 * ctas > 16 * kSMs && ctas <= 1024)
+      return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8, true>, 1, true) : go(fwd_cache_merge_kernel<128, 1, 8, true>, 1, true);
+    return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8, false>, 1, false) : go(fwd_cache_merge_kernel<128, 1, 8, false>, 1, false);
+  }
+  return d == 64 ? go(fwd_cache_merge_kernel<64, 2, 2, false>, 2, false) : go(fwd_cache_merge_kernel<128, 2, 2, false>, 2, false);
 }
 
 size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }
