@@ -32,9 +32,9 @@
 // the unit's blocks in turn, joined in tensor memory at the end.  With one tile idle a block took
 // its whole chain, 3850 cycles; taken in turn 2100.  One Q instead of two leaves room for four K slots.
 //
-// Measured: two prompts of 4096 over 8192 keys, 32 heads on 8, d = 128: 684 us, 1206 TFLOP/s (a
+// Measured: two prompts of 4096 over 8192 keys, 32 heads on 8, d = 128: 680 us, 1212 TFLOP/s (a
 // two-tile step of 128 keys takes 3900 cycles, of which the tensor cores need 2050 and shared memory
-// 2180); four pieces of up to 512 over up to 16000 keys: 238 us, 1075 TFLOP/s.  SPLIT: 16 sequences
+// 2180); four pieces of up to 512 over up to 16000 keys: 234 us, 1093 TFLOP/s.  SPLIT: 16 sequences
 // of 16000 keys, 8 K/V heads of 32 rows: 141 us, 3.7 TB/s of cache (198 us without).
 //
 // Shared memory (d = 128): Q1, Q2 2 x 32 KB, K8 ring 2 x 16 KB, V8 ring 3 x 16 KB, V16 2 x 32 KB.

@@ -144,7 +144,7 @@ size_t attn_fwd_kv_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d)
  *   inv_freq: DEVICE fp64 [rot/2], radians per position (scaling for long contexts is in these
  *       values and in mscale).  The angle is exact to 2^-32 turns plus 2^-52 of p * inv_freq.
  *   positions: DEVICE int32 [B,N], or NULL for 0 .. N-1.
- *   d: 64, 128, 192 or 256; rot even, 2 .. d; mscale finite.
+ *   d: 64, 128, 192 or 256; rot even, 2 .. d; mscale finite; N below 2^31 - 65536, Hq + Hk up to 65535.
  * Packed sequences ([H, total, d]): B = 1, N = total and the positions of each row.
  */
 int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const int* positions,
