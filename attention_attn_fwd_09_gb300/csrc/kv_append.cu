@@ -13,9 +13,9 @@
 // rows can touch; spare slots exit.  Two kernels:
 //   * prompts (bound by bytes, 2 read and 1 written per element): a CTA per slot, head and K or
 //     V holds the page's new rows in registers between the maximum and the rounding, one pass
-//     over the data.  8192 rows of 8 heads twice, d = 128: 20.6 us (4.9 TB/s);
-//   * a few rows per sequence (bound by latency), or many small pages: a warp per slot, head and
-//     K or V, no barrier behind the search for the slot.  One row of 64 sequences: 2.5 us in a graph.
+//     over the data.  8192 rows of 8 heads twice, d = 128: 14.6 us in a graph, 6.9 TB/s;
+//   * a few rows per sequence or page (bound by latency): a warp per slot, head and K or V, no
+//     barrier behind the search for the slot.  One row of 64 sequences: 2.5 us in a graph.
 #include <cstdint>
 
 #include "cache.cuh"
@@ -294,10 +294,12 @@ cudaError_t launch_kv_append(AppendParams p, int d, int sms, cudaStream_t s) {
   // Up to 4 rows per sequence on average: a warp per page and head (64 sequences, 8 heads, pages of 128:
   // 1 row each 2.8 us against 7.0 with a CTA each, 4 rows 3.2 against 7.1; a piece of 128 rows among 63
   // single ones, which the host cannot tell from 3 rows each, 9.8 against 7.2).
-  // So too many small pages, a CTA each of which comes and goes for little: 2 x 4096 rows of 8 heads,
-  // d = 128, over pages of 16: 9.7 us against 18.2, of 32: 9.5 against 11.9.  Fewer would leave SMs
-  // idle (of 2 heads, 14 CTAs per SM, 6.2 against 6.1; 1 head, 5.6 against 3.8).
-  const bool small = p.page <= 32 && 2 * slots * p.Hkv >= 16LL * sms;
+  // So too many pages with up to 32 new rows on average, a CTA each of which comes and goes for little:
+  // 256 pieces of 16 rows 7.5 us against 21.5 (pages of 64: 7.6 against 17.6), 2 x 4096 rows of 8 heads,
+  // d = 128, over pages of 16 9.7 against 18.2, of 32 9.5 against 11.9.  Fewer CTAs would leave SMs idle
+  // (2 heads, 14 CTAs per SM, 6.2 against 6.1; 1 head, 5.6 against 3.8), more rows are read at one go by
+  // a CTA (4 x 8192 over pages of 64 33 against 61 with a warp each).
+  const bool small = p.total <= 32 * slots && 2 * slots * p.Hkv >= 16LL * sms;
   if (p.total <= 4LL * p.B || small) {
     const dim3 grid((unsigned)(2 * slots), (unsigned)((p.Hkv + kStepWarps - 1) / kStepWarps));
     if (d == 64) kv_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
