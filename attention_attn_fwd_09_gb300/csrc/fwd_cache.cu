@@ -550,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp >= 2) put(warp - 2);
     __syncthreads();
     if (warp < 2) take(warp);
-    if (warp == 1) put(1);                   // only warp 1 has read this slot
+    if (warp == 1) {                         // only warp 1 reads this slot; its lanes share the statistics, so all
+      __syncwarp();                          // of them have read before some write
+      put(1);
+    }
     if (nan && warp == 3) {
       for (int i = lane; i < D; i += 32) first_nan[i] = kNoKey;
       if (lane == 0) *any_nan = 0;
