@@ -425,7 +425,9 @@ def _there(device, stream):
             yield
             return
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
+            # 0 is the legacy default stream; ExternalStream(0) would be some stream of torch's pool.
+            raw = int(stream)
+            stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
         with torch.cuda.stream(stream):
             yield
 

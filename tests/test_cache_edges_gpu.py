@@ -46,3 +46,47 @@ def test_warps_join_the_same_way_every_time(A, heads, n, d):
     for _ in range(100):
         o2, lse2 = call()
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_stream_zero_is_the_default_stream(A):
+    """The number 0 (cuda_stream of the default stream) names the default stream for the three
+    operators, as it does for the library's other calls: what they do comes after what is already on it."""
+    zero = torch.cuda.default_stream().cuda_stream
+    assert zero == 0
+    c = filled([700, 300], [2, 2], 8, 2, 64, 128, seed=2)
+    want = attend(A, c)
+    f, m = A.attn_rope_freqs(128)
+    x = bf16(np.random.RandomState(0).randn(2, 4, 128)).to(DEV)
+    want_x, _ = A.attn_rope(x, None, f)
+    g = {k: dev(c[k]) for k in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "cu", "lens")}
+    q, qx = torch.zeros_like(c["q"], device=DEV), torch.zeros_like(x)
+    src, busy = c["q"].to(DEV), torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                          # the current stream is another one
+        with A._there(q.device, zero):
+            assert torch.cuda.current_stream().cuda_stream == 0
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            for _ in range(20):
+                busy = (busy @ busy).clamp_(-1, 1)         # the inputs are written late
+            q.copy_(src)
+            qx.copy_(x)
+        o, lse = A.attn_fwd_kv_fp8(q, g["k_cache"], g["v_cache"], g["k_scale"], g["v_scale"], g["table"], g["cu"],
+                                   g["lens"], 2, stream=zero)
+        y, _ = A.attn_rope(qx, None, f, stream=zero)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, want_x)
+    table, pages = page_tables([4], 16)
+    cache = Cache(A, table, pages, 2, 16, 128)
+    late = torch.zeros_like(qx)
+    with torch.cuda.stream(side):
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            for _ in range(20):
+                busy = (busy @ busy).clamp_(-1, 1)
+            late.copy_(x)
+        A.attn_kv_append_fp8(late, late, cache.gpu["k"][0], cache.gpu["v"][0], cache.gpu["k"][1], cache.gpu["v"][1],
+                             cache.dtable, dev(offsets([4])), dev(np.array([4], np.int32)), stream=zero)
+    torch.cuda.synchronize()
+    for n in "kv":
+        oc.append(x.float().cpu().numpy(), *cache.host[n], table, offsets([4]), [4])
+    cache.same()
