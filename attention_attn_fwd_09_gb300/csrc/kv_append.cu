@@ -6,7 +6,8 @@
 // and code = e4m3(x / s), rounded to nearest even; when s > s_old the kept rows are coded
 // again, e4m3(decode(code) s_old / s).  A power of two makes both quotients exact (the codes
 // lose nothing by it: e4m3 is a floating-point format), so a row coded again keeps its value
-// but for results below 2^-6, and rows appended one by one end as rows appended at once.
+// but for results below 2^-6, and rows appended one by one end as rows appended at once.  (s_old = 0
+// too: rows that read 0, infinities among them, keep reading 0, and NaN stays NaN.)
 //
 // Nothing on the host knows the lengths: slots are numbered so that sequence b owns the slots
 // from floor(cu[b] / P) + 2 b on, which leaves it at least floor(n / P) + 2 >= the pages its n
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) kv_append_kernel(const AppendPa
     const int r = r0 + i * RPS;                        // rows behind the last one stay as they are
     if (r >= s.kept && r < s.rows) out[i * THREADS] = inv != 0.f ? code8(x[i], inv) : code8_div(x[i], sc);
   }
-  if (sc > s_old && s_old > 0.f) {                     // the kept rows' codes change
+  if (sc > s_old) {                                    // the kept rows' codes change (under a scale of 0: to 0)
 #pragma unroll 1
     for (int i = 0; i < NV && r0 + i * RPS < s.kept; ++i) out[i * THREADS] = recode8(out[i * THREADS], s_old, inv);
   }
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) kv_append_step_kernel(const A
   } else {
     for (int r = s.kept + r0; r < s.rows; r += RPW) *reinterpret_cast<uint2*>(t.dst + r * D + c) = code8_div(row_of(r), sc);
   }
-  if (sc > s_old && s_old > 0.f) {
+  if (sc > s_old) {
     for (int r = r0; r < s.kept; r += RPW) {
       uint2* out = reinterpret_cast<uint2*>(t.dst + r * D + c);
       *out = recode8(*out, s_old, inv);

@@ -6,7 +6,7 @@ row t of sequence b is row t % P of page table[b][t // P].
 
 append   the n new rows of sequence b become its rows lens[b] - n .. lens[b] - 1.  Per page and
          head touched: A = max |finite new value|, s = 2^ceil(log2(A / 448)) (0 for A = 0);
-         with earlier rows in the page s = max(s, s_old), and if s > s_old > 0 their codes
+         with earlier rows in the page s = max(s, s_old), and if s > s_old their codes
          become e4m3(decode(code) * s_old / s).  New codes are e4m3(x / s); infinities become
          +-448, NaN the NaN code.
 attend   softmax(scale q k~^T) v~ in fp64 over the visible keys: j < lens[b], with causal
@@ -57,7 +57,7 @@ def append(x, codes, scale, table, cu, lens) -> None:
                 if slot > 0:
                     s_old = float(scale[page, h])
                     s = max(s, s_old)
-                    if s > s_old > 0:
+                    if s > s_old:
                         old = (e4m3_decode(codes[page, h, :slot]).astype(np.float32) * np.float32(s_old)).astype(np.float64)
                         codes[page, h, :slot] = encode(old, s)
                 scale[page, h] = s

@@ -90,3 +90,23 @@ def test_stream_zero_is_the_default_stream(A):
     for n in "kv":
         oc.append(x.float().cpu().numpy(), *cache.host[n], table, offsets([4]), [4])
     cache.same()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P,n", [(16, 1), (128, 1), (16, 9), (128, 100)])
+def test_append_to_a_page_of_scale_zero(A, P, n, d):
+    """A first row without a finite value other than 0, then finite rows (few and many: both kernels).
+    The first row reads the same values before and after, byte for byte as the oracle has it."""
+    rng = np.random.RandomState(P + n)
+    table, pages = page_tables([1 + n], P)
+    c = Cache(A, table, pages, 2, P, d)
+    x = np.zeros((2, 1, d), np.float32)
+    x[:, 0, :6] = [np.inf, -np.inf, np.nan, 0.0, -0.0, np.inf]
+    y = np.where(np.isnan(x), x, -x)
+    c.append(bf16(x), bf16(y), [1], [1])
+    c.same()
+    assert (c.gpu["k"][1][int(table[0, 0])] == 0).all()
+    c.append(*kv(rng, 2, n, d), [n], [1 + n])
+    c.same()
+    first = c.gpu["k"][0][int(table[0, 0]), :, 0].cpu().numpy()
+    assert (first[:, [0, 1, 5]] & 0x7F == 0).all() and (first[:, 2] & 0x7F == 0x7F).all()
