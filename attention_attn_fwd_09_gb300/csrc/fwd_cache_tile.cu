@@ -17,10 +17,13 @@
 //   * a warpgroup that widens V and writes the results.
 // Numbers:
 //   * S on the 8-bit tensor path, K's codes as they lie in the cache.  Q, scaled by a power of two
-//     per row (largest |q| in [128, 256)), is the sum of two e4m3 tiles, Q1 = e4m3(q) and
-//     Q2 = e4m3(q - Q1): bf16 has 8 significant bits and e4m3 4, so the sum is q itself down to
-//     2^-9 of the row's largest component and off by at most 2^-18 of that below.  Both products
-//     together cost what one 16-bit product costs, and K needs no widening;
+//     per row (largest |q| in [128, 256)), is the sum of two 8-bit tiles, Q1 = e4m3(q) and
+//     Q2 = e5m2(q - Q1).  bf16 has 8 significant bits and e4m3 4, so what Q1 leaves of a component
+//     with exponent e >= -6 is 0 to 8 times 2^(e - 7): at most 3 significant bits and not below
+//     2^-13, which e5m2 holds (e4m3, whose step ends at 2^-9, does so from e = -2 on).  The sum is
+//     q itself down to 2^-13 of the row's largest component; below that Q1 leaves at most 2^-10, of
+//     which e5m2 misses at most 2^-14: 2^-21 of the row's largest (e4m3: all of it, 2^-17).
+//     Both products together cost what one 16-bit product costs, and K needs no widening;
 //   * V widened to f16, times its page's scale over the largest V scale so far, times 2^7 (448 * 2^7
 //     < 65504): a page's codes keep their bits down to 2^-17 of the largest scale.  Weights are held
 //     times 2^7 (2^8 at most times tau's 2^8) in f16.
@@ -60,7 +63,7 @@ constexpr float kMinFactor = 1e-30f;         // keeps -inf * factor = -inf for p
 
 template <int D, bool SPLIT>
 struct TileCfg {
-  static constexpr uint32_t Q8 = 128 * D;          // one e4m3 tile of Q
+  static constexpr uint32_t Q8 = 128 * D;          // one 8-bit tile of Q
   static constexpr uint32_t K8 = 128 * D;          // 128 keys of e4m3 K or V
   static constexpr uint32_t CH16 = 128 * 128;      // 128 keys x 64 f16 columns (a swizzled box)
   static constexpr uint32_t V16 = (D / 64) * CH16;
@@ -74,7 +77,8 @@ struct TileCfg {
   static constexpr uint32_t CTRL_BYTES = 512 + 256 + 6 * 128 * 4 + 64 + 2 * D * 4;
   static constexpr uint32_t SMEM = 1024 + OFF_CTRL + CTRL_BYTES;
   // K-major rows of D bytes: 128-byte swizzle for d = 128, 64-byte for d = 64.
-  static constexpr uint32_t IDESC_QK = idesc_f32acc(128, 128, FMT_E4M3, FMT_E4M3, false, false);
+  static constexpr uint32_t IDESC_Q1K = idesc_f32acc(128, 128, FMT_E4M3, FMT_E4M3, false, false);
+  static constexpr uint32_t IDESC_Q2K = idesc_f32acc(128, 128, FMT_E5M2, FMT_E4M3, false, false);
   static constexpr uint32_t IDESC_PV = idesc_f32acc(128, D, FMT_F16, FMT_F16, false, true);
   static constexpr uint32_t QK_HI = D == 128 ? sdesc_sw128_hi(1024) : ((512u >> 4) | (1u << 14) | (4u << 29));
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -172,10 +176,16 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-// Two fp32 values -> two e4m3 codes (low byte: a), and back.
+// Two fp32 values -> two e4m3 or e5m2 codes (low byte: a).
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 
@@ -494,7 +504,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < 2 * (D / 32); ++kk)
                 mma_ss_f8_w(tS, q_lo + (((kk / (D / 32)) * C::Q8 + (kk % (D / 32)) * 32) >> 4), C::QK_HI,
-                            k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                            k_lo + ((kk % (D / 32)) * 32 >> 4), C::QK_HI, kk < D / 32 ? C::IDESC_Q1K : C::IDESC_Q2K,
+                            kk > 0 ? 1u : 0u);
             }
             if (SPLIT) turn = j + 1 < nmax + LAG || t > 0;
             if (!SPLIT || turn) mbar_arrive(BAR(T_TURN + 1 - t));
@@ -634,7 +645,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               float y0, y1, y2, y3;
               e4m3x4_to_f32(hq, y0, y1, y2, y3);
               c1[x] = hq | poison;
-              c2[x] = to_e4m3x2(x0 - y0, x1 - y1) | (to_e4m3x2(x2 - y2, x3 - y3) << 16);
+              c2[x] = to_e5m2x2(x0 - y0, x1 - y1) | (to_e5m2x2(x2 - y2, x3 - y3) << 16);
             }
             const int rw = (i0 + k) * RPS + lane / LPR, ch = lane % LPR;   // row of the warp's 32, 8-byte piece
             const int off = rw * D + (((ch >> 1) ^ (D == 128 ? (rw & 7) : ((rw >> 1) & 3))) << 4) + (ch & 1) * 8;

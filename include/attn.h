@@ -196,6 +196,8 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  *       attn_fwd_varlen; the cache as above.
  *   max_q: an upper bound on the queries of one sequence (1 when decoding).
  *   scales finite and >= 0 (of pages in use; V scales best within 2^20 of each other).
+ *   Components of q that are small beside their row's largest lose bits where max_q * Hq / Hkv is above
+ *       16: below 2^-13 of the largest they are off by up to 2^-21 of it.
  *   Codes of rows behind kv_lens[b] are never used, whatever they are, and a NaN in the cache
  *   reaches the queries that see its row, no others.
  *   Hq / Hkv up to 256.

@@ -110,3 +110,52 @@ def test_append_to_a_page_of_scale_zero(A, P, n, d):
     c.same()
     first = c.gpu["k"][0][int(table[0, 0]), :, 0].cpu().numpy()
     assert (first[:, [0, 1, 5]] & 0x7F == 0).all() and (first[:, 2] & 0x7F == 0x7F).all()
+
+
+def check_with_query_error(o, lse, c, scale, bits):
+    """As cache_cases.check, with components of q off by up to 2^-bits of their row's largest: a score is
+    then off by 2^-bits scale max_c |q_c| sum_c |k_jc| more."""
+    O, L, W, Z = reference(c, scale=scale)
+    d, g = c["q"].shape[2], c["q"].shape[0] // c["k_cache"].shape[1]
+    peak = np.abs(c["q"].float().numpy()).max(axis=-1).astype(np.float64)                  # [Hq, T]
+    more = np.zeros_like(peak)
+    for b, n in enumerate(c["lens"]):
+        sl = slice(c["cu"][b], c["cu"][b + 1])
+        for h in range(peak.shape[0]):
+            k = oc.rows(c["k_cache"], c["k_scale"], c["table"][b], int(n), h // g)
+            more[h, sl] = 2.0 ** -bits * scale * peak[h, sl] * np.abs(k).sum(axis=1).max()
+    # (bounds multiplies Z by this)
+    check(o, lse, (O, L, W, Z + more / ((d + 8) * 2.0 ** -24 + 2.0 ** -22)), d)
+
+
+def one_large_component(n, factor, d, P, heads):
+    """Queries whose column 5 is `factor` times the others, keys that are 0 there: the scores are made of
+    the small components alone."""
+    lens = [n + 3, 200, 129]
+    c = filled(lens, [n] * 3, *heads, P, d, seed=n + d)
+    q = c["q"].float().numpy()
+    q[..., 5] *= factor
+    c["q"] = bf16(q)
+    c["k_cache"][..., 5] = 0
+    return c
+
+
+@pytest.mark.parametrize("factor", [10, 50, 200, 1000, 30000])
+@pytest.mark.parametrize("n,heads,P,d", [(5, (4, 1), 32, 128), (40, (4, 1), 16, 64), (90, (4, 1), 128, 128), (70, (6, 2), 64, 64)])
+def test_queries_with_one_large_component_on_the_tiles(A, n, heads, P, d, factor):
+    c = one_large_component(n, factor, d, P, heads)
+    o, lse = attend(A, c)
+    check_with_query_error(o, lse, c, d ** -0.5, 21)
+
+
+@pytest.mark.parametrize("n", [5, 90])
+def test_query_components_stay_exact_down_to_2_13_of_the_largest(A, n):
+    """128 beside 127 * 2^-10 (2^-10 of it) and 151 * 2^-13 (in the last binade that is held exactly), with
+    all bits of a bf16 in use: the small ones make the score, so what cache_cases.bounds claims for exact
+    operands holds."""
+    c = filled([n + 3, n + 200], [n] * 2, 4, 1, 32, 128, seed=1)
+    q = np.zeros(c["q"].shape, np.float32)
+    q[..., 0], q[..., 1], q[..., 2] = 128, 127 * 2.0 ** -10, 151 * 2.0 ** -13
+    c["q"] = bf16(q)
+    c["k_cache"][..., 0] = 0
+    run_check(A, c, scale=1.0)
