@@ -23,8 +23,8 @@
 // cache, 91 % of a copy's rate; 8 of 8192 keys 32.9 us in a graph, 4.1 TB/s (15 us of it are the
 // start, the first pieces' way from memory and the merge); one of 1024 keys 8.5 us in a graph.
 //
-// Numbers: q is scaled by a power of two per row (largest |q| in [1, 2)) and held in f16,
-// exact but for components 2^14 below the row's largest.  exp2(s - m + 14) <= 2^14 times the
+// Numbers: q is scaled by a power of two per row (largest |q| in [2^14, 2^15)) and held in f16: exact
+// down to 2^-31 of the row's largest component, off by at most 2^-39 of it below.  exp2(s - m + 14) <= 2^14 times the
 // page's V scale over the largest V scale so far is rounded to f16 (11 bits, against 8 of a
 // bf16 weight; the 2^14 keeps weights down to 2^-28 of the largest normal).  Scores, maxima,
 // sums and O are fp32.
@@ -291,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const uint32_t e = __float_as_uint(amax) >> 23;              // biased exponent
-      const bool usable = e > 0 && e < 254;                        // else (0, tiny, inf) leave the row as it is
-      const float inv = usable ? __uint_as_float((254u - e) << 23) : 1.f;
-      crow[i] = p.c * (usable ? __uint_as_float(e << 23) : 1.f);
+      const uint32_t up = min(268u - e, 253u);                     // of the factor: largest |q| to [2^14, 2^15)
+      const float inv = __uint_as_float(up << 23);
+      crow[i] = p.c * __uint_as_float((254u - up) << 23);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};

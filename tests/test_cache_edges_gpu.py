@@ -159,3 +159,26 @@ def test_query_components_stay_exact_down_to_2_13_of_the_largest(A, n):
     c["q"] = bf16(q)
     c["k_cache"][..., 0] = 0
     run_check(A, c, scale=1.0)
+
+
+@pytest.mark.parametrize("factor", [10, 1000, 30000, 2.0 ** 27])
+@pytest.mark.parametrize("n,heads,P,d", [(1, (8, 2), 16, 128), (4, (4, 1), 32, 128), (2, (3, 1), 128, 64)])
+def test_queries_with_one_large_component_on_few_rows(A, n, heads, P, d, factor):
+    c = one_large_component(n, factor, d, P, heads)
+    o, lse = attend(A, c)
+    check_with_query_error(o, lse, c, d ** -0.5, 39)
+
+
+@pytest.mark.parametrize("n", [1, 4, 5, 40, 90])
+def test_queries_at_both_ends_of_the_exponent(A, n):
+    """Rows whose largest component is in bf16's last binade, or near its first normal one, with a scale that
+    makes ordinary scores of them."""
+    for e in (127, 126, 100, -90):
+        c = filled([n + 3, 70 + n], [n] * 2, 4, 1, 32, 128, seed=3)
+        q = c["q"].float().numpy()
+        q = np.sign(q) * np.minimum(np.abs(q), 1.9)
+        q[..., 0] = 1.9                                    # a row's largest, in its exponent's binade
+        c["q"] = bf16(q * 2.0 ** e)
+        c["k_scale"] = (c["k_scale"] * 2.0 ** (-60 if e > 0 else 60)).astype(np.float32)
+        c["k_scale"][c["k_scale"] > 2.0 ** 90] = 0         # of pages that nobody uses
+        run_check(A, c, scale=128 ** -0.5 * 2.0 ** ((60 if e > 0 else -60) - e))
