@@ -293,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t e = __float_as_uint(amax) >> 23;              // biased exponent
       const uint32_t up = min(268u - e, 253u);                     // of the factor: largest |q| to [2^14, 2^15)
       const float inv = __uint_as_float(up << 23);
-      crow[i] = p.c * __uint_as_float((254u - up) << 23);
+      // A row that holds an infinity is NaN wherever it sees a key (as f16 it could be -inf at every key, which
+      // would read as a row that sees none).
+      crow[i] = p.c * (e < 255u ? __uint_as_float((254u - up) << 23) : __int_as_float(0x7fffffff));
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};

@@ -182,3 +182,22 @@ def test_queries_at_both_ends_of_the_exponent(A, n):
         c["k_scale"] = (c["k_scale"] * 2.0 ** (-60 if e > 0 else 60)).astype(np.float32)
         c["k_scale"][c["k_scale"] > 2.0 ** 90] = 0         # of pages that nobody uses
         run_check(A, c, scale=128 ** -0.5 * 2.0 ** ((60 if e > 0 else -60) - e))
+
+
+@pytest.mark.parametrize("n", [1, 4, 5, 40, 90])
+@pytest.mark.parametrize("what", [-np.inf, np.inf])
+def test_an_infinite_query_is_nan_where_it_sees_a_key(A, n, what):
+    """softmax of scores that are all -inf, or infinite in part, is NaN; a row that sees no key is still 0."""
+    c = filled([n + 3, 70 + n, 0], [n] * 3, 4, 1, 32, 128, seed=1)
+    c["k_cache"][..., 3] = 0x30                            # the same sign at every key
+    clean = attend(A, c, causal=False)
+    q = c["q"].float().numpy()
+    for row in (0, 2 * n):                                 # of the first sequence, and of the one without keys
+        q[0, row] = 0
+        q[0, row, 3] = what
+    o, lse = attend(A, dict(c, q=bf16(q)), causal=False)
+    assert torch.isnan(o[0, 0]).all() and torch.isnan(lse[0, 0])
+    assert (o[0, 2 * n] == 0).all() and torch.isneginf(lse[0, 2 * n])
+    keep = torch.ones(lse.shape, dtype=torch.bool, device=DEV)
+    keep[0, 0] = keep[0, 2 * n] = False
+    assert torch.equal(o[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
