@@ -772,6 +772,22 @@ int attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, 
 
 extern "C" {
 
+// Whether rows of d elements at these strides lie apart: in ascending order, every stride in use reaches
+// past all that the smaller ones span.
+static bool rows_apart(const int (&extent)[3], const long long (&stride)[3], int d) {
+  __int128 step[3];
+  int order[3] = {0, 1, 2};
+  for (int a = 0; a < 3; ++a) step[a] = stride[a] < 0 ? -(__int128)stride[a] : (__int128)stride[a];
+  std::sort(order, order + 3, [&](int a, int b) { return step[a] < step[b]; });
+  __int128 span = d;
+  for (int a : order) {
+    if (extent[a] <= 1) continue;
+    if (step[a] < span) return false;
+    span += (extent[a] - 1) * step[a];
+  }
+  return true;
+}
+
 // strides: {q, k, q_out, k_out} x {batch, head, token} in elements, or null for contiguous
 // [B, H, N, d] tensors.
 static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
@@ -806,10 +822,11 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
     for (int a = 0; a < 3; ++a) {
       if (ext[i][a] <= 1) continue;                    // the stride is not used
       bits |= (uintptr_t)(in[a] * 2) | (uintptr_t)(out[a] * 2);
-      if (out[a] < d && out[a] > -d) return fail(ATTN_ERR_INVALID_ARG, "output rows overlap (stride %lld)", out[a]);
       if (t.in == t.out && in[a] != out[a])
         return fail(ATTN_ERR_INVALID_ARG, "in place needs equal strides of input and output");
     }
+    if (!rows_apart(ext[i], out, d))
+      return fail(ATTN_ERR_INVALID_ARG, "output rows overlap (strides %lld, %lld, %lld)", out[0], out[1], out[2]);
   }
   if (bits & 1) return fail(ATTN_ERR_MISALIGNED, "bf16 tensors must be 2-byte aligned");
   if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))

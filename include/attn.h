@@ -139,7 +139,8 @@ size_t attn_fwd_kv_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d)
  *       and outputs do not overlap.
  *   strides: NULL for contiguous [B,H,N,d] tensors, or a HOST array of 12 element strides,
  *       {q, k, q_out, k_out} x {batch, head, token}; the d columns are contiguous.  The views
- *       of a fused projection [B,N,H,d] need no copy.  Rows that start on 16 bytes are fastest
+ *       of a fused projection [B,N,H,d] need no copy.  An output's rows lie apart: in ascending
+ *       order, each of its strides reaches past what the smaller ones span.  Rows that start on 16 bytes are fastest
  *       (with rot a multiple of 16); any 2-byte aligned ones work.
  *   inv_freq: DEVICE fp64 [rot/2], radians per position (scaling for long contexts is in these
  *       values and in mscale).  The angle is exact to 2^-32 turns plus 2^-52 of p * inv_freq.

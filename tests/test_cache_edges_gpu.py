@@ -201,3 +201,21 @@ def test_an_infinite_query_is_nan_where_it_sees_a_key(A, n, what):
     keep = torch.ones(lse.shape, dtype=torch.bool, device=DEV)
     keep[0, 0] = keep[0, 2 * n] = False
     assert torch.equal(o[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
+def test_rotary_outputs_in_wider_and_permuted_layouts(A):
+    """Outputs whose rows lie apart in any order of the strides: every other head of a wider buffer, tokens
+    outermost, batch innermost of the three."""
+    x = bf16(np.random.RandomState(3).randn(2, 3, 5, 64)).to(DEV)
+    f, m = A.attn_rope_freqs(64)
+    want, _ = A.attn_rope(x, None, f)
+    wide = torch.full((2, 5, 6, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    for view in (wide[:, :, ::2].transpose(1, 2), torch.empty((5, 3, 2, 64), dtype=torch.bfloat16, device=DEV).permute(2, 1, 0, 3),
+                 torch.empty((3, 5, 2, 64), dtype=torch.bfloat16, device=DEV).permute(2, 0, 1, 3)):
+        y, _ = A.attn_rope(x, None, f, q_out=view)
+        assert y is view and torch.equal(y, want)
+    assert (wide[:, :, 1::2] == 9.0).all()
+    buf = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(A.AttnError, match="overlap"):
+        A.attn_rope(x, None, f, q_out=buf.as_strided((2, 3, 5, 64), (1024, 64, 64, 1)))
+    assert (buf == 0).all()
