@@ -54,3 +54,34 @@ def test_rotary_outputs_whose_rows_overlap_are_refused(A, fn, which, out):
     p = [ctypes.c_void_p(0x10000 * i) for i in (1, 2, 3, 4, 5)]
     rc = getattr(A._lib, fn)(p[0], p[1], p[2], p[3], p[4], None, 2, 3, 3, 4, d, d, 0, 1.0, st, None)
     assert rc == -1 and "overlap" in A.attn_last_error()
+
+
+@pytest.mark.parametrize("rot,base,trained,factor", [(128, 1e4, 8192, 4.0), (64, 1e6, 32768, 8.0), (128, 5e5, 4096, 2.0), (96, 1e4, 2048, 1.5)])
+def test_yarn_frequencies_of_released_checkpoints(A, rot, base, trained, factor):
+    """The blend runs linearly over the pairs, from the last one with 32 turns or more over the trained length
+    to the first with one or fewer; here these pairs are found by counting turns.  ramp="turns" blends linearly
+    in the turns instead."""
+    f = base ** (-2.0 * np.arange(rot // 2) / rot)
+    turns = trained * f / (2 * np.pi)
+    first, last = int(np.flatnonzero(turns >= 32)[-1]), int(np.flatnonzero(turns <= 1)[0])
+    assert 0 < first < last < rot // 2 - 1
+    compressed = np.clip((np.arange(rot // 2) - first) / (last - first), 0, 1)
+    got, m = A.attn_rope_freqs(rot, base, "yarn", factor, trained, device="cpu")
+    np.testing.assert_allclose(got.numpy(), f * (1 - compressed) + f / factor * compressed, rtol=1e-13)
+    assert abs(m - (0.1 * np.log(factor) + 1)) < 1e-15
+    same = A.attn_rope_freqs(rot, base, "yarn", factor, trained, device="cpu", ramp="pairs")[0]
+    assert (same == got).all()
+    left = np.clip((turns - 1) / 31, 0, 1)
+    got, _ = A.attn_rope_freqs(rot, base, "yarn", factor, trained, device="cpu", ramp="turns")
+    np.testing.assert_allclose(got.numpy(), f * left + f / factor * (1 - left), rtol=1e-13)
+
+
+def test_yarn_refusals_and_far_ends(A):
+    for bad in (dict(ramp="other"), dict(beta_slow=0.0), dict(beta_slow=-1.0), dict(beta_fast=1.0)):
+        with pytest.raises(ValueError):
+            A.attn_rope_freqs(64, scaling="yarn", factor=2.0, trained_length=1024, device="cpu", **bad)
+    f = 1e4 ** (-2.0 * np.arange(32) / 64)
+    short = A.attn_rope_freqs(64, scaling="yarn", factor=2.0, trained_length=64, device="cpu")[0].numpy()   # no pair makes 32 turns
+    assert short[0] == 1.0 and (np.diff(short / f) <= 1e-12).all() and abs(short[-1] / f[-1] - 0.5) < 1e-12
+    long = A.attn_rope_freqs(64, scaling="yarn", factor=2.0, trained_length=1 << 40, device="cpu")[0].numpy()
+    np.testing.assert_allclose(long, f, rtol=1e-13)                                                         # all make more
