@@ -637,8 +637,8 @@ def attn_fwd_kv_fp8_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_
 def attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, max_q: int,
                     causal: bool = True, scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
     """O, LSE of packed queries q [Hq, total_q, d] (CUDA bf16) over a paged e4m3 cache (tensors as
-    ``attn_kv_append_fp8``): sequence b's n = cu_seqlens_q[b+1] - cu_seqlens_q[b] <= ``max_q``
-    queries stand at its last n of kv_lens[b] keys (causal: query i sees keys up to
+    ``attn_kv_append_fp8``): sequence b's n = cu_seqlens_q[b+1] - cu_seqlens_q[b] <= ``max_q`` <=
+    total_q queries stand at its last n of kv_lens[b] keys (causal: query i sees keys up to
     i + kv_lens[b] - n).  ``workspace``: a uint8 CUDA tensor of at least
     attn_fwd_kv_fp8_workspace_size(...) bytes (allocated when None).  The offsets, lengths and
     pages are checked on the device (attn_device_status())."""

@@ -195,7 +195,8 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  *
  *   q, o [Hq, total_q, d] bf16; lse [Hq, total_q] fp32 (natural log); cu_seqlens_q as
  *       attn_fwd_varlen; the cache as above.
- *   max_q: an upper bound on the queries of one sequence (1 when decoding).
+ *   max_q: an upper bound on the queries of one sequence (1 when decoding), from 1 to total_q: a
+ *       caller with a constant bound passes the smaller of the two.
  *   scales finite and >= 0 (of pages in use; V scales best within 2^20 of each other).
  *   Components of q that are small beside their row's largest lose bits where max_q * Hq / Hkv is above
  *       16: below 2^-13 of the largest they are off by up to 2^-21 of it.
@@ -215,7 +216,8 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
 
 /*
  * Bytes of workspace attn_fwd_kv_fp8 needs on the current device: depends on these sizes only,
- * not on the lengths; (size_t)-1 for invalid sizes.
+ * not on the lengths, and does not fall as max_q grows (the workspace for a bound serves every call
+ * with a smaller one; max_q may exceed total_q here); (size_t)-1 for invalid sizes.
  */
 size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d);
 

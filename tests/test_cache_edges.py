@@ -85,3 +85,10 @@ def test_yarn_refusals_and_far_ends(A):
     assert short[0] == 1.0 and (np.diff(short / f) <= 1e-12).all() and abs(short[-1] / f[-1] - 0.5) < 1e-12
     long = A.attn_rope_freqs(64, scaling="yarn", factor=2.0, trained_length=1 << 40, device="cpu")[0].numpy()
     np.testing.assert_allclose(long, f, rtol=1e-13)                                                         # all make more
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [(8, 2), (32, 1), (5, 5)])
+def test_workspace_does_not_fall_as_the_bound_grows(A, heads, d):
+    sizes = [A.attn_fwd_kv_fp8_workspace_size(3, *heads, total, mq, d) for total in (3, 70) for mq in range(1, 60)]
+    assert sizes[:59] == sizes[59:] == sorted(sizes[:59]) and sizes[0] > 0

@@ -219,3 +219,28 @@ def test_rotary_outputs_in_wider_and_permuted_layouts(A):
     with pytest.raises(A.AttnError, match="overlap"):
         A.attn_rope(x, None, f, q_out=buf.as_strided((2, 3, 5, 64), (1024, 64, 64, 1)))
     assert (buf == 0).all()
+
+
+@pytest.mark.parametrize("bound", [3, 4, 5, 64, 512])
+def test_a_constant_bound_over_short_steps(A, bound):
+    """A server keeps the workspace of its largest piece and passes min(bound, packed queries): steps with
+    fewer rows than the bound, down to a single token, give what the tightest bound gives."""
+    for ns, lens in (([1], [300]), ([1, 1], [40, 700]), ([3, 1, 2], [3, 90, 500])):
+        c = filled(lens, ns, 8, 2, 32, 64, seed=len(ns))
+        ws = torch.full((A.attn_fwd_kv_fp8_workspace_size(len(ns), 8, 2, sum(ns), bound, 64),), 0xFF, dtype=torch.uint8, device=DEV)
+        o, lse = attend(A, c, max_q=min(bound, sum(ns)), workspace=ws)
+        check(o, lse, reference(c), 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [(4, 1), (8, 2)])
+def test_sequences_without_keys_among_units_of_two_tiles(A, heads, d):
+    """Units of 256 rows beside sequences without keys, without queries, and short ones (not causal)."""
+    lens, ns = [0, 300, 0, 700, 0, 5, 0], [200, 300, 0, 130, 1, 0, 70]
+    c = filled(lens, ns, *heads, 64, d, seed=3)
+    o, lse = attend(A, c, causal=False)
+    check(o, lse, reference(c, False), d)
+    for b, n in enumerate(lens):
+        if n == 0:
+            sl = slice(c["cu"][b], c["cu"][b + 1])
+            assert (o[:, sl] == 0).all() and torch.isneginf(lse[:, sl]).all()
