@@ -107,8 +107,10 @@ enum {
 static_assert(T_COUNT * 8 <= 512, "barriers fit the control block's first 512 bytes");
 constexpr int kUnitSlots = 4, kUnitReaders = 15;   // producer, 2 MMA issuers, 8 softmax and 4 widening warps
 
-// sum_{i=0}^{n-1} floor((a i + b) / m) in O(log) steps, for a n + b < 2^32 (64-bit divisions made a
-// CTA's start 4 us longer).
+// sum_{i=0}^{n-1} floor((a i + b) / m), for a n + b < 2^32 (64-bit divisions made a CTA's start 4 us
+// longer).  The sum counts lattice points under a line; taking whole parts of a / m and b / m out and
+// then exchanging the axes turns (a, m) into (m, a mod m), as Euclid's algorithm does, so it ends after
+// O(log) steps.
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long s = 0;
   while (n > 0) {
@@ -534,37 +536,37 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const int kt0 = max(0, -ubeg - cost), kt1 = min(uend, end) - ubeg - cost;
           const bool over = ubeg >= end;
           if (over || kt1 > kt0) {
-          if (nu >= kUnitSlots && !mbar_wait(BAR(T_UFREE + nu % kUnitSlots), (nu / kUnitSlots - 1) & 1, wc)) break;
-          UnitDesc& U = desc[nu % kUnitSlots];
-          if (over) {
-            U.nmax = -1;
-            mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
-            break;
-          }
-          const int rows = min(qu, sq.n - rt * qu) * p.g;
-          int nt[2];
+            if (nu >= kUnitSlots && !mbar_wait(BAR(T_UFREE + nu % kUnitSlots), (nu / kUnitSlots - 1) & 1, wc)) break;
+            UnitDesc& U = desc[nu % kUnitSlots];
+            if (over) {
+              U.nmax = -1;
+              mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
+              break;
+            }
+            const int rows = min(qu, sq.n - rt * qu) * p.g;
+            int nt[2];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int r = min(rows, (t + 1) * 128) - t * 128;           // rows of the tile
-            const int lim = r > 0 ? (p.causal ? sq.len - sq.n + rt * qu + (t * 128 + r - 1) / p.g + 1 : sq.len) : 0;
-            nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
-          }
-          U.nmax = max(nt[0], nt[1]);
-          U.nt[0] = SPLIT ? (nt[0] + 1) / 2 : nt[0];
-          U.nt[1] = SPLIT ? nt[0] / 2 : nt[1];
-          U.kt0 = kt0;
-          U.len = sq.len;
-          U.b = b;
-          U.h = h;
-          U.rows = rows;
-          U.q0 = sq.q0 + rt * qu;
-          U.lim0 = p.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
-          U.whole = kt0 == 0 && uend <= end ? 1 : 0;
-          U.second = first ? 0 : 1;
-          U.more = kt0 == 0 ? (uend - 1) / step_run : -1;   // cut: the CTAs behind this one that go on with it
-          first = false;
-          mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
-          ++nu;
+            for (int t = 0; t < 2; ++t) {
+              const int r = min(rows, (t + 1) * 128) - t * 128;           // rows of the tile
+              const int lim = r > 0 ? (p.causal ? sq.len - sq.n + rt * qu + (t * 128 + r - 1) / p.g + 1 : sq.len) : 0;
+              nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
+            }
+            U.nmax = max(nt[0], nt[1]);
+            U.nt[0] = SPLIT ? (nt[0] + 1) / 2 : nt[0];
+            U.nt[1] = SPLIT ? nt[0] / 2 : nt[1];
+            U.kt0 = kt0;
+            U.len = sq.len;
+            U.b = b;
+            U.h = h;
+            U.rows = rows;
+            U.q0 = sq.q0 + rt * qu;
+            U.lim0 = p.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
+            U.whole = kt0 == 0 && uend <= end ? 1 : 0;
+            U.second = first ? 0 : 1;
+            U.more = kt0 == 0 ? (uend - 1) / step_run : -1;   // cut: the CTAs behind this one that go on with it
+            first = false;
+            mbar_arrive(BAR(T_UFULL + nu % kUnitSlots));
+            ++nu;
           }
           ubeg = uend;
           if (ubeg >= end) continue;

@@ -10,7 +10,8 @@
 // fixed-point number F_j = f_j / 2 pi mod 1 in units of 2^-64 turns; p F_j mod 2^64 is then
 // an exact integer product, its upper 32 bits the angle in turns with the whole turns
 // already dropped, so position 10^6 is as exact as position 1 and no argument reduction is
-// needed (sincospif of a number in [-1, 1)).  fp32 p f_j would be wrong by 0.06 rad there.
+// needed (sincospif of a number in [-1, 1), rounded from these bits by at most 2^-25 half turns, 9.4e-8
+// rad).  fp32 p f_j would be wrong by 0.06 rad there.
 //
 // Bound by bytes (2 read and 2 written per element).  A CTA takes a tile of tokens of one
 // sequence and every head of them: the cosines and sines are computed once per token into

@@ -142,8 +142,9 @@ size_t attn_fwd_kv_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d)
  *       of a fused projection [B,N,H,d] need no copy.  An output's rows lie apart: in ascending
  *       order, each of its strides reaches past what the smaller ones span.  Rows that start on 16 bytes are fastest
  *       (with rot a multiple of 16); any 2-byte aligned ones work.
- *   inv_freq: DEVICE fp64 [rot/2], radians per position (scaling for long contexts is in these
- *       values and in mscale).  The angle is exact to 2^-32 turns plus 2^-52 of p * inv_freq.
+ *   inv_freq: DEVICE fp64 [rot/2], radians per position, finite (scaling for long contexts is in
+ *       these values and in mscale).  The angle is exact to 2^-26 turns (9.4e-8 radians) plus 2^-52 of
+ *       p * inv_freq.
  *   positions: DEVICE int32 [B,N], or NULL for 0 .. N-1.
  *   d: 64, 128, 192 or 256; rot even, 2 .. d; mscale finite; N below 2^31 - 65536, Hq + Hk up to 65535.
  * Packed sequences ([H, total, d]): B = 1, N = total and the positions of each row.
@@ -173,7 +174,7 @@ int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, co
  *   cu_seqlens[b+1]-1 (n of them; DEVICE int32, B + 1 offsets) become rows kv_lens[b] - n ..
  *   kv_lens[b] - 1 of sequence b.  Per page and head touched, with amax the largest finite |x|
  *   of the new rows: scale = the smallest power of two with amax / scale <= 448 (0 for amax =
- *   0), code = e4m3(x / scale) rounded to nearest even, infinities saturated to +-448, NaN kept.
+ *   0, else not below 2^-126), code = e4m3(x / scale) rounded to nearest even, infinities saturated to +-448, NaN kept.
  *   Where earlier rows stay in the page its scale may only grow, and if it does their codes are
  *   rounded again at the new scale.  Rows behind the last one are left as they were.
  *   strides: NULL for contiguous rows, or a HOST array {k head, k token, v head, v token} of
@@ -192,14 +193,16 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  * LSE, K~ and V~ the dequantised rows.  Decoding (one query per sequence), drafts of a few tokens
  * and pieces of prompts, mixed freely.  Query i of sequence b's n stands at key position
  * i + kv_lens[b] - n (causal: it sees keys up to there; otherwise all kv_lens[b]).
+ * max_q * Hq / Hkv up to 16 takes the kernel for few rows, more the one for many, for all sequences
+ * of the call: single tokens beside a piece of a prompt take longer than in a call of their own.
  *
  *   q, o [Hq, total_q, d] bf16; lse [Hq, total_q] fp32 (natural log); cu_seqlens_q as
  *       attn_fwd_varlen; the cache as above.
  *   max_q: an upper bound on the queries of one sequence (1 when decoding), from 1 to total_q: a
  *       caller with a constant bound passes the smaller of the two.
  *   scales finite and >= 0 (of pages in use; V scales best within 2^20 of each other).
- *   Components of q that are small beside their row's largest lose bits where max_q * Hq / Hkv is above
- *       16: below 2^-13 of the largest they are off by up to 2^-21 of it.
+ *   Components of q that are small beside their row's largest lose bits where max_q * Hq / Hkv is
+ *       above 16: below 2^-13 of the largest they are off by up to 2^-21 of it.
  *   Codes of rows behind kv_lens[b] are never used, whatever they are, and a NaN in the cache
  *   reaches the queries that see its row, no others.
  *   Hq / Hkv up to 256.
