@@ -38,7 +38,8 @@
 // Measured: two prompts of 4096 over 8192 keys, 32 heads on 8, d = 128: 680 us, 1212 TFLOP/s (a
 // two-tile step of 128 keys takes 3900 cycles, of which the tensor cores need 2050 and shared memory
 // 2180); four pieces of up to 512 over up to 16000 keys: 234 us, 1093 TFLOP/s.  SPLIT: 16 sequences
-// of 16000 keys, 8 K/V heads of 32 rows: 141 us, 3.7 TB/s of cache (198 us without).
+// of 16000 keys, 8 K/V heads of 32 rows: 141 us, 3.7 TB/s of cache (198 us without).  d = 64, where a
+// key's exponentials cost the same for half the products: the prompts 577 us, 715 TFLOP/s.
 //
 // Shared memory (d = 128): Q1, Q2 2 x 32 KB, K8 ring 2 x 16 KB, V8 ring 3 x 16 KB, V16 2 x 32 KB.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P_t (f16 pairs) overwrites S_t.

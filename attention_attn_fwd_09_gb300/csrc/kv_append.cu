@@ -15,7 +15,7 @@
 //   * prompts (bound by bytes, 2 read and 1 written per element): a CTA per slot, head and K or
 //     V holds the page's new rows in registers between the maximum and the rounding, one pass
 //     over the data.  8192 rows of 8 heads twice, d = 128: 20.5 us from memory, 4.9
-//     TB/s (again and again on rows that L2 holds 14.6);
+//     TB/s (again and again on rows that L2 holds 15.1; d = 64 9.2);
 //   * a few rows per sequence or page (bound by latency): a warp per slot, head and K or V, no
 //     barrier behind the search for the slot.  One row of 64 sequences: 2.5 us in a graph.
 #include <cstdint>
