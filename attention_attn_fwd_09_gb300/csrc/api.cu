@@ -939,7 +939,8 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
   if (max_q < 1 || max_q > total_q)
-    return fail(ATTN_ERR_INVALID_ARG, "max_q=%d must be between 1 and the %d packed queries (pass the smaller of a constant bound and these)",
+    return fail(ATTN_ERR_INVALID_ARG,
+                "max_q=%d must be between 1 and the %d packed queries (of a constant bound and these pass the smaller)",
                 max_q, total_q);
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens_q || !kv_lens || !o || !lse)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");

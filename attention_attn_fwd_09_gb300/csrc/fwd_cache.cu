@@ -25,9 +25,9 @@
 // With d = 64 (half the bytes, as many scores) the same take 0.78, 0.76 and 0.98 of these times.
 //
 // Numbers: q is scaled by a power of two per row (largest |q| in [2^14, 2^15)) and held in f16: exact
-// down to 2^-31 of the row's largest component, off by at most 2^-39 of it below.  exp2(s - m + 14) <= 2^14 times the
-// page's V scale over the largest V scale so far is rounded to f16 (11 bits, against 8 of a
-// bf16 weight; the 2^14 keeps weights down to 2^-28 of the largest normal).  Scores, maxima,
+// down to 2^-31 of the row's largest component, off by at most 2^-39 of it below.  exp2(s - m + 14)
+// <= 2^14 times the page's V scale over the largest V scale so far is rounded to f16 (11 bits, against
+// 8 of a bf16 weight; the 2^14 keeps weights down to 2^-28 of the largest normal).  Scores, maxima,
 // sums and O are fp32.
 #include <cstdint>
 #include <mutex>
