@@ -208,7 +208,7 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  *   Hq / Hkv up to 256.
  *   A query that sees no key (kv_lens[b] = 0, not causal) gets O = 0 and LSE = -inf.
  *   workspace: device memory of attn_fwd_kv_fp8_workspace_size(...) bytes, 16-byte aligned, owned
- *       by the caller, contents on entry irrelevant.
+ *       by the caller, contents on entry irrelevant; calls (graphs) that may run at once need one each.
  * Errors as attn_kv_append_fp8's (with causal: n <= kv_lens[b]; and n <= max_q), plus
  *   ATTN_ERR_WORKSPACE; the results of a sequence with a bad page are undefined.
  */
