@@ -91,6 +91,14 @@ _lib.attn_fwd_kv_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i,
 _lib.attn_fwd_kv_fp8.restype = _i
 _lib.attn_fwd_kv_fp8_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.attn_fwd_kv_fp8_workspace_size.restype = _sz
+_lib.attn_fwd_kv_fp8_pages.argtypes = [_p] * 11 + [_i] * 10 + [_f, _p, _sz, _p]
+_lib.attn_fwd_kv_fp8_pages.restype = _i
+_lib.attn_fwd_kv_fp8_pages_workspace_size.argtypes = [_i, _i, _i, _i]
+_lib.attn_fwd_kv_fp8_pages_workspace_size.restype = _sz
+_lib.attn_fwd_kv_fp8_prefix.argtypes = [_p] * 13 + [_i] * 13 + [_f, _p, _sz, _p]
+_lib.attn_fwd_kv_fp8_prefix.restype = _i
+_lib.attn_fwd_kv_fp8_prefix_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+_lib.attn_fwd_kv_fp8_prefix_workspace_size.restype = _sz
 _lib.attn_exp2_sw.argtypes = [_p, _p, _ll, _i, _p]
 _lib.attn_exp2_sw.restype = _i
 
@@ -676,6 +684,118 @@ def attn_fwd_kv_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlen
     return o, lse
 
 
+def _outputs(q, o, lse, dev):
+    """q [H, T, d] checked, and o, lse like it: made here unless given."""
+    shape = Hq, T, _ = q.shape
+    if o is None:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    if not (q.dtype is torch.bfloat16 and o.dtype is torch.bfloat16 and lse.dtype is torch.float32 and o.shape == shape
+            and lse.shape == (Hq, T) and o.device == dev and lse.device == dev and q.is_contiguous() and o.is_contiguous()
+            and lse.is_contiguous()):
+        _plain("q", q, torch.bfloat16, shape, dev)
+        _plain("o", o, torch.bfloat16, shape, dev)
+        _plain("lse", lse, torch.float32, (Hq, T), dev)
+    return o, lse
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, checked, or one of need() bytes."""
+    if workspace is None:
+        return torch.empty((max(need(), 16),), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
+    return workspace
+
+
+def attn_fwd_kv_fp8_pages_workspace_size(Hq: int, Hkv: int, total_q: int, d: int) -> int:
+    n = _lib.attn_fwd_kv_fp8_pages_workspace_size(Hq, Hkv, total_q, d)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(-1, attn_last_error())
+    return int(n)
+
+
+def attn_fwd_kv_fp8_pages(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, pages,
+                          causal: bool = True, scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """O, LSE of packed queries over listed pages only: ``pages`` int32 [Hkv, total_q, count] holds
+    for each K/V head and query distinct page numbers within the query's sequence (0 is its first
+    page, as ``attn_select_pages_fp8`` returns them), negative ones being left out.  Keys the query
+    does not see (causal) are masked; other arguments as ``attn_fwd_kv_fp8``.  ``workspace``: a uint8 CUDA
+    tensor of at least attn_fwd_kv_fp8_pages_workspace_size(...) bytes (allocated when None)."""
+    if not q.is_cuda or q.dim() != 3:
+        raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
+    dev = q.device
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_fwd_kv_fp8_pages(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, pages,
+                                         causal, scale, o, lse, workspace)
+    num_pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q,
+                                                    "cu_seqlens_q", kv_lens, dev)
+    Hq, T, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has {dq} columns, the cache {d}")
+    o, lse = _outputs(q, o, lse, dev)
+    if pages.dim() != 3:
+        raise ValueError(f"pages: expected [Hkv, total_q, count], got {tuple(pages.shape)}")
+    count = pages.shape[2]
+    _plain("pages", pages, torch.int32, (Hkv, T, count), dev)
+    ws = _workspace(workspace, lambda: attn_fwd_kv_fp8_pages_workspace_size(Hq, Hkv, T, d), dev)
+    _check(_lib.attn_fwd_kv_fp8_pages(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                      v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+                                      pages.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, count, d, num_pages, P,
+                                      width, 1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(),
+                                      ws.nbytes, _current_stream(dev.index)))
+    return o, lse
+
+
+def attn_fwd_kv_fp8_prefix_workspace_size(Hq: int, Hkv: int, total_q: int, max_prefix_q: int, max_q: int, d: int) -> int:
+    n = _lib.attn_fwd_kv_fp8_prefix_workspace_size(Hq, Hkv, total_q, max_prefix_q, max_q, d)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(-1, attn_last_error())
+    return int(n)
+
+
+def attn_fwd_kv_fp8_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, cu_prefix_q, prefix_lens,
+                           max_prefix_q: int, page_table, cu_seqlens_q, kv_lens, max_q: int, causal: bool = True,
+                           scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """``attn_fwd_kv_fp8`` of sequences that begin with shared prefixes, whose keys are read once for
+    all their queries: packed queries cu_prefix_q[g] .. cu_prefix_q[g+1]-1 (at most ``max_prefix_q``)
+    see all prefix_lens[g] keys of the pages prefix_table[g] (int32 [G, max_prefix_pages]), then,
+    as in ``attn_fwd_kv_fp8``, the kv_lens[b] keys of their own sequence's pages page_table[b].  A length
+    may be 0.  ``workspace``: a uint8 CUDA tensor of at least
+    attn_fwd_kv_fp8_prefix_workspace_size(...) bytes (allocated when None)."""
+    if not q.is_cuda or q.dim() != 3:
+        raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
+    dev = q.device
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_fwd_kv_fp8_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, cu_prefix_q, prefix_lens,
+                                          max_prefix_q, page_table, cu_seqlens_q, kv_lens, max_q, causal, scale, o, lse,
+                                          workspace)
+    num_pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q,
+                                                    "cu_seqlens_q", kv_lens, dev)
+    Hq, T, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has {dq} columns, the cache {d}")
+    if prefix_table.dim() != 2:
+        raise ValueError(f"prefix_table: expected [G, max_prefix_pages], got {tuple(prefix_table.shape)}")
+    G, prefix_width = prefix_table.shape
+    for name, t, shape in (("prefix_table", prefix_table, (G, prefix_width)), ("cu_prefix_q", cu_prefix_q, (G + 1,)),
+                           ("prefix_lens", prefix_lens, (G,))):
+        _plain(name, t, torch.int32, shape, dev)
+    o, lse = _outputs(q, o, lse, dev)
+    ws = _workspace(workspace, lambda: attn_fwd_kv_fp8_prefix_workspace_size(Hq, Hkv, T, max_prefix_q, max_q, d), dev)
+    _check(_lib.attn_fwd_kv_fp8_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), prefix_table.data_ptr(), cu_prefix_q.data_ptr(),
+                                       prefix_lens.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(),
+                                       kv_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), G, B, Hq, Hkv, T, max_prefix_q, max_q,
+                                       d, num_pages, P, prefix_width, width, 1 if causal else 0,
+                                       d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
+                                       _current_stream(dev.index)))
+    return o, lse
+
+
 def attn_set_debug_knobs(tau: float = 8.0, poly_per_16: int = 0, wait_limit_ns: int = 2_000_000_000,
                          sync_check: bool = False):
     _check(_lib.attn_set_debug_knobs(float(tau), int(poly_per_16), int(wait_limit_ns), int(bool(sync_check))))
@@ -715,4 +835,6 @@ def attn_exp2_sw(x, variant: int = 0, stream=None):
 __all__ = ["attn_fwd", "attn_fwd_fp8", "attn_quantize_fp8", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_workspace_size", "attn_last_error", "attn_version",
            "attn_set_debug_knobs", "attn_get_debug_knobs", "attn_device_status", "attn_rescale_counter",
            "attn_exp2_sw", "attn_set_test_hooks", "attn_rope", "attn_rope_bwd", "attn_rope_freqs", "attn_kv_append_fp8",
-           "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "AttnError", "LIB_PATH"]
+           "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "attn_fwd_kv_fp8_pages",
+           "attn_fwd_kv_fp8_pages_workspace_size", "attn_fwd_kv_fp8_prefix", "attn_fwd_kv_fp8_prefix_workspace_size",
+           "AttnError", "LIB_PATH"]

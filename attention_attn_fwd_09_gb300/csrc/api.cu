@@ -927,63 +927,209 @@ size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int m
   return cache_workspace_bytes(Hq, Hkv, max_q, d, sms);
 }
 
-int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
-                    const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o,
-                    float* lse, int B, int Hq, int Hkv, int total_q, int max_q, int d, int num_pages, int page_size,
-                    int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_cache(B, Hkv, total_q, d, num_pages, page_size, max_pages);
+// The checks and parameters that the calls of attention over the cache share.
+struct CacheCall {
+  const void *q, *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int *page_table, *cu_seqlens_q, *kv_lens;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, total_q, d, num_pages, page_size, max_pages, causal;
+  float scale;
+};
+static int check_cache_call(const CacheCall& c) {
+  int rc = check_cache(c.B, c.Hkv, c.total_q, c.d, c.num_pages, c.page_size, c.max_pages);
   if (rc != ATTN_OK) return rc;
-  if ((rc = check_shape(B, Hq, Hkv, total_q, d, scale)) != ATTN_OK) return rc;
-  if (Hq > 65535) return fail(ATTN_ERR_UNSUPPORTED, "Hq=%d: packed sequences support at most 65535 heads", Hq);
-  if (Hq / Hkv > 256) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv = %d (supported: up to 256)", Hq / Hkv);
-  if (B == 0 || total_q == 0) return ATTN_OK;
-  if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
+  if ((rc = check_shape(c.B, c.Hq, c.Hkv, c.total_q, c.d, c.scale)) != ATTN_OK) return rc;
+  if (c.Hq > 65535) return fail(ATTN_ERR_UNSUPPORTED, "Hq=%d: packed sequences support at most 65535 heads", c.Hq);
+  if (c.Hq / c.Hkv > 256) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv = %d (supported: up to 256)", c.Hq / c.Hkv);
+  if (c.B == 0 || c.total_q == 0) return ATTN_OK;
+  if (c.num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", c.total_q);
+  return ATTN_OK;
+}
+static int check_max_q(const char* name, int max_q, int total_q) {
   if (max_q < 1 || max_q > total_q)
     return fail(ATTN_ERR_INVALID_ARG,
-                "max_q=%d must be between 1 and the %d packed queries (of a constant bound and these pass the smaller)",
-                max_q, total_q);
-  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens_q || !kv_lens || !o || !lse)
+                "%s=%d must be between 1 and the %d packed queries (of a constant bound and these pass the smaller)",
+                name, max_q, total_q);
+  return ATTN_OK;
+}
+static int check_cache_pointers(const CacheCall& c) {
+  if (!c.q || !c.k_cache || !c.v_cache || !c.k_scale || !c.v_scale || !c.page_table || !c.cu_seqlens_q || !c.kv_lens ||
+      !c.o || !c.lse)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(q) || !aligned16(o) || !aligned16(k_cache) || !aligned16(v_cache))
+  if (!aligned16(c.q) || !aligned16(c.o) || !aligned16(c.k_cache) || !aligned16(c.v_cache))
     return fail(ATTN_ERR_MISALIGNED, "q, o and the cache must be 16-byte aligned");
-  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) || !aligned4(cu_seqlens_q) ||
-      !aligned4(kv_lens) || !aligned4(lse))
+  if (!aligned4(c.k_scale) || !aligned4(c.v_scale) || !aligned4(c.page_table) || !aligned4(c.cu_seqlens_q) ||
+      !aligned4(c.kv_lens) || !aligned4(c.lse))
     return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets, lengths and lse must be 4-byte aligned");
-  const DevSyms* s = dev_syms(nullptr);
-  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
-  const size_t need = cache_workspace_bytes(Hq, Hkv, max_q, d, sms);
-  if (!workspace || workspace_bytes < need)
-    return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  return ATTN_OK;
+}
+static int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need) return fail(ATTN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", bytes, need);
   if (!aligned16(workspace)) return fail(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
-  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  return ATTN_OK;
+}
+static CacheParams cache_params(const CacheCall& c, int max_q, void* workspace, const DevSyms* s) {
   CacheParams p{};
-  p.q = q;
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.k_scale = k_scale; p.v_scale = v_scale;
-  p.table = page_table; p.cu_q = cu_seqlens_q; p.kv_lens = kv_lens;
-  p.o = o; p.lse = lse;
-  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.total_q = total_q; p.max_q = max_q;
-  p.num_pages = num_pages; p.page = page_size; p.max_pages = max_pages; p.max_len = max_pages * page_size;
-  p.causal = causal ? 1 : 0;
-  p.c = scale * 1.4426950408889634f;
+  p.q = c.q;
+  p.k_cache = static_cast<const uint8_t*>(c.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(c.v_cache);
+  p.k_scale = c.k_scale; p.v_scale = c.v_scale;
+  p.table = c.page_table; p.cu_q = c.cu_seqlens_q; p.kv_lens = c.kv_lens;
+  p.o = c.o; p.lse = c.lse;
+  p.B = c.B; p.Hq = c.Hq; p.Hkv = c.Hkv; p.g = c.Hq / c.Hkv; p.total_q = c.total_q; p.max_q = max_q;
+  p.num_pages = c.num_pages; p.page = c.page_size; p.max_pages = c.max_pages; p.max_len = c.max_pages * c.page_size;
+  p.causal = c.causal ? 1 : 0;
+  p.c = c.scale * 1.4426950408889634f;
   p.ws = workspace;
   p.wait_ns = (unsigned long long)g_wait_ns.load();
   p.status = s->status;
   p.test_skip_first_kv = g_test_skip_kv.load();
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  const bool few = (long long)max_q * p.g <= kCacheDecodeRows;
-  const int box = std::min(page_size, few ? 32 : 128);       // keys per copy
-  const long long slabs = (long long)num_pages * Hkv;
+  return p;
+}
+// few: the kernels for few rows (pieces of 32 keys), else the tiles (blocks of 128).
+static int cache_maps(const CacheCall& c, bool few, CacheMaps* maps) {
+  const int box = std::min(c.page_size, few ? 32 : 128), d = c.d;      // keys per copy
+  const long long slabs = (long long)c.num_pages * c.Hkv;
   const int kline = few ? 128 : d;
+  const int rc = make_map_cache(&maps->k, c.k_cache, kline, c.page_size * d / kline, slabs, box * d / kline, "k_cache");
+  if (rc != ATTN_OK) return rc;
+  return make_map_cache(&maps->v, c.v_cache, 128, c.page_size * d / 128, slabs, box * d / 128, "v_cache");
+}
+static bool few_rows(const CacheParams& p) { return (long long)p.max_q * p.g <= kCacheDecodeRows; }
+static int launch_cache(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t st) {
+  const cudaError_t e = few_rows(p) ? launch_fwd_cache_decode(maps, p, d, sms, st) : launch_fwd_cache_tile(maps, p, d, sms, st);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "cached attention launch");
+}
+
+int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o,
+                    float* lse, int B, int Hq, int Hkv, int total_q, int max_q, int d, int num_pages, int page_size,
+                    int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const CacheCall c{q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, o, lse,
+                    B, Hq, Hkv, total_q, d, num_pages, page_size, max_pages, causal, scale};
+  int rc = check_cache_call(c);
+  if (rc != ATTN_OK || B == 0 || total_q == 0) return rc;
+  if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
+  if ((rc = check_cache_pointers(c)) != ATTN_OK) return rc;
+  const DevSyms* s = dev_syms(nullptr);
+  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
+  if ((rc = check_workspace(workspace, workspace_bytes, cache_workspace_bytes(Hq, Hkv, max_q, d, sms))) != ATTN_OK) return rc;
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const CacheParams p = cache_params(c, max_q, workspace, s);
   CacheMaps maps;
-  if ((rc = make_map_cache(&maps.k, k_cache, kline, page_size * d / kline, slabs, box * d / kline, "k_cache")) != ATTN_OK)
-    return rc;
-  if ((rc = make_map_cache(&maps.v, v_cache, 128, page_size * d / 128, slabs, box * d / 128, "v_cache")) != ATTN_OK)
-    return rc;
-  e = few ? launch_fwd_cache_decode(maps, p, d, sms, st) : launch_fwd_cache_tile(maps, p, d, sms, st);
-  if (e != cudaSuccess) return cuda_fail(e, "cached attention launch");
+  if ((rc = cache_maps(c, few_rows(p), &maps)) != ATTN_OK) return rc;
+  if ((rc = launch_cache(maps, p, d, sms, st)) != ATTN_OK) return rc;
+  return post_launch(s, st);
+}
+
+// Query heads that one unit of the listed pages' kernel holds: a group's, or its largest share of at most 16.
+static int list_group(int g) {
+  int share = std::min(g, kCacheDecodeRows);
+  while (g % share != 0) --share;
+  return share;
+}
+
+size_t attn_fwd_kv_fp8_pages_workspace_size(int Hq, int Hkv, int total_q, int d) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total_q < 0 || (d != 64 && d != 128)) {
+    set_last_error("attn_fwd_kv_fp8_pages_workspace_size: invalid sizes");
+    return (size_t)-1;
+  }
+  if (total_q == 0) return 0;
+  const DevSyms* s = dev_syms(nullptr);
+  return cache_decode_workspace_bytes(list_group(Hq / Hkv), d, s->err == cudaSuccess ? std::max(1, s->sms) : 1);
+}
+
+int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens,
+                          const int* pages, void* o, float* lse, int B, int Hq, int Hkv, int total_q, int count, int d,
+                          int num_pages, int page_size, int max_pages, int causal, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const CacheCall c{q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, o, lse,
+                    B, Hq, Hkv, total_q, d, num_pages, page_size, max_pages, causal, scale};
+  int rc = check_cache_call(c);
+  if (rc != ATTN_OK) return rc;
+  if (count < 0) return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 0", count);
+  if (B == 0 || total_q == 0) return ATTN_OK;
+  if ((rc = check_cache_pointers(c)) != ATTN_OK) return rc;
+  if (count > 0 && !pages) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned4(pages)) return fail(ATTN_ERR_MISALIGNED, "pages must be 4-byte aligned");
+  const DevSyms* s = dev_syms(nullptr);
+  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1, share = list_group(Hq / Hkv);
+  if ((rc = check_workspace(workspace, workspace_bytes, cache_decode_workspace_bytes(share, d, sms))) != ATTN_OK) return rc;
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  CacheParams p = cache_params(c, total_q, workspace, s);
+  p.list = pages;
+  p.list_count = count;
+  p.rep = Hq / Hkv / share;
+  p.Hkv = Hkv * p.rep;
+  p.g = share;
+  CacheMaps maps;
+  if ((rc = cache_maps(c, true, &maps)) != ATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_fwd_cache_pages(maps, p, d, sms, st);
+  if (e != cudaSuccess) return cuda_fail(e, "listed pages attention launch");
+  return post_launch(s, st);
+}
+
+// Both parts' workspace, used one after the other, then the first part's results and whether it was valid.
+struct PrefixWs {
+  size_t lse, o, bad, total;
+};
+static PrefixWs prefix_ws(int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d, int sms) {
+  PrefixWs w;
+  const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  w.lse = up(std::max(cache_workspace_bytes(Hq, Hkv, max_prefix_q, d, sms), cache_workspace_bytes(Hq, Hkv, max_q, d, sms)));
+  w.o = w.lse + up((size_t)Hq * total_q * 4);
+  w.bad = w.o + up((size_t)Hq * total_q * d * 4);
+  w.total = w.bad + 256;
+  return w;
+}
+
+size_t attn_fwd_kv_fp8_prefix_workspace_size(int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total_q < 0 || max_prefix_q < 0 || max_q < 0 || (d != 64 && d != 128)) {
+    set_last_error("attn_fwd_kv_fp8_prefix_workspace_size: invalid sizes");
+    return (size_t)-1;
+  }
+  if (total_q == 0) return 0;
+  const DevSyms* s = dev_syms(nullptr);
+  return prefix_ws(Hq, Hkv, total_q, max_prefix_q, max_q, d, s->err == cudaSuccess ? std::max(1, s->sms) : 1).total;
+}
+
+int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* prefix_table, const int* cu_prefix_q, const int* prefix_lens,
+                           const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o, float* lse, int G,
+                           int B, int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d, int num_pages,
+                           int page_size, int max_prefix_pages, int max_pages, int causal, float scale, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const CacheCall shared{q, k_cache, v_cache, k_scale, v_scale, prefix_table, cu_prefix_q, prefix_lens, o, lse,
+                         G, Hq, Hkv, total_q, d, num_pages, page_size, max_prefix_pages, 0, scale};
+  const CacheCall mine{q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, kv_lens, o, lse,
+                       B, Hq, Hkv, total_q, d, num_pages, page_size, max_pages, causal, scale};
+  int rc = check_cache_call(shared);
+  if (rc != ATTN_OK || (rc = check_cache_call(mine)) != ATTN_OK || total_q == 0) return rc;
+  if ((rc = check_max_q("max_prefix_q", max_prefix_q, total_q)) != ATTN_OK) return rc;
+  if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
+  if ((rc = check_cache_pointers(shared)) != ATTN_OK || (rc = check_cache_pointers(mine)) != ATTN_OK) return rc;
+  const DevSyms* s = dev_syms(nullptr);
+  const int sms = s->err == cudaSuccess ? std::max(1, s->sms) : 1;
+  const PrefixWs w = prefix_ws(Hq, Hkv, total_q, max_prefix_q, max_q, d, sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total)) != ATTN_OK) return rc;
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CacheParams p[2] = {cache_params(shared, max_prefix_q, workspace, s), cache_params(mine, max_q, workspace, s)};
+  CacheMaps maps[2];
+  for (int i = 0; i < 2; ++i) {
+    p[i].side = i == 0 ? SIDE_OUT : SIDE_IN;
+    p[i].side_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.lse);
+    p[i].side_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
+    p[i].side_bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.bad);
+    if ((rc = cache_maps(mine, few_rows(p[i]), &maps[i])) != ATTN_OK) return rc;
+  }
+  for (int i = 0; i < 2; ++i)
+    if ((rc = launch_cache(maps[i], p[i], d, sms, st)) != ATTN_OK) return rc;
   return post_launch(s, st);
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -76,6 +77,15 @@ __device__ __forceinline__ void take_nan_codes(uint8_t* piece, int key, int* fir
   }
 }
 constexpr int kNoKey = 0x7fffffff;
+
+// Keys in two parts: a row's O is x own O + y O of the first part, lse2 (log2) of all keys goes to `joint`.
+// 0 and -inf where neither part has a key.
+__device__ __forceinline__ float2 join_side(const CacheParams& p, long long row, float lse2, float& joint) {
+  const float other = p.side_lse[row], mx = fmaxf(lse2, other), mu = mx == -INFINITY ? 0.f : mx;
+  const float a = ex2_mufu(lse2 - mu), b = ex2_mufu(other - mu), sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
+  joint = mx + __log2f(sum);
+  return make_float2(a * inv, b * inv);
+}
 
 // How long a CTA that gives up waits for its own copies and products in flight: not less than 10 ms,
 // however short a wait may be.

@@ -72,27 +72,63 @@ __device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {
   return n > 0 ? max(1, (__ldg(p.kv_lens + b) + kPiece - 1) / kPiece) : 0;
 }
 
+// LIST: a unit is one query and K/V head with a list of pages of its own, laid end to end in pieces.
+// The sequence of packed query t: the last one that starts at or before it (decoding: its own number).
+__device__ __forceinline__ int seq_of(const CacheParams& p, int t) {
+  if (p.B == p.total_q && __ldg(p.cu_q + t) == t && __ldg(p.cu_q + t + 1) == t + 1) return t;
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (__ldg(p.cu_q + mid) <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+// Keys that query t of sequence b sees.
+__device__ __forceinline__ int keys_seen(const CacheParams& p, int b, int t) {
+  const int len = __ldg(p.kv_lens + b);
+  return p.causal ? len - (__ldg(p.cu_q + b + 1) - 1 - t) : len;
+}
+// Pages it sees; as many entries of its list are read at most (they are distinct).
+__device__ __forceinline__ int pages_seen(const CacheParams& p, int b, int t) {
+  return (int)(((unsigned)max(keys_seen(p, b, t), 0) + p.page - 1) / p.page);
+}
+__device__ __forceinline__ int list_pieces(const CacheParams& p, int seen) {
+  return max(1, (min(seen, p.list_count) * p.page + kPiece - 1) / kPiece);
+}
+
 // Where a warp is in the CTA's run of pieces.
+template <bool LIST>
 struct Cursor {
   int b, h;
+  int t, seen;                               // LIST: packed query, the pages it sees
   long long f, ubeg, uend;                   // piece, and the unit's first and last + 1
   __device__ __forceinline__ void settle(const CacheParams& p, long long end) {   // into the unit that holds f
     while (f < end && f >= uend) {
       ubeg = uend;
       if (++h == p.Hkv) {
         h = 0;
-        int np;
-        do np = pieces_of(p, ++b);           // f < end: there is another unit
-        while (np == 0);
-        uend = ubeg + np;
+        if constexpr (LIST) {
+          ++t;                               // f < end: there is another unit
+          while (t >= __ldg(p.cu_q + b + 1)) ++b;
+          seen = pages_seen(p, b, t);
+          uend = ubeg + list_pieces(p, seen);
+        } else {
+          int np;
+          do np = pieces_of(p, ++b);         // f < end: there is another unit
+          while (np == 0);
+          uend = ubeg + np;
+        }
       } else {
-        uend = ubeg + pieces_of(p, b);
+        uend = ubeg + (LIST ? list_pieces(p, seen) : pieces_of(p, b));
       }
     }
   }
 };
 
-template <int D>
+// LIST: attention over listed pages.  p.list [K/V head][query][list_count] holds page numbers within the
+// query's sequence; p.rep virtual heads of p.g query heads share a K/V head (p.Hkv counts virtual ones).
+template <int D, bool LIST>
 __global__ void __launch_bounds__(kThreads, 2)
     fwd_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const CacheParams p, const int rows_max) {
@@ -130,7 +166,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b), n = c1 - c0;
     wrong |= c0 < 0 || c1 < c0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
              (b == 0 && c0 != 0) || (b == p.B - 1 && c1 != p.total_q);
-    if (n > 0) mine += max(1, (len + kPiece - 1) / kPiece);
+    if (!LIST && n > 0) mine += max(1, (len + kPiece - 1) / kPiece);
+  }
+  // LIST: thread t adds up queries [t per_query, ...) instead.
+  const int per_query = (p.total_q + kThreads - 1) / kThreads;
+  const int t_lo = min(tid * per_query, p.total_q), t_hi = min(t_lo + per_query, p.total_q);
+  int b_first = 0;
+  if constexpr (LIST) {
+    if (t_lo < t_hi) b_first = seq_of(p, t_lo);
+    int b = b_first;
+    for (int t = t_lo; t < t_hi; ++t) {
+      while (b < p.B - 1 && t >= __ldg(p.cu_q + b + 1)) ++b;
+      mine += list_pieces(p, pages_seen(p, b, t));
+    }
   }
   long long incl = mine;
 #pragma unroll
@@ -143,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
+    if (p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
   }
-  if (bad) return;
+  if (bad || (p.side == SIDE_IN && *p.side_bad)) return;
   long long before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -160,22 +209,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (rs >= total) return;
   __syncthreads();                           // misc has been read
   if (before <= rs && rs < before + mine) {
-    int b = b_lo;
+    int b = LIST ? b_first : b_lo, t = t_lo;
     long long at = before;
     for (;;) {
-      const long long step = (long long)pieces_of(p, b) * p.Hkv;
+      if constexpr (LIST) {
+        while (t >= __ldg(p.cu_q + b + 1)) ++b;
+      }
+      const long long step = (long long)(LIST ? list_pieces(p, pages_seen(p, b, t)) : pieces_of(p, b)) * p.Hkv;
       if (rs < at + step) break;
       at += step;
-      ++b;
+      if (LIST) ++t;
+      else ++b;
     }
     misc[0] = b;
     misc[1] = at;
+    if (LIST) misc[2] = t;
   }
   __syncthreads();
-  Cursor seg;                                // the unit being worked on
+  Cursor<LIST> seg;                          // the unit being worked on
   seg.b = (int)misc[0];
+  seg.t = seg.seen = 0;
+  if constexpr (LIST) {
+    seg.t = (int)misc[2];
+    seg.seen = pages_seen(p, seg.b, seg.t);
+  }
   {
-    const int np = pieces_of(p, seg.b);
+    const int np = LIST ? list_pieces(p, seg.seen) : pieces_of(p, seg.b);
     seg.h = (int)((rs - misc[1]) / np);
     seg.ubeg = misc[1] + (long long)seg.h * np;
     seg.uend = seg.ubeg + np;
@@ -186,14 +245,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int page_shift = 31 - __clz(p.page);
   const int grp = lane & 1;                  // half of a piece (16 keys) this lane looks after
   uint8_t* ring = smem + warp * C::STAGES * 2 * C::KB;
-  Cursor ahead = seg;
+  Cursor<LIST> ahead = seg;
   ahead.f = rs + warp;
   ahead.settle(p, re);
+  const int kv_heads = LIST ? p.Hkv / p.rep : p.Hkv;
+  auto kv_head = [&](int h) -> int { return LIST && p.rep > 1 ? h / p.rep : h; };
+  int key_ahead = 0;                         // LIST: the first key of this lane's half of the piece at `ahead`
   // The page of this lane's half of the piece at `ahead`: -1 behind the last key, -2 bad.
   auto page_at = [&]() -> int {
     if (ahead.f >= re) return -1;
-    const int key = (int)(ahead.f - ahead.ubeg) * kPiece + grp * 16;
-    if (key >= __ldg(p.kv_lens + ahead.b)) return -1;
+    int key = (int)(ahead.f - ahead.ubeg) * kPiece + grp * 16;
+    if constexpr (LIST) {
+      const int e = key >> page_shift;
+      if (e >= min(ahead.seen, p.list_count)) return -1;
+      const int lp = __ldg(p.list + ((long long)kv_head(ahead.h) * p.total_q + ahead.t) * p.list_count + e);
+      if (lp < 0) return -1;
+      if (lp >= ahead.seen) {                // a page that the query does not see
+        atomicExch(p.status, DEV_BAD_PAGE);
+        return -2;
+      }
+      key = key_ahead = (lp << page_shift) + (key & (p.page - 1));
+    } else {
+      if (key >= __ldg(p.kv_lens + ahead.b)) return -1;
+    }
     const int pg = __ldg(p.table + (long long)ahead.b * p.max_pages + (key >> page_shift));
     if (pg < 0 || pg >= p.num_pages) {
       atomicExch(p.status, DEV_BAD_PAGE);
@@ -203,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   // Scale of this lane's half: K for lanes with bit 1 clear, V with it set.
   auto scale_of = [&](int pg, int h) -> float {
-    return pg >= 0 ? __ldg(((lane & 2) ? p.v_scale : p.k_scale) + (long long)pg * p.Hkv + h) : 0.f;
+    return pg >= 0 ? __ldg(((lane & 2) ? p.v_scale : p.k_scale) + (long long)pg * kv_heads + h) : 0.f;
   };
   auto issue = [&](int stage, int pg) {
     // Pages of 16 rows: two boxes, by lanes 0 and 1; larger ones hold the whole piece.
@@ -219,18 +293,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane < (two ? 2 : 1) && pg >= 0) {
       const int key = (int)(ahead.f - ahead.ubeg) * kPiece + lane * 16;
       const int line = (key & (p.page - 1)) * D / 128;
-      const int z = pg * p.Hkv + ahead.h;
+      const int z = pg * kv_heads + kv_head(ahead.h);
       const uint32_t dst = smem_u32(ring + stage * 2 * C::KB) + lane * box;
       tma_load_3d(dst, &tm_k, 0, line, z, bar);
       tma_load_3d(dst + C::KB, &tm_v, 0, line, z, bar);
     }
   };
   int pages[C::STAGES + 1], heads[C::STAGES + 1];     // of the pieces under way, oldest first; one more looked up
+  int keys[LIST ? C::STAGES + 1 : 1];                 // LIST: first key of this lane's half of each
   bool ok = true;
 #pragma unroll
   for (int i = 0; i <= C::STAGES; ++i) {
     pages[i] = page_at();
-    heads[i] = ahead.h;
+    heads[i] = kv_head(ahead.h);
+    if (LIST) keys[i] = key_ahead;
     if (i < C::STAGES) {
       if (ahead.f < re && !(p.test_skip_first_kv && i == 0)) issue(i, pages[i]);
       ahead.f += kWarps;
@@ -266,7 +342,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = p.g;
   // ---- units
   while (seg.f < re) {
-    const int q0 = __ldg(p.cu_q + seg.b), n = __ldg(p.cu_q + seg.b + 1) - q0, len = __ldg(p.kv_lens + seg.b);
+    const int q0 = LIST ? seg.t : __ldg(p.cu_q + seg.b), n = LIST ? 1 : __ldg(p.cu_q + seg.b + 1) - q0;
+    const int len = LIST ? keys_seen(p, seg.b, seg.t) : __ldg(p.kv_lens + seg.b);
+    if (LIST && seg.f == seg.ubeg) {         // entries behind as many as the query sees pages are not read: none counts
+      const int* entries = p.list + ((long long)kv_head(seg.h) * p.total_q + seg.t) * p.list_count;
+      for (int e = seg.seen + tid; e < p.list_count; e += kThreads)
+        if (__ldg(entries + e) >= 0) atomicExch(p.status, DEV_BAD_PAGE);
+    }
     const long long send = min(seg.uend, re);
     const int rows = n * g;
     // Visible keys of this thread's two rows.
@@ -362,7 +444,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ks[2] = {__shfl_sync(0xffffffffu, sc, 0), __shfl_sync(0xffffffffu, sc, 1)};
         const float vs[2] = {__shfl_sync(0xffffffffu, sc, 2), __shfl_sync(0xffffffffu, sc, 3)};
         const bool got0 = __shfl_sync(0xffffffffu, pg, 0) >= 0, got1 = __shfl_sync(0xffffffffu, pg, 1) >= 0;
-        const bool partial = key0 + kPiece > min_lim || !got0 || !got1;
+        // First key of each half (LIST: on pages of their own).
+        const int kh[2] = {LIST ? __shfl_sync(0xffffffffu, keys[0], 0) : key0,
+                           LIST ? __shfl_sync(0xffffffffu, keys[0], 1) - 16 : key0};
+        const bool partial = (LIST ? max(kh[0], kh[1]) : key0) + kPiece > min_lim || !got0 || !got1;
         // Key of fragment column 2c + e of block nb, relative to the piece.
         auto key_of = [&](int nb, int e) -> int {
           if constexpr (D == 128) return nb * 8 + (e ? ((2 * c) ^ 4) + 1 : 2 * c);
@@ -374,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < 4; ++i) s[nb][i] *= ks[nb >> 1] * crow[i >> 1];
         if (partial) {
           // V of a key that some queries do not see (its row: D / 16 pieces, for d = 64 half a line).
-          const int key = key0 + lane;
-          if (key >= min_lim && key < len && (lane < 16 ? got0 : got1)) {
+          const int key = key0 + lane;       // (LIST: all rows see the same keys)
+          if (!LIST && key >= min_lim && key < len && (lane < 16 ? got0 : got1)) {
             const int line = D == 128 ? lane : lane >> 1, at = D == 128 ? 0 : (lane & 1) * 4;
             uint8_t* row = ring + stage * 2 * C::KB + C::KB + line * 128;
 #pragma unroll 1
@@ -392,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (key0 + key_of(nb, i & 1) >= lim[i >> 1] || !((nb >> 1) ? got1 : got0)) s[nb][i] = -INFINITY;
+              if (kh[nb >> 1] + key_of(nb, i & 1) >= lim[i >> 1] || !((nb >> 1) ? got1 : got0)) s[nb][i] = -INFINITY;
         }
         float mx[2];
 #pragma unroll
@@ -443,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           bool live[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            live[x] = key0 + key_of(2 * t + (x >> 1), x & 1) < len && (t ? got1 : got0);
+            live[x] = kh[t] + key_of(2 * t + (x >> 1), x & 1) < len && (t ? got1 : got0);
           if constexpr (D == 128) {
             uint4 v[4];
 #pragma unroll
@@ -490,11 +575,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < C::STAGES; ++i) {
         pages[i] = pages[i + 1];
         heads[i] = heads[i + 1];
+        if (LIST) keys[i] = keys[i + 1];
       }
       ahead.f += kWarps;
       ahead.settle(p, re);
       pages[C::STAGES] = page_at();
-      heads[C::STAGES] = ahead.h;
+      heads[C::STAGES] = kv_head(ahead.h);
+      if (LIST) keys[C::STAGES] = key_ahead;
       if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1;
@@ -575,8 +662,37 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (r >= rows) continue;
         // Columns of o[j][2i] and o[j][2i + 1]: for d = 128, 32 c + j and 32 c + 16 + j; d = 64, 16 c + j and 16 c + 8 + j.
         if (whole) {
-          const float inv = l[i] == 0.f ? 0.f : rref / l[i];
+          float inv = l[i] == 0.f ? 0.f : rref / l[i];
+          float lse2 = m[i] - kShift + __log2f(l[i]);
           const long long row = (long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi;
+          if (p.side != SIDE_NONE) {         // columns 8 k .. 8 k + 7 of each half: two pieces of 4
+            float4* side = reinterpret_cast<float4*>(p.side_o + row * D + c * (D / 4));
+            float2 w = make_float2(1.f, 0.f);
+            if (p.side == SIDE_IN) w = join_side(p, row, lse2, lse2);
+            inv *= w.x;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < C::NACC / 4; ++k) {
+                float4 y = make_float4(o[4 * k][2 * i + e] * inv, o[4 * k + 1][2 * i + e] * inv, o[4 * k + 2][2 * i + e] * inv,
+                                       o[4 * k + 3][2 * i + e] * inv);
+                float4* at = side + e * (C::NACC / 4) + k;
+                if (p.side == SIDE_OUT) {
+                  *at = y;
+                  continue;
+                }
+                const float4 x = *at;
+                o[4 * k][2 * i + e] = y.x + w.y * x.x;
+                o[4 * k + 1][2 * i + e] = y.y + w.y * x.y;
+                o[4 * k + 2][2 * i + e] = y.z + w.y * x.z;
+                o[4 * k + 3][2 * i + e] = y.w + w.y * x.w;
+              }
+            if (p.side == SIDE_OUT) {
+              if (c == 0) p.side_lse[row] = lse2;
+              continue;
+            }
+            inv = 1.f;
+          }
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + c * (D / 4));
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -588,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 w[x] = pack_bf16x2(o[8 * k + 2 * x][2 * i + e] * inv, o[8 * k + 2 * x + 1][2 * i + e] * inv);
               out[e * (C::NACC / 8) + k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          if (c == 0) p.lse[row] = (m[i] - kShift + __log2f(l[i])) * kLn2;
+          if (c == 0) p.lse[row] = lse2 * kLn2;
         } else {
           float4* out = reinterpret_cast<float4*>(ws + W.part) + ((long long)part * (D / 4) + c * (D / 16)) * rows_max + r;
 #pragma unroll
@@ -699,7 +815,28 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
       ref = rn;
     }
     const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
-    const float inv = l == 0.f ? 0.f : ref / l;
+    float inv = l == 0.f ? 0.f : ref / l, lse2 = m + __log2f(l);
+    if (p.side != SIDE_NONE) {
+      float4* side = reinterpret_cast<float4*>(p.side_o + row * D) + cg * CPT;
+      float2 w = make_float2(1.f, 0.f);
+      if (p.side == SIDE_IN) w = join_side(p, row, lse2, lse2);
+      inv *= w.x;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        o[c] = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
+        if (p.side == SIDE_OUT) {
+          side[c] = o[c];
+          continue;
+        }
+        const float4 x = side[c];
+        o[c] = make_float4(o[c].x + w.y * x.x, o[c].y + w.y * x.y, o[c].z + w.y * x.z, o[c].w + w.y * x.w);
+      }
+      if (p.side == SIDE_OUT) {
+        if (cg == 0) p.side_lse[row] = lse2;
+        continue;
+      }
+      inv = 1.f;
+    }
     uint32_t y[2 * CPT];
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
@@ -709,11 +846,11 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     uint16_t* out = static_cast<uint16_t*>(p.o) + row * D + cg * CPT * 4;
     if constexpr (CPT == 1) *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
     else *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (cg == 0) p.lse[row] = (m + __log2f(l)) * kLn2;
+    if (cg == 0) p.lse[row] = lse2 * kLn2;
   }
 }
 
-template <int D>
+template <int D, bool LIST>
 cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows, int grid, cudaStream_t s) {
   using C = DecCfg<D>;
   static std::once_flag flags[64];
@@ -722,11 +859,11 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::call_once(flags[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
-  e = launch_pdl(fwd_cache_decode_kernel<D>, dim3(grid), dim3(kThreads), C::SMEM, s, maps.k, maps.v, p, rows);
+  e = launch_pdl(fwd_cache_decode_kernel<D, LIST>, dim3(grid), dim3(kThreads), C::SMEM, s, maps.k, maps.v, p, rows);
   if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, rows, grid, s);
 }
@@ -755,7 +892,12 @@ size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(
 
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
   const int rows = p.max_q * p.g, grid = 2 * sms;      // as in the workspace's size
-  return d == 64 ? launch_decode<64>(maps, p, rows, grid, s) : launch_decode<128>(maps, p, rows, grid, s);
+  return d == 64 ? launch_decode<64, false>(maps, p, rows, grid, s) : launch_decode<128, false>(maps, p, rows, grid, s);
+}
+
+cudaError_t launch_fwd_cache_pages(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
+  const int grid = 2 * sms;
+  return d == 64 ? launch_decode<64, true>(maps, p, p.g, grid, s) : launch_decode<128, true>(maps, p, p.g, grid, s);
 }
 
 }  // namespace attn

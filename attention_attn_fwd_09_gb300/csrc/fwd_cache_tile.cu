@@ -43,6 +43,9 @@
 //
 // Shared memory (d = 128): Q1, Q2 2 x 32 KB, K8 ring 2 x 16 KB, V8 ring 3 x 16 KB, V16 2 x 32 KB.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P_t (f16 pairs) overwrites S_t.
+#ifndef CACHE_TILE_SIDE
+#define CACHE_TILE_SIDE false                // fwd_cache_tile_side.cu: this file again, keys in two parts
+#endif
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -207,8 +210,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// NG: groups of columns of a key block that may have scales of their own, one per page of it. 
-template <int D, int NG, bool SPLIT>
+// NG: groups of columns of a key block that may have scales of their own, one per page of it.
+// SIDE: keys in two parts (p.side); a template, since its registers would spill in the ordinary epilogue.
+template <int D, int NG, bool SPLIT, bool SIDE>
 __global__ void __launch_bounds__(kTThreads, 1)
     fwd_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const CacheParams p) {
@@ -304,8 +308,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
+    if (SIDE && p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
   }
-  if (bad) return;
+  if (bad || (SIDE && p.side == SIDE_IN && *p.side_bad)) return;
   blocks_to -= blocks;
   units_to -= units;
   long long all_blocks = 0, all_units = 0;
@@ -943,7 +948,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const bool live = r < rows;
         const long long orow = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
         const long long prow = (long long)part * kTRows + r;
-        const float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f;
+        float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f, lse2 = m - kPShift + __log2f(l), w_side = 0.f;
+        float4* side = reinterpret_cast<float4*>(p.side_o + orow * D);     // (used where the row is live)
+        if (whole && live && SIDE && p.side == SIDE_IN) {
+          const float2 w = join_side(p, orow, lse2, lse2);
+          inv *= w.x;
+          w_side = w.y;
+        }
         const uint32_t tO = tmem + lane_off + 256u + uint32_t(t * 128);
         // Whole units go through shared memory (V16 slot t: no product reads it any more), so that rows
         // leave in whole lines; a warp stages its own 32 rows.
@@ -959,13 +970,30 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0u;
           }
+          if constexpr (SIDE) if (whole && live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4 y = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
+                                     __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
+              if (SIDE && p.side == SIDE_OUT) {
+                side[q * 8 + i] = y;
+                continue;
+              }
+              const float4 z = side[q * 8 + i];
+              x[4 * i] = __float_as_uint(y.x + w_side * z.x);
+              x[4 * i + 1] = __float_as_uint(y.y + w_side * z.y);
+              x[4 * i + 2] = __float_as_uint(y.z + w_side * z.z);
+              x[4 * i + 3] = __float_as_uint(y.w + w_side * z.w);
+            }
+          }
+          const float inv_out = SIDE && p.side == SIDE_IN ? 1.f : inv;
           if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv, __uint_as_float(x[8 * i + 2 * k + 1]) * inv);
+                y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv_out, __uint_as_float(x[8 * i + 2 * k + 1]) * inv_out);
               *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((q * 4 + i) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else if (live) {
@@ -975,7 +1003,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           __syncwarp();
         }
-        if (whole) {
+        if (whole && !(SIDE && p.side == SIDE_OUT)) {
           constexpr int LPR = D / 8, RPS = 32 / LPR;
           const long long mine = live ? orow : -1;
 #pragma unroll 4
@@ -995,12 +1023,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < D; ++i) {
             if (nan_keys[(nu & 1) * D + i] >= U.lim0 + qi) continue;
-            if (whole) static_cast<uint16_t*>(p.o)[orow * D + i] = 0x7fff;
+            if (whole && SIDE && p.side == SIDE_OUT) p.side_o[orow * D + i] = __int_as_float(0x7fffffff);
+            else if (whole) static_cast<uint16_t*>(p.o)[orow * D + i] = 0x7fff;
             else reinterpret_cast<uint32_t*>(ws + W.part)[(((long long)part * (D / 4) + i / 4) * kTRows + r) * 4 + i % 4] = 0x7fffffffu;
           }
         }
         if (live) {
-          if (whole) p.lse[orow] = (m - kPShift + __log2f(l)) * kLn2;
+          if (whole && SIDE && p.side == SIDE_OUT) p.side_lse[orow] = lse2;
+          else if (whole) p.lse[orow] = lse2 * kLn2;
           else reinterpret_cast<float4*>(ws + W.stat)[prow] = make_float4(m - kPShift, l, ref, 0.f);
         }
       }
@@ -1019,7 +1049,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 }
 
-template <int D, int NG, bool SPLIT>
+template <int D, int NG, bool SPLIT, bool SIDE>
 cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, cudaStream_t s) {
   using C = TileCfg<D, SPLIT>;
   static std::once_flag flags[64];
@@ -1028,24 +1058,30 @@ cudaError_t launch_tile(const CacheMaps& maps, const CacheParams& p, int grid, c
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::call_once(flags[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_tile_kernel<D, NG, SPLIT, SIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
-  e = launch_pdl(fwd_cache_tile_kernel<D, NG, SPLIT>, dim3(grid), dim3(kTThreads), C::SMEM, s, maps.k, maps.v, p);
+  e = launch_pdl(fwd_cache_tile_kernel<D, NG, SPLIT, SIDE>, dim3(grid), dim3(kTThreads), C::SMEM, s, maps.k, maps.v, p);
   if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, kTRows, grid, s);
 }
 
 }  // namespace
 
+#if CACHE_TILE_SIDE
+cudaError_t launch_fwd_cache_tile_side(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
+#else
 size_t cache_tile_workspace_bytes(int d, int sms) { return cache_ws(sms, kTRows, d).total; }
 
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
+  if (p.side != SIDE_NONE) return launch_fwd_cache_tile_side(maps, p, d, sms, s);
+#endif
   // 16 sequences of 16000 keys, 128 rows per K/V head: 145 us against 203; 32 rows 141 against 198.
   const bool split = (long long)p.max_q * p.g <= 128;
   auto go = [&](auto dim, auto groups) {
-    return split ? launch_tile<dim, groups, true>(maps, p, sms, s) : launch_tile<dim, groups, false>(maps, p, sms, s);
+    constexpr bool side = CACHE_TILE_SIDE;
+    return split ? launch_tile<dim, groups, true, side>(maps, p, sms, s) : launch_tile<dim, groups, false, side>(maps, p, sms, s);
   };
   using I1 = std::integral_constant<int, 1>;
   using I8 = std::integral_constant<int, 8>;

@@ -217,7 +217,17 @@ struct CacheParams {
   unsigned long long wait_ns;
   int* status;
   int test_skip_first_kv;    // test hook: each CTA never issues its first K copy
+  // Listed pages (launch_fwd_cache_pages): page numbers within each query's sequence, [K/V heads][total_q]
+  // [list_count], negative ones left out; g, Hkv count virtual heads, rep of which share a K/V head.
+  const int* list;
+  int list_count, rep;
+  // Keys in two parts (a shared prefix, then a sequence's own): the first part's result goes to side_o
+  // [Hq, total_q, d] and side_lse [Hq, total_q] (log2) instead of o and lse, the second part's is joined with it.
+  int side;                  // SIDE_NONE, SIDE_OUT (first part) or SIDE_IN (second)
+  float *side_o, *side_lse;
+  int* side_bad;             // the first part's offsets were invalid: the second writes nothing
 };
+enum : int { SIDE_NONE = 0, SIDE_OUT = 1, SIDE_IN = 2 };
 // Tensor maps over the codes as 128-byte lines, [num_pages * Hkv][page * d / 128][128], boxes of
 // 32 keys (a page of 16: 16 keys), 128-byte swizzle.
 struct CacheMaps {
@@ -230,9 +240,12 @@ size_t cache_decode_workspace_bytes(int rows, int d, int sms);
 // Joins what the main kernel's ctas CTAs left of units cut between them, a dependent launch.
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s);
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
+// Every query by itself, over its list of pages (max_q = 1, g up to kCacheDecodeRows).
+cudaError_t launch_fwd_cache_pages(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
 // More rows: fwd_cache_tile.cu.  Maps as above, but boxes of 128 keys (a smaller page: its keys), and
 // K's lines are keys (d bytes; 64-byte swizzle for d = 64).  g <= 256.
 size_t cache_tile_workspace_bytes(int d, int sms);
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
+cudaError_t launch_fwd_cache_tile_side(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
 
 }  // namespace attn

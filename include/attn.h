@@ -225,6 +225,67 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
 size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d);
 
 /*
+ * attn_fwd_kv_fp8 over listed pages only (sparse attention over blocks of the cache, decoding and
+ * drafts): for each K/V head and query the pages whose keys it reads.
+ *
+ *   pages: DEVICE int32 [Hkv, total_q, count]: page numbers within the query's sequence (page j
+ *       holds its rows j * page_size ..; attn_select_pages_fp8 writes such lists).  The numbers of a list
+ *       are distinct and of pages that the query sees a key of; negative entries are left out, and where
+ *       the list is longer than the pages the query sees, what lies behind as many entries is negative
+ *       (so it is in lists that are filled from the front).  count may be 0.
+ *   Keys of a listed page that the query does not see (causal, or behind kv_lens[b]) are masked.  A
+ *       query without a visible listed key gets O = 0 and LSE = -inf.
+ *   Groups: Hq / Hkv heads share a list and its pages; up to 16 (or their largest divisor up to 16)
+ *       read them together, so 17 or 19 heads would read them once each.
+ *   workspace: attn_fwd_kv_fp8_pages_workspace_size(...) bytes; other arguments, ownership and
+ *       limits as attn_fwd_kv_fp8 (there is no bound on a sequence's queries).
+ * Errors as attn_fwd_kv_fp8.  A listed page that the query does not see, or a number behind as many
+ *   entries as it sees pages, is found on the device: the device status word reads ATTN_ERR_INVALID_ARG and the results of
+ *   that query and head are undefined; a page listed twice counts twice.
+ */
+int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens,
+                          const int* pages, void* o, float* lse, int B, int Hq, int Hkv, int total_q, int count, int d,
+                          int num_pages, int page_size, int max_pages, int causal, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_fwd_kv_fp8_pages needs on the current device, whatever the lists' length;
+ * (size_t)-1 for invalid sizes.
+ */
+size_t attn_fwd_kv_fp8_pages_workspace_size(int Hq, int Hkv, int total_q, int d);
+
+/*
+ * attn_fwd_kv_fp8 of sequences that begin with shared prefixes (a system prompt, a document, several
+ * samples of one prompt), each prefix's keys read once for all queries behind it.
+ *
+ *   prefix_table [G, max_prefix_pages], prefix_lens [G], cu_prefix_q [G + 1] (DEVICE int32): packed
+ *       queries cu_prefix_q[j] .. cu_prefix_q[j+1]-1 see the prefix_lens[j] keys in the pages
+ *       prefix_table[j], all of them, before those of their own sequence.  The offsets obey
+ *       attn_fwd_varlen's rules and need not fall on sequences' borders; a length may be 0.
+ *   page_table, cu_seqlens_q, kv_lens: each sequence's own keys, which start on a page of their own
+ *       (kv_lens counts these only), as attn_fwd_kv_fp8; causal concerns these only.
+ *   max_prefix_q: an upper bound on the queries that share one prefix, from 1 to total_q; max_q as
+ *       attn_fwd_kv_fp8.  Each chooses the kernel of its part as there.
+ *   workspace: attn_fwd_kv_fp8_prefix_workspace_size(...) bytes, which holds the prefix part's results
+ *       in fp32; other arguments and ownership as attn_fwd_kv_fp8.
+ * Errors as attn_fwd_kv_fp8, of both parts; if either part's offsets or lengths break a rule nothing is
+ *   written to o and lse.
+ */
+int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* prefix_table, const int* cu_prefix_q, const int* prefix_lens,
+                           const int* page_table, const int* cu_seqlens_q, const int* kv_lens, void* o, float* lse, int G,
+                           int B, int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d, int num_pages,
+                           int page_size, int max_prefix_pages, int max_pages, int causal, float scale, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_fwd_kv_fp8_prefix needs on the current device; grows with total_q, and does not
+ * fall as the bounds grow; (size_t)-1 for invalid sizes.
+ */
+size_t attn_fwd_kv_fp8_prefix_workspace_size(int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d);
+
+/*
  * Forward over B packed sequences of different lengths ("FlashAttention-4 explained"
  * page, section 06: sequences of different lengths, the CTAs with the most work started
  * first).  Each sequence is its own attention problem; sequence b owns query rows
