@@ -86,6 +86,8 @@ _lib.attn_rope_bwd.restype = _i
 _lib.attn_kv_append_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
                                     ctypes.POINTER(_ll), _p]
 _lib.attn_kv_append_fp8.restype = _i
+_lib.attn_rope_kv_append_fp8.argtypes = [_p] * 14 + [_i] * 7 + [_f, _i, _i, _i, ctypes.POINTER(_ll), _p]
+_lib.attn_rope_kv_append_fp8.restype = _i
 _lib.attn_fwd_kv_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p,
                                  _sz, _p]
 _lib.attn_fwd_kv_fp8.restype = _i
@@ -504,7 +506,7 @@ def attn_rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", fact
     return f.to(device), mscale
 
 
-_Strides12, _Strides4 = _ll * 12, _ll * 4
+_Strides12, _Strides8, _Strides4 = _ll * 12, _ll * 8, _ll * 4
 
 
 def _bad_rows(dev, *rows):
@@ -633,6 +635,66 @@ def attn_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_
                                    k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(),
                                    kv_lens.data_ptr(), B, Hkv, T, d, pages, P, width,
                                    _Strides4(sk[0], sk[1], sv[0], sv[1]), _current_stream(dev.index)))
+
+
+def attn_rope_kv_append_fp8(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
+                            positions=None, interleaved: bool = False, mscale: float = 1.0, k_bounds=None, q_out=None,
+                            stream=None):
+    """``attn_rope`` and ``attn_kv_append_fp8`` in one call: packed q [Hq, total, d] (or None) is returned
+    rotated, k and v [Hkv, total, d] go into the paged cache, k rotated in fp32 and rounded once, to
+    its codes.  ``inv_freq`` (``attn_rope_freqs``; None: k goes in as it is, and q must be None), ``interleaved``,
+    ``mscale``: as ``attn_rope``; ``positions`` int32 [total], by default each row's place in its
+    sequence.  ``k_bounds`` uint8 [num_pages, Hkv, 2, d], if given, is kept up to date: the smallest and
+    the largest e4m3 code of each column over the page's rows, which ``attn_select_pages_fp8`` goes by
+    (a page's bounds must have been kept since its first row).  ``q_out``: a new contiguous tensor unless given;
+    it may be q (in place).  Cache tensors, offsets and lengths as ``attn_kv_append_fp8``."""
+    if not k.is_cuda or k.dim() != 3:
+        raise ValueError(f"k: expected a CUDA tensor [Hkv, total, d], got {tuple(k.shape)} on {k.device}")
+    dev = k.device
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_rope_kv_append_fp8(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
+                                           kv_lens, positions, interleaved, mscale, k_bounds, q_out)
+    pages, Hkv, P, d, B, width = _cache_tensors(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, "cu_seqlens",
+                                                kv_lens, dev)
+    T = k.shape[1]
+    shape, bf16 = (Hkv, T, d), torch.bfloat16
+    sk, sv = k.stride(), v.stride()
+    if not (k.dtype is bf16 and v.dtype is bf16 and k.shape == shape and v.shape == shape and v.device == dev
+            and sk[2] == 1 and sv[2] == 1):
+        _bad_rows(dev, ("k", k, shape), ("v", v, shape))
+    Hq, pq, pqo, sq, so = 0, None, None, sk, sk
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q: expected a CUDA tensor [Hq, total, d], got {tuple(q.shape)}")
+        Hq = q.shape[0]
+        qshape = (Hq, T, d)
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=bf16, device=dev)
+        sq, so = q.stride(), q_out.stride()
+        if not (q.dtype is bf16 and q_out.dtype is bf16 and q.shape == qshape and q_out.shape == qshape and q.device == dev
+                and q_out.device == dev and sq[2] == 1 and so[2] == 1):
+            _bad_rows(dev, ("q", q, qshape), ("q_out", q_out, qshape))
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _plain("inv_freq", inv_freq, torch.float64, (rot // 2,), dev)
+    if positions is not None:
+        _plain("positions", positions, torch.int32, (T,), dev)
+    if k_bounds is not None:
+        _plain("k_bounds", k_bounds, torch.uint8, (pages, Hkv, 2, d), dev)
+    _check(_lib.attn_rope_kv_append_fp8(pq, pqo, k.data_ptr(), v.data_ptr(), inv_freq.data_ptr() if rot else None,
+                                        None if positions is None else positions.data_ptr(), k_cache.data_ptr(),
+                                        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                        None if k_bounds is None else k_bounds.data_ptr(), page_table.data_ptr(),
+                                        cu_seqlens.data_ptr(), kv_lens.data_ptr(), B, Hq, Hkv, T, d, rot,
+                                        1 if interleaved else 0, mscale, pages, P, width,
+                                        _Strides8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]),
+                                        _current_stream(dev.index)))
+    return q_out
 
 
 def attn_fwd_kv_fp8_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_q: int, d: int) -> int:
@@ -835,6 +897,7 @@ def attn_exp2_sw(x, variant: int = 0, stream=None):
 __all__ = ["attn_fwd", "attn_fwd_fp8", "attn_quantize_fp8", "attn_bwd", "attn_bwd_noalloc", "attn_bwd_workspace_size", "attn_last_error", "attn_version",
            "attn_set_debug_knobs", "attn_get_debug_knobs", "attn_device_status", "attn_rescale_counter",
            "attn_exp2_sw", "attn_set_test_hooks", "attn_rope", "attn_rope_bwd", "attn_rope_freqs", "attn_kv_append_fp8",
+           "attn_rope_kv_append_fp8",
            "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "attn_fwd_kv_fp8_pages",
            "attn_fwd_kv_fp8_pages_workspace_size", "attn_fwd_kv_fp8_prefix", "attn_fwd_kv_fp8_prefix_workspace_size",
            "AttnError", "LIB_PATH"]

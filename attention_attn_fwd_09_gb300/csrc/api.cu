@@ -790,9 +790,11 @@ static bool rows_apart(const int (&extent)[3], const long long (&stride)[3], int
 
 // strides: {q, k, q_out, k_out} x {batch, head, token} in elements, or null for contiguous
 // [B, H, N, d] tensors.
-static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
-                     const int* positions, int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale,
-                     const long long* strides, int backward, void* stream) {
+// Checks the arguments and fills in *p and the elements per access; *nothing: an empty call.
+static int rope_params(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
+                       const int* positions, int B, int Hq, int Hk, int N, int d, int rot, float mscale,
+                       const long long* strides, int backward, RopeParams* out, int* vec, bool* nothing) {
+  *nothing = false;
   if (B < 0 || N < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d and N=%d must be >= 0", B, N);
   if (Hq <= 0 || Hk < 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d must be >= 1 and Hk=%d >= 0", Hq, Hk);
   if (d != 64 && d != 128 && d != 192 && d != 256)
@@ -802,9 +804,13 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
   if (!std::isfinite(mscale)) return fail(ATTN_ERR_INVALID_ARG, "mscale must be finite");
   if (N > 0x7fff0000) return fail(ATTN_ERR_INVALID_ARG, "N must stay below 2^31 - 65536");
   if ((long long)Hq + Hk > 65535) return fail(ATTN_ERR_INVALID_ARG, "Hq + Hk too large");
-  if (B == 0 || N == 0) return ATTN_OK;
+  if (B == 0 || N == 0) {
+    *nothing = true;
+    return ATTN_OK;
+  }
   if (!q || !q_out || !inv_freq || (Hk > 0 && (!k || !k_out))) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
-  RopeParams p{};
+  RopeParams& p = *out;
+  p = RopeParams{};
   p.q.in = q; p.q.out = q_out; p.k.in = k; p.k.out = k_out;
   const long long cq[3] = {(long long)Hq * N * d, (long long)N * d, d}, ck[3] = {(long long)Hk * N * d, (long long)N * d, d};
   const long long* sq = strides ? strides : cq;
@@ -831,12 +837,24 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
   if (bits & 1) return fail(ATTN_ERR_MISALIGNED, "bf16 tensors must be 2-byte aligned");
   if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
     return fail(ATTN_ERR_MISALIGNED, "inv_freq must be 8-byte aligned, positions 4-byte aligned");
-  const int vec = (bits & 15) == 0 && rot % 16 == 0 ? 8 : ((bits & 7) == 0 && rot % 8 == 0 ? 4 : 1);
+  *vec = (bits & 15) == 0 && rot % 16 == 0 ? 8 : ((bits & 7) == 0 && rot % 8 == 0 ? 4 : 1);
   p.inv_freq = inv_freq;
   p.positions = positions;
   p.B = B; p.N = N; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot;
   p.mscale = mscale;
   p.sign = backward ? -1.f : 1.f;
+  return ATTN_OK;
+}
+
+static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq,
+                     const int* positions, int B, int Hq, int Hk, int N, int d, int rot, int interleaved, float mscale,
+                     const long long* strides, int backward, void* stream) {
+  RopeParams p;
+  int vec;
+  bool nothing;
+  const int rc = rope_params(q, k, q_out, k_out, inv_freq, positions, B, Hq, Hk, N, d, rot, mscale, strides, backward, &p,
+                             &vec, &nothing);
+  if (rc != ATTN_OK || nothing) return rc;
   const DevSyms* s = dev_syms(nullptr);
   if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -876,18 +894,13 @@ static int check_cache(int B, int Hkv, int total, int d, int num_pages, int page
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// strides: {k head, k token, v head, v token} in elements, or null for contiguous [Hkv, total, d].
-int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
-                       const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hkv, int total,
-                       int d, int num_pages, int page_size, int max_pages, const long long* strides, void* stream) {
-  int rc = check_cache(B, Hkv, total, d, num_pages, page_size, max_pages);
-  if (rc != ATTN_OK) return rc;
-  if (B == 0 || total == 0) return ATTN_OK;
+// Checks of an append's rows and cache, and its parameters.
+static int append_params(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hkv, int total, int d,
+                         int num_pages, int page_size, int max_pages, const long long (&st4)[4], AppendParams* out) {
   if (num_pages == 0 || max_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d rows to append, but no pages", total);
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens || !kv_lens)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");
-  const long long contiguous[4] = {(long long)total * d, d, (long long)total * d, d};
-  const long long* st4 = strides ? strides : contiguous;
   uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
   for (int i = 0; i < 4; ++i)
     if ((i & 1 ? total : Hkv) > 1) bits |= (uintptr_t)(st4[i] * 2);
@@ -895,19 +908,91 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
     return fail(ATTN_ERR_MISALIGNED, "k, v (their strides too) and the cache must be 16-byte aligned");
   if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page_table) || !aligned4(cu_seqlens) || !aligned4(kv_lens))
     return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets and lengths must be 4-byte aligned");
-  const DevSyms* s = dev_syms(nullptr);
-  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
-  AppendParams p{};
+  AppendParams& p = *out;
+  p = AppendParams{};
   p.k = k; p.v = v;
   p.k_h = st4[0]; p.k_t = st4[1]; p.v_h = st4[2]; p.v_t = st4[3];
   p.k_cache = k_cache; p.v_cache = v_cache; p.k_scale = k_scale; p.v_scale = v_scale;
   p.table = page_table; p.cu = cu_seqlens; p.kv_lens = kv_lens;
   p.B = B; p.Hkv = Hkv; p.total = total; p.num_pages = num_pages; p.page = page_size; p.max_pages = max_pages;
   p.max_len = max_pages * page_size;
+  return ATTN_OK;
+}
+
+// strides: {k head, k token, v head, v token} in elements, or null for contiguous [Hkv, total, d].
+int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hkv, int total,
+                       int d, int num_pages, int page_size, int max_pages, const long long* strides, void* stream) {
+  int rc = check_cache(B, Hkv, total, d, num_pages, page_size, max_pages);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || total == 0) return ATTN_OK;
+  const long long td = (long long)total * d;
+  const long long st4[4] = {strides ? strides[0] : td, strides ? strides[1] : d, strides ? strides[2] : td,
+                            strides ? strides[3] : d};
+  AppendParams p;
+  rc = append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens, B, Hkv, total, d, num_pages,
+                     page_size, max_pages, st4, &p);
+  if (rc != ATTN_OK) return rc;
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   p.status = s->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_kv_append(p, d, std::max(1, s->sms), st);
   if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+  return post_launch(s, st);
+}
+
+// strides: {q head, q token, k head, k token, v head, v token, q_out head, q_out token} in elements, or null.
+int attn_rope_kv_append_fp8(const void* q, void* q_out, const void* k, const void* v, const double* inv_freq,
+                            const int* positions, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            void* k_bounds, const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hq,
+                            int Hkv, int total, int d, int rot, int interleaved, float mscale, int num_pages, int page_size,
+                            int max_pages, const long long* strides, void* stream) {
+  int rc = check_cache(B, Hkv, total, d, num_pages, page_size, max_pages);
+  if (rc != ATTN_OK) return rc;
+  if (rot < 0 || rot > d || (rot & 1)) return fail(ATTN_ERR_INVALID_ARG, "rot=%d must be even and between 0 and d=%d", rot, d);
+  if (!std::isfinite(mscale)) return fail(ATTN_ERR_INVALID_ARG, "mscale must be finite");
+  if (Hq < 0) return fail(ATTN_ERR_INVALID_ARG, "Hq=%d must be >= 0", Hq);
+  if (Hq > 0 && rot == 0) return fail(ATTN_ERR_INVALID_ARG, "rot = 0 leaves the queries as they are: pass none (Hq = 0)");
+  if (B == 0 || total == 0) return ATTN_OK;
+  const long long td = (long long)total * d;
+  const long long contiguous[8] = {td, d, td, d, td, d, td, d};
+  const long long* st8 = strides ? strides : contiguous;
+  const long long st4[4] = {st8[2], st8[3], st8[4], st8[5]};
+  RopeAppendParams p{};
+  rc = append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens, B, Hkv, total, d, num_pages,
+                     page_size, max_pages, st4, &p.a);
+  if (rc != ATTN_OK) return rc;
+  if (rot > 0 && !inv_freq) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) || !aligned4(positions))
+    return fail(ATTN_ERR_MISALIGNED, "inv_freq must be 8-byte aligned, positions 4-byte aligned");
+  if (!aligned16(k_bounds)) return fail(ATTN_ERR_MISALIGNED, "k_bounds must be 16-byte aligned");
+  RopeParams r{};
+  int vec = 1;
+  if (Hq > 0) {
+    const long long st12[12] = {0, st8[0], st8[1], 0, 0, 0, 0, st8[6], st8[7], 0, 0, 0};
+    bool nothing;
+    rc = rope_params(q, nullptr, q_out, nullptr, inv_freq, positions, 1, Hq, 0, total, d, rot, mscale, st12, 0, &r, &vec,
+                     &nothing);
+    if (rc != ATTN_OK) return rc;
+    r.cu = cu_seqlens;
+    r.kv_lens = kv_lens;
+    r.seqs = B;
+    r.beside = 1;
+  }
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  p.a.status = s->status;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.rot = rot;
+  p.interleaved = interleaved ? 1 : 0;
+  p.mscale = mscale;
+  p.bounds = static_cast<uint8_t*>(k_bounds);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_rope_append(p, d, std::max(1, s->sms), st);
+  if (e == cudaSuccess && Hq > 0) e = launch_rope(r, vec, p.interleaved, std::max(1, s->sms), st);
+  if (e != cudaSuccess) return cuda_fail(e, "rotating cache append launch");
   return post_launch(s, st);
 }
 

@@ -185,6 +185,10 @@ struct RopeParams {
   int B, N, Hq, Hk, d, rot;
   float mscale, sign;        // factor on the rotated part; +1 forward, -1 transposed
   int tile_shift, tiles, head_group;   // filled in by launch_rope: log2(tokens per CTA), tiles per sequence, heads per CTA
+  // Packed rows (B = 1) that end their sequences, where positions is null: offsets [seqs + 1], lengths [seqs].
+  const int *cu, *kv_lens;
+  int seqs;
+  int beside;                // 1: runs beside the kernel launched before it, which calls pdl_trigger; d = 64 or 128
 };
 // vec: elements per access (8, 4 or 1) that every pointer, stride and rot allow.
 cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s);
@@ -201,6 +205,17 @@ struct AppendParams {
   int* status;
 };
 cudaError_t launch_kv_append(AppendParams p, int d, int sms, cudaStream_t s);
+
+// The same with K rotated on the way and bounds of each page's K codes (rope_append.cu).
+struct RopeAppendParams {
+  AppendParams a;
+  const double* inv_freq;    // [rot / 2] radians per position (device); rot = 0: K as it is
+  const int* positions;      // [total] (device) or null: the rows' places in their sequences
+  int rot, interleaved;
+  float mscale;
+  uint8_t* bounds;           // [num_pages, Hkv, 2, d] smallest and largest code per column, or null
+};
+cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s);
 
 // Packed queries over the paged e4m3 cache (fwd_cache.cu).
 struct CacheParams {

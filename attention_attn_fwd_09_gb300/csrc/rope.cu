@@ -23,11 +23,24 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+
+// Position of packed row t: the sequences' new rows (cu) end at their lengths.  Invalid offsets only make it wrong.
+__device__ __forceinline__ long long packed_position(const RopeParams& p, int t) {
+  int lo = 0, hi = p.seqs - 1;               // the last sequence that starts at or before t
+  if (p.seqs == p.N && p.cu[t] == t && p.cu[t + 1] == t + 1) lo = hi = t;      // decoding
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (p.cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return (long long)p.kv_lens[lo] - p.cu[lo + 1] + t;
+}
 
 // V bf16 values (V = 8, 4, 1) as 32-bit words / one half word.
 template <int V>
@@ -115,16 +128,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     if (i0 == (int)threadIdx.x) {
       // The angles, while the first rows are under way.
       for (int j = threadIdx.x; j < half; j += kRopeThreads) {
-        const double t = p.inv_freq[j] * 0.15915494309189535;          // turns per position
-        turn[j] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+        turn[j] = turns_per_position(p.inv_freq[j]);
       }
       __syncthreads();
       for (int i = threadIdx.x; i < tn * half; i += kRopeThreads) {
         const int n = i / half, j = i - n * half;
-        const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : n0 + n;
-        const unsigned long long ph = turn[j] * (unsigned long long)pos;
+        const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : p.cu ? packed_position(p, n0 + n) : n0 + n;
         float s, c;
-        sincospif(__int2float_rn((int)(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        turn_sincos(turn[j], pos, s, c);
         // Pairs 2k, 2k + 1 of all items of a row lie side by side: neighbouring threads' 16-byte reads then
         // touch all banks (pair after pair they met in a quarter of them).
         const int slot = V == 1 ? j : (j % V / 2) * (half / V) * 2 + j / V * 2 + (j & 1);
@@ -186,10 +197,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       st_vec<V>(dst_b, pack<V>(yo));
     }
   }
+  // Started beside the kernel before it in the stream (rope_append.cu): done only when that one is.
+  if (p.beside) pdl_wait();
 }
 
 template <int V, bool INTER>
 cudaError_t launch_v(const RopeParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  if (p.beside)                              // (the cache's head dims)
+    return p.d == 64 ? launch_pdl(rope_kernel<V, INTER, 64>, grid, dim3(kRopeThreads), smem, s, p)
+                     : launch_pdl(rope_kernel<V, INTER, 128>, grid, dim3(kRopeThreads), smem, s, p);
   if (p.d == 64) rope_kernel<V, INTER, 64><<<grid, kRopeThreads, smem, s>>>(p);
   else if (p.d == 128) rope_kernel<V, INTER, 128><<<grid, kRopeThreads, smem, s>>>(p);
   else if (p.d == 192) rope_kernel<V, INTER, 192><<<grid, kRopeThreads, smem, s>>>(p);

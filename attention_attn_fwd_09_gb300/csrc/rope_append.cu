@@ -1,0 +1,435 @@
+// New K and V rows into a paged e4m3 cache, K rotated on the way, and bounds of each page's keys.
+//
+// Page scales, codes and slots are kv_append.cu's.  K differs in what is coded: with the rotation
+// of rope.cu in fp32, y = R(pos) x, the page's largest finite |y| sets the scale and code =
+// e4m3(y / s).  Rotated rows are never rounded to bf16 in between, nor do they cross memory.
+// Bounds: per page, K/V head and column the smallest and the largest code of the page's rows (a
+// NaN code where a column holds one), which a choice of pages to read goes by.  Codes of earlier
+// rows that are rounded again at a grown scale keep their order, so the bounds kept with them are
+// rounded the same way and stay exact, without a look at the rows.
+//
+// Bound by bytes (2 read, 1 written per element); what must not show is the sines and cosines, one
+// pair per token and two columns, the same for all heads.  Two kernels, by kv_append.cu's rule:
+//   * few rows per sequence or page: a CTA per slot, 8 heads and K or V, a warp per head.  The CTA
+//     fills a table of 16 rows' sines and cosines, so each is made once for 8 heads;
+//   * prompts: a CTA per slot, head and K or V; the table of the whole page is made while its rows
+//     are on their way from memory.
+#include <cstdint>
+#include <mutex>
+
+#include "append.cuh"
+#include "rope.cuh"
+
+namespace attn {
+namespace {
+
+// How K's columns turn: not at all; halves (rot a multiple of 16); neighbours (of 8); any even rot.
+enum : int { TURN_NONE = 0, TURN_SPLIT = 1, TURN_INTER = 2, TURN_ANY = 3 };
+__device__ __forceinline__ int turn_mode(const RopeAppendParams& p, bool is_v) {
+  if (is_v || p.rot == 0) return TURN_NONE;
+  return p.interleaved ? (p.rot % 8 == 0 ? TURN_INTER : TURN_ANY) : (p.rot % 16 == 0 ? TURN_SPLIT : TURN_ANY);
+}
+// Where pair j's (cos, sin) lies in a row of the table: 16-byte pieces (two pairs) that the threads of a
+// row read at the same time lie side by side.
+template <int mode>
+__device__ __forceinline__ int turn_slot(int rot, int j) {
+  const int f = j >> 1;
+  if (mode == TURN_SPLIT) return ((f & 3) * (rot / 16) + (f >> 2)) * 2 + (j & 1);
+  if (mode == TURN_INTER) return ((f & 1) * (rot / 8) + (f >> 1)) * 2 + (j & 1);
+  return j;
+}
+// Rows r .. r + n - 1 of the slot's page into the table, by all threads.
+template <int mode, int THREADS>
+__device__ __forceinline__ void fill_turns(const RopeAppendParams& p, const Slot& s, int r, int n,
+                                           const unsigned long long* turn, float2* cs) {
+  const int half = p.rot / 2;
+  for (int i = threadIdx.x; i < n * half; i += THREADS) {
+    const int row = i / half, j = i - row * half;
+    const long long pos = p.positions ? __ldg(p.positions + s.src0 + r + row) : s.first + r + row;
+    float sn, c;
+    turn_sincos_near(turn[j], pos, sn, c);
+    cs[row * half + turn_slot<mode>(p.rot, j)] = make_float2(c * p.mscale, sn * p.mscale);
+  }
+}
+
+// Columns 8 c .. 8 c + 7 of a row, rotated: own are they, row the whole row in memory (TURN_ANY), cs the
+// row's sines and cosines.  All lanes of a warp call it together; lane holds column group c of its row.
+template <int mode>
+__device__ __forceinline__ void turned(const RopeAppendParams& p, const uint4& own, const uint16_t* row, int c,
+                                       const float2* cs, float (&y)[8]) {
+  bf16x8(own, y);
+  const int rot = p.rot;
+  if constexpr (mode == TURN_NONE) {
+  } else if constexpr (mode == TURN_SPLIT) {
+    const int hc = rot / 16, lane = threadIdx.x & 31;            // column groups of a half
+    const bool upper = c >= hc, turns = c < 2 * hc;
+    const int from = turns ? (upper ? lane - hc : lane + hc) : lane;
+    uint4 w;
+    w.x = __shfl_sync(0xffffffffu, own.x, from);
+    w.y = __shfl_sync(0xffffffffu, own.y, from);
+    w.z = __shfl_sync(0xffffffffu, own.z, from);
+    w.w = __shfl_sync(0xffffffffu, own.w, from);
+    if (!turns) return;
+    float z[8];
+    bf16x8(w, z);
+    const float4* at = reinterpret_cast<const float4*>(cs) + (upper ? c - hc : c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 e = at[q * hc];
+      y[2 * q] = y[2 * q] * e.x + (upper ? z[2 * q] : -z[2 * q]) * e.y;
+      y[2 * q + 1] = y[2 * q + 1] * e.z + (upper ? z[2 * q + 1] : -z[2 * q + 1]) * e.w;
+    }
+  } else if constexpr (mode == TURN_INTER) {
+    if (8 * c >= rot) return;
+    const float4* at = reinterpret_cast<const float4*>(cs) + c;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 e = at[q * (rot / 8)];
+      const float a = y[4 * q], b = y[4 * q + 1], d = y[4 * q + 2], f = y[4 * q + 3];
+      y[4 * q] = a * e.x - b * e.y;
+      y[4 * q + 1] = b * e.x + a * e.y;
+      y[4 * q + 2] = d * e.z - f * e.w;
+      y[4 * q + 3] = f * e.z + d * e.w;
+    }
+  } else {
+    const int half = rot / 2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int col = 8 * c + k;
+      if (col >= rot) continue;
+      const bool second = p.interleaved ? (col & 1) != 0 : col >= half;
+      const int j = p.interleaved ? col >> 1 : (second ? col - half : col);
+      const int other = p.interleaved ? col ^ 1 : (second ? col - half : col + half);
+      const float z = __uint_as_float((uint32_t)__ldg(row + other) << 16);
+      const float2 e = cs[j];
+      y[k] = y[k] * e.x + (second ? z : -z) * e.y;
+    }
+  }
+}
+
+// Rows are rotated once for their maximum and once more for their codes; left to itself the compiler keeps the
+// first results in local memory instead.
+template <int N>
+__device__ __forceinline__ void forget(uint4 (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
+}
+
+// Bits of the largest finite |y|.
+__device__ __forceinline__ uint32_t largest8(const float (&y)[8], uint32_t m) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t a = __float_as_uint(y[k]) & 0x7fffffffu;
+    m = max(m, a < 0x7f800000u ? a : 0u);
+  }
+  return m;
+}
+// (inv = 0: a scale that is no power of two, by division.)
+__device__ __noinline__ float divided(float y, float scale) { return __fdiv_rn(y, scale); }
+__device__ __forceinline__ uint2 coded8(const float (&y)[8], float inv, float scale) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = y[k] * inv;
+  if (inv == 0.f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = divided(y[k], scale);
+  }
+  return e4m3x8(f);
+}
+
+// Smallest and largest of codes, column by column, in f16 (which holds every e4m3 value); NaN wins.
+struct Bounds {
+  __half2 lo[4], hi[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __float2half2_rn(INFINITY);
+      hi[i] = __float2half2_rn(-INFINITY);
+    }
+  }
+  static __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+  __device__ __forceinline__ void add(const uint2& low, const uint2& high) {
+    const uint32_t l[4] = {e4m3x2_f16x2(low.x), e4m3x2_f16x2_hi(low.x), e4m3x2_f16x2(low.y), e4m3x2_f16x2_hi(low.y)};
+    const uint32_t h[4] = {e4m3x2_f16x2(high.x), e4m3x2_f16x2_hi(high.x), e4m3x2_f16x2(high.y), e4m3x2_f16x2_hi(high.y)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __hmin2_nan(lo[i], as_half2(l[i]));
+      hi[i] = __hmax2_nan(hi[i], as_half2(h[i]));
+    }
+  }
+  __device__ __forceinline__ void add(const Bounds& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __hmin2_nan(lo[i], b.lo[i]);
+      hi[i] = __hmax2_nan(hi[i], b.hi[i]);
+    }
+  }
+  // Over the lanes that hold the same columns of other rows (D / 8 lanes per row).
+  __device__ __forceinline__ void over_rows(int lanes_per_row) {
+    for (int o = lanes_per_row; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      }
+    }
+  }
+  static __device__ __forceinline__ uint2 codes(const __half2 (&x)[4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t c;
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t*>(&x[i])));
+      r[i] = c;
+    }
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+  }
+  // With the bounds of the earlier rows, whose codes became recode8(code, s_old, inv) if the scale grew.
+  __device__ __forceinline__ void store(uint8_t* page, int d, int c, bool earlier, bool grown, float s_old, float inv) {
+    uint2* low = reinterpret_cast<uint2*>(page + c * 8);
+    uint2* high = reinterpret_cast<uint2*>(page + d + c * 8);
+    if (earlier) {
+      const uint2 l = *low, h = *high;
+      add(grown ? recode8(l, s_old, inv) : l, grown ? recode8(h, s_old, inv) : h);
+    }
+    *low = codes(lo);
+    *high = codes(hi);
+  }
+};
+
+constexpr int kStepWarps = 8, kStepRows = 16;          // rows of the table
+
+// A slot's page of 8 heads of K or V, a warp per head.
+template <int D, int mode>
+__device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slot& s, bool is_v, const unsigned long long* turn,
+                                            float2* cs) {
+  constexpr int THREADS = kStepWarps * 32, LPR = D / 8, RPW = 32 / LPR, STEPS = kStepRows / RPW;   // lanes per row, rows at once
+  const int lane = threadIdx.x & 31, head = blockIdx.y * kStepWarps + (threadIdx.x >> 5), half = p.rot / 2;
+  const bool live = head < p.a.Hkv;
+  const Target t(p.a, s, live ? head : 0, is_v, D);
+  const int r0 = lane / LPR, c = lane % LPR;
+  const float s_old = s.kept > 0 && live ? *t.scale : 0.f;
+  uint4 x[STEPS];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = base + i * RPW + r0;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && r < s.rows) x[i] = *reinterpret_cast<const uint4*>(t.src + (s.src0 + r) * t.st + c * 8);
+    }
+  };
+  auto table = [&](int base) {                         // after the loads: they are under way meanwhile
+    if (mode == TURN_NONE) return;
+    __syncthreads();                                   // the rows before have been used
+    fill_turns<mode, THREADS>(p, s, base, min(kStepRows, s.rows - base), turn, cs);
+    __syncthreads();
+  };
+  auto row = [&](int base, int i, float (&y)[8]) {
+    const int r = min(i * RPW + r0, s.rows - base - 1);          // (lanes without a row: any one, as 0)
+    turned<mode>(p, x[i], t.src + (s.src0 + base + r) * t.st, c, cs + r * half, y);
+  };
+  const bool one = s.rows - s.kept <= kStepRows;       // the rows and the table are kept for the second pass
+  uint32_t amax = 0;
+  for (int base = s.kept; base < s.rows; base += kStepRows) {
+    load(base);
+    table(base);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (base + i * RPW >= s.rows) break;
+      float y[8];
+      row(base, i, y);
+      if (base + i * RPW + r0 < s.rows) amax = largest8(y, amax);
+    }
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax)));
+  const float inv = exact_inverse(sc);
+  const bool keep_bounds = p.bounds != nullptr && !is_v;
+  Bounds b;
+  b.clear();
+  forget(x);
+  for (int base = s.kept; base < s.rows; base += kStepRows) {
+    if (!one) {
+      load(base);
+      table(base);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (base + i * RPW >= s.rows) break;
+      float y[8];
+      row(base, i, y);
+      const int r = base + i * RPW + r0;
+      if (!live || r >= s.rows) continue;
+      const uint2 code = coded8(y, inv, sc);
+      *reinterpret_cast<uint2*>(t.dst + r * D + c * 8) = code;
+      if (keep_bounds) b.add(code, code);
+    }
+  }
+  if (!live) return;                                   // (whole warps; no barrier follows)
+  if (sc > s_old) {
+    for (int r = r0; r < s.kept; r += RPW) {
+      uint2* out = reinterpret_cast<uint2*>(t.dst + r * D + c * 8);
+      *out = recode8(*out, s_old, inv);
+    }
+  }
+  if (keep_bounds) {
+    b.over_rows(LPR);
+    if (r0 == 0) b.store(p.bounds + ((long long)s.page * p.a.Hkv + head) * 2 * D, D, c, s.kept > 0, sc > s_old, s_old, inv);
+  }
+  __syncwarp();                                        // every lane has read the old scale
+  if (lane == 0) *t.scale = sc;
+}
+
+// Block (x, y): slot x / 2, K or V by x & 1, heads 8 y + warp.
+template <int D>
+__global__ void __launch_bounds__(kStepWarps * 32) rope_append_step_kernel(const RopeAppendParams p) {
+  __shared__ unsigned long long turn[D / 2];
+  __shared__ __align__(16) float2 cs[kStepRows * D / 2];
+  constexpr int THREADS = kStepWarps * 32;
+  pdl_trigger();                                       // the queries' rotation may start
+  const bool is_v = blockIdx.x & 1;
+  const int mode = turn_mode(p, is_v);
+  if (mode != TURN_NONE)
+    for (int j = threadIdx.x; j < p.rot / 2; j += THREADS) turn[j] = turns_per_position(p.inv_freq[j]);
+  Slot s;
+  if (!find_slot<THREADS>(p.a, blockIdx.x >> 1, s)) return;      // (its barrier stands behind the writes of turn)
+  if (mode == TURN_NONE) append_step<D, TURN_NONE>(p, s, is_v, turn, cs);
+  else if (mode == TURN_SPLIT) append_step<D, TURN_SPLIT>(p, s, is_v, turn, cs);
+  else if (mode == TURN_INTER) append_step<D, TURN_INTER>(p, s, is_v, turn, cs);
+  else append_step<D, TURN_ANY>(p, s, is_v, turn, cs);
+}
+
+// A slot's page of one head of K or V by a CTA: 8 elements per thread and step, NV steps cover it.
+template <int D, int NV, int THREADS, int mode>
+__device__ __forceinline__ void append_page(const RopeAppendParams& p, const Slot& s, bool is_v, const unsigned long long* turn,
+                                            float2* cs, uint32_t* red, Bounds (*parts)[D / 8]) {
+  constexpr int LPR = D / 8, RPS = THREADS / LPR;      // lanes per row, rows per step
+  const int tid = threadIdx.x, head = blockIdx.y, half = p.rot / 2;
+  const Target t(p.a, s, head, is_v, D);
+  const int r0 = tid / LPR, c = tid % LPR;
+  const float s_old = s.kept > 0 ? *t.scale : 0.f;
+  uint4 x[NV];
+  const uint16_t* src = t.src + (s.src0 + r0) * t.st;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int r = r0 + i * RPS;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= s.kept && r < s.rows) x[i] = *reinterpret_cast<const uint4*>(src + i * RPS * t.st + c * 8);
+  }
+  if (mode != TURN_NONE) {
+    fill_turns<mode, THREADS>(p, s, s.kept, s.rows - s.kept, turn, cs);
+    __syncthreads();
+  }
+  auto row = [&](int i, float (&y)[8]) {               // (threads without a row: any one, as 0)
+    const int r = max(min(r0 + i * RPS, s.rows - 1), s.kept);
+    turned<mode>(p, x[i], t.src + (s.src0 + r) * t.st, c, cs + (r - s.kept) * half, y);
+  };
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float y[8];
+    row(i, y);
+    const int r = r0 + i * RPS;
+    if (r >= s.kept && r < s.rows) amax = largest8(y, amax);
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  __syncthreads();
+  amax = red[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 32; ++i) amax = max(amax, red[i]);
+  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax)));
+  if (tid == 0) *t.scale = sc;
+  const float inv = exact_inverse(sc);
+  const bool keep_bounds = p.bounds != nullptr && !is_v;
+  Bounds b;
+  b.clear();
+  forget(x);
+  uint2* out = reinterpret_cast<uint2*>(t.dst + tid * 8);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float y[8];
+    row(i, y);
+    const int r = r0 + i * RPS;                        // rows behind the last one stay as they are
+    if (r < s.kept || r >= s.rows) continue;
+    const uint2 code = coded8(y, inv, sc);
+    out[i * THREADS] = code;
+    if (keep_bounds) b.add(code, code);
+  }
+  if (sc > s_old) {                                    // the kept rows' codes change (under a scale of 0: to 0)
+#pragma unroll 1
+    for (int i = 0; i < NV && r0 + i * RPS < s.kept; ++i) out[i * THREADS] = recode8(out[i * THREADS], s_old, inv);
+  }
+  if (keep_bounds) {
+    b.over_rows(LPR);
+    if ((tid & 31) < LPR) parts[tid >> 5][c] = b;
+    __syncthreads();
+    if (tid < LPR) {
+      for (int w = 1; w < THREADS / 32; ++w) b.add(parts[w][tid]);
+      b.store(p.bounds + ((long long)s.page * p.a.Hkv + head) * 2 * D, D, tid, s.kept > 0, sc > s_old, s_old, inv);
+    }
+  }
+}
+
+// Block: slot x, head y, K or V z.
+template <int D, int NV, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) rope_append_kernel(const RopeAppendParams p) {
+  extern __shared__ __align__(16) float2 cs[];         // [new rows][rot / 2]
+  __shared__ unsigned long long turn[D / 2];
+  __shared__ uint32_t red[THREADS / 32];
+  __shared__ Bounds parts[THREADS / 32][D / 8];
+  pdl_trigger();                                       // the queries' rotation may start
+  const bool is_v = blockIdx.z != 0;
+  const int mode = turn_mode(p, is_v);
+  if (mode != TURN_NONE)
+    for (int j = threadIdx.x; j < p.rot / 2; j += THREADS) turn[j] = turns_per_position(p.inv_freq[j]);
+  Slot s;
+  if (!find_slot<THREADS>(p.a, blockIdx.x, s)) return; // (its barrier stands behind the writes of turn)
+  if (mode == TURN_NONE) append_page<D, NV, THREADS, TURN_NONE>(p, s, is_v, turn, cs, red, parts);
+  else if (mode == TURN_SPLIT) append_page<D, NV, THREADS, TURN_SPLIT>(p, s, is_v, turn, cs, red, parts);
+  else if (mode == TURN_INTER) append_page<D, NV, THREADS, TURN_INTER>(p, s, is_v, turn, cs, red, parts);
+  else append_page<D, NV, THREADS, TURN_ANY>(p, s, is_v, turn, cs, red, parts);
+}
+
+template <int D>
+cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
+  const int vecs = p.a.page * D / 8;                   // 16-byte pieces of a page
+  const size_t smem = (size_t)p.a.page * (p.rot / 2) * sizeof(float2);
+  if (vecs == 128) rope_append_kernel<D, 1, 128, 8><<<grid, 128, smem, s>>>(p);
+  else if (vecs == 256) rope_append_kernel<D, 1, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 512) rope_append_kernel<D, 2, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 2048) {
+    // The only table of more than 40 KB (d = 128, a page of 128: 64 KB).
+    static std::once_flag flags[64];
+    static cudaError_t attr_err[64];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::call_once(flags[dev & 63], [&] {
+      attr_err[dev & 63] = cudaFuncSetAttribute(rope_append_kernel<D, 8, 256, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * D / 2 * 8);
+    });
+    if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
+    rope_append_kernel<D, 8, 256, 3><<<grid, 256, smem, s>>>(p);
+  } else return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s) {
+  p.a.page_shift = p.a.page == 16 ? 4 : p.a.page == 32 ? 5 : p.a.page == 64 ? 6 : 7;
+  const long long slots = (long long)p.a.total / p.a.page + 2LL * p.a.B;
+  if (slots > 0x3fffffffLL || p.a.Hkv > 65535) return cudaErrorInvalidValue;
+  const bool small = p.a.total <= 32 * slots && 2 * slots * p.a.Hkv >= 16LL * sms;
+  if (p.a.total <= 4LL * p.a.B || small) {
+    const dim3 grid((unsigned)(2 * slots), (unsigned)((p.a.Hkv + kStepWarps - 1) / kStepWarps));
+    if (d == 64) rope_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
+    else rope_append_step_kernel<128><<<grid, kStepWarps * 32, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const dim3 grid((unsigned)slots, (unsigned)p.a.Hkv, 2);
+  return d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);
+}
+
+}  // namespace attn

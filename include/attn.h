@@ -189,6 +189,34 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
                        int d, int num_pages, int page_size, int max_pages, const long long* strides, void* stream);
 
 /*
+ * attn_rope and attn_kv_append_fp8 in one call: packed rows' queries rotated, keys rotated and
+ * values appended to the paged cache.  Rotated keys are coded from fp32, rounded once (rotating to
+ * bf16 first rounds them twice).
+ *
+ *   q, q_out [Hq, total, d] bf16 in and out (Hq = 0: none; q_out may be q with equal strides: in place);
+ *       k, v [Hkv, total, d] bf16; cache, cu_seqlens, kv_lens as attn_kv_append_fp8.
+ *   inv_freq, rot, interleaved, mscale: as attn_rope.  rot = 0: k goes in as it is (keys rotated before, or
+ *       a model without rotary positions), with Hq = 0.
+ *   positions: DEVICE int32 [total], or NULL for each row's place in its sequence (0 for its first row;
+ *       behind a shared prefix the rows need positions of their own).
+ *   k_bounds: uint8 [num_pages, Hkv, 2, d] e4m3 codes in and out, 16-byte aligned, or NULL: per page, K/V
+ *       head and column the smallest [0] and the largest [1] code of the page's rows (NaN if one is), before
+ *       the page's scale.  Bounds of a page that receives rows are updated from what they were, so every
+ *       call that writes to the page since its first row must have kept them.
+ *   strides: NULL for contiguous tensors, or a HOST array {q head, q token, k head, k token, v head, v
+ *       token, q_out head, q_out token} of element strides: k's and v's multiples of 8, q's and
+ *       q_out's as attn_rope.  q_out overlaps neither k nor v.
+ * Infinite or NaN keys: what the rotation in fp32 makes of them, then as attn_kv_append_fp8.
+ * Errors as attn_kv_append_fp8 and attn_rope.  If the offsets break a rule nothing is written to the cache
+ *   and its bounds, and q_out is undefined.
+ */
+int attn_rope_kv_append_fp8(const void* q, void* q_out, const void* k, const void* v, const double* inv_freq,
+                            const int* positions, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            void* k_bounds, const int* page_table, const int* cu_seqlens, const int* kv_lens, int B, int Hq,
+                            int Hkv, int total, int d, int rot, int interleaved, float mscale, int num_pages, int page_size,
+                            int max_pages, const long long* strides, void* stream);
+
+/*
  * Forward of packed queries over the paged 8-bit cache: O = softmax(scale Q K~^T [causal]) V~ and
  * LSE, K~ and V~ the dequantised rows.  Decoding (one query per sequence), drafts of a few tokens
  * and pieces of prompts, mixed freely.  Query i of sequence b's n stands at key position
