@@ -93,6 +93,10 @@ _lib.attn_fwd_kv_fp8.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i,
 _lib.attn_fwd_kv_fp8.restype = _i
 _lib.attn_fwd_kv_fp8_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
 _lib.attn_fwd_kv_fp8_workspace_size.restype = _sz
+_lib.attn_select_pages_fp8.argtypes = [_p] * 7 + [_i] * 13 + [_p, _sz, _p]
+_lib.attn_select_pages_fp8.restype = _i
+_lib.attn_select_pages_fp8_workspace_size.argtypes = [_i, _i, _i]
+_lib.attn_select_pages_fp8_workspace_size.restype = _sz
 _lib.attn_fwd_kv_fp8_pages.argtypes = [_p] * 11 + [_i] * 10 + [_f, _p, _sz, _p]
 _lib.attn_fwd_kv_fp8_pages.restype = _i
 _lib.attn_fwd_kv_fp8_pages_workspace_size.argtypes = [_i, _i, _i, _i]
@@ -771,6 +775,62 @@ def _workspace(workspace, need, dev):
     return workspace
 
 
+def attn_select_pages_fp8_workspace_size(Hkv: int, total_q: int, max_pages: int) -> int:
+    n = _lib.attn_select_pages_fp8_workspace_size(Hkv, total_q, max_pages)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(-1, attn_last_error())
+    return int(n)
+
+
+def attn_select_pages_fp8(q, k_bounds, k_scale, page_table, cu_seqlens_q, kv_lens, page_size: int, count: int, max_q: int,
+                          first: int = 1, last: int = 1, causal: bool = True, pages=None, workspace=None, stream=None):
+    """The pages that packed queries q [Hq, total_q, d] (CUDA bf16) are to read, int32 [Hkv, total_q,
+    ``count``]: page numbers within the query's sequence, ascending, -1 behind the last one.  The first
+    ``first`` and the last ``last`` pages that the query sees are listed, and the best of the others by
+    the largest score that a key within the page's bounds could have (``k_bounds`` uint8 [num_pages,
+    Hkv, 2, d] as ``attn_rope_kv_append_fp8`` keeps them, times ``k_scale``) with any head of the group;
+    a query that sees no more than ``count`` pages lists them all.  Equal scores go by number.
+    Other tensors and ``max_q`` as ``attn_fwd_kv_fp8``; ``workspace``: a uint8 CUDA tensor of at least
+    attn_select_pages_fp8_workspace_size(...) bytes (allocated when None)."""
+    if not q.is_cuda or q.dim() != 3:
+        raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
+    dev = q.device
+    if stream is not None or dev.index != _current_device():
+        with _there(dev, stream):
+            return attn_select_pages_fp8(q, k_bounds, k_scale, page_table, cu_seqlens_q, kv_lens, page_size, count, max_q,
+                                         first, last, causal, pages, workspace)
+    Hq, T, d = q.shape
+    if k_bounds.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"expected k_bounds [num_pages, Hkv, 2, d] and page_table [B, max_pages], got {tuple(k_bounds.shape)} "
+                         f"and {tuple(page_table.shape)}")
+    num_pages, Hkv = k_bounds.shape[:2]
+    B, width = page_table.shape
+    if count < 1:
+        raise ValueError(f"count={count} must be at least 1")
+    if pages is None:
+        pages = torch.empty((Hkv, T, count), dtype=torch.int32, device=dev)
+    i32 = torch.int32
+    if not (q.dtype is torch.bfloat16 and k_bounds.dtype is torch.uint8 and k_scale.dtype is torch.float32
+            and page_table.dtype is i32 and cu_seqlens_q.dtype is i32 and kv_lens.dtype is i32 and pages.dtype is i32
+            and k_bounds.shape == (num_pages, Hkv, 2, d) and k_scale.shape == (num_pages, Hkv) and cu_seqlens_q.shape == (B + 1,)
+            and kv_lens.shape == (B,) and pages.shape == (Hkv, T, count)
+            and k_bounds.device == dev and k_scale.device == dev and page_table.device == dev and cu_seqlens_q.device == dev
+            and kv_lens.device == dev and pages.device == dev and q.is_contiguous() and k_bounds.is_contiguous()
+            and k_scale.is_contiguous() and page_table.is_contiguous() and cu_seqlens_q.is_contiguous()
+            and kv_lens.is_contiguous() and pages.is_contiguous()):
+        for name, t, dtype, want in (("q", q, torch.bfloat16, (Hq, T, d)), ("k_bounds", k_bounds, torch.uint8, (num_pages, Hkv, 2, d)),
+                                     ("k_scale", k_scale, torch.float32, (num_pages, Hkv)), ("page_table", page_table, i32, (B, width)),
+                                     ("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,)), ("kv_lens", kv_lens, i32, (B,)),
+                                     ("pages", pages, i32, (Hkv, T, count))):
+            _plain(name, t, dtype, want, dev)
+    ws = _workspace(workspace, lambda: attn_select_pages_fp8_workspace_size(Hkv, T, width), dev)
+    _check(_lib.attn_select_pages_fp8(q.data_ptr(), k_bounds.data_ptr(), k_scale.data_ptr(), page_table.data_ptr(),
+                                      cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), pages.data_ptr(), B, Hq, Hkv, T, max_q, d,
+                                      num_pages, page_size, width, count, first, last, 1 if causal else 0, ws.data_ptr(),
+                                      ws.nbytes, _current_stream(dev.index)))
+    return pages
+
+
 def attn_fwd_kv_fp8_pages_workspace_size(Hq: int, Hkv: int, total_q: int, d: int) -> int:
     n = _lib.attn_fwd_kv_fp8_pages_workspace_size(Hq, Hkv, total_q, d)
     if n == ctypes.c_size_t(-1).value:
@@ -898,6 +958,7 @@ __all__ = ["attn_fwd", "attn_fwd_fp8", "attn_quantize_fp8", "attn_bwd", "attn_bw
            "attn_set_debug_knobs", "attn_get_debug_knobs", "attn_device_status", "attn_rescale_counter",
            "attn_exp2_sw", "attn_set_test_hooks", "attn_rope", "attn_rope_bwd", "attn_rope_freqs", "attn_kv_append_fp8",
            "attn_rope_kv_append_fp8",
-           "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "attn_fwd_kv_fp8_pages",
+           "attn_fwd_kv_fp8", "attn_fwd_kv_fp8_workspace_size", "attn_select_pages_fp8",
+           "attn_select_pages_fp8_workspace_size", "attn_fwd_kv_fp8_pages",
            "attn_fwd_kv_fp8_pages_workspace_size", "attn_fwd_kv_fp8_prefix", "attn_fwd_kv_fp8_prefix_workspace_size",
            "AttnError", "LIB_PATH"]

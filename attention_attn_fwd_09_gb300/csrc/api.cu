@@ -1110,6 +1110,59 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   return post_launch(s, st);
 }
 
+size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages) {
+  if (Hkv <= 0 || total_q < 0 || max_pages < 0) {
+    set_last_error("attn_select_pages_fp8_workspace_size: invalid sizes");
+    return (size_t)-1;
+  }
+  return total_q == 0 || max_pages == 0 ? 0 : select_ws(Hkv, total_q, max_pages).total;
+}
+
+int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_scale, const int* page_table,
+                          const int* cu_seqlens_q, const int* kv_lens, int* pages, int B, int Hq, int Hkv, int total_q,
+                          int max_q, int d, int num_pages, int page_size, int max_pages, int count, int first, int last,
+                          int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache(B, Hkv, total_q, d, num_pages, page_size, max_pages);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_shape(B, Hq, Hkv, total_q, d, 1.f)) != ATTN_OK) return rc;
+  if (Hq > 65535) return fail(ATTN_ERR_UNSUPPORTED, "Hq=%d: packed sequences support at most 65535 heads", Hq);
+  if (Hq / Hkv > 256) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv = %d (supported: up to 256)", Hq / Hkv);
+  if (count < 1 || first < 0 || last < 0 || first > count || last > count - first)
+    return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 1, first=%d and last=%d >= 0 and together within it", count, first,
+                last);
+  if (B == 0 || total_q == 0) return ATTN_OK;
+  if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
+  if (!q || !k_bounds || !k_scale || !page_table || !cu_seqlens_q || !kv_lens || !pages)
+    return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(k_bounds)) return fail(ATTN_ERR_MISALIGNED, "q and k_bounds must be 16-byte aligned");
+  if (!aligned4(k_scale) || !aligned4(page_table) || !aligned4(cu_seqlens_q) || !aligned4(kv_lens) || !aligned4(pages))
+    return fail(ATTN_ERR_MISALIGNED, "scales, page table, offsets, lengths and pages must be 4-byte aligned");
+  const SelectWs w = select_ws(Hkv, total_q, max_pages);
+  if (max_pages > 0 && (rc = check_workspace(workspace, workspace_bytes, w.total)) != ATTN_OK) return rc;
+  const DevSyms* s = dev_syms(nullptr);
+  if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
+  char* ws = static_cast<char*>(workspace);
+  SelectParams p{};
+  p.q = q;
+  p.bounds = static_cast<const uint8_t*>(k_bounds);
+  p.k_scale = k_scale;
+  p.table = page_table; p.cu_q = cu_seqlens_q; p.kv_lens = kv_lens;
+  p.out = pages;
+  p.B = B; p.Hkv = Hkv; p.g = Hq / Hkv; p.total_q = total_q; p.max_q = max_q;
+  p.num_pages = num_pages; p.page = page_size; p.max_pages = max_pages; p.max_len = max_pages * page_size;
+  p.count = count; p.first = first; p.last = last;
+  p.causal = causal ? 1 : 0;
+  p.scores = reinterpret_cast<float*>(ws);
+  p.exact = reinterpret_cast<unsigned long long*>(ws + w.exact);
+  p.near = reinterpret_cast<int*>(ws + w.near);
+  p.errors = reinterpret_cast<float*>(ws + w.errors);
+  p.status = s->status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_select_pages(p, d, std::max(1, s->sms), st);
+  if (e != cudaSuccess) return cuda_fail(e, "page selection launch");
+  return post_launch(s, st);
+}
+
 // Query heads that one unit of the listed pages' kernel holds: a group's, or its largest share of at most 16.
 static int list_group(int g) {
   int share = std::min(g, kCacheDecodeRows);

@@ -217,6 +217,26 @@ struct RopeAppendParams {
 };
 cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s);
 
+// Choice of pages by their bounds (select_pages.cu); d = 64 or 128.
+struct SelectParams {
+  const void* q;             // bf16 [Hq, total_q, d]
+  const uint8_t* bounds;     // [num_pages, Hkv, 2, d]
+  const float* k_scale;      // [num_pages, Hkv]
+  const int *table, *cu_q, *kv_lens;
+  int* out;                  // [Hkv, total_q, count]
+  int B, Hkv, g, total_q, max_q, num_pages, page, max_pages, max_len, count, first, last, causal;
+  float *scores, *errors;    // workspace, see select_ws
+  unsigned long long* exact;
+  int* near;
+  int* status;
+  int page_shift, qn, chunk, chunks;   // filled in by launch_select_pages
+};
+struct SelectWs {
+  size_t exact, near, errors, total;   // scores come first
+};
+SelectWs select_ws(int Hkv, int total_q, int max_pages);
+cudaError_t launch_select_pages(SelectParams p, int d, int sms, cudaStream_t s);
+
 // Packed queries over the paged e4m3 cache (fwd_cache.cu).
 struct CacheParams {
   const void* q;             // bf16 [Hq, total_q, d]

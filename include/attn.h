@@ -253,6 +253,37 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
 size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int max_q, int d);
 
 /*
+ * The pages of the 8-bit cache that each query is to read (for attn_fwd_kv_fp8_pages), by an upper bound
+ * of the scores of a page's keys: with lo, hi the page's smallest and largest code per column,
+ *     score(page) = k_scale max_h sum_c max(q_hc, 0) hi_c + min(q_hc, 0) lo_c
+ * over the Hq / Hkv heads h of the group.
+ *
+ *   k_bounds [num_pages, Hkv, 2, d] (16-byte aligned) and k_scale as attn_rope_kv_append_fp8 keeps them; q,
+ *       page_table, cu_seqlens_q, kv_lens, max_q, causal as attn_fwd_kv_fp8.
+ *   pages: DEVICE int32 [Hkv, total_q, count] out: numbers of pages within the query's sequence, ascending, -1
+ *       behind the last one.  A query that sees up to count pages lists them all.  Otherwise its list
+ *       holds the first `first` and the last `last` of them (together at most count; the last one holds the
+ *       query's own key) and, of the others, the count - first - last with the largest scores.
+ *   The choice is that of exact scores: equal ones by number, NaN (of the query or the bounds) above
+ *       all.  Scores come in fp32 first, and pages whose order that cannot tell are scored again in 64 bits, which
+ *       takes long when a great many are alike.
+ *   workspace: attn_select_pages_fp8_workspace_size(...) bytes, 16-byte aligned, owned by the caller,
+ *       contents on entry irrelevant; calls (graphs) that may run at once need one each.
+ * Errors as attn_fwd_kv_fp8: invalid offsets or lengths write nothing; with a page table entry outside the
+ *   cache that query's lists are undefined.
+ */
+int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_scale, const int* page_table,
+                          const int* cu_seqlens_q, const int* kv_lens, int* pages, int B, int Hq, int Hkv, int total_q,
+                          int max_q, int d, int num_pages, int page_size, int max_pages, int count, int first, int last,
+                          int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace attn_select_pages_fp8 needs: about 16 per query, K/V head and entry of a page table's row;
+ * (size_t)-1 for invalid sizes.
+ */
+size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages);
+
+/*
  * attn_fwd_kv_fp8 over listed pages only (sparse attention over blocks of the cache, decoding and
  * drafts): for each K/V head and query the pages whose keys it reads.
  *
