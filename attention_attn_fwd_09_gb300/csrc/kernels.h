@@ -229,7 +229,7 @@ struct SelectParams {
   unsigned long long* exact;
   int* near;
   int* status;
-  int page_shift, qn, chunk, chunks;   // filled in by launch_select_pages
+  int page_shift, qn, groups;   // filled in by launch_select_pages
 };
 struct SelectWs {
   size_t exact, near, errors, total;   // scores come first

@@ -12,11 +12,15 @@
 // tell are scored again in 64 bits.  So the list depends on nothing but the query and the bounds.
 //
 // Two dependent launches:
-//   * scores, bound by the bounds' bytes (2 d per page and K/V head): a warp takes 8 pages as the
-//     columns of mma.m16n8k16, the rows are queries x heads of a group (as in fwd_cache.cu), the
-//     products run over [max(q, 0), min(q, 0)] against [hi, lo].  f16 holds the codes and, scaled by a power
-//     of two per row, q (exact down to 2^-31 of the row's largest component, off by 2^-39 of it below);
-//   * choice, bound by latency: a CTA per query and K/V head bisects for the border.
+//   * scores, bound by the bounds' bytes (2 d per page and K/V head): a warp takes 16 pages as the rows
+//     of mma.m16n8k16 (read straight into the fragments: a lane's share of a page is 16 neighbouring
+//     columns), the columns are queries x heads of a group, 8 or 16 of them; the products run over
+//     [max(q, 0), min(q, 0)] against [hi, lo].  f16 holds the codes and, scaled by a power of two per row, q
+//     (exact down to 2^-31 of the row's largest component, off by 2^-39 of it below).  The work is cut
+//     evenly: all units' steps of 16 pages end to end, every warp an equal run.  (Pages as the columns of
+//     the same instruction took twice the products and three times the instructions: 64 ragged sequences
+//     of up to 32768 keys in pages of 32, 37 us);
+//   * choice, bound by latency: a CTA per query and K/V head looks for the border with histograms.
 #include <cstdint>
 #include <mutex>
 
@@ -27,14 +31,15 @@
 namespace attn {
 namespace {
 
+constexpr int kScoreThreads = 128, kScoreWarps = kScoreThreads / 32, kScoreCtas = 4;   // CTAs per SM
+constexpr int kStep = 16;                    // pages that a warp scores at once
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kStepPages = kSelWarps * 8;    // pages that a CTA scores at once
 constexpr float kBig = 3.0e38f;
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t positive(uint32_t x) {
   const __half2 z = __float2half2_rn(0.f), r = __hmax2(*reinterpret_cast<const __half2*>(&x), z);
@@ -44,115 +49,111 @@ __device__ __forceinline__ uint32_t negative(uint32_t x) {
   const __half2 z = __float2half2_rn(0.f), r = __hmin2(*reinterpret_cast<const __half2*>(&x), z);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {       // NaN wins
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// Where a tile of queries stands.
-struct Tile {
-  int b, q0, n, len;         // sequence, its first packed query, queries, keys
+// A sequence's queries and keys.
+struct Seq {
+  int q0, n, len;
+  __device__ __forceinline__ Seq(const SelectParams& p, int b) {
+    q0 = __ldg(p.cu_q + b);
+    n = __ldg(p.cu_q + b + 1) - q0;
+    len = __ldg(p.kv_lens + b);
+  }
+  __device__ __forceinline__ bool wrong(const SelectParams& p, int b) const {
+    const int c1 = q0 + n;
+    return q0 < 0 || n < 0 || c1 < 0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
+           (b == 0 && q0 != 0) || (b == p.B - 1 && c1 != p.total_q);
+  }
+  // Pages that query i sees.
+  __device__ __forceinline__ int seen(const SelectParams& p, int i) const {
+    const int keys = p.causal ? len - n + i + 1 : len;
+    return (keys + p.page - 1) >> p.page_shift;
+  }
+  // Steps of 16 pages (numbers 16 s .. 16 s + 15) that hold candidates of its last query: [first_step, first_step + steps).
+  __device__ __forceinline__ int steps(const SelectParams& p) const {
+    const int all = seen(p, n - 1), end = all - p.last;
+    return n == 0 || all <= p.count || end <= p.first ? 0 : (end + kStep - 1) / kStep - p.first / kStep;
+  }
+  __device__ __forceinline__ int tiles(const SelectParams& p) const { return (n + p.qn - 1) / p.qn; }
 };
-// The sequence of `slot`, the last one with first slot cu[b] / qn (+ b, when qn > 1) <= slot; false where the
-// offsets or lengths are wrong.  All threads of the CTA.
-__device__ __forceinline__ bool find_tile(const SelectParams& p, int slot, Tile& out) {
-  __shared__ int below;
-  bool wrong = false;
-  int mine = 0;
-  if (threadIdx.x == 0) below = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.B; i += kSelThreads) {
-    const int c0 = __ldg(p.cu_q + i), c1 = __ldg(p.cu_q + i + 1), len = __ldg(p.kv_lens + i), n = c1 - c0;
-    wrong |= c0 < 0 || c1 < c0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
-             (i == 0 && c0 != 0) || (i == p.B - 1 && c1 != p.total_q);
-    mine += (p.qn > 1 ? c0 / p.qn + i : c0) <= slot ? 1 : 0;
-  }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&below, mine);
-  if (__syncthreads_or(wrong)) {
-    if (threadIdx.x == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
-    return false;
-  }
-  out.b = below - 1;
-  out.q0 = __ldg(p.cu_q + out.b);
-  out.n = __ldg(p.cu_q + out.b + 1) - out.q0;
-  out.len = __ldg(p.kv_lens + out.b);
-  return true;
-}
-// Pages that query i of the sequence sees.
-__device__ __forceinline__ int pages_seen(const SelectParams& p, const Tile& t, int i) {
-  const int keys = p.causal ? t.len - t.n + i + 1 : t.len;
-  return (keys + p.page - 1) >> p.page_shift;
-}
 
-// Block: (tile slot, K/V head, chunk of p.chunk pages).  Writes scores [K/V head][query][max_pages] and,
-// per chunk, a bound on their error.
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_score_kernel(const SelectParams p) {
+// Scores [K/V head][query][max_pages] and, per step of 16 pages, a bound on their error.  A unit is a tile of
+// queries of one sequence (as many as make 8 NT rows with their heads) and a K/V head.
+template <int D, int NT>
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) select_score_kernel(const SelectParams p) {
   constexpr int KS = D / 16;                 // products of 16 columns
-  __shared__ float sums[kSelWarps][16][9];
-  __shared__ float norms[16], scale_max[kSelWarps];
+  __shared__ float rows_of[kScoreWarps][kStep][8 * NT + 1];        // groups of other sizes than powers of two
+  __shared__ float row_norm[kScoreWarps][8 * NT];
+  __shared__ long long starts[kScoreThreads], sums[kScoreWarps];
   pdl_wait();                                // nothing of global memory before this
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3, rq = lane >> 2;
-  const int chunk = blockIdx.x % p.chunks, unit = blockIdx.x / p.chunks, h = unit % p.Hkv, slot = unit / p.Hkv;
-  Tile t;
-  if (!find_tile(p, slot, t)) return;
-  // Queries i0 .. i1 - 1 of the sequence.
-  const int i0 = p.qn > 1 ? (slot - (t.q0 / p.qn + t.b)) * p.qn : slot - t.q0, i1 = min(i0 + p.qn, t.n);
-  if (i0 >= i1) return;                      // a spare slot
-  const int seen = pages_seen(p, t, i1 - 1);
-  const int begin = max(p.first, chunk * p.chunk), end = min(seen - p.last, (chunk + 1) * p.chunk);
-  if (seen <= p.count || begin >= end) return;
-  const int* table = p.table + (long long)t.b * p.max_pages;
-  const int tiles = p.g > 16 ? (p.g + 15) / 16 : 1;                // of 16 heads, when a group has more
-  if (tid < 16) norms[tid] = 0.f;
-  float big = 0.f;
-  for (int rt = 0; rt < tiles; ++rt) {
-    const int heads = min(p.g - rt * 16, 16), rows = tiles > 1 ? heads : (i1 - i0) * p.g;
-    // ---- Q: row r is query r / g, head r % g.  As in fwd_cache.cu a thread's columns are 16 neighbouring ones.
-    uint32_t qp[KS][4], qm[KS][4];
-    float unscale[2];
-    __syncthreads();                         // norms
+  // ---- the run of steps of this warp; thread t adds up sequences [t per_thread, ...)
+  const int per_thread = (p.B + kScoreThreads - 1) / kScoreThreads;
+  const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
+  long long mine = 0;
+  bool wrong = false;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Seq s(p, b);
+    const bool w = s.wrong(p, b);
+    wrong |= w;
+    if (!w) mine += (long long)s.tiles(p) * s.steps(p);
+  }
+  mine *= p.Hkv;
+  long long incl = mine;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = rq + 8 * i, qi = tiles > 1 ? 0 : r / p.g, hd = tiles > 1 ? rt * 16 + r : r - qi * p.g;
-      uint4 w[D / 32];
-      float amax = 0.f, norm = 0.f;
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + hd) * p.total_q + t.q0 + i0 + qi) * D + c * 16;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  const bool bad = __syncthreads_or(wrong) != 0;
+  if (bad) {
+    if (tid == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
+    return;
+  }
+  long long before = incl - mine, total = 0;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        w[k] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + (k >> 1) * 64) + (k & 1)) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+  for (int w = 0; w < kScoreWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  starts[tid] = before;
+  __syncthreads();
+  const long long warps = (long long)gridDim.x * kScoreWarps, run = (total + warps - 1) / warps;
+  // (neighbouring runs on different SMs: few units leave no SM with several)
+  const long long rs = run * ((long long)warp * gridDim.x + blockIdx.x), re = min(rs + run, total);
+  if (rs >= total) return;
+  int at = 0;                                // the last thread whose sequences start at or before rs
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = fabsf(__uint_as_float(u[j] << 16)), b = fabsf(__uint_as_float(u[j] & 0xffff0000u));
-          amax = fmax3(amax, a, b);
-          norm += a + b;
-        }
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      norm += __shfl_xor_sync(0xffffffffu, norm, 1);
-      norm += __shfl_xor_sync(0xffffffffu, norm, 2);
-      const uint32_t e = __float_as_uint(amax) >> 23;              // biased exponent
-      const uint32_t up = min(268u - e, 253u);                     // of the factor: largest |q| to [2^14, 2^15)
-      const float inv = __uint_as_float(up << 23);
-      unscale[i] = __uint_as_float((254u - up) << 23);
-      // Infinite or NaN: scores that say nothing (all pages are then scored in 64 bits).
-      if (!(norm <= kBig)) norm = INFINITY;
-      if (c == 0 && r < rows && warp == 0) atomicMax(reinterpret_cast<int*>(norms + qi), __float_as_int(norm));   // >= 0
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h2 = pack_f16x2(__uint_as_float(u[j] << 16) * inv, __uint_as_float(u[j] & 0xffff0000u) * inv);
-          const int word = (k & 1) * 4 + j;
-          qp[(k >> 1) * 4 + (word >> 1)][(word & 1) * 2 + i] = positive(h2);
-          qm[(k >> 1) * 4 + (word >> 1)][(word & 1) * 2 + i] = negative(h2);
-        }
-      }
-    }
-    // ---- pages, 8 at a time: column rq of the products is page base + rq
-    auto page_at = [&](int base) -> int {
-      const int j = base + rq;
+  for (int i = 0; i < kScoreThreads / 32; ++i) at += __popc(__ballot_sync(0xffffffffu, starts[i * 32 + lane] <= rs));
+  int b = (at - 1) * per_thread;
+  long long f = starts[at - 1];              // first step of sequence b
+  Seq seq(p, b);
+  int steps = seq.steps(p);
+  long long all = (long long)seq.tiles(p) * p.Hkv * steps;
+  while (f + all <= rs) {
+    f += all;
+    seq = Seq(p, ++b);
+    steps = seq.steps(p);
+    all = (long long)seq.tiles(p) * p.Hkv * steps;
+  }
+  int unit = (int)((rs - f) / steps), step = (int)((rs - f) - (long long)unit * steps);
+  constexpr int ROWS = 8 * NT;
+  const int row_tiles = p.g > ROWS ? (p.g + ROWS - 1) / ROWS : 1;  // of 16 heads, when a group has more
+  const bool pow2 = (p.g & (p.g - 1)) == 0;
+
+  for (long long left = re - rs; left > 0;) {
+    const int tile = unit / p.Hkv, h = unit - tile * p.Hkv, i0 = tile * p.qn, nq = min(p.qn, seq.n - i0);
+    const int todo = (int)min((long long)(steps - step), left);    // steps of this unit here
+    const int begin = p.first, end = seq.seen(p, i0 + nq - 1) - p.last;      // candidates of the tile's queries
+    const int* table = p.table + (long long)b * p.max_pages;
+    const long long out_row = (long long)h * p.total_q + seq.q0 + i0;        // of the first query
+    auto page_at = [&](int j) -> int {
       if (j < begin || j >= end) return -1;
       const int pg = __ldg(table + j);
       if (pg < 0 || pg >= p.num_pages) {
@@ -161,71 +162,194 @@ __global__ void __launch_bounds__(kSelThreads) select_score_kernel(const SelectP
       }
       return pg;
     };
-    int base = begin / 8 * 8 + warp * 8, pg = page_at(base);
-    for (; base < end; base += kStepPages) {
-      const int pg_now = pg;
-      pg = page_at(base + kStepPages);
-      uint4 lo[D / 64], hi[D / 64];
-      float scale = 0.f;
+    for (int rt = 0; rt < row_tiles; ++rt) {
+      int j = (p.first / kStep + step) * kStep + rq;               // this lane's pages: j and j + 8
+      int pg[2] = {page_at(j), page_at(j + 8)};
+      const int heads = min(p.g - rt * ROWS, ROWS), rows = row_tiles > 1 ? heads : nq * p.g;
+      // ---- Q: row r is query r / g, head r % g; this lane's columns of rows rq (and rq + 8)
+      uint32_t qp[NT][KS][2], qm[NT][KS][2];
+      float us[NT][2];                       // what undoes the scaling of rows 2 c, 2 c + 1
+      __syncwarp();                          // the norms before have been read
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) lo[k] = hi[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (pg_now >= 0) {
-        const long long ph = (long long)pg_now * p.Hkv + h;
-        const uint8_t* row = p.bounds + ph * 2 * D + c * 16;
+      for (int i = 0; i < NT; ++i) {
+        const int r = rq + 8 * i, qi = row_tiles > 1 ? 0 : r / p.g, hd = row_tiles > 1 ? rt * ROWS + r : r - qi * p.g;
+        uint4 w[D / 32];
+        float amax = 0.f, sum = 0.f;
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + hd) * p.total_q + seq.q0 + i0 + qi) * D + c * 16;
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          lo[k] = __ldg(reinterpret_cast<const uint4*>(row + k * 64));
-          hi[k] = __ldg(reinterpret_cast<const uint4*>(row + D + k * 64));
+        for (int k = 0; k < D / 32; ++k)
+          w[k] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + (k >> 1) * 64) + (k & 1)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float y = fabsf(__uint_as_float(u[x] << 16)), z = fabsf(__uint_as_float(u[x] & 0xffff0000u));
+            amax = fmax3(amax, y, z);
+            sum += y + z;
+          }
         }
-        scale = __ldg(p.k_scale + ph);
-      }
-      big = fmaxf(big, scale <= kBig ? scale : INFINITY);
-      // Four sums of their own for the products that one takes in turn: a quarter of the rounding.
-      float acc[4][4];
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const uint32_t e = __float_as_uint(amax) >> 23;            // biased exponent
+        const uint32_t up = min(268u - e, 253u);                   // of the factor: largest |q| to [2^14, 2^15)
+        const float inv = __uint_as_float(up << 23), unscale = __uint_as_float((254u - up) << 23);
+        us[i][0] = __shfl_sync(0xffffffffu, unscale, c * 8);
+        us[i][1] = __shfl_sync(0xffffffffu, unscale, c * 8 + 4);
+        // Infinite or NaN: scores that say nothing (all pages are then scored exactly).
+        if (c == 0) row_norm[warp][r] = r < rows ? (sum <= kBig ? sum : INFINITY) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        for (int k = 0; k < D / 32; ++k) {
+          const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) {
-        const uint32_t l[4] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w}, u[4] = {hi[k].x, hi[k].y, hi[k].z, hi[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma_f16(acc[j], qp[k * 4 + j], e4m3x2_f16x2(u[j]), e4m3x2_f16x2_hi(u[j]));
-          mma_f16(acc[j], qm[k * 4 + j], e4m3x2_f16x2(l[j]), e4m3x2_f16x2_hi(l[j]));
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t h2 = pack_f16x2(__uint_as_float(u[x] << 16) * inv, __uint_as_float(u[x] & 0xffff0000u) * inv);
+            const int word = (k & 1) * 4 + x;
+            qp[i][(k >> 1) * 4 + (word >> 1)][word & 1] = positive(h2);
+            qm[i][(k >> 1) * 4 + (word >> 1)][word & 1] = negative(h2);
+          }
         }
-      }
-      const float s0 = __shfl_sync(0xffffffffu, scale, c * 8), s1 = __shfl_sync(0xffffffffu, scale, c * 8 + 4);
-      __syncwarp();                          // the sums before have been read
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sums[warp][rq + 8 * i][2 * c] = ((acc[0][2 * i] + acc[1][2 * i]) + (acc[2][2 * i] + acc[3][2 * i])) * unscale[i] * s0;
-        sums[warp][rq + 8 * i][2 * c + 1] = ((acc[0][2 * i + 1] + acc[1][2 * i + 1]) + (acc[2][2 * i + 1] + acc[3][2 * i + 1])) * unscale[i] * s1;
       }
       __syncwarp();
-      // The largest of each query's heads; NaN wins.
-      for (int x = lane; x < (i1 - i0) * 8; x += 32) {
-        const int qi = x >> 3, j = base + (x & 7);
-        if (j < begin || j >= end) continue;
-        const int r0 = tiles > 1 ? 0 : qi * p.g, r1 = tiles > 1 ? heads : r0 + p.g;
-        float* out = p.scores + ((long long)h * p.total_q + t.q0 + i0 + qi) * p.max_pages + j;
-        float m = rt > 0 ? *out : -INFINITY;
-        for (int r = r0; r < r1; ++r) {
-          const float v = sums[warp][r][x & 7];
-          m = v != v || v > m ? v : m;
+      float norm = 0.f;                      // lane qi: the largest |q|_1 of query qi's heads here
+      if (lane < nq) {
+        const int r0 = row_tiles > 1 ? 0 : lane * p.g, r1 = row_tiles > 1 ? heads : r0 + p.g;
+        for (int r = r0; r < r1; ++r) norm = fmaxf(norm, row_norm[warp][r]);
+      }
+      // |error| of a score: products are exact, and each of the 2 d / 64 products of 16 terms behind one another
+      // adds 17 numbers, off by 2^-23 of what they can come to at most, 448 scale |q|_1; four roundings more.
+      norm *= (2 * D / 64 * 17 + 4) * 1.1920929e-7f * 448.f;
+
+      for (int s = 0; s < todo; ++s, j += kStep) {
+        float scale[2];
+        uint4 lo[2][D / 64], hi[2][D / 64];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const long long ph = (long long)max(pg[x], 0) * p.Hkv + h;
+          const uint8_t* row = p.bounds + ph * 2 * D + c * 16;     // (no page: page 0, which counts for nothing)
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            lo[x][k] = __ldg(reinterpret_cast<const uint4*>(row + k * 64));
+            hi[x][k] = __ldg(reinterpret_cast<const uint4*>(row + D + k * 64));
+          }
+          scale[x] = __ldg(p.k_scale + ph);
         }
-        *out = m;
+        const bool got[2] = {pg[0] >= 0, pg[1] >= 0};
+        if (s + 1 < todo) {
+          pg[0] = page_at(j + kStep);
+          pg[1] = page_at(j + kStep + 8);
+        }
+        // Four sums of their own for the products that one takes in turn: a quarter of the rounding.
+        float acc[NT][4][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[i][x][0] = acc[i][x][1] = acc[i][x][2] = acc[i][x][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const uint32_t l0[4] = {lo[0][k].x, lo[0][k].y, lo[0][k].z, lo[0][k].w}, l1[4] = {lo[1][k].x, lo[1][k].y, lo[1][k].z, lo[1][k].w};
+          const uint32_t u0[4] = {hi[0][k].x, hi[0][k].y, hi[0][k].z, hi[0][k].w}, u1[4] = {hi[1][k].x, hi[1][k].y, hi[1][k].z, hi[1][k].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t a0 = e4m3x2_f16x2(u0[x]), a1 = e4m3x2_f16x2(u1[x]), a2 = e4m3x2_f16x2_hi(u0[x]), a3 = e4m3x2_f16x2_hi(u1[x]);
+            const uint32_t d0 = e4m3x2_f16x2(l0[x]), d1 = e4m3x2_f16x2(l1[x]), d2 = e4m3x2_f16x2_hi(l0[x]), d3 = e4m3x2_f16x2_hi(l1[x]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              mma_f16(acc[i][x], a0, a1, a2, a3, qp[i][k * 4 + x][0], qp[i][k * 4 + x][1]);
+              mma_f16(acc[i][x], d0, d1, d2, d3, qm[i][k * 4 + x][0], qm[i][k * 4 + x][1]);
+            }
+          }
+        }
+        float v[NT][2][2];                   // rows 2 c, 2 c + 1 (+ 8 i), pages j, j + 8
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              v[i][y][x] = ((acc[i][0][2 * x + y] + acc[i][1][2 * x + y]) + (acc[i][2][2 * x + y] + acc[i][3][2 * x + y])) * us[i][y] * scale[x];
+        auto put = [&](int qi, int x, float y) {         // the largest over all row tiles so far
+          if (!got[x]) return;
+          float* out = p.scores + (out_row + qi) * p.max_pages + j + 8 * x;
+          *out = rt > 0 ? max_nan(*out, y) : y;
+        };
+        if (pow2) {                          // the largest of each query's heads, lane to lane
+          if (p.g == 1) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int qi = 8 * i + 2 * c + y;
+                if (qi >= nq) continue;
+                put(qi, 0, v[i][y][0]);
+                put(qi, 1, v[i][y][1]);
+              }
+          } else {
+            float m[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float y = max_nan(v[i][0][x], v[i][1][x]);
+                if (p.g >= 4) y = max_nan(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                if (p.g >= 8) y = max_nan(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                m[i][x] = y;
+              }
+            if (NT > 1 && p.g >= 16) {
+              m[0][0] = max_nan(m[0][0], m[NT - 1][0]);
+              m[0][1] = max_nan(m[0][1], m[NT - 1][1]);
+            }
+            if ((2 * c & (min(p.g, 8) - 1)) == 0) {
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                const int qi = row_tiles > 1 ? 0 : (8 * i + 2 * c) / p.g;
+                if (qi >= nq || (i > 0 && p.g >= 16)) continue;
+                put(qi, 0, m[i][0]);
+                put(qi, 1, m[i][1]);
+              }
+            }
+          }
+        } else {
+          __syncwarp();                      // the rows before have been read
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) rows_of[warp][rq + 8 * x][8 * i + 2 * c + y] = v[i][y][x];
+          __syncwarp();
+          for (int z = lane; z < nq * kStep; z += 32) {
+            const int qi = z / kStep, x = z % kStep, page = j - rq + x;
+            const int r0 = row_tiles > 1 ? 0 : qi * p.g, r1 = row_tiles > 1 ? heads : r0 + p.g;
+            float m = rows_of[warp][x][r0];
+            for (int r = r0 + 1; r < r1; ++r) m = max_nan(m, rows_of[warp][x][r]);
+            if (page < begin || page >= end) continue;
+            float* out = p.scores + (out_row + qi) * p.max_pages + page;
+            *out = rt > 0 ? max_nan(*out, m) : m;
+          }
+        }
+        const float s0 = got[0] ? (scale[0] <= kBig ? scale[0] : INFINITY) : 0.f, s1 = got[1] ? (scale[1] <= kBig ? scale[1] : INFINITY) : 0.f;
+        const float error = norm * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s0, s1))));
+        if (lane < nq) {
+          float* out = p.errors + (out_row + lane) * p.groups + p.first / kStep + step + s;
+          *out = rt > 0 ? fmaxf(*out, error) : error;
+        }
       }
     }
-  }
-  // |error| of a score: products are exact, each of the 2 d / 64 products of 16 terms behind one another adds 17
-  // numbers, off by 2^-23 of what they can come to at most, 448 scale |q|_1; four roundings more.
-  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-  if (lane == 0) scale_max[warp] = big;
-  __syncthreads();
-  if (tid < i1 - i0) {
-    for (int w = 1; w < kSelWarps; ++w) big = fmaxf(big, scale_max[w]);
-    big = fmaxf(big, scale_max[0]);
-    p.errors[((long long)h * p.total_q + t.q0 + i0 + tid) * p.chunks + chunk] =
-        (2 * D / 64 * 17 + 4) * 1.1920929e-7f * 448.f * big * norms[tid];
+    left -= todo;
+    step += todo;
+    if (left > 0 && step == steps) {         // the next unit, or the next sequence that has any
+      step = 0;
+      if (++unit == seq.tiles(p) * p.Hkv) {
+        unit = 0;
+        do {
+          seq = Seq(p, ++b);
+          steps = seq.steps(p);
+        } while (steps == 0);
+      }
+    }
   }
 }
 
@@ -235,26 +359,158 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
   const long long b = __double_as_longlong(x + 0.0);
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | (1ull << 63);
 }
+// The same of a float, as a signed number.
+__device__ __forceinline__ int ordered32(float x) {
+  const int b = __float_as_int(x);
+  return b < 0 ? b ^ 0x7fffffff : b;
+}
+__device__ __forceinline__ float unordered32(int b) { return __int_as_float(b < 0 ? b ^ 0x7fffffff : b); }
+
+// The exact score of page pg for packed query q and K/V head h, as ordered() bits; by a warp.  Codes are m 2^x
+// with 4 bits of m and q's components with 8, so that their products, as whole numbers times one power of two, add up
+// exactly in 64 bits where q's components lie within 2^29 of each other; elsewhere doubles do it (ten times as
+// long: an SM has two 64-bit multiply-adds a cycle).
+template <int D>
+__device__ unsigned long long exact_score(const SelectParams& p, int q, int h, int pg) {
+  constexpr int COLS = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long ph = (long long)pg * p.Hkv + h;
+  const uint8_t* row = p.bounds + ph * 2 * D + lane * COLS;
+  const uint32_t lo = COLS == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row)) : __ldg(reinterpret_cast<const uint16_t*>(row));
+  const uint32_t hi = COLS == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row + D)) : __ldg(reinterpret_cast<const uint16_t*>(row + D));
+  const double scale = (double)__ldg(p.k_scale + ph);
+  bool nan = false;
+#pragma unroll
+  for (int x = 0; x < COLS; ++x) nan |= (lo >> 8 * x & 0x7f) == 0x7f || (hi >> 8 * x & 0x7f) == 0x7f;
+  if (__any_sync(0xffffffffu, nan)) return ~0ull;
+  unsigned long long best = 0;               // below every number
+  for (int r0 = 0; r0 < p.g; r0 += 32) {
+    double own = -INFINITY;                  // of head r0 + lane
+    uint32_t ahead[4][2];                    // four heads' loads under way at once
+    for (int r = r0; r < min(p.g, r0 + 32); ++r) {
+      if ((r & 3) == 0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + min(r + x, p.g - 1)) * p.total_q + q) * D + lane * COLS;
+          if constexpr (COLS == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+            ahead[x][0] = u.x;
+            ahead[x][1] = u.y;
+          } else {
+            ahead[x][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          }
+        }
+      }
+      uint32_t w[2] = {ahead[0][0], ahead[0][1]};
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        ahead[x][0] = ahead[x + 1][0];
+        ahead[x][1] = ahead[x + 1][1];
+      }
+      int top = 0;
+#pragma unroll
+      for (int x = 0; x < COLS; ++x) top = max(top, (int)(w[x >> 1] >> (x & 1) * 16 + 7 & 0xff));
+      top = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(top, 1));
+      bool far = top == 255;                 // an infinity or NaN
+      long long sum = 0;
+#pragma unroll
+      for (int x = 0; x < COLS; ++x) {
+        const uint32_t y = w[x >> 1] >> (x & 1) * 16 & 0xffffu, e = y >> 7 & 0xff;
+        const int m = (int)((y & 0x7f) | (e ? 0x80 : 0)), below = top - max((int)e, 1);
+        far |= m != 0 && below > 29;
+        const uint32_t code = ((y >> 15 ? lo : hi) >> 8 * x) & 0xff, ce = code >> 3 & 15;
+        const int n = (int)((code & 7) | (ce ? 8 : 0));
+        const long long product = (long long)(m * n) << (max(29 - below, 0) + max((int)ce, 1) - 1);
+        sum += (y >> 15) != (code >> 7) ? -product : product;
+      }
+      double s;
+      if (!__any_sync(0xffffffffu, far)) {
+        const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffffu);
+        const unsigned b = __reduce_add_sync(0xffffffffu, (unsigned)(sum >> 24) & 0xffffffu);
+        const int d = __reduce_add_sync(0xffffffffu, (int)(sum >> 48));
+        sum = (long long)a + ((long long)b << 24) + ((long long)d << 48);
+        if (lane != r - r0) continue;
+        s = (double)sum * __longlong_as_double((long long)(top - 172 + 1023) << 52);
+      } else {
+        s = 0.0;
+#pragma unroll
+        for (int x = 0; x < COLS; ++x) {
+          const float y = __uint_as_float((w[x >> 1] >> (x & 1) * 16) << 16);
+          const float plus = y > 0.f || y != y ? y : 0.f, minus = y < 0.f || y != y ? y : 0.f;
+          float l, u, unused;
+          e4m3x4_to_f32(lo >> 8 * x & 0xff, l, unused, unused, unused);
+          e4m3x4_to_f32(hi >> 8 * x & 0xff, u, unused, unused, unused);
+          s = fma((double)plus, (double)u, s);
+          s = fma((double)minus, (double)l, s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      }
+      if (lane == r - r0) own = s;
+    }
+    const unsigned long long key = lane < p.g - r0 ? ordered(own * scale) : 0ull;
+    const unsigned high = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32));
+    const unsigned low = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32) == high ? (unsigned)key : 0u);
+    best = max(best, (unsigned long long)high << 32 | low);
+  }
+  return best;
+}
 
 // Block: (query, K/V head).
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_choose_kernel(const SelectParams p, const int in_smem) {
   extern __shared__ float local[];
+  constexpr int kBins = 256, kFew = kSelThreads;         // kFew: pages near the border that are ranked in shared memory
+  __shared__ __align__(16) int bins[2][kBins + 4];       // [kBins]: above the range
   __shared__ int red[2][kSelWarps][2];
-  __shared__ float redf[kSelWarps][3];
-  constexpr int kFew = kSelThreads;          // pages near the border that are ranked in shared memory
+  __shared__ int4 redf[kSelWarps];
   __shared__ unsigned long long few_keys[kFew];
   __shared__ int few_at[kFew];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  bins[0][tid] = bins[1][tid] = 0;
+  if (tid == 0) bins[0][kBins] = bins[1][kBins] = 0;
   pdl_wait();                                // nothing of global memory before this
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.Hkv, q = blockIdx.x / p.Hkv;
-  SelectParams one = p;
-  one.qn = 1;
-  Tile t;
-  if (!find_tile(one, q, t)) return;
-  const int seen = pages_seen(p, t, q - t.q0);
   const long long unit = (long long)h * p.total_q + q;
+  float* scores = p.scores + unit * p.max_pages;
+  // The first scores on their way already; what they say of pages that are no candidates is not looked at.
+  constexpr int kAhead = 4;
+  float ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i] = p.first + i * kSelThreads + tid < p.max_pages ? scores[p.first + i * kSelThreads + tid] : 0.f;
+  // ---- the query's sequence, the last that starts at or before it
+  int b = -1;
+  {
+    bool wrong = false;
+    auto look = [&](int i) -> bool {
+      const Seq s(p, i);
+      wrong |= s.wrong(p, i);
+      return s.q0 <= q;
+    };
+    if (p.B <= kSelThreads) {
+      const bool below = tid < p.B && look(tid);
+      if (__syncthreads_or(wrong)) b = -2;
+      else b += __syncthreads_count(below);
+    } else {
+      int below = 0;
+      for (int i = tid; i < p.B; i += kSelThreads) below += look(i) ? 1 : 0;
+      below = __reduce_add_sync(0xffffffffu, below);
+      if (lane == 0) red[0][warp][0] = below;
+      if (__syncthreads_or(wrong)) b = -2;
+      else {
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) b += red[0][w][0];
+      }
+      __syncthreads();
+    }
+    if (b == -2) {
+      if (tid == 0) atomicExch(p.status, DEV_BAD_OFFSETS);
+      return;
+    }
+  }
+  const Seq t(p, b);
+  const int seen = t.seen(p, q - t.q0);
   int* out = p.out + unit * p.count;
   if (seen <= p.count) {
     for (int e = tid; e < p.count; e += kSelThreads) out[e] = e < seen ? e : -1;
@@ -264,245 +520,230 @@ __global__ void __launch_bounds__(kSelThreads) select_choose_kernel(const Select
   for (int e = tid; e < p.last; e += kSelThreads) out[p.count - p.last + e] = seen - p.last + e;
   const int n = seen - p.first - p.last, k = p.count - p.first - p.last;   // k of n candidates
   if (k == 0) return;
-  float* scores = p.scores + unit * p.max_pages + p.first;
+  scores += p.first;
   float* v = in_smem ? local : scores;
   // ---- candidates and their range; NaN ranks above all
-  float low = INFINITY, high = -INFINITY, eps = 0.f;
+  int low_bits = 0x7fffffff, high_bits = -0x7fffffff - 1;
+  float eps = 0.f;
   bool strange = false;
-  for (int i = tid; i < n; i += kSelThreads) {
-    float x = scores[i];
+  for (int i = p.first / kStep + tid; i <= (seen - p.last - 1) / kStep; i += kSelThreads) eps = fmaxf(eps, p.errors[unit * p.groups + i]);
+  for (int i = tid, a = 0; i < n; i += kSelThreads, ++a) {
+    float x = a == 0 ? ahead[0] : a == 1 ? ahead[1] : a == 2 ? ahead[2] : a == 3 ? ahead[3] : scores[i];
     if (x != x) x = INFINITY;
     else {
       strange |= !(fabsf(x) <= kBig);
-      low = fminf(low, x);
-      high = fmaxf(high, x);
+      low_bits = min(low_bits, ordered32(x));
+      high_bits = max(high_bits, ordered32(x));
     }
     v[i] = x;
   }
-  for (int i = p.first / p.chunk + tid; i <= (seen - p.last - 1) / p.chunk; i += kSelThreads)
-    eps = fmaxf(eps, p.errors[unit * p.chunks + i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-    eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, o));
-  }
-  if (lane == 0) {
-    redf[warp][0] = low;
-    redf[warp][1] = high;
-    redf[warp][2] = eps;
-  }
+  low_bits = __reduce_min_sync(0xffffffffu, low_bits);
+  high_bits = __reduce_max_sync(0xffffffffu, high_bits);
+  eps = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(eps)));
+  if (lane == 0) redf[warp] = make_int4(low_bits, high_bits, __float_as_int(eps), 0);
   strange = __syncthreads_or(strange) != 0;
 #pragma unroll
   for (int w = 0; w < kSelWarps; ++w) {
-    low = fminf(low, redf[w][0]);
-    high = fmaxf(high, redf[w][1]);
-    eps = fmaxf(eps, redf[w][2]);
+    const int4 r = redf[w];
+    low_bits = min(low_bits, r.x);
+    high_bits = max(high_bits, r.y);
+    eps = fmaxf(eps, __int_as_float(r.z));
   }
-  // Sums over all threads of two small counts; every second call has its own slots.
+  float low = unordered32(low_bits), high = unordered32(high_bits);
+  // Sums over all threads of two counts, and what the threads before this one have; every second call has its
+  // own slots.
   int turn = 0;
-  auto count2 = [&](int a, int b) -> int2 {
-    a = __reduce_add_sync(0xffffffffu, a);
-    b = __reduce_add_sync(0xffffffffu, b);
-    if (lane == 0) {
-      red[turn][warp][0] = a;
-      red[turn][warp][1] = b;
+  auto scan2 = [&](int a, int b2, int2& before) -> int2 {
+    int ia = a, ib = b2;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
+      if (lane >= o) {
+        ia += xa;
+        ib += xb;
+      }
+    }
+    if (lane == 31) {
+      red[turn][warp][0] = ia;
+      red[turn][warp][1] = ib;
     }
     __syncthreads();
-    a = b = 0;
+    before = make_int2(ia - a, ib - b2);
+    int2 sum = make_int2(0, 0);
 #pragma unroll
     for (int w = 0; w < kSelWarps; ++w) {
-      a += red[turn][w][0];
-      b += red[turn][w][1];
+      const int xa = red[turn][w][0], xb = red[turn][w][1];
+      if (w < warp) {
+        before.x += xa;
+        before.y += xb;
+      }
+      sum.x += xa;
+      sum.y += xb;
     }
     turn ^= 1;
-    return make_int2(a, b);
+    return sum;
   };
-  auto above = [&](float x) -> int {
-    int m = 0;
-    for (int i = tid; i < n; i += kSelThreads) m += v[i] > x ? 1 : 0;
-    return count2(m, 0).x;
-  };
-  // ---- the border: pages above `top` are among the k best for sure, those below `bottom` are not
-  float top, bottom;
-  const bool all = strange || !(eps <= kBig / 131072.f);           // scores that may have overflowed: none is sure
-  if (all) {
-    top = INFINITY;
-    bottom = -INFINITY;
-  } else if (above(kBig) >= k) {             // enough NaN pages to fill the list
-    top = INFINITY;
+  // ---- the border: pages above `top` are among the k best for sure, those below `bottom` are not.  Of [low, high]
+  // the k-th largest score is known to lie there: at least k are >= low, fewer than k above high.
+  float top = INFINITY, bottom = -INFINITY;
+  // None is sure where scores may have overflowed, or differ by less than the bins' arithmetic holds.
+  const bool all = strange || !(eps <= kBig / 1048576.f) || (high - low > eps && high - low < 1e-30f);
+  if (!all && low_bits > high_bits) {        // NaN pages only
     bottom = kBig;
-  } else {
-    // The k-th largest of the scores lies in [low, high]: at least k are >= low, fewer than k above high.
-    for (int it = 0; it < 64 && high - low > eps; ++it) {
-      const float mid = low + (high - low) * 0.5f;
-      if (mid <= low || mid >= high) break;
-      if (above(mid) < k) high = mid;
-      else low = mid;
+  } else if (!all) {
+    // Histograms of the range, which becomes the bin that holds the k-th largest until it is narrower than the error.
+    bool found = false;
+    for (int it = 0; it < 8 && !found; ++it) {
+      int* hist = bins[it & 1];
+      const float width = high - low, to_bin = width > 0.f ? kBins / width : 0.f;
+      for (int i = tid; i < n; i += kSelThreads) {
+        const float x = v[i];
+        if (x > high) atomicAdd(hist + kBins, 1);
+        else if (x >= low) atomicAdd(hist + min((int)((x - low) * to_bin), kBins - 1), 1);
+      }
+      __syncthreads();
+      // Every warp looks: lane l has bins 8 l .. 8 l + 7.
+      const int4 y = reinterpret_cast<const int4*>(hist)[2 * lane], z = reinterpret_cast<const int4*>(hist)[2 * lane + 1];
+      const int c8[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w}, sum = ((y.x + y.y) + (y.z + y.w)) + ((z.x + z.y) + (z.z + z.w));
+      int above = sum;                       // in this lane's bins and all higher ones
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += x;
+      }
+      const int over = hist[kBins];
+      above += over;
+      if (over >= k) {                       // enough NaN pages to fill the list
+        bottom = kBig;
+        found = true;
+        break;
+      }
+      const uint32_t votes = __ballot_sync(0xffffffffu, above >= k);
+      const int owner = 31 - __clz(votes);   // (at least k are >= low)
+      int bin = 0, run = above - sum;
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        if (run < k && run + c8[i] >= k) bin = lane * 8 + i;
+        run += c8[i];
+      }
+      bin = __shfl_sync(0xffffffffu, bin, owner);
+      const float slack = width * 9.5367431640625e-7f;             // 2^-20: bins are found by rounded arithmetic
+      const float lo2 = low + bin * (width / kBins) - slack, hi2 = low + (bin + 1) * (width / kBins) + slack;
+      low = fmaxf(low, lo2);
+      high = fminf(high, hi2);
+      found = high - low <= eps || high - low >= width;
+      if (!found) {                          // the other histogram is the next one; this one's turn comes after it
+        __syncthreads();
+        hist[tid] = 0;
+        if (tid == 0) hist[kBins] = 0;
+      }
     }
-    top = high + 2.01f * eps;
-    bottom = low - 2.01f * eps;
+    if (bottom != kBig) {
+      // Twice the error, and a few roundings of the bins' borders, which are far below it.
+      top = high + 2.1f * eps;
+      bottom = low - 2.1f * eps;
+    }
   }
+  // ---- thread t has candidates [t per, ...): sure ones and those near the border
+  const int per = (n + kSelThreads - 1) / kSelThreads, mine_lo = min(tid * per, n), mine_hi = min(mine_lo + per, n);
   int in = 0, near = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
+  for (int i = mine_lo; i < mine_hi; ++i) {
     const float x = v[i];
     if (x > top) ++in;
     else if (x >= bottom) ++near;
   }
-  const int2 both = count2(in, near);
+  int2 before;
+  const int2 both = scan2(in, near, before);
   const int need = k - both.x, m = both.y;   // of the m pages near the border
-  const float emit = m == need ? (all ? -INFINITY : nextafterf(bottom, -INFINITY)) : fminf(top, kBig);
+  int place = before.x + before.y;
+  float emit = bottom;                       // listed: v >= emit
   if (m != need) {
-    // ---- these in 64 bits, in the order of their numbers
+    // ---- these exactly, in the order of their numbers
     unsigned long long* keys = m <= kFew ? few_keys : p.exact + unit * p.max_pages;
     int* at = m <= kFew ? few_at : p.near + unit * p.max_pages;
-    for (int i0 = 0, found = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const float x = i < n ? v[i] : 0.f;
-      const bool is = i < n && !(x > top) && x >= bottom;
-      const uint32_t votes = __ballot_sync(0xffffffffu, is);
-      if (lane == 0) red[turn][warp][0] = __popc(votes);
-      __syncthreads();
-      int before = found;
-#pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) {
-        if (w < warp) before += red[turn][w][0];
-        found += red[turn][w][0];
-      }
-      turn ^= 1;
-      if (is) at[before + __popc(votes & ((1u << lane) - 1))] = i;
-    }
+    for (int i = mine_lo, x = before.y; i < mine_hi; ++i)
+      if (!(v[i] > top) && v[i] >= bottom) at[x++] = i;
     __syncthreads();
-    const int* table = p.table + (long long)t.b * p.max_pages;
+    const int* table = p.table + (long long)b * p.max_pages + p.first;
     for (int a = warp; a < m; a += kSelWarps) {
-      const int pg = __ldg(table + p.first + at[a]);
-      double best = -INFINITY;
-      if (eps == 0.f) best = 0.0;            // every scale is 0, or q
-      else if (pg >= 0 && pg < p.num_pages) {
-        constexpr int COLS = D / 32;
-        const long long ph = (long long)pg * p.Hkv + h;
-        const uint8_t* row = p.bounds + ph * 2 * D + lane * COLS;
-        float lo[4], hi[4];
-        if constexpr (COLS == 4) {
-          e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(row)), lo[0], lo[1], lo[2], lo[3]);
-          e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(row + D)), hi[0], hi[1], hi[2], hi[3]);
-        } else {
-          e4m3x4_to_f32(__ldg(reinterpret_cast<const uint16_t*>(row)), lo[0], lo[1], lo[2], lo[3]);
-          e4m3x4_to_f32(__ldg(reinterpret_cast<const uint16_t*>(row + D)), hi[0], hi[1], hi[2], hi[3]);
-        }
-        const double scale = (double)__ldg(p.k_scale + ph);
-        bool nan = false;
-        for (int r = 0; r < p.g; ++r) {
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + r) * p.total_q + q) * D + lane * COLS;
-          double s = 0.0;
-#pragma unroll
-          for (int x = 0; x < COLS; ++x) {
-            const float y = __uint_as_float((uint32_t)__ldg(src + x) << 16);
-            const float plus = y > 0.f || y != y ? y : 0.f, minus = y < 0.f || y != y ? y : 0.f;
-            s = fma((double)plus, (double)hi[x], s);
-            s = fma((double)minus, (double)lo[x], s);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          nan |= s != s;
-          best = fmax(best, s);
-        }
-        best = nan ? __longlong_as_double(0x7ff8000000000000ll) : best * scale;
-      }
-      if (lane == 0) keys[a] = ordered(best);
+      const int pg = __ldg(table + at[a]);
+      unsigned long long key = 1ull << 63;   // 0
+      if (eps != 0.f && pg >= 0 && pg < p.num_pages) key = exact_score<D>(p, q, h, pg);   // (eps = 0: q is, or the scales)
+      if (lane == 0) keys[a] = key;
     }
     __syncthreads();
     if (m <= kFew) {
       if (tid < m) {                         // rank: better ones, and equal ones before it
         const unsigned long long mine = keys[tid];
-        int ahead = 0;
-        for (int a = 0; a < m; ++a) ahead += keys[a] > mine || (keys[a] == mine && a < tid) ? 1 : 0;
-        v[at[tid]] = ahead < need ? INFINITY : -INFINITY;
+        int better = 0;
+        for (int a = 0; a < m; ++a) better += keys[a] > mine || (keys[a] == mine && a < tid) ? 1 : 0;
+        v[at[tid]] = better < need ? INFINITY : -INFINITY;
       }
     } else {
       // The need-th largest key, bit by bit; then of the keys equal to it the first ones.
+      int2 unused;
       unsigned long long key = 0;
       for (int bit = 63; bit >= 0; --bit) {
         const unsigned long long trial = key | (1ull << bit);
         int enough = 0;
         for (int a = tid; a < m; a += kSelThreads) enough += keys[a] >= trial ? 1 : 0;
-        if (count2(enough, 0).x >= need) key = trial;
+        if (scan2(enough, 0, unused).x >= need) key = trial;
       }
-      int better = 0;
-      for (int a = tid; a < m; a += kSelThreads) better += keys[a] > key ? 1 : 0;
-      const int equal_need = need - count2(better, 0).x;
-      for (int a0 = 0, found = 0; a0 < m; a0 += kSelThreads) {
-        const int a = a0 + tid;
-        const bool equal = a < m && keys[a] == key;
-        const uint32_t votes = __ballot_sync(0xffffffffu, equal);
-        if (lane == 0) red[turn][warp][0] = __popc(votes);
-        __syncthreads();
-        int before = found;
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
-          if (w < warp) before += red[turn][w][0];
-          found += red[turn][w][0];
-        }
-        turn ^= 1;
-        const bool take = a < m && (keys[a] > key || (equal && before + __popc(votes & ((1u << lane) - 1)) < equal_need));
-        if (a < m) v[at[a]] = take ? INFINITY : -INFINITY;
+      const int per_key = (m + kSelThreads - 1) / kSelThreads, a_lo = min(tid * per_key, m), a_hi = min(a_lo + per_key, m);
+      int better = 0, equal = 0;
+      for (int a = a_lo; a < a_hi; ++a) {
+        better += keys[a] > key ? 1 : 0;
+        equal += keys[a] == key ? 1 : 0;
+      }
+      int2 ahead_of;
+      const int equal_need = need - scan2(better, equal, ahead_of).x;
+      for (int a = a_lo, x = ahead_of.y; a < a_hi; ++a) {
+        const bool take = keys[a] > key || (keys[a] == key && x++ < equal_need);
+        v[at[a]] = take ? INFINITY : -INFINITY;
       }
     }
     __syncthreads();
+    emit = fminf(top, kBig);                 // the chosen ones are infinite now, the others -inf
+    if (top < kBig) emit = nextafterf(top, INFINITY);
+    in = 0;
+    for (int i = mine_lo; i < mine_hi; ++i) in += v[i] >= emit ? 1 : 0;
+    scan2(in, 0, before);
+    place = before.x;
   }
   // ---- out, ascending
-  for (int i0 = 0, found = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const bool is = i < n && v[i] > emit;
-    const uint32_t votes = __ballot_sync(0xffffffffu, is);
-    if (lane == 0) red[turn][warp][0] = __popc(votes);
-    __syncthreads();
-    int before = found;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) before += red[turn][w][0];
-      found += red[turn][w][0];
-    }
-    turn ^= 1;
-    const int place = before + __popc(votes & ((1u << lane) - 1));
-    if (is && place < k) out[p.first + place] = p.first + i;
-  }
-}
-
-// Pages of a chunk: as many as leave 8 CTAs per SM, from one step of a CTA on.
-int chunk_pages(long long units, int max_pages, int sms) {
-  int steps = 8;
-  while (steps > 1 && units * ((max_pages + steps * kStepPages - 1) / (steps * kStepPages)) < 8LL * sms) steps /= 2;
-  return steps * kStepPages;
+  for (int i = mine_lo; i < mine_hi; ++i)
+    if (v[i] >= emit && place < k) out[p.first + place++] = p.first + i;
 }
 
 }  // namespace
 
-// [Hkv][total_q] rows: scores, the 64-bit keys and numbers of pages near the border, the chunks' errors.
+// [Hkv][total_q] rows: scores, the exact keys and numbers of pages near the border, the steps' errors.
 SelectWs select_ws(int Hkv, int total_q, int max_pages) {
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  const size_t rows = (size_t)Hkv * total_q, chunks = ((size_t)max_pages + kStepPages - 1) / kStepPages;
+  const size_t rows = (size_t)Hkv * total_q, groups = ((size_t)max_pages + kStep - 1) / kStep;
   SelectWs w;
   w.exact = up(rows * max_pages * 4);
   w.near = w.exact + up(rows * max_pages * 8);
   w.errors = w.near + up(rows * max_pages * 4);
-  w.total = w.errors + up(rows * chunks * 4);
+  w.total = w.errors + up(rows * groups * 4);
   return w;
 }
 
 cudaError_t launch_select_pages(SelectParams p, int d, int sms, cudaStream_t s) {
   p.page_shift = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
-  // Queries of a tile: as many as fill 16 rows, but no more than a sequence has.
+  // Queries of a tile: as many as fill 16 rows (8 rows, when all of a sequence's fit), but no more than it has.
+  const bool small = (long long)p.max_q * p.g <= 8;
   p.qn = p.g >= 16 ? 1 : (p.max_q < 16 / p.g ? p.max_q : 16 / p.g);
-  const long long slots = p.qn > 1 ? (long long)p.total_q / p.qn + p.B : p.total_q, units = slots * p.Hkv;
-  p.chunk = chunk_pages(units, p.max_pages, sms);
-  p.chunks = (p.max_pages + p.chunk - 1) / p.chunk;
-  const long long grid = units * p.chunks, lists = (long long)p.total_q * p.Hkv;
-  if (slots > 0x7fffffffLL || grid > 0x7fffffffLL || lists > 0x7fffffffLL) return cudaErrorInvalidValue;
+  p.groups = (p.max_pages + kStep - 1) / kStep;
+  const long long lists = (long long)p.total_q * p.Hkv;
+  if (lists > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  if (p.max_pages > p.count)                 // (else every list holds all pages)
-    e = d == 64 ? launch_pdl(select_score_kernel<64>, dim3((unsigned)grid), dim3(kSelThreads), 0, s, p)
-                : launch_pdl(select_score_kernel<128>, dim3((unsigned)grid), dim3(kSelThreads), 0, s, p);
+  const dim3 grid((unsigned)(kScoreCtas * sms));
+  auto score = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kScoreThreads), 0, s, p); };
+  if (p.max_pages > p.count) {               // (else every list holds all pages)
+    if (d == 64) e = small ? score(select_score_kernel<64, 1>) : score(select_score_kernel<64, 2>);
+    else e = small ? score(select_score_kernel<128, 1>) : score(select_score_kernel<128, 2>);
+  }
   if (e != cudaSuccess) return e;
   const size_t bytes = (size_t)p.max_pages * 4;
   const int in_smem = bytes <= 40 * 1024 ? 1 : 0;      // (longer tables: in the workspace)
