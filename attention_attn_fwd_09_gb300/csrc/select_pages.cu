@@ -366,94 +366,82 @@ __device__ __forceinline__ int ordered32(float x) {
 }
 __device__ __forceinline__ float unordered32(int b) { return __int_as_float(b < 0 ? b ^ 0x7fffffff : b); }
 
-// The exact score of page pg for packed query q and K/V head h, as ordered() bits; by a warp.  Codes are m 2^x
-// with 4 bits of m and q's components with 8, so that their products, as whole numbers times one power of two, add up
-// exactly in 64 bits where q's components lie within 2^29 of each other; elsewhere doubles do it (ten times as
-// long: an SM has two 64-bit multiply-adds a cycle).
+// The exact score of page pg for packed query q and heads r0 .. r0 + 3 of the group of K/V head h, as ordered()
+// bits; by a warp.  Codes are m 2^x with 4 bits of m and q's components with 8, so that their products, as whole
+// numbers times one power of two, add up exactly in 64 bits where q's components lie within 2^29 of each other;
+// elsewhere doubles do it (ten times as long: an SM has two 64-bit multiply-adds a cycle).
+constexpr int kExactHeads = 4;
 template <int D>
-__device__ unsigned long long exact_score(const SelectParams& p, int q, int h, int pg) {
+__device__ unsigned long long exact_score(const SelectParams& p, int q, int h, int r0, int pg) {
   constexpr int COLS = D / 32;
   const int lane = threadIdx.x & 31;
+  uint32_t w[kExactHeads][2];
+#pragma unroll
+  for (int r = 0; r < kExactHeads; ++r) {
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + min(r0 + r, p.g - 1)) * p.total_q + q) * D + lane * COLS;
+    if constexpr (COLS == 4) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+      w[r][0] = u.x;
+      w[r][1] = u.y;
+    } else {
+      w[r][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    }
+  }
   const long long ph = (long long)pg * p.Hkv + h;
   const uint8_t* row = p.bounds + ph * 2 * D + lane * COLS;
   const uint32_t lo = COLS == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row)) : __ldg(reinterpret_cast<const uint16_t*>(row));
   const uint32_t hi = COLS == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row + D)) : __ldg(reinterpret_cast<const uint16_t*>(row + D));
-  const double scale = (double)__ldg(p.k_scale + ph);
+  const float scale = __ldg(p.k_scale + ph);
   bool nan = false;
 #pragma unroll
   for (int x = 0; x < COLS; ++x) nan |= (lo >> 8 * x & 0x7f) == 0x7f || (hi >> 8 * x & 0x7f) == 0x7f;
   if (__any_sync(0xffffffffu, nan)) return ~0ull;
-  unsigned long long best = 0;               // below every number
-  for (int r0 = 0; r0 < p.g; r0 += 32) {
-    double own = -INFINITY;                  // of head r0 + lane
-    uint32_t ahead[4][2];                    // four heads' loads under way at once
-    for (int r = r0; r < min(p.g, r0 + 32); ++r) {
-      if ((r & 3) == 0) {
+  double own = -INFINITY;                    // of head r0 + lane
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((long long)(h * p.g + min(r + x, p.g - 1)) * p.total_q + q) * D + lane * COLS;
-          if constexpr (COLS == 4) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-            ahead[x][0] = u.x;
-            ahead[x][1] = u.y;
-          } else {
-            ahead[x][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-          }
-        }
-      }
-      uint32_t w[2] = {ahead[0][0], ahead[0][1]};
+  for (int r = 0; r < kExactHeads; ++r) {    // (behind the last head: the last again)
+    int top = 1;
 #pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        ahead[x][0] = ahead[x + 1][0];
-        ahead[x][1] = ahead[x + 1][1];
-      }
-      int top = 0;
+    for (int x = 0; x < COLS; ++x) top = max(top, (int)(w[r][x >> 1] >> (x & 1) * 16 + 7 & 0xff));
+    top = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+    bool far = top == 255;                   // an infinity or NaN
+    long long sum = 0;
 #pragma unroll
-      for (int x = 0; x < COLS; ++x) top = max(top, (int)(w[x >> 1] >> (x & 1) * 16 + 7 & 0xff));
-      top = (int)__reduce_max_sync(0xffffffffu, (unsigned)max(top, 1));
-      bool far = top == 255;                 // an infinity or NaN
-      long long sum = 0;
+    for (int x = 0; x < COLS; ++x) {
+      const uint32_t y = w[r][x >> 1] >> (x & 1) * 16 & 0xffffu, e = y >> 7 & 0xff;
+      const int m = (int)((y & 0x7f) | (e ? 0x80 : 0)), below = top - max((int)e, 1);
+      far |= m != 0 && below > 29;
+      const uint32_t code = ((y >> 15 ? lo : hi) >> 8 * x) & 0xff, ce = code >> 3 & 15;
+      const int n = (int)((code & 7) | (ce ? 8 : 0));
+      const long long product = (long long)(m * n) << (max(29 - below, 0) + max((int)ce, 1) - 1);
+      sum += (y >> 15) != (code >> 7) ? -product : product;
+    }
+    double s;
+    if (!__any_sync(0xffffffffu, far)) {
+      const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffffu);
+      const unsigned b = __reduce_add_sync(0xffffffffu, (unsigned)(sum >> 24) & 0xffffffu);
+      const int d = __reduce_add_sync(0xffffffffu, (int)(sum >> 48));
+      s = (double)((long long)a + ((long long)b << 24) + ((long long)d << 48)) * __longlong_as_double((long long)(top - 172 + 1023) << 52);
+    } else {
+      s = 0.0;
 #pragma unroll
       for (int x = 0; x < COLS; ++x) {
-        const uint32_t y = w[x >> 1] >> (x & 1) * 16 & 0xffffu, e = y >> 7 & 0xff;
-        const int m = (int)((y & 0x7f) | (e ? 0x80 : 0)), below = top - max((int)e, 1);
-        far |= m != 0 && below > 29;
-        const uint32_t code = ((y >> 15 ? lo : hi) >> 8 * x) & 0xff, ce = code >> 3 & 15;
-        const int n = (int)((code & 7) | (ce ? 8 : 0));
-        const long long product = (long long)(m * n) << (max(29 - below, 0) + max((int)ce, 1) - 1);
-        sum += (y >> 15) != (code >> 7) ? -product : product;
+        const float y = __uint_as_float((w[r][x >> 1] >> (x & 1) * 16) << 16);
+        const float plus = y > 0.f || y != y ? y : 0.f, minus = y < 0.f || y != y ? y : 0.f;
+        float l, u, unused;
+        e4m3x4_to_f32(lo >> 8 * x & 0xff, l, unused, unused, unused);
+        e4m3x4_to_f32(hi >> 8 * x & 0xff, u, unused, unused, unused);
+        s = fma((double)plus, (double)u, s);
+        s = fma((double)minus, (double)l, s);
       }
-      double s;
-      if (!__any_sync(0xffffffffu, far)) {
-        const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffffu);
-        const unsigned b = __reduce_add_sync(0xffffffffu, (unsigned)(sum >> 24) & 0xffffffu);
-        const int d = __reduce_add_sync(0xffffffffu, (int)(sum >> 48));
-        sum = (long long)a + ((long long)b << 24) + ((long long)d << 48);
-        if (lane != r - r0) continue;
-        s = (double)sum * __longlong_as_double((long long)(top - 172 + 1023) << 52);
-      } else {
-        s = 0.0;
 #pragma unroll
-        for (int x = 0; x < COLS; ++x) {
-          const float y = __uint_as_float((w[x >> 1] >> (x & 1) * 16) << 16);
-          const float plus = y > 0.f || y != y ? y : 0.f, minus = y < 0.f || y != y ? y : 0.f;
-          float l, u, unused;
-          e4m3x4_to_f32(lo >> 8 * x & 0xff, l, unused, unused, unused);
-          e4m3x4_to_f32(hi >> 8 * x & 0xff, u, unused, unused, unused);
-          s = fma((double)plus, (double)u, s);
-          s = fma((double)minus, (double)l, s);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      }
-      if (lane == r - r0) own = s;
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
-    const unsigned long long key = lane < p.g - r0 ? ordered(own * scale) : 0ull;
-    const unsigned high = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32));
-    const unsigned low = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32) == high ? (unsigned)key : 0u);
-    best = max(best, (unsigned long long)high << 32 | low);
+    if (lane == r) own = s;
   }
-  return best;
+  const unsigned long long key = lane < kExactHeads ? ordered(own * (double)scale) : 0ull;
+  const unsigned high = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32));
+  const unsigned low = __reduce_max_sync(0xffffffffu, (unsigned)(key >> 32) == high ? (unsigned)key : 0u);
+  return (unsigned long long)high << 32 | low;
 }
 
 // Block: (query, K/V head).
@@ -662,14 +650,19 @@ __global__ void __launch_bounds__(kSelThreads) select_choose_kernel(const Select
     unsigned long long* keys = m <= kFew ? few_keys : p.exact + unit * p.max_pages;
     int* at = m <= kFew ? few_at : p.near + unit * p.max_pages;
     for (int i = mine_lo, x = before.y; i < mine_hi; ++i)
-      if (!(v[i] > top) && v[i] >= bottom) at[x++] = i;
+      if (!(v[i] > top) && v[i] >= bottom) {
+        keys[x] = 0;                         // below every number
+        at[x++] = i;
+      }
     __syncthreads();
     const int* table = p.table + (long long)b * p.max_pages + p.first;
-    for (int a = warp; a < m; a += kSelWarps) {
-      const int pg = __ldg(table + at[a]);
+    // A warp takes a few heads of a page; the largest of them all counts.
+    const long long shares = (p.g + kExactHeads - 1) / kExactHeads;
+    for (long long a = warp; a < m * shares; a += kSelWarps) {
+      const int near_at = (int)(a / shares), r0 = (int)(a - near_at * shares) * kExactHeads, pg = __ldg(table + at[near_at]);
       unsigned long long key = 1ull << 63;   // 0
-      if (eps != 0.f && pg >= 0 && pg < p.num_pages) key = exact_score<D>(p, q, h, pg);   // (eps = 0: q is, or the scales)
-      if (lane == 0) keys[a] = key;
+      if (eps != 0.f && pg >= 0 && pg < p.num_pages) key = exact_score<D>(p, q, h, r0, pg);   // (eps = 0: q is, or the scales)
+      if (lane == 0) atomicMax(keys + near_at, key);
     }
     __syncthreads();
     if (m <= kFew) {
