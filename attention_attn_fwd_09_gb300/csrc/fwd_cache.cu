@@ -97,15 +97,18 @@ __device__ __forceinline__ int list_pieces(const CacheParams& p, int seen) {
   return max(1, (min(seen, p.list_count) * p.page + kPiece - 1) / kPiece);
 }
 
-// Where a warp is in the CTA's run of pieces.
+// Where a warp is in the CTA's run of pieces.  Positions count pieces and, before each unit's, `cost` places
+// for starting and ending it, which nobody fills.
 template <bool LIST>
 struct Cursor {
   int b, h;
   int t, seen;                               // LIST: packed query, the pages it sees
+  int cost;
   long long f, ubeg, uend;                   // piece, and the unit's first and last + 1
   __device__ __forceinline__ void settle(const CacheParams& p, long long end) {   // into the unit that holds f
     while (f < end && f >= uend) {
-      ubeg = uend;
+      ubeg = uend + cost;
+      f += cost;
       if (++h == p.Hkv) {
         h = 0;
         if constexpr (LIST) {
@@ -115,7 +118,7 @@ struct Cursor {
           uend = ubeg + list_pieces(p, seen);
         } else {
           int np;
-          do np = pieces_of(p, ++b);         // f < end: there is another unit
+          do np = pieces_of(p, ++b);
           while (np == 0);
           uend = ubeg + np;
         }
@@ -161,12 +164,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int per_thread = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
   long long mine = 0;
+  int units = 0;                             // (per K/V head)
   bool wrong = false;
   for (int b = b_lo; b < b_hi; ++b) {
     const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b), n = c1 - c0;
     wrong |= c0 < 0 || c1 < c0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
              (b == 0 && c0 != 0) || (b == p.B - 1 && c1 != p.total_q);
-    if (!LIST && n > 0) mine += max(1, (len + kPiece - 1) / kPiece);
+    if (!LIST && n > 0) {
+      mine += max(1, (len + kPiece - 1) / kPiece);
+      ++units;
+    }
   }
   // LIST: thread t adds up queries [t per_query, ...) instead.
   const int per_query = (p.total_q + kThreads - 1) / kThreads;
@@ -179,6 +186,23 @@ __global__ void __launch_bounds__(kThreads, 2)
       while (b < p.B - 1 && t >= __ldg(p.cu_q + b + 1)) ++b;
       mine += list_pieces(p, pages_seen(p, b, t));
     }
+    units = t_hi - t_lo;
+  }
+  // A unit costs as much as p.unit_cost pieces, or, with little work, a quarter of a CTA's pieces.  (Where 0,
+  // pieces alone are counted.)
+  int cost = 0;
+  if (p.unit_cost > 0) {
+    long long all = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) misc[warp] = all;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all += misc[w];
+    cost = (int)min((long long)p.unit_cost, all * p.Hkv / gridDim.x / 4);
+    mine += (long long)cost * units;
+    __syncthreads();                         // misc has been read
   }
   long long incl = mine;
 #pragma unroll
@@ -215,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (LIST) {
         while (t >= __ldg(p.cu_q + b + 1)) ++b;
       }
-      const long long step = (long long)(LIST ? list_pieces(p, pages_seen(p, b, t)) : pieces_of(p, b)) * p.Hkv;
+      const int np = LIST ? list_pieces(p, pages_seen(p, b, t)) : pieces_of(p, b);
+      const long long step = np > 0 ? (long long)(np + cost) * p.Hkv : 0;
       if (rs < at + step) break;
       at += step;
       if (LIST) ++t;
@@ -228,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   Cursor<LIST> seg;                          // the unit being worked on
   seg.b = (int)misc[0];
+  seg.cost = cost;
   seg.t = seg.seen = 0;
   if constexpr (LIST) {
     seg.t = (int)misc[2];
@@ -235,18 +261,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   {
     const int np = LIST ? list_pieces(p, seg.seen) : pieces_of(p, seg.b);
-    seg.h = (int)((rs - misc[1]) / np);
-    seg.ubeg = misc[1] + (long long)seg.h * np;
+    seg.h = (int)((rs - misc[1]) / (np + cost));
+    seg.ubeg = misc[1] + (long long)seg.h * (np + cost) + cost;
     seg.uend = seg.ubeg + np;
-    seg.f = rs;
+    seg.f = max(rs, seg.ubeg);
   }
+  const long long first = seg.f;             // the CTA's first piece
 
   // ---- this warp's loads, STAGES pieces ahead of its work
   const int page_shift = 31 - __clz(p.page);
   const int grp = lane & 1;                  // half of a piece (16 keys) this lane looks after
   uint8_t* ring = smem + warp * C::STAGES * 2 * C::KB;
   Cursor<LIST> ahead = seg;
-  ahead.f = rs + warp;
+  ahead.f = first + warp;
   ahead.settle(p, re);
   const int kv_heads = LIST ? p.Hkv / p.rep : p.Hkv;
   auto kv_head = [&](int h) -> int { return LIST && p.rep > 1 ? h / p.rep : h; };
@@ -317,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float sc_next = scale_of(pages[0], heads[0]);
   int stage = 0;
   uint32_t phase = 0;
-  long long f = rs + warp;                   // this warp's next piece
+  long long f = first + warp;                // this warp's next piece
 
   // Shared-memory offsets of this thread's fragments within a piece.
   uint32_t koff[2], voff[2];
@@ -719,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     seg.f = send;
+    if (send == seg.uend && send < re) f += cost;      // on to the next unit
     seg.settle(p, re);
   }
 }
