@@ -214,6 +214,7 @@ struct RopeAppendParams {
   int rot, interleaved;
   float mscale;
   uint8_t* bounds;           // [num_pages, Hkv, 2, d] smallest and largest code per column, or null
+  int heads_per_cta;         // filled in by launch_rope_append
 };
 cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s);
 

@@ -23,32 +23,41 @@
 namespace attn {
 namespace {
 
-// How K's columns turn: not at all; halves (rot a multiple of 16); neighbours (of 8); any even rot.
+// How K's columns turn: not at all; halves, neighbours (rot a multiple of 8); any even rot.
 enum : int { TURN_NONE = 0, TURN_SPLIT = 1, TURN_INTER = 2, TURN_ANY = 3 };
 __device__ __forceinline__ int turn_mode(const RopeAppendParams& p, bool is_v) {
   if (is_v || p.rot == 0) return TURN_NONE;
-  return p.interleaved ? (p.rot % 8 == 0 ? TURN_INTER : TURN_ANY) : (p.rot % 16 == 0 ? TURN_SPLIT : TURN_ANY);
+  return p.rot % 8 != 0 ? TURN_ANY : p.interleaved ? TURN_INTER : TURN_SPLIT;
 }
 // Where pair j's (cos, sin) lies in a row of the table: 16-byte pieces (two pairs) that the threads of a
 // row read at the same time lie side by side.
 template <int mode>
 __device__ __forceinline__ int turn_slot(int rot, int j) {
   const int f = j >> 1;
-  if (mode == TURN_SPLIT) return ((f & 3) * (rot / 16) + (f >> 2)) * 2 + (j & 1);
+  if (mode == TURN_SPLIT) {                  // groups of 4 columns: pairs 4 g .. 4 g + 3, two pieces
+    const int g = f >> 1;
+    return (((f & 1) * 2 + (g & 1)) * ((rot / 8 + 1) / 2) + (g >> 1)) * 2 + (j & 1);
+  }
   if (mode == TURN_INTER) return ((f & 1) * (rot / 8) + (f >> 1)) * 2 + (j & 1);
   return j;
 }
-// Rows r .. r + n - 1 of the slot's page into the table, by all threads.
+// Pairs that a row of the table has room for.
+__host__ __device__ inline int turn_row(int rot) { return rot % 8 == 0 ? (rot / 8 + 1) / 2 * 8 : rot / 2; }
+// Rows r .. r + n - 1 of the slot's page into the table, by all threads: a thread has one pair of every few rows.
 template <int mode, int THREADS>
 __device__ __forceinline__ void fill_turns(const RopeAppendParams& p, const Slot& s, int r, int n,
                                            const unsigned long long* turn, float2* cs) {
-  const int half = p.rot / 2;
-  for (int i = threadIdx.x; i < n * half; i += THREADS) {
-    const int row = i / half, j = i - row * half;
+  const int half = p.rot / 2, stride = turn_row(p.rot), step = THREADS / half;     // (half <= 64)
+  const int row0 = threadIdx.x / half, j = threadIdx.x - row0 * half;
+  if (row0 >= step) return;
+  const unsigned long long t = turn[j];
+  float2* out = cs + turn_slot<mode>(p.rot, j);
+#pragma unroll 2
+  for (int row = row0; row < n; row += step) {
     const long long pos = p.positions ? __ldg(p.positions + s.src0 + r + row) : s.first + r + row;
     float sn, c;
-    turn_sincos_near(turn[j], pos, sn, c);
-    cs[row * half + turn_slot<mode>(p.rot, j)] = make_float2(c * p.mscale, sn * p.mscale);
+    turn_sincos_near(t, pos, sn, c);
+    out[row * stride] = make_float2(c * p.mscale, sn * p.mscale);
   }
 }
 
@@ -61,23 +70,27 @@ __device__ __forceinline__ void turned(const RopeAppendParams& p, const uint4& o
   const int rot = p.rot;
   if constexpr (mode == TURN_NONE) {
   } else if constexpr (mode == TURN_SPLIT) {
-    const int hc = rot / 16, lane = threadIdx.x & 31;            // column groups of a half
-    const bool upper = c >= hc, turns = c < 2 * hc;
-    const int from = turns ? (upper ? lane - hc : lane + hc) : lane;
-    uint4 w;
-    w.x = __shfl_sync(0xffffffffu, own.x, from);
-    w.y = __shfl_sync(0xffffffffu, own.y, from);
-    w.z = __shfl_sync(0xffffffffu, own.z, from);
-    w.w = __shfl_sync(0xffffffffu, own.w, from);
-    if (!turns) return;
-    float z[8];
-    bf16x8(w, z);
-    const float4* at = reinterpret_cast<const float4*>(cs) + (upper ? c - hc : c);
+    // Four columns at a time: group g of the first half turns with g + q, whose lane and whose place there (one
+    // for all lanes) follow.
+    const int q = rot / 8, lane = threadIdx.x & 31, width = (q + 1) / 2;
+    const float4* table = reinterpret_cast<const float4*>(cs);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 e = at[q * hc];
-      y[2 * q] = y[2 * q] * e.x + (upper ? z[2 * q] : -z[2 * q]) * e.y;
-      y[2 * q + 1] = y[2 * q + 1] * e.z + (upper ? z[2 * q + 1] : -z[2 * q + 1]) * e.w;
+    for (int k = 0; k < 2; ++k) {
+      const int g = 2 * c + k;
+      const bool upper = g >= q, turns = g < 2 * q;
+      const int other = turns ? (upper ? g - q : g + q) : g, from = lane - c + (other >> 1);
+      const bool odd = ((k + q) & 1) != 0;
+      const uint32_t a = __shfl_sync(0xffffffffu, odd ? own.z : own.x, from), b = __shfl_sync(0xffffffffu, odd ? own.w : own.y, from);
+      if (!turns) continue;
+      const int pair = upper ? other : g;    // group of pairs
+      const float z[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 e = table[(i * 2 + (pair & 1)) * width + (pair >> 1)];
+        const int x = 4 * k + 2 * i;
+        y[x] = y[x] * e.x + (upper ? z[2 * i] : -z[2 * i]) * e.y;
+        y[x + 1] = y[x + 1] * e.z + (upper ? z[2 * i + 1] : -z[2 * i + 1]) * e.w;
+      }
     }
   } else if constexpr (mode == TURN_INTER) {
     if (8 * c >= rot) return;
@@ -115,25 +128,35 @@ __device__ __forceinline__ void forget(uint4 (&x)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
 }
 
-// Bits of the largest finite |y|.
-__device__ __forceinline__ uint32_t largest8(const float (&y)[8], uint32_t m) {
+// Largest finite |y|; where an infinity hides it (a maximum passes NaN by), they are looked at one by one.
+__device__ __forceinline__ float largest8(const float (&y)[8], float m) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t a = __float_as_uint(y[k]) & 0x7fffffffu;
-    m = max(m, a < 0x7f800000u ? a : 0u);
-  }
+  for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(y[k]));
   return m;
 }
+__device__ __noinline__ float largest_finite8(float4 a, float4 b) {
+  const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = fabsf(y[k]) < INFINITY ? fmaxf(m, fabsf(y[k])) : m;
+  return m;
+}
+__device__ __forceinline__ float finite8(const float (&y)[8], float m) {
+  return fmaxf(m, largest_finite8(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7])));
+}
 // (inv = 0: a scale that is no power of two, by division.)
-__device__ __noinline__ float divided(float y, float scale) { return __fdiv_rn(y, scale); }
+__device__ __noinline__ uint2 divided8(float4 a, float4 b, float scale) {
+  const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(y[k], scale);
+  return e4m3x8(f);
+}
 __device__ __forceinline__ uint2 coded8(const float (&y)[8], float inv, float scale) {
+  if (inv == 0.f) return divided8(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), scale);
   float f[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] = y[k] * inv;
-  if (inv == 0.f) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = divided(y[k], scale);
-  }
   return e4m3x8(f);
 }
 
@@ -204,7 +227,8 @@ template <int D, int mode>
 __device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slot& s, bool is_v, const unsigned long long* turn,
                                             float2* cs) {
   constexpr int THREADS = kStepWarps * 32, LPR = D / 8, RPW = 32 / LPR, STEPS = kStepRows / RPW;   // lanes per row, rows at once
-  const int lane = threadIdx.x & 31, head = blockIdx.y * kStepWarps + (threadIdx.x >> 5), half = p.rot / 2;
+  const int lane = threadIdx.x & 31, head = blockIdx.y * kStepWarps + (threadIdx.x >> 5);
+  const int stride = turn_row(p.rot);
   const bool live = head < p.a.Hkv;
   const Target t(p.a, s, live ? head : 0, is_v, D);
   const int r0 = lane / LPR, c = lane % LPR;
@@ -226,23 +250,38 @@ __device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slo
   };
   auto row = [&](int base, int i, float (&y)[8]) {
     const int r = min(i * RPW + r0, s.rows - base - 1);          // (lanes without a row: any one, as 0)
-    turned<mode>(p, x[i], t.src + (s.src0 + base + r) * t.st, c, cs + r * half, y);
+    turned<mode>(p, x[i], t.src + (s.src0 + base + r) * t.st, c, cs + r * stride, y);
   };
   const bool one = s.rows - s.kept <= kStepRows;       // the rows and the table are kept for the second pass
-  uint32_t amax = 0;
+  float amax = 0.f;
   for (int base = s.kept; base < s.rows; base += kStepRows) {
     load(base);
     table(base);
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       if (base + i * RPW >= s.rows) break;
       float y[8];
       row(base, i, y);
-      if (base + i * RPW + r0 < s.rows) amax = largest8(y, amax);
+      if (base + i * RPW + r0 < s.rows) m = largest8(y, m);
     }
+    if (__any_sync(0xffffffffu, m == INFINITY)) {
+      m = 0.f;
+#pragma unroll 1
+      for (int r = 0; r < kStepRows; r += RPW) {
+        uint4 w = x[0];
+#pragma unroll
+        for (int i = 1; i < STEPS; ++i)
+          if (r == i * RPW) w = x[i];
+        float y[8];
+        turned<mode>(p, w, t.src + (s.src0 + min(base + r + r0, s.rows - 1)) * t.st, c, cs + min(r + r0, s.rows - base - 1) * stride, y);
+        if (base + r + r0 < s.rows) m = finite8(y, m);
+      }
+    }
+    amax = fmaxf(amax, m);
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax)));
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  const float sc = fmaxf(s_old, pow2_scale(amax));
   const float inv = exact_inverse(sc);
   const bool keep_bounds = p.bounds != nullptr && !is_v;
   Bounds b;
@@ -284,7 +323,7 @@ __device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slo
 template <int D>
 __global__ void __launch_bounds__(kStepWarps * 32) rope_append_step_kernel(const RopeAppendParams p) {
   __shared__ unsigned long long turn[D / 2];
-  __shared__ __align__(16) float2 cs[kStepRows * D / 2];
+  __shared__ __align__(16) float2 cs[kStepRows * D / 2];         // (a row of the table: at most D / 2 pairs)
   constexpr int THREADS = kStepWarps * 32;
   pdl_trigger();                                       // the queries' rotation may start
   const bool is_v = blockIdx.x & 1;
@@ -299,84 +338,93 @@ __global__ void __launch_bounds__(kStepWarps * 32) rope_append_step_kernel(const
   else append_step<D, TURN_ANY>(p, s, is_v, turn, cs);
 }
 
-// A slot's page of one head of K or V by a CTA: 8 elements per thread and step, NV steps cover it.
+// A slot's page of p.heads_per_cta heads of K or V by a CTA: 8 elements per thread and step, NV steps cover a
+// head's.  The next head's rows are under way while one is worked on.
 template <int D, int NV, int THREADS, int mode>
 __device__ __forceinline__ void append_page(const RopeAppendParams& p, const Slot& s, bool is_v, const unsigned long long* turn,
                                             float2* cs, uint32_t* red, Bounds (*parts)[D / 8]) {
   constexpr int LPR = D / 8, RPS = THREADS / LPR;      // lanes per row, rows per step
-  const int tid = threadIdx.x, head = blockIdx.y, half = p.rot / 2;
-  const Target t(p.a, s, head, is_v, D);
-  const int r0 = tid / LPR, c = tid % LPR;
-  const float s_old = s.kept > 0 ? *t.scale : 0.f;
-  uint4 x[NV];
-  const uint16_t* src = t.src + (s.src0 + r0) * t.st;
+  const int tid = threadIdx.x, stride = turn_row(p.rot), r0 = tid / LPR, c = tid % LPR;
+  const int h_begin = blockIdx.y * p.heads_per_cta, h_end = min(h_begin + p.heads_per_cta, p.a.Hkv);
+  uint4 ahead[NV];
+  auto load = [&](const Target& t) {
+    const uint16_t* src = t.src + (s.src0 + r0) * t.st + c * 8;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int r = r0 + i * RPS;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= s.kept && r < s.rows) x[i] = *reinterpret_cast<const uint4*>(src + i * RPS * t.st + c * 8);
-  }
+    for (int i = 0; i < NV; ++i) {
+      const int r = r0 + i * RPS;
+      ahead[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= s.kept && r < s.rows) ahead[i] = *reinterpret_cast<const uint4*>(src + i * RPS * t.st);
+    }
+  };
+  load(Target(p.a, s, h_begin, is_v, D));
   if (mode != TURN_NONE) {
     fill_turns<mode, THREADS>(p, s, s.kept, s.rows - s.kept, turn, cs);
     __syncthreads();
   }
-  auto row = [&](int i, float (&y)[8]) {               // (threads without a row: any one, as 0)
-    const int r = max(min(r0 + i * RPS, s.rows - 1), s.kept);
-    turned<mode>(p, x[i], t.src + (s.src0 + r) * t.st, c, cs + (r - s.kept) * half, y);
-  };
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float y[8];
-    row(i, y);
-    const int r = r0 + i * RPS;
-    if (r >= s.kept && r < s.rows) amax = largest8(y, amax);
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();
-  amax = red[0];
-#pragma unroll
-  for (int i = 1; i < THREADS / 32; ++i) amax = max(amax, red[i]);
-  const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(amax)));
-  if (tid == 0) *t.scale = sc;
-  const float inv = exact_inverse(sc);
   const bool keep_bounds = p.bounds != nullptr && !is_v;
-  Bounds b;
-  b.clear();
-  forget(x);
-  uint2* out = reinterpret_cast<uint2*>(t.dst + tid * 8);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float y[8];
-    row(i, y);
-    const int r = r0 + i * RPS;                        // rows behind the last one stay as they are
-    if (r < s.kept || r >= s.rows) continue;
-    const uint2 code = coded8(y, inv, sc);
-    out[i * THREADS] = code;
-    if (keep_bounds) b.add(code, code);
-  }
-  if (sc > s_old) {                                    // the kept rows' codes change (under a scale of 0: to 0)
 #pragma unroll 1
-    for (int i = 0; i < NV && r0 + i * RPS < s.kept; ++i) out[i * THREADS] = recode8(out[i * THREADS], s_old, inv);
-  }
-  if (keep_bounds) {
-    b.over_rows(LPR);
-    if ((tid & 31) < LPR) parts[tid >> 5][c] = b;
+  for (int head = h_begin; head < h_end; ++head) {
+    const Target t(p.a, s, head, is_v, D);
+    const float s_old = s.kept > 0 ? *t.scale : 0.f;
+    // The rotated rows stay in registers until the page's scale is known.
+    float y[NV][8], amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {                     // (threads without a row: any one, as 0)
+      const int r = max(min(r0 + i * RPS, s.rows - 1), s.kept);
+      turned<mode>(p, ahead[i], t.src + (s.src0 + r) * t.st, c, cs + (r - s.kept) * stride, y[i]);
+      amax = largest8(y[i], amax);                     // (a row read as 0 stays 0, but for TURN_ANY: below)
+    }
+    if (head + 1 < h_end) load(Target(p.a, s, head + 1, is_v, D));
+    if (amax == INFINITY || mode == TURN_ANY) {
+      amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = r0 + i * RPS;
+        if (r >= s.kept && r < s.rows) amax = finite8(y[i], amax);
+      }
+    }
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    if ((tid & 31) == 0) red[(head & 1) * (THREADS / 32) + (tid >> 5)] = bits;     // (every second head its own: one barrier)
     __syncthreads();
-    if (tid < LPR) {
-      for (int w = 1; w < THREADS / 32; ++w) b.add(parts[w][tid]);
-      b.store(p.bounds + ((long long)s.page * p.a.Hkv + head) * 2 * D, D, tid, s.kept > 0, sc > s_old, s_old, inv);
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) bits = max(bits, red[(head & 1) * (THREADS / 32) + i]);
+    const float sc = fmaxf(s_old, pow2_scale(__uint_as_float(bits)));
+    if (tid == 0) *t.scale = sc;                       // (all have read the old one before the barrier)
+    const float inv = exact_inverse(sc);
+    Bounds b;
+    b.clear();
+    uint2* out = reinterpret_cast<uint2*>(t.dst + tid * 8);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int r = r0 + i * RPS;                      // rows behind the last one stay as they are
+      if (r < s.kept || r >= s.rows) continue;
+      const uint2 code = coded8(y[i], inv, sc);
+      out[i * THREADS] = code;
+      if (keep_bounds) b.add(code, code);
+    }
+    if (sc > s_old) {                                  // the kept rows' codes change (under a scale of 0: to 0)
+#pragma unroll 1
+      for (int i = 0; i < NV && r0 + i * RPS < s.kept; ++i) out[i * THREADS] = recode8(out[i * THREADS], s_old, inv);
+    }
+    if (keep_bounds) {
+      b.over_rows(LPR);
+      if (head > h_begin) __syncthreads();             // the parts before have been read
+      if ((tid & 31) < LPR) parts[tid >> 5][c] = b;
+      __syncthreads();
+      if (tid < LPR) {
+        for (int w = 1; w < THREADS / 32; ++w) b.add(parts[w][tid]);
+        b.store(p.bounds + ((long long)s.page * p.a.Hkv + head) * 2 * D, D, tid, s.kept > 0, sc > s_old, s_old, inv);
+      }
     }
   }
 }
 
-// Block: slot x, head y, K or V z.
+// Block: slot x, heads y, K or V z.
 template <int D, int NV, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) rope_append_kernel(const RopeAppendParams p) {
-  extern __shared__ __align__(16) float2 cs[];         // [new rows][rot / 2]
+  extern __shared__ __align__(16) float2 cs[];         // [new rows][turn_row]
   __shared__ unsigned long long turn[D / 2];
-  __shared__ uint32_t red[THREADS / 32];
+  __shared__ uint32_t red[2 * (THREADS / 32)];
   __shared__ Bounds parts[THREADS / 32][D / 8];
   pdl_trigger();                                       // the queries' rotation may start
   const bool is_v = blockIdx.z != 0;
@@ -394,11 +442,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) rope_append_kernel(const RopeAp
 template <int D>
 cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
   const int vecs = p.a.page * D / 8;                   // 16-byte pieces of a page
-  const size_t smem = (size_t)p.a.page * (p.rot / 2) * sizeof(float2);
+  const size_t smem = (size_t)p.a.page * turn_row(p.rot) * sizeof(float2);
   if (vecs == 128) rope_append_kernel<D, 1, 128, 8><<<grid, 128, smem, s>>>(p);
   else if (vecs == 256) rope_append_kernel<D, 1, 256, 4><<<grid, 256, smem, s>>>(p);
   else if (vecs == 512) rope_append_kernel<D, 2, 256, 4><<<grid, 256, smem, s>>>(p);
-  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 3><<<grid, 256, smem, s>>>(p);
   else if (vecs == 2048) {
     // The only table of more than 40 KB (d = 128, a page of 128: 64 KB).
     static std::once_flag flags[64];
@@ -407,10 +455,10 @@ cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::call_once(flags[dev & 63], [&] {
-      attr_err[dev & 63] = cudaFuncSetAttribute(rope_append_kernel<D, 8, 256, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * D / 2 * 8);
+      attr_err[dev & 63] = cudaFuncSetAttribute(rope_append_kernel<D, 8, 256, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * D / 2 * 8);
     });
     if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
-    rope_append_kernel<D, 8, 256, 3><<<grid, 256, smem, s>>>(p);
+    rope_append_kernel<D, 8, 256, 2><<<grid, 256, smem, s>>>(p);
   } else return cudaErrorInvalidValue;
   return cudaGetLastError();
 }
@@ -428,7 +476,12 @@ cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t 
     else rope_append_step_kernel<128><<<grid, kStepWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
   }
-  const dim3 grid((unsigned)slots, (unsigned)p.a.Hkv, 2);
+  // Heads per CTA: as many as leave every SM work (the table is made once for them).
+  p.heads_per_cta = 1;
+  while (p.heads_per_cta < p.a.Hkv && p.heads_per_cta < 8 &&
+         2 * slots * ((p.a.Hkv + 2 * p.heads_per_cta - 1) / (2 * p.heads_per_cta)) >= 3LL * sms)
+    p.heads_per_cta *= 2;
+  const dim3 grid((unsigned)slots, (unsigned)((p.a.Hkv + p.heads_per_cta - 1) / p.heads_per_cta), 2);
   return d == 64 ? launch_d<64>(p, grid, s) : launch_d<128>(p, grid, s);
 }
 
