@@ -9,11 +9,16 @@
 // rounded the same way and stay exact, without a look at the rows.
 //
 // Bound by bytes (2 read, 1 written per element); what must not show is the sines and cosines, one
-// pair per token and two columns, the same for all heads.  Two kernels, by kv_append.cu's rule:
+// pair per token and two columns, the same for all heads (made per head they took 30 us of 107, below).
+// Two kernels:
 //   * few rows per sequence or page: a CTA per slot, 8 heads and K or V, a warp per head.  The CTA
-//     fills a table of 16 rows' sines and cosines, so each is made once for 8 heads;
-//   * prompts: a CTA per slot, head and K or V; the table of the whole page is made while its rows
-//     are on their way from memory.
+//     fills a table of 16 rows' sines and cosines, so each is made once for 8 heads.  One row of 64
+//     sequences, 32 + 8 heads: 5.7 us in a graph, queries included;
+//   * prompts: a CTA per slot, up to 8 heads and K or V.  The page's table is made while the first
+//     head's rows are on their way from memory; a head's rows stay in registers between the rotation,
+//     the maximum and the rounding, and the next head's are under way meanwhile.  Two prompts of 8192,
+//     32 + 8 heads, d = 128: 74 us with the queries' 42 (5.0 TB/s); K and V alone 36.
+// The queries rotate in rope.cu's kernel, beside this one where it leaves room.
 #include <cstdint>
 #include <mutex>
 
@@ -446,7 +451,7 @@ cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
   if (vecs == 128) rope_append_kernel<D, 1, 128, 8><<<grid, 128, smem, s>>>(p);
   else if (vecs == 256) rope_append_kernel<D, 1, 256, 4><<<grid, 256, smem, s>>>(p);
   else if (vecs == 512) rope_append_kernel<D, 2, 256, 4><<<grid, 256, smem, s>>>(p);
-  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 3><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 2><<<grid, 256, smem, s>>>(p);
   else if (vecs == 2048) {
     // The only table of more than 40 KB (d = 128, a page of 128: 64 KB).
     static std::once_flag flags[64];
@@ -469,7 +474,11 @@ cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t 
   p.a.page_shift = p.a.page == 16 ? 4 : p.a.page == 32 ? 5 : p.a.page == 64 ? 6 : 7;
   const long long slots = (long long)p.a.total / p.a.page + 2LL * p.a.B;
   if (slots > 0x3fffffffLL || p.a.Hkv > 65535) return cudaErrorInvalidValue;
-  const bool small = p.a.total <= 32 * slots && 2 * slots * p.a.Hkv >= 16LL * sms;
+  // Up to 4 rows per sequence on average, and pages that get less than half their rows, a warp per page and head;
+  // so that every SM has work (as in kv_append.cu): 256 pieces of 16 rows over pages of 64 / 128, 32 + 8 heads,
+  // d = 128, 25 / 26 us against 37 / 54 with a CTA per page and heads.  Whole pages take CTAs, whatever their size (two
+  // prompts of 8192: pages of 32 74 against 84; of 16 with d = 64 28 against 40, with d = 128 84 against 80).
+  const bool small = 2LL * p.a.total <= slots * p.a.page && 2 * slots * p.a.Hkv >= 16LL * sms;
   if (p.a.total <= 4LL * p.a.B || small) {
     const dim3 grid((unsigned)(2 * slots), (unsigned)((p.a.Hkv + kStepWarps - 1) / kStepWarps));
     if (d == 64) rope_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
