@@ -766,15 +766,6 @@ def _outputs(q, o, lse, dev):
     return o, lse
 
 
-def _workspace(workspace, need, dev):
-    """The caller's workspace, checked, or one of need() bytes."""
-    if workspace is None:
-        return torch.empty((max(need(), 16),), dtype=torch.uint8, device=dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
-    return workspace
-
-
 def attn_select_pages_fp8_workspace_size(Hkv: int, total_q: int, max_pages: int) -> int:
     n = _lib.attn_select_pages_fp8_workspace_size(Hkv, total_q, max_pages)
     if n == ctypes.c_size_t(-1).value:
@@ -823,7 +814,11 @@ def attn_select_pages_fp8(q, k_bounds, k_scale, page_table, cu_seqlens_q, kv_len
                                      ("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,)), ("kv_lens", kv_lens, i32, (B,)),
                                      ("pages", pages, i32, (Hkv, T, count))):
             _plain(name, t, dtype, want, dev)
-    ws = _workspace(workspace, lambda: attn_select_pages_fp8_workspace_size(Hkv, T, width), dev)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty((max(attn_select_pages_fp8_workspace_size(Hkv, T, width), 16),), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
     _check(_lib.attn_select_pages_fp8(q.data_ptr(), k_bounds.data_ptr(), k_scale.data_ptr(), page_table.data_ptr(),
                                       cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), pages.data_ptr(), B, Hq, Hkv, T, max_q, d,
                                       num_pages, page_size, width, count, first, last, 1 if causal else 0, ws.data_ptr(),
@@ -858,11 +853,16 @@ def attn_fwd_kv_fp8_pages(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_
     if dq != d:
         raise ValueError(f"q has {dq} columns, the cache {d}")
     o, lse = _outputs(q, o, lse, dev)
-    if pages.dim() != 3:
-        raise ValueError(f"pages: expected [Hkv, total_q, count], got {tuple(pages.shape)}")
-    count = pages.shape[2]
+    listed = pages.shape
+    if len(listed) != 3:
+        raise ValueError(f"pages: expected [Hkv, total_q, count], got {tuple(listed)}")
+    count = listed[2]
     _plain("pages", pages, torch.int32, (Hkv, T, count), dev)
-    ws = _workspace(workspace, lambda: attn_fwd_kv_fp8_pages_workspace_size(Hq, Hkv, T, d), dev)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty((max(attn_fwd_kv_fp8_pages_workspace_size(Hq, Hkv, T, d), 16),), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
     _check(_lib.attn_fwd_kv_fp8_pages(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                       v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
                                       pages.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, count, d, num_pages, P,
@@ -903,11 +903,21 @@ def attn_fwd_kv_fp8_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, 
     if prefix_table.dim() != 2:
         raise ValueError(f"prefix_table: expected [G, max_prefix_pages], got {tuple(prefix_table.shape)}")
     G, prefix_width = prefix_table.shape
-    for name, t, shape in (("prefix_table", prefix_table, (G, prefix_width)), ("cu_prefix_q", cu_prefix_q, (G + 1,)),
-                           ("prefix_lens", prefix_lens, (G,))):
-        _plain(name, t, torch.int32, shape, dev)
+    i32 = torch.int32
+    if not (prefix_table.dtype is i32 and cu_prefix_q.dtype is i32 and prefix_lens.dtype is i32
+            and cu_prefix_q.shape == (G + 1,) and prefix_lens.shape == (G,) and prefix_table.device == dev
+            and cu_prefix_q.device == dev and prefix_lens.device == dev and prefix_table.is_contiguous()
+            and cu_prefix_q.is_contiguous() and prefix_lens.is_contiguous()):
+        for name, t, shape in (("prefix_table", prefix_table, (G, prefix_width)), ("cu_prefix_q", cu_prefix_q, (G + 1,)),
+                               ("prefix_lens", prefix_lens, (G,))):
+            _plain(name, t, i32, shape, dev)
     o, lse = _outputs(q, o, lse, dev)
-    ws = _workspace(workspace, lambda: attn_fwd_kv_fp8_prefix_workspace_size(Hq, Hkv, T, max_prefix_q, max_q, d), dev)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty((max(attn_fwd_kv_fp8_prefix_workspace_size(Hq, Hkv, T, max_prefix_q, max_q, d), 16),),
+                         dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}")
     _check(_lib.attn_fwd_kv_fp8_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                        v_scale.data_ptr(), prefix_table.data_ptr(), cu_prefix_q.data_ptr(),
                                        prefix_lens.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(),

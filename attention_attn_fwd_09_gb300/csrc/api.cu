@@ -990,8 +990,14 @@ int attn_rope_kv_append_fp8(const void* q, void* q_out, const void* k, const voi
   p.mscale = mscale;
   p.bounds = static_cast<uint8_t*>(k_bounds);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_rope_append(p, d, std::max(1, s->sms), st);
-  if (e == cudaSuccess && Hq > 0) e = launch_rope(r, vec, p.interleaved, std::max(1, s->sms), st);
+  bool queries = Hq > 0 && rot % 8 == 0 && aligned16(q) && aligned16(q_out);
+  for (int i : {0, 1, 6, 7}) queries = queries && ((i & 1 ? total : Hq) <= 1 || st8[i] % 8 == 0);
+  p.q = q;
+  p.q_out = q_out;
+  p.q_h = st8[0]; p.q_t = st8[1]; p.o_h = st8[6]; p.o_t = st8[7];
+  p.Hq = Hq;
+  cudaError_t e = launch_rope_append(p, d, std::max(1, s->sms), &queries, st);
+  if (e == cudaSuccess && Hq > 0 && !queries) e = launch_rope(r, vec, p.interleaved, std::max(1, s->sms), st);
   if (e != cudaSuccess) return cuda_fail(e, "rotating cache append launch");
   return post_launch(s, st);
 }
@@ -1266,7 +1272,8 @@ int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cac
     p[i].side_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.lse);
     p[i].side_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
     p[i].side_bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.bad);
-    if ((rc = cache_maps(mine, few_rows(p[i]), &maps[i])) != ATTN_OK) return rc;
+    if (i == 1 && few_rows(p[0]) == few_rows(p[1])) maps[1] = maps[0];       // (of the same cache)
+    else if ((rc = cache_maps(mine, few_rows(p[i]), &maps[i])) != ATTN_OK) return rc;
   }
   for (int i = 0; i < 2; ++i)
     if ((rc = launch_cache(maps[i], p[i], d, sms, st)) != ATTN_OK) return rc;

@@ -214,9 +214,14 @@ struct RopeAppendParams {
   int rot, interleaved;
   float mscale;
   uint8_t* bounds;           // [num_pages, Hkv, 2, d] smallest and largest code per column, or null
-  int heads_per_cta;         // filled in by launch_rope_append
+  const void* q;             // bf16 [Hq, total, d], element strides of head and row; rows on 16 bytes, rot a multiple of 8
+  void* q_out;
+  long long q_h, q_t, o_h, o_t;
+  int Hq;
+  int heads_per_cta, slots;  // filled in by launch_rope_append
 };
-cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s);
+// *queries in: whether q may rotate in the same launch; out: whether it does.
+cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, bool* queries, cudaStream_t s);
 
 // Choice of pages by their bounds (select_pages.cu); d = 64 or 128.
 struct SelectParams {

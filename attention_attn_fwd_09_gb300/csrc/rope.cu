@@ -181,16 +181,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       if constexpr (INTER && V > 1) {
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) {
-          xo[2 * j] = x[2 * j] * cw[j] - x[2 * j + 1] * sw[j];
-          xo[2 * j + 1] = x[2 * j + 1] * cw[j] + x[2 * j] * sw[j];
-          yo[2 * j] = y[2 * j] * cw[V / 2 + j] - y[2 * j + 1] * sw[V / 2 + j];
-          yo[2 * j + 1] = y[2 * j + 1] * cw[V / 2 + j] + y[2 * j] * sw[V / 2 + j];
+          turn_pair(x[2 * j], x[2 * j + 1], cw[j], sw[j], xo[2 * j], xo[2 * j + 1]);
+          turn_pair(y[2 * j], y[2 * j + 1], cw[V / 2 + j], sw[V / 2 + j], yo[2 * j], yo[2 * j + 1]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          xo[j] = x[j] * cw[j] - y[j] * sw[j];
-          yo[j] = y[j] * cw[j] + x[j] * sw[j];
+          turn_pair(x[j], y[j], cw[j], sw[j], xo[j], yo[j]);
         }
       }
       st_vec<V>(dst + ca, pack<V>(xo));

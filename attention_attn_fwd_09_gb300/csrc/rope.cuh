@@ -31,4 +31,15 @@ __device__ __forceinline__ void turn_sincos_near(unsigned long long turn, long l
   }
 }
 
+// A pair (a, b) turned: x = a c - b s, y = b c + a s.  Which product is rounded by itself is written down, so that
+// all kernels turn a pair to the same bits.
+__device__ __forceinline__ void turn_pair(float a, float b, float c, float s, float& x, float& y) {
+  x = __fmaf_rn(a, c, -__fmul_rn(b, s));
+  y = __fmaf_rn(b, c, __fmul_rn(a, s));
+}
+// One of the two: x turned, z its partner.
+__device__ __forceinline__ float turn_one(float x, float z, float c, float s, bool second) {
+  return __fmaf_rn(x, c, __fmul_rn(second ? z : -z, s));
+}
+
 }  // namespace attn

@@ -18,7 +18,8 @@
 //     head's rows are on their way from memory; a head's rows stay in registers between the rotation,
 //     the maximum and the rounding, and the next head's are under way meanwhile.  Two prompts of 8192,
 //     32 + 8 heads, d = 128: 74 us with the queries' 42 (5.0 TB/s); K and V alone 36.
-// The queries rotate in rope.cu's kernel, beside this one where it leaves room.
+// The queries rotate in the same launch where there are few of them, else in rope.cu's kernel, beside this one where
+// it leaves room.
 #include <cstdint>
 #include <mutex>
 
@@ -93,8 +94,8 @@ __device__ __forceinline__ void turned(const RopeAppendParams& p, const uint4& o
       for (int i = 0; i < 2; ++i) {
         const float4 e = table[(i * 2 + (pair & 1)) * width + (pair >> 1)];
         const int x = 4 * k + 2 * i;
-        y[x] = y[x] * e.x + (upper ? z[2 * i] : -z[2 * i]) * e.y;
-        y[x + 1] = y[x + 1] * e.z + (upper ? z[2 * i + 1] : -z[2 * i + 1]) * e.w;
+        y[x] = turn_one(y[x], z[2 * i], e.x, e.y, upper);
+        y[x + 1] = turn_one(y[x + 1], z[2 * i + 1], e.z, e.w, upper);
       }
     }
   } else if constexpr (mode == TURN_INTER) {
@@ -104,10 +105,8 @@ __device__ __forceinline__ void turned(const RopeAppendParams& p, const uint4& o
     for (int q = 0; q < 2; ++q) {
       const float4 e = at[q * (rot / 8)];
       const float a = y[4 * q], b = y[4 * q + 1], d = y[4 * q + 2], f = y[4 * q + 3];
-      y[4 * q] = a * e.x - b * e.y;
-      y[4 * q + 1] = b * e.x + a * e.y;
-      y[4 * q + 2] = d * e.z - f * e.w;
-      y[4 * q + 3] = f * e.z + d * e.w;
+      turn_pair(a, b, e.x, e.y, y[4 * q], y[4 * q + 1]);
+      turn_pair(d, f, e.z, e.w, y[4 * q + 2], y[4 * q + 3]);
     }
   } else {
     const int half = rot / 2;
@@ -120,7 +119,7 @@ __device__ __forceinline__ void turned(const RopeAppendParams& p, const uint4& o
       const int other = p.interleaved ? col ^ 1 : (second ? col - half : col + half);
       const float z = __uint_as_float((uint32_t)__ldg(row + other) << 16);
       const float2 e = cs[j];
-      y[k] = y[k] * e.x + (second ? z : -z) * e.y;
+      y[k] = turn_one(y[k], z, e.x, e.y, second);
     }
   }
 }
@@ -232,7 +231,7 @@ template <int D, int mode>
 __device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slot& s, bool is_v, const unsigned long long* turn,
                                             float2* cs) {
   constexpr int THREADS = kStepWarps * 32, LPR = D / 8, RPW = 32 / LPR, STEPS = kStepRows / RPW;   // lanes per row, rows at once
-  const int lane = threadIdx.x & 31, head = blockIdx.y * kStepWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, head = blockIdx.x / (2 * p.slots) * kStepWarps + (threadIdx.x >> 5);
   const int stride = turn_row(p.rot);
   const bool live = head < p.a.Hkv;
   const Target t(p.a, s, live ? head : 0, is_v, D);
@@ -324,19 +323,64 @@ __device__ __forceinline__ void append_step(const RopeAppendParams& p, const Slo
   if (lane == 0) *t.scale = sc;
 }
 
-// Block (x, y): slot x / 2, K or V by x & 1, heads 8 y + warp.
+// The queries of packed row t, rotated as rope.cu's kernel does (the same bits); few rows only.
+template <int D, int mode>
+__device__ __forceinline__ void turn_queries(const RopeAppendParams& p, int t, const unsigned long long* turn, float2* cs) {
+  constexpr int THREADS = kStepWarps * 32, LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, r0 = lane / LPR, c = lane % LPR;
+  const int h0 = (threadIdx.x >> 5) * RPW;             // this warp's first heads
+  const uint16_t* src = static_cast<const uint16_t*>(p.q) + t * p.q_t + c * 8;
+  uint16_t* dst = static_cast<uint16_t*>(p.q_out) + t * p.o_t + c * 8;
+  auto load = [&](int h) -> uint4 {
+    return h + r0 < p.Hq ? *reinterpret_cast<const uint4*>(src + (h + r0) * p.q_h) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 x = load(h0);
+  long long pos;
+  if (p.positions) {
+    pos = __ldg(p.positions + t);
+  } else {                                             // the last sequence that starts at or before it
+    int b = -1;
+    for (int i = 0; i < p.a.B; i += THREADS) b += __syncthreads_count(i + threadIdx.x < p.a.B && __ldg(p.a.cu + min(i + (int)threadIdx.x, p.a.B - 1)) <= t);
+    b = max(b, 0);                                     // (invalid offsets only make it wrong)
+    pos = (long long)__ldg(p.a.kv_lens + b) - __ldg(p.a.cu + b + 1) + t;
+  }
+  __syncthreads();                                     // turn
+  for (int j = threadIdx.x; j < p.rot / 2; j += THREADS) {
+    float sn, co;
+    turn_sincos(turn[j], pos, sn, co);
+    cs[turn_slot<mode>(p.rot, j)] = make_float2(co * p.mscale, sn * p.mscale);
+  }
+  __syncthreads();
+  for (int h = h0; h < p.Hq; h += kStepWarps * RPW) {
+    const uint4 now = x;
+    x = load(h + kStepWarps * RPW);
+    float y[8];
+    turned<mode>(p, now, nullptr, c, cs, y);
+    if (h + r0 < p.Hq)
+      *reinterpret_cast<uint4*>(dst + (h + r0) * p.o_h) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+  }
+}
+
+// Block x: of the first 2 slots x head groups, slot x / 2 mod slots, K or V by x & 1, 8 heads a group; behind
+// them the queries of a row each.
 template <int D>
 __global__ void __launch_bounds__(kStepWarps * 32) rope_append_step_kernel(const RopeAppendParams p) {
   __shared__ unsigned long long turn[D / 2];
   __shared__ __align__(16) float2 cs[kStepRows * D / 2];         // (a row of the table: at most D / 2 pairs)
   constexpr int THREADS = kStepWarps * 32;
   pdl_trigger();                                       // the queries' rotation may start
-  const bool is_v = blockIdx.x & 1;
+  const int kv_blocks = 2 * p.slots * ((p.a.Hkv + kStepWarps - 1) / kStepWarps), x = blockIdx.x % (2 * p.slots);
+  const bool queries = (int)blockIdx.x >= kv_blocks, is_v = !queries && (x & 1);
   const int mode = turn_mode(p, is_v);
   if (mode != TURN_NONE)
     for (int j = threadIdx.x; j < p.rot / 2; j += THREADS) turn[j] = turns_per_position(p.inv_freq[j]);
+  if (queries) {
+    if (mode == TURN_SPLIT) turn_queries<D, TURN_SPLIT>(p, (int)blockIdx.x - kv_blocks, turn, cs);
+    else turn_queries<D, TURN_INTER>(p, (int)blockIdx.x - kv_blocks, turn, cs);
+    return;
+  }
   Slot s;
-  if (!find_slot<THREADS>(p.a, blockIdx.x >> 1, s)) return;      // (its barrier stands behind the writes of turn)
+  if (!find_slot<THREADS>(p.a, x >> 1, s)) return;     // (its barrier stands behind the writes of turn)
   if (mode == TURN_NONE) append_step<D, TURN_NONE>(p, s, is_v, turn, cs);
   else if (mode == TURN_SPLIT) append_step<D, TURN_SPLIT>(p, s, is_v, turn, cs);
   else if (mode == TURN_INTER) append_step<D, TURN_INTER>(p, s, is_v, turn, cs);
@@ -470,7 +514,9 @@ cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t s) {
+cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, bool* queries, cudaStream_t s) {
+  const bool want = *queries;
+  *queries = false;
   p.a.page_shift = p.a.page == 16 ? 4 : p.a.page == 32 ? 5 : p.a.page == 64 ? 6 : 7;
   const long long slots = (long long)p.a.total / p.a.page + 2LL * p.a.B;
   if (slots > 0x3fffffffLL || p.a.Hkv > 65535) return cudaErrorInvalidValue;
@@ -480,9 +526,14 @@ cudaError_t launch_rope_append(RopeAppendParams p, int d, int sms, cudaStream_t 
   // prompts of 8192: pages of 32 74 against 84; of 16 with d = 64 28 against 40, with d = 128 84 against 80).
   const bool small = 2LL * p.a.total <= slots * p.a.page && 2 * slots * p.a.Hkv >= 16LL * sms;
   if (p.a.total <= 4LL * p.a.B || small) {
-    const dim3 grid((unsigned)(2 * slots), (unsigned)((p.a.Hkv + kStepWarps - 1) / kStepWarps));
-    if (d == 64) rope_append_step_kernel<64><<<grid, kStepWarps * 32, 0, s>>>(p);
-    else rope_append_step_kernel<128><<<grid, kStepWarps * 32, 0, s>>>(p);
+    // A few rows' queries in the same launch (a token each of 64 sequences: 5.8 us in a graph either way, but 2.4 us
+    // less of the host's time).
+    *queries = want && p.a.total <= 4 * sms;
+    p.slots = (int)slots;
+    const long long grid = 2 * slots * ((p.a.Hkv + kStepWarps - 1) / kStepWarps) + (*queries ? p.a.total : 0);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (d == 64) rope_append_step_kernel<64><<<(unsigned)grid, kStepWarps * 32, 0, s>>>(p);
+    else rope_append_step_kernel<128><<<(unsigned)grid, kStepWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
   }
   // Heads per CTA: as many as leave every SM work (the table is made once for them).

@@ -233,6 +233,30 @@ def test_zero_extreme_and_nonfinite_rows(A, P):
     c.append(None, x[:, 9:], x[:, 9:], [11], [20], f)
 
 
+@pytest.mark.parametrize("rot,inter,lead", [(128, False, 0), (40, False, 0), (40, True, 0), (128, True, 0), (36, False, 0), (128, False, 1)])
+@pytest.mark.parametrize("B", [5, 300])
+def test_queries_of_a_few_rows(A, rot, inter, lead, B):
+    """Few rows' queries: the same bits as attn_rope's whether or not they go in the same launch (rows off 16
+    bytes, and a rotated part that is no multiple of 8 columns, do not), some sequences without rows."""
+    rng = np.random.RandomState(B + rot)
+    H, Hq, P, d = 1, 37, 16, 128
+    ns = [0, 1, 1, 3, 1] if B == 5 else rng.randint(0, 3, B).tolist()
+    lens = [n + int(x) for n, x in zip(ns, rng.randint(0, 30, B))]
+    table, pages = page_tables(lens, P)
+    c = Cache(A, pages, table, H, P, d)
+    T = sum(ns)
+    q, k, v = rows(rng, Hq, H, T, d)
+    flat = torch.empty(Hq * T * d + 8, dtype=torch.bfloat16, device=DEV)
+    view = flat[lead:lead + Hq * T * d].view(Hq, T, d)
+    view.copy_(q)
+    c.used[:] = 0
+    for b, n in enumerate(lens):                           # the rows before: whatever is there
+        for blk in range(-(-n // P)):
+            c.used[table[b, blk]] = 0
+    c.bounds = None
+    c.append(q, k, v, ns, lens, freqs(A, rot), inter=inter, m=0.75, views=(view, k.to(DEV), v.to(DEV)))
+
+
 def test_many_sequences(A):
     """More sequences than a block has threads, some without new rows."""
     rng = np.random.RandomState(8)
