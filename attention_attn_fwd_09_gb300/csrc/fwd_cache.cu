@@ -268,15 +268,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const long long first = seg.f;             // the CTA's first piece
 
-  // The first unit's queries, on their way while its pages are looked up.
-  if (lane < 16 && lane < p.max_q * p.g) {   // (row lane; rows that the unit does not have: some row)
-    const int q0 = LIST ? seg.t : __ldg(p.cu_q + seg.b), n = LIST ? 1 : __ldg(p.cu_q + seg.b + 1) - q0;
-    const int qi = LIST ? 0 : min(lane / p.g, n - 1), hd = LIST ? min(lane, p.g - 1) : lane % p.g;
-    const char* row = static_cast<const char*>(p.q) + ((long long)(seg.h * p.g + hd) * p.total_q + q0 + qi) * (2 * D);
-#pragma unroll
-    for (int i = 0; i < 2 * D; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + i));
-  }
-
   // ---- this warp's loads, STAGES pieces ahead of its work
   const int page_shift = 31 - __clz(p.page);
   const int grp = lane & 1;                  // half of a piece (16 keys) this lane looks after
@@ -315,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto scale_of = [&](int pg, int h) -> float {
     return pg >= 0 ? __ldg(((lane & 2) ? p.v_scale : p.k_scale) + (long long)pg * kv_heads + h) : 0.f;
   };
-  auto issue = [&](int stage, int pg, const Cursor<LIST>& at) {      // the piece at `at`
+  auto issue = [&](int stage, int pg) {
     // Pages of 16 rows: two boxes, by lanes 0 and 1; larger ones hold the whole piece.
     const int p0 = __shfl_sync(0xffffffffu, pg, 0), p1 = __shfl_sync(0xffffffffu, pg, 1);
     const bool two = p.page == 16;
@@ -327,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     if (lane < (two ? 2 : 1) && pg >= 0) {
-      const int key = (int)(at.f - at.ubeg) * kPiece + lane * 16;
+      const int key = (int)(ahead.f - ahead.ubeg) * kPiece + lane * 16;
       const int line = (key & (p.page - 1)) * D / 128;
-      const int z = pg * kv_heads + kv_head(at.h);
+      const int z = pg * kv_heads + kv_head(ahead.h);
       const uint32_t dst = smem_u32(ring + stage * 2 * C::KB) + lane * box;
       tma_load_3d(dst, &tm_k, 0, line, z, bar);
       tma_load_3d(dst + C::KB, &tm_v, 0, line, z, bar);
@@ -338,23 +329,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   int pages[C::STAGES + 1], heads[C::STAGES + 1];     // of the pieces under way, oldest first; one more looked up
   int keys[LIST ? C::STAGES + 1 : 1];                 // LIST: first key of this lane's half of each
   bool ok = true;
-  // Where the first pieces lie (look-ups overlap: nothing is issued between them), then their copies.
-  Cursor<LIST> at = ahead;
 #pragma unroll
   for (int i = 0; i <= C::STAGES; ++i) {
     pages[i] = page_at();
     heads[i] = kv_head(ahead.h);
     if (LIST) keys[i] = key_ahead;
     if (i < C::STAGES) {
+      if (ahead.f < re && !(p.test_skip_first_kv && i == 0)) issue(i, pages[i]);
       ahead.f += kWarps;
       ahead.settle(p, re);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < C::STAGES; ++i) {
-    if (at.f < re && !(p.test_skip_first_kv && i == 0)) issue(i, pages[i], at);
-    at.f += kWarps;
-    at.settle(p, re);
   }
   // `ahead` now stands at piece number STAGES of this warp, whose page is pages[STAGES].
   float sc_next = scale_of(pages[0], heads[0]);
@@ -613,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // The stage is read: the next piece into it.
       __syncwarp();
-      if (ok && ahead.f < re) issue(stage, pages[C::STAGES], ahead);
+      if (ok && ahead.f < re) issue(stage, pages[C::STAGES]);
 #pragma unroll
       for (int i = 0; i < C::STAGES; ++i) {
         pages[i] = pages[i + 1];
