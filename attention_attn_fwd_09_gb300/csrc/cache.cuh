@@ -78,7 +78,16 @@ __device__ __forceinline__ void take_nan_codes(uint8_t* piece, int key, int* fir
 }
 constexpr int kNoKey = 0x7fffffff;
 
-// Keys in two parts: a row's O is x own O + y O of the first part, lse2 (log2) of all keys goes to `joint`.
+// Keys in two parts: where row r of the unit at packed query q0 of K/V head h lies (side_lse; side_o: its piece of 4
+// columns i).  Rows of a unit lie side by side, as the threads that have them.
+__device__ __forceinline__ long long side_row(const CacheParams& p, int h, int q0, int r) {
+  return ((long long)h * p.total_q + q0) * p.g + r;
+}
+template <int D>
+__device__ __forceinline__ float4* side_piece(const CacheParams& p, int h, int q0, int r, int i) {
+  return reinterpret_cast<float4*>(p.side_o) + ((long long)h * (D / 4) + i) * p.total_q * p.g + (long long)q0 * p.g + r;
+}
+// A row's O is x own O + y O of the first part, lse2 (log2) of all keys goes to `joint`.
 // 0 and -inf where neither part has a key.
 __device__ __forceinline__ float2 join_side(const CacheParams& p, long long row, float lse2, float& joint) {
   const float other = p.side_lse[row], mx = fmaxf(lse2, other), mu = mx == -INFINITY ? 0.f : mx;

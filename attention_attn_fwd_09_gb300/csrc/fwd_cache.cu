@@ -693,9 +693,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           float lse2 = m[i] - kShift + __log2f(l[i]);
           const long long row = (long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi;
           if (p.side != SIDE_NONE) {         // columns 8 k .. 8 k + 7 of each half: two pieces of 4
-            float4* side = reinterpret_cast<float4*>(p.side_o + row * D + c * (D / 4));
+            const long long pieces = (long long)p.total_q * g;     // from one piece of the row to the next
+            float4* side = side_piece<D>(p, seg.h, q0, r, c * (D / 16));
             float2 w = make_float2(1.f, 0.f);
-            if (p.side == SIDE_IN) w = join_side(p, row, lse2, lse2);
+            if (p.side == SIDE_IN) w = join_side(p, side_row(p, seg.h, q0, r), lse2, lse2);
             inv *= w.x;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int k = 0; k < C::NACC / 4; ++k) {
                 float4 y = make_float4(o[4 * k][2 * i + e] * inv, o[4 * k + 1][2 * i + e] * inv, o[4 * k + 2][2 * i + e] * inv,
                                        o[4 * k + 3][2 * i + e] * inv);
-                float4* at = side + e * (C::NACC / 4) + k;
+                float4* at = side + (e * (C::NACC / 4) + k) * pieces;
                 if (p.side == SIDE_OUT) {
                   *at = y;
                   continue;
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 o[4 * k + 3][2 * i + e] = y.w + w.y * x.w;
               }
             if (p.side == SIDE_OUT) {
-              if (c == 0) p.side_lse[row] = lse2;
+              if (c == 0) p.side_lse[side_row(p, seg.h, q0, r)] = lse2;
               continue;
             }
             inv = 1.f;
@@ -845,22 +846,23 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
     float inv = l == 0.f ? 0.f : ref / l, lse2 = m + __log2f(l);
     if (p.side != SIDE_NONE) {
-      float4* side = reinterpret_cast<float4*>(p.side_o + row * D) + cg * CPT;
+      const long long pieces = (long long)p.total_q * p.g;         // from one piece of the row to the next
+      float4* side = side_piece<D>(p, rec.x, rec.y, r, cg * CPT);
       float2 w = make_float2(1.f, 0.f);
-      if (p.side == SIDE_IN) w = join_side(p, row, lse2, lse2);
+      if (p.side == SIDE_IN) w = join_side(p, side_row(p, rec.x, rec.y, r), lse2, lse2);
       inv *= w.x;
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
         o[c] = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
         if (p.side == SIDE_OUT) {
-          side[c] = o[c];
+          side[c * pieces] = o[c];
           continue;
         }
-        const float4 x = side[c];
+        const float4 x = side[c * pieces];
         o[c] = make_float4(o[c].x + w.y * x.x, o[c].y + w.y * x.y, o[c].z + w.y * x.z, o[c].w + w.y * x.w);
       }
       if (p.side == SIDE_OUT) {
-        if (cg == 0) p.side_lse[row] = lse2;
+        if (cg == 0) p.side_lse[side_row(p, rec.x, rec.y, r)] = lse2;
         continue;
       }
       inv = 1.f;

@@ -949,9 +949,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const long long orow = (long long)(h * p.g + (r - qi * p.g)) * p.total_q + q0 + qi;
         const long long prow = (long long)part * kTRows + r;
         float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f, lse2 = m - kPShift + __log2f(l), w_side = 0.f;
-        float4* side = reinterpret_cast<float4*>(p.side_o + orow * D);     // (used where the row is live)
+        const long long pieces = (long long)p.total_q * p.g;       // from one piece of 4 columns to the next
+        float4* side = side_piece<D>(p, h, q0, r, 0);              // (used where the row is live)
         if (whole && live && SIDE && p.side == SIDE_IN) {
-          const float2 w = join_side(p, orow, lse2, lse2);
+          const float2 w = join_side(p, side_row(p, h, q0, r), lse2, lse2);
           inv *= w.x;
           w_side = w.y;
         }
@@ -976,10 +977,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
               float4 y = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
                                      __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
               if (SIDE && p.side == SIDE_OUT) {
-                side[q * 8 + i] = y;
+                side[(q * 8 + i) * pieces] = y;
                 continue;
               }
-              const float4 z = side[q * 8 + i];
+              const float4 z = side[(q * 8 + i) * pieces];
               x[4 * i] = __float_as_uint(y.x + w_side * z.x);
               x[4 * i + 1] = __float_as_uint(y.y + w_side * z.y);
               x[4 * i + 2] = __float_as_uint(y.z + w_side * z.z);
@@ -1023,13 +1024,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < D; ++i) {
             if (nan_keys[(nu & 1) * D + i] >= U.lim0 + qi) continue;
-            if (whole && SIDE && p.side == SIDE_OUT) p.side_o[orow * D + i] = __int_as_float(0x7fffffff);
+            if (whole && SIDE && p.side == SIDE_OUT) reinterpret_cast<float*>(side + (i / 4) * pieces)[i % 4] = __int_as_float(0x7fffffff);
             else if (whole) static_cast<uint16_t*>(p.o)[orow * D + i] = 0x7fff;
             else reinterpret_cast<uint32_t*>(ws + W.part)[(((long long)part * (D / 4) + i / 4) * kTRows + r) * 4 + i % 4] = 0x7fffffffu;
           }
         }
         if (live) {
-          if (whole && SIDE && p.side == SIDE_OUT) p.side_lse[orow] = lse2;
+          if (whole && SIDE && p.side == SIDE_OUT) p.side_lse[side_row(p, h, q0, r)] = lse2;
           else if (whole) p.lse[orow] = lse2 * kLn2;
           else reinterpret_cast<float4*>(ws + W.stat)[prow] = make_float4(m - kPShift, l, ref, 0.f);
         }

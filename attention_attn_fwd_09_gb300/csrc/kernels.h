@@ -264,7 +264,8 @@ struct CacheParams {
   const int* list;
   int list_count, rep;
   // Keys in two parts (a shared prefix, then a sequence's own): the first part's result goes to side_o
-  // [Hq, total_q, d] and side_lse [Hq, total_q] (log2) instead of o and lse, the second part's is joined with it.
+  // [Hkv][d / 4][total_q g] (pieces of 4 columns; a K/V head's rows are query by query, its heads side by side) and
+  // side_lse [Hkv][total_q g] (log2) instead of o and lse, the second part's is joined with it.
   int side;                  // SIDE_NONE, SIDE_OUT (first part) or SIDE_IN (second)
   float *side_o, *side_lse;
   int* side_bad;             // the first part's offsets were invalid: the second writes nothing
