@@ -960,9 +960,47 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // Whole units go through shared memory (V16 slot t: no product reads it any more), so that rows
         // leave in whole lines; a warp stages its own 32 rows.
         uint8_t* stage = smem + C::OFF_V16 + t * C::V16 + (warp & 3) * 32 * (2 * D);
+        bool done = false;
+        if constexpr (SIDE) {
+          if (whole) {                       // 16 columns at a time: more would spill
+            done = true;
+            float4* at = side;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t x[16];
+              float4 z[4];
+              if (p.side == SIDE_IN) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = live ? at[i * pieces] : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+              if (n_t > 0) {
+                tmem_ld16(tO + q * 16, x);
+                tmem_wait_ld();
+                reg_fence(x);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = 0u;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float4 y = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
+                                       __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
+                if (p.side == SIDE_OUT) {
+                  if (live) at[i * pieces] = y;
+                  continue;
+                }
+                y = make_float4(y.x + w_side * z[i].x, y.y + w_side * z[i].y, y.z + w_side * z[i].z, y.w + w_side * z[i].w);
+                *reinterpret_cast<uint2*>(stage + lane * (2 * D) + (((q * 2 + (i >> 1)) ^ (lane & 7)) << 4) + (i & 1) * 8) =
+                    make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+              }
+              at += 4 * pieces;
+              __syncwarp();
+            }
+          }
+        }
         uint32_t x[32];
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = 0; q < D / 32 && !done; ++q) {
           if (n_t > 0) {
             tmem_ld32(tO + q * 32, x);
             tmem_wait_ld();
@@ -971,30 +1009,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0u;
           }
-          if constexpr (SIDE) if (whole && live) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 y = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
-                                     __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
-              if (SIDE && p.side == SIDE_OUT) {
-                side[(q * 8 + i) * pieces] = y;
-                continue;
-              }
-              const float4 z = side[(q * 8 + i) * pieces];
-              x[4 * i] = __float_as_uint(y.x + w_side * z.x);
-              x[4 * i + 1] = __float_as_uint(y.y + w_side * z.y);
-              x[4 * i + 2] = __float_as_uint(y.z + w_side * z.z);
-              x[4 * i + 3] = __float_as_uint(y.w + w_side * z.w);
-            }
-          }
-          const float inv_out = SIDE && p.side == SIDE_IN ? 1.f : inv;
-          if (whole) {
+          if (!SIDE && whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv_out, __uint_as_float(x[8 * i + 2 * k + 1]) * inv_out);
+                y[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * inv, __uint_as_float(x[8 * i + 2 * k + 1]) * inv);
               *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((q * 4 + i) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else if (live) {
