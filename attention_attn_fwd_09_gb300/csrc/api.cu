@@ -1205,7 +1205,6 @@ int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cach
   if ((rc = check_workspace(workspace, workspace_bytes, cache_decode_workspace_bytes(share, d, sms))) != ATTN_OK) return rc;
   if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   CacheParams p = cache_params(c, total_q, workspace, s);
-  p.unit_cost = kCacheUnitCost;
   p.list = pages;
   p.list_count = count;
   p.rep = Hq / Hkv / share;
@@ -1267,7 +1266,6 @@ int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cac
   CacheParams p[2] = {cache_params(shared, max_prefix_q, workspace, s), cache_params(mine, max_q, workspace, s)};
   CacheMaps maps[2];
   for (int i = 0; i < 2; ++i) {
-    p[i].unit_cost = kCacheUnitCost;
     p[i].side = i == 0 ? SIDE_OUT : SIDE_IN;
     p[i].side_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.lse);
     p[i].side_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);

@@ -31,6 +31,7 @@
 // sums and O are fp32.
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "kernels.h"
@@ -43,6 +44,10 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kPiece = 32;                   // keys per piece
 constexpr int kSMs = 152;                  // blocks of the merge kernel are a multiple of these
 constexpr float kShift = 14.f;               // weights are held times 2^14
+// What starting and ending a unit counts for when work is cut, in pieces (shared prefixes before 64 sequences of up
+// to 1024 keys: 90 us, without it 114, as one CTA had all the short ones; 6 and 20 alike).  attn_fwd_kv_fp8 counts
+// pieces alone.
+constexpr int kUnitCost = 12;
 
 template <int D>
 struct DecCfg {
@@ -97,18 +102,26 @@ __device__ __forceinline__ int list_pieces(const CacheParams& p, int seen) {
   return max(1, (min(seen, p.list_count) * p.page + kPiece - 1) / kPiece);
 }
 
+// What the kernel works on: sequences; queries with lists of pages (p.list); sequences whose keys come in two parts
+// (p.side).  The latter two count what starting and ending a unit costs when they cut the work.
+enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };
+
 // Where a warp is in the CTA's run of pieces.  Positions count pieces and, before each unit's, `cost` places
-// for starting and ending it, which nobody fills.
-template <bool LIST>
+// for starting and ending it, which nobody fills (KIND_PLAIN: none).
+template <int KIND>
 struct Cursor {
+  static constexpr bool LIST = KIND == KIND_LIST;
   int b, h;
   int t, seen;                               // LIST: packed query, the pages it sees
   int cost;
   long long f, ubeg, uend;                   // piece, and the unit's first and last + 1
   __device__ __forceinline__ void settle(const CacheParams& p, long long end) {   // into the unit that holds f
     while (f < end && f >= uend) {
-      ubeg = uend + cost;
-      f += cost;
+      ubeg = uend;
+      if constexpr (KIND != KIND_PLAIN) {
+        ubeg += cost;
+        f += cost;
+      }
       if (++h == p.Hkv) {
         h = 0;
         if constexpr (LIST) {
@@ -131,11 +144,12 @@ struct Cursor {
 
 // LIST: attention over listed pages.  p.list [K/V head][query][list_count] holds page numbers within the
 // query's sequence; p.rep virtual heads of p.g query heads share a K/V head (p.Hkv counts virtual ones).
-template <int D, bool LIST>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 2)
     fwd_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const CacheParams p, const int rows_max) {
   using C = DecCfg<D>;
+  constexpr bool LIST = KIND == KIND_LIST, SIDE = KIND == KIND_SIDE;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane & 3, rq = lane >> 2;    // fragment column group and row
@@ -188,10 +202,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     units = t_hi - t_lo;
   }
-  // A unit costs as much as p.unit_cost pieces, or, with little work, a quarter of a CTA's pieces.  (Where 0,
-  // pieces alone are counted.)
+  // A unit costs as much as kUnitCost pieces, or, with little work, a quarter of a CTA's pieces.
   int cost = 0;
-  if (p.unit_cost > 0) {
+  if constexpr (KIND != KIND_PLAIN) {
     long long all = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) all += misc[w];
-    cost = (int)min((long long)p.unit_cost, all * p.Hkv / gridDim.x / 4);
+    cost = (int)min((long long)kUnitCost, all * p.Hkv / gridDim.x / 4);
     mine += (long long)cost * units;
     __syncthreads();                         // misc has been read
   }
@@ -215,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
-    if (p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
+    if (SIDE && p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
   }
-  if (bad || (p.side == SIDE_IN && *p.side_bad)) return;
+  if (bad || (SIDE && p.side == SIDE_IN && *p.side_bad)) return;
   long long before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (LIST) misc[2] = t;
   }
   __syncthreads();
-  Cursor<LIST> seg;                          // the unit being worked on
+  Cursor<KIND> seg;                          // the unit being worked on
   seg.b = (int)misc[0];
   seg.cost = cost;
   seg.t = seg.seen = 0;
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int page_shift = 31 - __clz(p.page);
   const int grp = lane & 1;                  // half of a piece (16 keys) this lane looks after
   uint8_t* ring = smem + warp * C::STAGES * 2 * C::KB;
-  Cursor<LIST> ahead = seg;
+  Cursor<KIND> ahead = seg;
   ahead.f = first + warp;
   ahead.settle(p, re);
   const int kv_heads = LIST ? p.Hkv / p.rep : p.Hkv;
@@ -692,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float inv = l[i] == 0.f ? 0.f : rref / l[i];
           float lse2 = m[i] - kShift + __log2f(l[i]);
           const long long row = (long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi;
-          if (p.side != SIDE_NONE) {         // columns 8 k .. 8 k + 7 of each half: two pieces of 4
+          if constexpr (SIDE) {              // columns 8 k .. 8 k + 7 of each half: two pieces of 4
             const long long pieces = (long long)p.total_q * g;     // from one piece of the row to the next
             float4* side = side_piece<D>(p, seg.h, q0, r, c * (D / 16));
             float2 w = make_float2(1.f, 0.f);
@@ -747,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     seg.f = send;
-    if (send == seg.uend && send < re) f += cost;      // on to the next unit
+    if (KIND != KIND_PLAIN && send == seg.uend && send < re) f += cost;      // on to the next unit
     seg.settle(p, re);
   }
 }
@@ -762,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // takes item i of all CTAs, which is one look-up shorter but comes to several waves of blocks that find
 // nothing when few CTAs leave a unit of many items (4 drafted tokens, 8 units: 25.1 us against 26.1;
 // 16 sequences of 16 rows in 1216 blocks 99.6 against 97.6, with many units 3 us more).
-template <int D, int CPT, int JOIN, bool COMPACT>
+template <int D, int CPT, int JOIN, bool COMPACT, bool SIDE>
 __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams p, const int rows_max, const int row_shift,
                                                               const int ctas) {
   constexpr int GROUPS = D / 4 / CPT;
@@ -845,7 +858,7 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     }
     const long long row = (long long)(rec.x * p.g + r - qi * p.g) * p.total_q + rec.y + qi;
     float inv = l == 0.f ? 0.f : ref / l, lse2 = m + __log2f(l);
-    if (p.side != SIDE_NONE) {
+    if constexpr (SIDE) {
       const long long pieces = (long long)p.total_q * p.g;         // from one piece of the row to the next
       float4* side = side_piece<D>(p, rec.x, rec.y, r, cg * CPT);
       float2 w = make_float2(1.f, 0.f);
@@ -880,7 +893,7 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
   }
 }
 
-template <int D, bool LIST>
+template <int D, int KIND>
 cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows, int grid, cudaStream_t s) {
   using C = DecCfg<D>;
   static std::once_flag flags[64];
@@ -889,11 +902,11 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::call_once(flags[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    attr_err[dev & 63] = cudaFuncSetAttribute(fwd_cache_decode_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
   // A dependent launch of whatever runs before: the kernel waits for it to be done, but is in place by then.
-  e = launch_pdl(fwd_cache_decode_kernel<D, LIST>, dim3(grid), dim3(kThreads), C::SMEM, s, maps.k, maps.v, p, rows);
+  e = launch_pdl(fwd_cache_decode_kernel<D, KIND>, dim3(grid), dim3(kThreads), C::SMEM, s, maps.k, maps.v, p, rows);
   if (e != cudaSuccess) return e;
   return launch_fwd_cache_merge(p, D, rows, grid, s);
 }
@@ -910,24 +923,33 @@ cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ct
   };
   // Few units of many partials each: latency again (a sequence of 30000 keys, 32 rows: 33 us against 35).
   const long long units = (long long)p.B * p.Hkv * (((long long)p.max_q * p.g + rows - 1) / rows);
-  if (rows <= kCacheDecodeRows || units * 4 <= ctas) {
-    if (((d / 4) << shift) / 128 * ctas > 16 * kSMs && ctas <= 1024)
-      return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8, true>, 1, true) : go(fwd_cache_merge_kernel<128, 1, 8, true>, 1, true);
-    return d == 64 ? go(fwd_cache_merge_kernel<64, 1, 8, false>, 1, false) : go(fwd_cache_merge_kernel<128, 1, 8, false>, 1, false);
-  }
-  return d == 64 ? go(fwd_cache_merge_kernel<64, 2, 2, false>, 2, false) : go(fwd_cache_merge_kernel<128, 2, 2, false>, 2, false);
+  auto pick = [&](auto dim, auto side) {
+    constexpr int D = dim;
+    constexpr bool S = side;
+    if (rows <= kCacheDecodeRows || units * 4 <= ctas) {
+      if (((d / 4) << shift) / 128 * ctas > 16 * kSMs && ctas <= 1024) return go(fwd_cache_merge_kernel<D, 1, 8, true, S>, 1, true);
+      return go(fwd_cache_merge_kernel<D, 1, 8, false, S>, 1, false);
+    }
+    return go(fwd_cache_merge_kernel<D, 2, 2, false, S>, 2, false);
+  };
+  using I64 = std::integral_constant<int, 64>;
+  using I128 = std::integral_constant<int, 128>;
+  if (p.side != SIDE_NONE) return d == 64 ? pick(I64(), std::true_type()) : pick(I128(), std::true_type());
+  return d == 64 ? pick(I64(), std::false_type()) : pick(I128(), std::false_type());
 }
 
 size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }
 
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
   const int rows = p.max_q * p.g, grid = 2 * sms;      // as in the workspace's size
-  return d == 64 ? launch_decode<64, false>(maps, p, rows, grid, s) : launch_decode<128, false>(maps, p, rows, grid, s);
+  if (p.side != SIDE_NONE)
+    return d == 64 ? launch_decode<64, KIND_SIDE>(maps, p, rows, grid, s) : launch_decode<128, KIND_SIDE>(maps, p, rows, grid, s);
+  return d == 64 ? launch_decode<64, KIND_PLAIN>(maps, p, rows, grid, s) : launch_decode<128, KIND_PLAIN>(maps, p, rows, grid, s);
 }
 
 cudaError_t launch_fwd_cache_pages(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
   const int grid = 2 * sms;
-  return d == 64 ? launch_decode<64, true>(maps, p, p.g, grid, s) : launch_decode<128, true>(maps, p, p.g, grid, s);
+  return d == 64 ? launch_decode<64, KIND_LIST>(maps, p, p.g, grid, s) : launch_decode<128, KIND_LIST>(maps, p, p.g, grid, s);
 }
 
 }  // namespace attn

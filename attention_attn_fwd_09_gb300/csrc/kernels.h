@@ -258,7 +258,6 @@ struct CacheParams {
   unsigned long long wait_ns;
   int* status;
   int test_skip_first_kv;    // test hook: each CTA never issues its first K copy
-  int unit_cost;             // few rows: what starting and ending a unit counts for when work is cut, in pieces
   // Listed pages (launch_fwd_cache_pages): page numbers within each query's sequence, [K/V heads][total_q]
   // [list_count], negative ones left out; g, Hkv count virtual heads, rep of which share a K/V head.
   const int* list;
@@ -279,9 +278,6 @@ struct CacheMaps {
 // At most 16 rows (queries x heads of a group) per sequence and K/V head: fwd_cache.cu.  (16 rows, 16
 // sequences of 16000 keys: 96 us, the tiles 146; one of 4000: 15.0 against 16.3.)
 constexpr int kCacheDecodeRows = 16;
-// (Shared prefixes before 64 sequences of up to 1024 keys: 90 us, without it 114, as one CTA had all the short
-// ones; 6 and 20 alike.)  attn_fwd_kv_fp8 counts pieces alone.
-constexpr int kCacheUnitCost = 12;
 size_t cache_decode_workspace_bytes(int rows, int d, int sms);
 // Joins what the main kernel's ctas CTAs left of units cut between them, a dependent launch.
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s);
