@@ -978,7 +978,6 @@ int attn_rope_kv_append_fp8(const void* q, void* q_out, const void* k, const voi
     r.cu = cu_seqlens;
     r.kv_lens = kv_lens;
     r.seqs = B;
-    r.beside = 1;
   }
   const DevSyms* s = dev_syms(nullptr);
   if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");

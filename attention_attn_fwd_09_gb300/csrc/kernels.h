@@ -185,10 +185,11 @@ struct RopeParams {
   int B, N, Hq, Hk, d, rot;
   float mscale, sign;        // factor on the rotated part; +1 forward, -1 transposed
   int tile_shift, tiles, head_group;   // filled in by launch_rope: log2(tokens per CTA), tiles per sequence, heads per CTA
-  // Packed rows (B = 1) that end their sequences, where positions is null: offsets [seqs + 1], lengths [seqs].
+  // Not null: packed rows (B = 1; d = 64 or 128) that end their sequences, which gives their positions where
+  // positions is null (offsets [seqs + 1], lengths [seqs]); the launch runs beside the kernel before it in the
+  // stream, which calls pdl_trigger and whose outputs it does not touch.
   const int *cu, *kv_lens;
   int seqs;
-  int beside;                // 1: runs beside the kernel launched before it, which calls pdl_trigger; d = 64 or 128
 };
 // vec: elements per access (8, 4 or 1) that every pointer, stride and rot allow.
 cudaError_t launch_rope(RopeParams p, int vec, int interleaved, int sms, cudaStream_t s);

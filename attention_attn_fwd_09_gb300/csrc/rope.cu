@@ -99,7 +99,8 @@ __device__ __forceinline__ BfVec<V> pack(const float (&f)[V]) {
 // partners at + rot/2, interleaved columns c .. c+2V-1, or 2 V columns of the part that
 // passes through.  V = 8 needs rot % 16 == 0 and 16-byte rows, V = 4 rot % 8 == 0 and 8-byte
 // rows; V = 1 takes every even rot and alignment.
-template <int V, bool INTER, int D>
+// PACKED: packed rows that end their sequences, beside the kernel launched before (RopeParams).
+template <int V, bool INTER, int D, bool PACKED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   extern __shared__ __align__(16) float2 cs[];                       // [tokens][rot / 2] (m cos, m sin)
   constexpr int UPR = D / (2 * V);                     // items per head row
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       __syncthreads();
       for (int i = threadIdx.x; i < tn * half; i += kRopeThreads) {
         const int n = i / half, j = i - n * half;
-        const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : p.cu ? packed_position(p, n0 + n) : n0 + n;
+        const long long pos = p.positions ? p.positions[(long long)b * p.N + n0 + n] : PACKED ? packed_position(p, n0 + n) : n0 + n;
         float s, c;
         turn_sincos(turn[j], pos, s, c);
         // Pairs 2k, 2k + 1 of all items of a row lie side by side: neighbouring threads' 16-byte reads then
@@ -195,18 +196,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     }
   }
   // Started beside the kernel before it in the stream (rope_append.cu): done only when that one is.
-  if (p.beside) pdl_wait();
+  if constexpr (PACKED) pdl_wait();
 }
 
 template <int V, bool INTER>
 cudaError_t launch_v(const RopeParams& p, dim3 grid, size_t smem, cudaStream_t s) {
-  if (p.beside)                              // (the cache's head dims)
-    return p.d == 64 ? launch_pdl(rope_kernel<V, INTER, 64>, grid, dim3(kRopeThreads), smem, s, p)
-                     : launch_pdl(rope_kernel<V, INTER, 128>, grid, dim3(kRopeThreads), smem, s, p);
-  if (p.d == 64) rope_kernel<V, INTER, 64><<<grid, kRopeThreads, smem, s>>>(p);
-  else if (p.d == 128) rope_kernel<V, INTER, 128><<<grid, kRopeThreads, smem, s>>>(p);
-  else if (p.d == 192) rope_kernel<V, INTER, 192><<<grid, kRopeThreads, smem, s>>>(p);
-  else rope_kernel<V, INTER, 256><<<grid, kRopeThreads, smem, s>>>(p);
+  if (p.cu)                                  // (the cache's head dims)
+    return p.d == 64 ? launch_pdl(rope_kernel<V, INTER, 64, true>, grid, dim3(kRopeThreads), smem, s, p)
+                     : launch_pdl(rope_kernel<V, INTER, 128, true>, grid, dim3(kRopeThreads), smem, s, p);
+  if (p.d == 64) rope_kernel<V, INTER, 64, false><<<grid, kRopeThreads, smem, s>>>(p);
+  else if (p.d == 128) rope_kernel<V, INTER, 128, false><<<grid, kRopeThreads, smem, s>>>(p);
+  else if (p.d == 192) rope_kernel<V, INTER, 192, false><<<grid, kRopeThreads, smem, s>>>(p);
+  else rope_kernel<V, INTER, 256, false><<<grid, kRopeThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
