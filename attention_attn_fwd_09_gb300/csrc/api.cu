@@ -1217,16 +1217,21 @@ int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cach
   return post_launch(s, st);
 }
 
-// Both parts' workspace, used one after the other, then the first part's results and whether it was valid.
+// The parts' workspace for partial results (used one after the other, or by one launch), then the parts' results and
+// whether their offsets were valid.
 struct PrefixWs {
-  size_t lse, o, bad, total;
+  size_t lse[2], o[2], bad, total;
 };
 static PrefixWs prefix_ws(int Hq, int Hkv, int total_q, int max_prefix_q, int max_q, int d, int sms) {
   PrefixWs w;
   const auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  w.lse = up(std::max(cache_workspace_bytes(Hq, Hkv, max_prefix_q, d, sms), cache_workspace_bytes(Hq, Hkv, max_q, d, sms)));
-  w.o = w.lse + up((size_t)Hq * total_q * 4);
-  w.bad = w.o + up((size_t)Hq * total_q * d * 4);
+  size_t at = up(std::max(cache_workspace_bytes(Hq, Hkv, max_prefix_q, d, sms), cache_workspace_bytes(Hq, Hkv, max_q, d, sms)));
+  for (int i = 0; i < 2; ++i) {
+    w.lse[i] = at;
+    w.o[i] = w.lse[i] + up((size_t)Hq * total_q * 4);
+    at = w.o[i] + up((size_t)Hq * total_q * d * 4);
+  }
+  w.bad = at;
   w.total = w.bad + 256;
   return w;
 }
@@ -1263,15 +1268,28 @@ int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cac
   if (s->err != cudaSuccess) return cuda_fail(s->err, "device setup");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CacheParams p[2] = {cache_params(shared, max_prefix_q, workspace, s), cache_params(mine, max_q, workspace, s)};
-  CacheMaps maps[2];
+  char* ws = static_cast<char*>(workspace);
   for (int i = 0; i < 2; ++i) {
+    for (int k = 0; k < 2; ++k) {
+      p[i].side_lse[k] = reinterpret_cast<float*>(ws + w.lse[k]);
+      p[i].side_o[k] = reinterpret_cast<float*>(ws + w.o[k]);
+    }
+    p[i].side_bad = reinterpret_cast<int*>(ws + w.bad);
     p[i].side = i == 0 ? SIDE_OUT : SIDE_IN;
-    p[i].side_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.lse);
-    p[i].side_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.o);
-    p[i].side_bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.bad);
-    if (i == 1 && few_rows(p[0]) == few_rows(p[1])) maps[1] = maps[0];       // (of the same cache)
-    else if ((rc = cache_maps(mine, few_rows(p[i]), &maps[i])) != ATTN_OK) return rc;
   }
+  CacheMaps maps[2];
+  if ((rc = cache_maps(mine, few_rows(p[0]), &maps[0])) != ATTN_OK) return rc;
+  if (few_rows(p[0]) == few_rows(p[1])) {
+    // The same kernel for both parts: one launch of it and one that joins them (a prefix of 5000 and one of 16001 keys
+    // before 24 pieces of up to 60 queries, 16 heads on 2, d = 64: XX us against 85 one after the other).
+    p[0].side = SIDE_BOTH;
+    p[0].two = {page_table, cu_seqlens_q, kv_lens, B, max_q, max_pages, max_pages * page_size, causal ? 1 : 0};
+    if ((rc = launch_cache(maps[0], p[0], d, sms, st)) != ATTN_OK) return rc;
+    const cudaError_t e = launch_fwd_cache_join(p[0], d, st);
+    if (e != cudaSuccess) return cuda_fail(e, "join launch");
+    return post_launch(s, st);
+  }
+  if ((rc = cache_maps(mine, few_rows(p[1]), &maps[1])) != ATTN_OK) return rc;
   for (int i = 0; i < 2; ++i)
     if ((rc = launch_cache(maps[i], p[i], d, sms, st)) != ATTN_OK) return rc;
   return post_launch(s, st);

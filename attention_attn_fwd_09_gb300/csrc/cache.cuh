@@ -78,22 +78,45 @@ __device__ __forceinline__ void take_nan_codes(uint8_t* piece, int key, int* fir
 }
 constexpr int kNoKey = 0x7fffffff;
 
-// Keys in two parts: where row r of the unit at packed query q0 of K/V head h lies (side_lse; side_o: its piece of 4
-// columns i).  Rows of a unit lie side by side, as the threads that have them.
+// A sequence of either part: sequences of the second are counted behind those of the first.
+struct PartSeq {
+  const int *cu, *lens, *table;              // of its part
+  int b, B, max_q, max_pages, max_len, causal, part;
+  __device__ __forceinline__ PartSeq(const CacheParams& p, int i) {
+    part = i >= p.B ? 1 : 0;
+    if (part) {
+      cu = p.two.cu_q; lens = p.two.kv_lens; table = p.two.table;
+      b = i - p.B; B = p.two.B; max_q = p.two.max_q; max_pages = p.two.max_pages; max_len = p.two.max_len; causal = p.two.causal;
+    } else {
+      cu = p.cu_q; lens = p.kv_lens; table = p.table;
+      b = i; B = p.B; max_q = p.max_q; max_pages = p.max_pages; max_len = p.max_len; causal = p.causal;
+    }
+  }
+  __device__ __forceinline__ bool wrong(const CacheParams& p, int q0, int n, int len) const {
+    const int c1 = q0 + n;
+    return q0 < 0 || n < 0 || c1 < 0 || n > max_q || len < 0 || len > max_len || (causal && n > len) || (b == 0 && q0 != 0) ||
+           (b == B - 1 && c1 != p.total_q);
+  }
+};
+// Where row r of the unit at packed query q0 of K/V head h lies (side_lse; side_o: its piece of 4 columns i).  Rows of a
+// unit lie side by side, as the threads that have them.
 __device__ __forceinline__ long long side_row(const CacheParams& p, int h, int q0, int r) {
   return ((long long)h * p.total_q + q0) * p.g + r;
 }
 template <int D>
-__device__ __forceinline__ float4* side_piece(const CacheParams& p, int h, int q0, int r, int i) {
-  return reinterpret_cast<float4*>(p.side_o) + ((long long)h * (D / 4) + i) * p.total_q * p.g + (long long)q0 * p.g + r;
+__device__ __forceinline__ float4* side_piece(const CacheParams& p, int part, int h, int q0, int r, int i) {
+  return reinterpret_cast<float4*>(p.side_o[part]) + ((long long)h * (D / 4) + i) * p.total_q * p.g + (long long)q0 * p.g + r;
 }
 // A row's O is x own O + y O of the first part, lse2 (log2) of all keys goes to `joint`.
 // 0 and -inf where neither part has a key.
-__device__ __forceinline__ float2 join_side(const CacheParams& p, long long row, float lse2, float& joint) {
-  const float other = p.side_lse[row], mx = fmaxf(lse2, other), mu = mx == -INFINITY ? 0.f : mx;
+__device__ __forceinline__ float2 join_two(float lse2, float other, float& joint) {
+  const float mx = fmaxf(lse2, other), mu = mx == -INFINITY ? 0.f : mx;
   const float a = ex2_mufu(lse2 - mu), b = ex2_mufu(other - mu), sum = a + b, inv = sum == 0.f ? 0.f : 1.f / sum;
   joint = mx + __log2f(sum);
   return make_float2(a * inv, b * inv);
+}
+__device__ __forceinline__ float2 join_side(const CacheParams& p, long long row, float lse2, float& joint) {
+  return join_two(lse2, p.side_lse[0][row], joint);
 }
 
 // How long a CTA that gives up waits for its own copies and products in flight: not less than 10 ms,

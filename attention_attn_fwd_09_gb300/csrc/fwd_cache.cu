@@ -72,9 +72,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// What the kernel works on: sequences; queries with lists of pages (p.list); sequences whose keys come in two parts
+// (p.side).  The latter two count what starting and ending a unit costs when they cut the work.
+enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };
+
+template <int KIND>
 __device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {
-  const int n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
-  return n > 0 ? max(1, (__ldg(p.kv_lens + b) + kPiece - 1) / kPiece) : 0;
+  int n, len;
+  if constexpr (KIND == KIND_SIDE) {
+    const PartSeq s(p, b);
+    n = __ldg(s.cu + s.b + 1) - __ldg(s.cu + s.b);
+    len = __ldg(s.lens + s.b);
+  } else {
+    n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b);
+    len = __ldg(p.kv_lens + b);
+  }
+  return n > 0 ? max(1, (len + kPiece - 1) / kPiece) : 0;
 }
 
 // LIST: a unit is one query and K/V head with a list of pages of its own, laid end to end in pieces.
@@ -102,10 +115,6 @@ __device__ __forceinline__ int list_pieces(const CacheParams& p, int seen) {
   return max(1, (min(seen, p.list_count) * p.page + kPiece - 1) / kPiece);
 }
 
-// What the kernel works on: sequences; queries with lists of pages (p.list); sequences whose keys come in two parts
-// (p.side).  The latter two count what starting and ending a unit costs when they cut the work.
-enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };
-
 // Where a warp is in the CTA's run of pieces.  Positions count pieces and, before each unit's, `cost` places
 // for starting and ending it, which nobody fills (KIND_PLAIN: none).
 template <int KIND>
@@ -131,12 +140,12 @@ struct Cursor {
           uend = ubeg + list_pieces(p, seen);
         } else {
           int np;
-          do np = pieces_of(p, ++b);
+          do np = pieces_of<KIND>(p, ++b);
           while (np == 0);
           uend = ubeg + np;
         }
       } else {
-        uend = ubeg + (LIST ? list_pieces(p, seen) : pieces_of(p, b));
+        uend = ubeg + (LIST ? list_pieces(p, seen) : pieces_of<KIND>(p, b));
       }
     }
   }
@@ -175,12 +184,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait();                                // nothing of global memory before this
   pdl_trigger();
   // ---- the run of pieces of this CTA; thread t adds up sequences [t per_thread, ...)
-  const int per_thread = (p.B + kThreads - 1) / kThreads;
-  const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
+  const int seqs = SIDE && p.side == SIDE_BOTH ? p.B + p.two.B : p.B;
+  const int per_thread = (seqs + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * per_thread, seqs), b_hi = min(b_lo + per_thread, seqs);
   long long mine = 0;
   int units = 0;                             // (per K/V head)
   bool wrong = false;
   for (int b = b_lo; b < b_hi; ++b) {
+    if constexpr (SIDE) {
+      const PartSeq s(p, b);
+      const int c0 = __ldg(s.cu + s.b), n = __ldg(s.cu + s.b + 1) - c0, len = __ldg(s.lens + s.b);
+      wrong |= s.wrong(p, c0, n, len);
+      if (n > 0) {
+        mine += max(1, (len + kPiece - 1) / kPiece);
+        ++units;
+      }
+      continue;
+    }
     const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_lens + b), n = c1 - c0;
     wrong |= c0 < 0 || c1 < c0 || n > p.max_q || len < 0 || len > p.max_len || (p.causal && n > len) ||
              (b == 0 && c0 != 0) || (b == p.B - 1 && c1 != p.total_q);
@@ -228,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
-    if (SIDE && p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
+    if (SIDE && p.side != SIDE_IN && blockIdx.x == 0) *p.side_bad = bad;
   }
   if (bad || (SIDE && p.side == SIDE_IN && *p.side_bad)) return;
   long long before = incl - mine, total = 0;
@@ -252,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (LIST) {
         while (t >= __ldg(p.cu_q + b + 1)) ++b;
       }
-      const int np = LIST ? list_pieces(p, pages_seen(p, b, t)) : pieces_of(p, b);
+      const int np = LIST ? list_pieces(p, pages_seen(p, b, t)) : pieces_of<KIND>(p, b);
       const long long step = np > 0 ? (long long)(np + cost) * p.Hkv : 0;
       if (rs < at + step) break;
       at += step;
@@ -273,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     seg.seen = pages_seen(p, seg.b, seg.t);
   }
   {
-    const int np = LIST ? list_pieces(p, seg.seen) : pieces_of(p, seg.b);
+    const int np = LIST ? list_pieces(p, seg.seen) : pieces_of<KIND>(p, seg.b);
     seg.h = (int)((rs - misc[1]) / (np + cost));
     seg.ubeg = misc[1] + (long long)seg.h * (np + cost) + cost;
     seg.uend = seg.ubeg + np;
@@ -305,10 +325,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         return -2;
       }
       key = key_ahead = (lp << page_shift) + (key & (p.page - 1));
+    } else if constexpr (SIDE) {
+      if (key >= __ldg(PartSeq(p, ahead.b).lens + PartSeq(p, ahead.b).b)) return -1;
     } else {
       if (key >= __ldg(p.kv_lens + ahead.b)) return -1;
     }
-    const int pg = __ldg(p.table + (long long)ahead.b * p.max_pages + (key >> page_shift));
+    const int* table = p.table + (long long)ahead.b * p.max_pages;
+    if constexpr (SIDE) table = PartSeq(p, ahead.b).table + (long long)PartSeq(p, ahead.b).b * PartSeq(p, ahead.b).max_pages;
+    const int pg = __ldg(table + (key >> page_shift));
     if (pg < 0 || pg >= p.num_pages) {
       atomicExch(p.status, DEV_BAD_PAGE);
       return -2;
@@ -382,8 +406,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = p.g;
   // ---- units
   while (seg.f < re) {
-    const int q0 = LIST ? seg.t : __ldg(p.cu_q + seg.b), n = LIST ? 1 : __ldg(p.cu_q + seg.b + 1) - q0;
-    const int len = LIST ? keys_seen(p, seg.b, seg.t) : __ldg(p.kv_lens + seg.b);
+    int q0, n, len, causal = p.causal;
+    if constexpr (SIDE) {
+      const PartSeq s(p, seg.b);
+      q0 = __ldg(s.cu + s.b);
+      n = __ldg(s.cu + s.b + 1) - q0;
+      len = __ldg(s.lens + s.b);
+      causal = s.causal;
+    } else {
+      q0 = LIST ? seg.t : __ldg(p.cu_q + seg.b);
+      n = LIST ? 1 : __ldg(p.cu_q + seg.b + 1) - q0;
+      len = LIST ? keys_seen(p, seg.b, seg.t) : __ldg(p.kv_lens + seg.b);
+    }
+    const int part_of_keys = SIDE && seg.b >= p.B ? 1 : 0;
     if (LIST && seg.f == seg.ubeg) {         // entries behind as many as the query sees pages are not read: none counts
       const int* entries = p.list + ((long long)kv_head(seg.h) * p.total_q + seg.t) * p.list_count;
       for (int e = seg.seen + tid; e < p.list_count; e += kThreads)
@@ -398,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = rq + 8 * i, qi = r / g;
-      lim[i] = p.causal && r < rows ? len - n + qi + 1 : len;
+      lim[i] = causal && r < rows ? len - n + qi + 1 : len;
       uint4 w[D / 32];
       float amax = 0.f;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) +
@@ -431,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    const int min_lim = p.causal ? len - n + 1 : len;
+    const int min_lim = causal ? len - n + 1 : len;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, rref = kMinScale, rinv = 1.f / kMinScale;
     float o[C::NACC][4];
 #pragma unroll
@@ -695,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // First unit of the CTA: partial 0, its last one: partial 1.
       const int second = seg.ubeg > rs ? 1 : 0, part = 2 * blockIdx.x + second;
       if (seg.ubeg >= rs && !whole && lane == 0)
-        *rec = make_int4(seg.h, q0, n, 2 * ((int)((seg.uend - 1) / run) - (int)blockIdx.x) + second);
+        *rec = make_int4(seg.h | part_of_keys << 30, q0, n, 2 * ((int)((seg.uend - 1) / run) - (int)blockIdx.x) + second);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = rq + 8 * i, qi = r / g;
@@ -707,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const long long row = (long long)(seg.h * g + (r - qi * g)) * p.total_q + q0 + qi;
           if constexpr (SIDE) {              // columns 8 k .. 8 k + 7 of each half: two pieces of 4
             const long long pieces = (long long)p.total_q * g;     // from one piece of the row to the next
-            float4* side = side_piece<D>(p, seg.h, q0, r, c * (D / 16));
+            float4* side = side_piece<D>(p, part_of_keys, seg.h, q0, r, c * (D / 16));
             float2 w = make_float2(1.f, 0.f);
             if (p.side == SIDE_IN) w = join_side(p, side_row(p, seg.h, q0, r), lse2, lse2);
             inv *= w.x;
@@ -718,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float4 y = make_float4(o[4 * k][2 * i + e] * inv, o[4 * k + 1][2 * i + e] * inv, o[4 * k + 2][2 * i + e] * inv,
                                        o[4 * k + 3][2 * i + e] * inv);
                 float4* at = side + (e * (C::NACC / 4) + k) * pieces;
-                if (p.side == SIDE_OUT) {
+                if (p.side != SIDE_IN) {
                   *at = y;
                   continue;
                 }
@@ -728,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 o[4 * k + 2][2 * i + e] = y.z + w.y * x.z;
                 o[4 * k + 3][2 * i + e] = y.w + w.y * x.w;
               }
-            if (p.side == SIDE_OUT) {
-              if (c == 0) p.side_lse[side_row(p, seg.h, q0, r)] = lse2;
+            if (p.side != SIDE_IN) {
+              if (c == 0) p.side_lse[part_of_keys][side_row(p, seg.h, q0, r)] = lse2;
               continue;
             }
             inv = 1.f;
@@ -811,7 +846,9 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     const int qi = r / p.g;
     const float4* stat = reinterpret_cast<const float4*>(ws + W.stat) + r;
     const float4* part = reinterpret_cast<const float4*>(ws + W.part) + (long long)cg * CPT * rows_max + r;
-    const int4 rec = recs[cta];
+    int4 rec = recs[cta];
+    const int part_of_keys = SIDE ? rec.x >> 30 : 0;
+    if (SIDE) rec.x &= (1 << 30) - 1;
     if (rec.w < 2 || qi >= rec.z || cg >= GROUPS) continue;
     const int first = 2 * cta + (rec.w & 1), more = rec.w >> 1;
     // The unit's partials: the first CTA's, then partial 0 of each CTA behind it.
@@ -860,22 +897,22 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     float inv = l == 0.f ? 0.f : ref / l, lse2 = m + __log2f(l);
     if constexpr (SIDE) {
       const long long pieces = (long long)p.total_q * p.g;         // from one piece of the row to the next
-      float4* side = side_piece<D>(p, rec.x, rec.y, r, cg * CPT);
+      float4* side = side_piece<D>(p, part_of_keys, rec.x, rec.y, r, cg * CPT);
       float2 w = make_float2(1.f, 0.f);
       if (p.side == SIDE_IN) w = join_side(p, side_row(p, rec.x, rec.y, r), lse2, lse2);
       inv *= w.x;
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
         o[c] = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
-        if (p.side == SIDE_OUT) {
+        if (p.side != SIDE_IN) {
           side[c * pieces] = o[c];
           continue;
         }
         const float4 x = side[c * pieces];
         o[c] = make_float4(o[c].x + w.y * x.x, o[c].y + w.y * x.y, o[c].z + w.y * x.z, o[c].w + w.y * x.w);
       }
-      if (p.side == SIDE_OUT) {
-        if (cg == 0) p.side_lse[side_row(p, rec.x, rec.y, r)] = lse2;
+      if (p.side != SIDE_IN) {
+        if (cg == 0) p.side_lse[part_of_keys][side_row(p, rec.x, rec.y, r)] = lse2;
         continue;
       }
       inv = 1.f;
@@ -891,6 +928,30 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const CacheParams 
     else *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
     if (cg == 0) p.lse[row] = lse2 * kLn2;
   }
+}
+
+// Both parts of each row joined.  Block: 256 rows of a K/V head and two pieces of 4 columns, a row per thread, so that
+// neighbours read side by side.
+template <int D>
+__global__ void __launch_bounds__(256) fwd_cache_join_kernel(const CacheParams p, const int chunks) {
+  pdl_wait();
+  pdl_trigger();
+  if (*p.side_bad) return;
+  const long long rows = (long long)p.total_q * p.g;
+  const int u = blockIdx.x / chunks, h = u / (D / 8), pair = u - h * (D / 8);
+  const long long r = (long long)(blockIdx.x - u * chunks) * 256 + threadIdx.x;
+  if (r >= rows) return;
+  const long long at = 2LL * u * rows + r;             // piece h D / 4 + 2 pair
+  const float4* a = reinterpret_cast<const float4*>(p.side_o[0]) + at;
+  const float4* b = reinterpret_cast<const float4*>(p.side_o[1]) + at;
+  const float4 a0 = a[0], a1 = a[rows], b0 = b[0], b1 = b[rows];
+  float joint;
+  const float2 w = join_two(p.side_lse[1][h * rows + r], p.side_lse[0][h * rows + r], joint);
+  const long long t = r / p.g, row = ((long long)h * p.g + (r - t * p.g)) * p.total_q + t;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + pair * 8) = make_uint4(
+      pack_bf16x2(b0.x * w.x + a0.x * w.y, b0.y * w.x + a0.y * w.y), pack_bf16x2(b0.z * w.x + a0.z * w.y, b0.w * w.x + a0.w * w.y),
+      pack_bf16x2(b1.x * w.x + a1.x * w.y, b1.y * w.x + a1.y * w.y), pack_bf16x2(b1.z * w.x + a1.z * w.y, b1.w * w.x + a1.w * w.y));
+  if (pair == 0) p.lse[row] = joint * kLn2;
 }
 
 template <int D, int KIND>
@@ -915,14 +976,15 @@ cudaError_t launch_decode(const CacheMaps& maps, const CacheParams& p, int rows,
 
 cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ctas, cudaStream_t s) {
   int shift = 0;
-  while ((1 << shift) < rows && (1 << shift) < (long long)p.max_q * p.g) ++shift;     // rows in use
+  const int max_q = p.side == SIDE_BOTH && p.two.max_q > p.max_q ? p.two.max_q : p.max_q;
+  while ((1 << shift) < rows && (1 << shift) < (long long)max_q * p.g) ++shift;       // rows in use
   auto go = [&](auto kernel, int cpt, bool compact) {
     const int shares = (((d / 4 / cpt) << shift) + 127) / 128;
     const int blocks = compact ? 4 * kSMs : ctas * shares;
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(128), 0, s, p, rows, shift, ctas);
   };
   // Few units of many partials each: latency again (a sequence of 30000 keys, 32 rows: 33 us against 35).
-  const long long units = (long long)p.B * p.Hkv * (((long long)p.max_q * p.g + rows - 1) / rows);
+  const long long units = ((long long)p.B + (p.side == SIDE_BOTH ? p.two.B : 0)) * p.Hkv * (((long long)max_q * p.g + rows - 1) / rows);
   auto pick = [&](auto dim, auto side) {
     constexpr int D = dim;
     constexpr bool S = side;
@@ -938,10 +1000,19 @@ cudaError_t launch_fwd_cache_merge(const CacheParams& p, int d, int rows, int ct
   return d == 64 ? pick(I64(), std::false_type()) : pick(I128(), std::false_type());
 }
 
+cudaError_t launch_fwd_cache_join(const CacheParams& p, int d, cudaStream_t s) {
+  const long long chunks = ((long long)p.total_q * p.g + 255) / 256, blocks = chunks * p.Hkv * (d / 8);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)blocks);
+  return d == 64 ? launch_pdl(fwd_cache_join_kernel<64>, grid, dim3(256), 0, s, p, (int)chunks)
+                 : launch_pdl(fwd_cache_join_kernel<128>, grid, dim3(256), 0, s, p, (int)chunks);
+}
+
 size_t cache_decode_workspace_bytes(int rows, int d, int sms) { return cache_ws(2 * sms, rows, d).total; }
 
 cudaError_t launch_fwd_cache_decode(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s) {
-  const int rows = p.max_q * p.g, grid = 2 * sms;      // as in the workspace's size
+  const int max_q = p.side == SIDE_BOTH && p.two.max_q > p.max_q ? p.two.max_q : p.max_q;
+  const int rows = max_q * p.g, grid = 2 * sms;        // as in the workspace's size
   if (p.side != SIDE_NONE)
     return d == 64 ? launch_decode<64, KIND_SIDE>(maps, p, rows, grid, s) : launch_decode<128, KIND_SIDE>(maps, p, rows, grid, s);
   return d == 64 ? launch_decode<64, KIND_PLAIN>(maps, p, rows, grid, s) : launch_decode<128, KIND_PLAIN>(maps, p, rows, grid, s);

@@ -135,22 +135,33 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 // A sequence: its units per K/V head and their blocks of 128 keys.  Unit rt holds queries rt qu ..
 // rt qu + qu - 1, qu = 256 / g.  Work is counted in steps: a unit's blocks and `cost` steps before
 // them (CTAs with many short units took 1.4 times as long when blocks alone were counted).
+// SIDE: sequences of either part.
+template <bool SIDE>
 struct TileSeq {
-  int q0, n, len, units;
+  int q0, n, len, units, causal;
   __device__ __forceinline__ TileSeq(const CacheParams& p, int b, int qu) {
-    q0 = __ldg(p.cu_q + b);
-    n = __ldg(p.cu_q + b + 1) - q0;
-    len = __ldg(p.kv_lens + b);
+    if constexpr (SIDE) {
+      const PartSeq s(p, b);
+      q0 = __ldg(s.cu + s.b);
+      n = __ldg(s.cu + s.b + 1) - q0;
+      len = __ldg(s.lens + s.b);
+      causal = s.causal;
+    } else {
+      q0 = __ldg(p.cu_q + b);
+      n = __ldg(p.cu_q + b + 1) - q0;
+      len = __ldg(p.kv_lens + b);
+      causal = p.causal;
+    }
     units = (int)(((unsigned)max(n, 0) + qu - 1) / qu);
   }
   __device__ __forceinline__ int blocks(const CacheParams& p, int qu, int rt) const {
-    const int lim = p.causal ? len - n + min(n, (rt + 1) * qu) : len;
+    const int lim = causal ? len - n + min(n, (rt + 1) * qu) : len;
     return (max(lim, 1) + 127) / 128;
   }
   // Blocks of the units before rt (a unit without keys counts as one).
   __device__ __forceinline__ long long blocks_before(const CacheParams& p, int qu, int rt) const {
     if (rt <= 0) return 0;
-    if (!p.causal) return (long long)rt * ((max(len, 1) + 127) / 128);
+    if (!causal) return (long long)rt * ((max(len, 1) + 127) / 128);
     if (rt < units) return floor_sum(rt, 128, qu, (uint32_t)(len - n) + qu + 127);
     return floor_sum(units - 1, 128, qu, (uint32_t)(len - n) + qu + 127) + (len + 127) / 128;
   }
@@ -169,7 +180,7 @@ struct __align__(16) UnitDesc {
   int whole;                                 // the unit is this CTA's alone
   int second;                                // partial 1 of the CTA, else partial 0
   int more;                                  // CTAs behind this one that go on with it, if it starts here (else -1)
-  int pad[3];
+  int causal, part, pad;                     // SIDE: of the sequence's part
 };
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
@@ -276,14 +287,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
   pdl_wait();                                // nothing of global memory before this
   pdl_trigger();
   // ---- the run of steps of this CTA; thread t adds up sequences [t per_thread, ...)
-  const int per_thread = (p.B + kTThreads - 1) / kTThreads;
-  const int b_lo = min(tid * per_thread, p.B), b_hi = min(b_lo + per_thread, p.B);
+  const int seqs = SIDE && p.side == SIDE_BOTH ? p.B + p.two.B : p.B;
+  const int per_thread = (seqs + kTThreads - 1) / kTThreads;
+  const int b_lo = min(tid * per_thread, seqs), b_hi = min(b_lo + per_thread, seqs);
   long long blocks = 0, units = 0;
   bool wrong = false;
   for (int b = b_lo; b < b_hi; ++b) {
-    const TileSeq s(p, b, qu);
+    const TileSeq<SIDE> s(p, b, qu);
     const int c1 = s.q0 + s.n;
-    const bool w = s.q0 < 0 || s.n < 0 || c1 < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_len ||
+    const bool w = SIDE ? PartSeq(p, b).wrong(p, s.q0, s.n, s.len) : s.q0 < 0 || s.n < 0 || c1 < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_len ||
                    (p.causal && s.n > s.len) || (b == 0 && s.q0 != 0) || (b == p.B - 1 && c1 != p.total_q);
     wrong |= w;
     if (!w) {
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (tid == 0) {
     *rec = make_int4(0, 0, 0, 0);            // no unit cut, unless found below
     if (bad) atomicExch(p.status, DEV_BAD_OFFSETS);
-    if (SIDE && p.side == SIDE_OUT && blockIdx.x == 0) *p.side_bad = bad;
+    if (SIDE && p.side != SIDE_IN && blockIdx.x == 0) *p.side_bad = bad;
   }
   if (bad || (SIDE && p.side == SIDE_IN && *p.side_bad)) return;
   blocks_to -= blocks;
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     int b = b_lo;
     long long at = before;
     for (;;) {
-      const TileSeq s(p, b, qu);
+      const TileSeq<SIDE> s(p, b, qu);
       auto steps_before = [&](int rt) -> long long { return s.blocks_before(p, qu, rt) + (long long)rt * cost; };
       const long long per_head = steps_before(s.units);
       if (rs < at + per_head * p.Hkv) {
@@ -365,6 +377,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int page_shift = 31 - __clz(p.page);
+  auto table_of = [&](const UnitDesc& U) -> const int* {
+    if constexpr (SIDE) {
+      const PartSeq s(p, U.b);
+      return s.table + (long long)s.b * s.max_pages;
+    } else {
+      return p.table + (long long)U.b * p.max_pages;
+    }
+  };
   // The roles' view of unit u: wait for its descriptor, and hand it back (one lane per warp).
   auto unit_ready = [&](uint32_t u) -> bool { return mbar_wait(BAR(T_UFULL + u % kUnitSlots), (u / kUnitSlots) & 1, wc); };
   // Release barrier of a product group, and its phase.
@@ -388,7 +408,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
         const UnitDesc& U = desc[nu % kUnitSlots];
         const int nmax = U.nmax, key0 = U.kt0 * 128 + lane * box_keys, len = U.len, h = U.h;
-        const int* table = p.table + (long long)U.b * p.max_pages;
+        const int* table = table_of(U);
         __syncwarp();
         if (lane == 0) unit_done(nu);
         if (nmax < 0) break;
@@ -534,7 +554,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (lane == 0) {
         int b = (int)misc[0], h = (int)misc[1], rt = (int)misc[2], ubeg = (int)(misc[3] - rs);
         const int end = (int)(re - rs), step_run = (int)run;
-        TileSeq sq(p, b, qu);
+        TileSeq<SIDE> sq(p, b, qu);
         bool first = true;
         for (uint32_t nu = 0;;) {
           const int uend = ubeg + cost + sq.blocks(p, qu, rt);
@@ -554,7 +574,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int r = min(rows, (t + 1) * 128) - t * 128;           // rows of the tile
-              const int lim = r > 0 ? (p.causal ? sq.len - sq.n + rt * qu + (t * 128 + r - 1) / p.g + 1 : sq.len) : 0;
+              const int lim = r > 0 ? (sq.causal ? sq.len - sq.n + rt * qu + (t * 128 + r - 1) / p.g + 1 : sq.len) : 0;
               nt[t] = max(0, min((lim + 127) / 128, kt1) - kt0);
             }
             U.nmax = max(nt[0], nt[1]);
@@ -566,7 +586,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
             U.h = h;
             U.rows = rows;
             U.q0 = sq.q0 + rt * qu;
-            U.lim0 = p.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
+            U.lim0 = sq.causal ? sq.len - sq.n + rt * qu + 1 : sq.len;
+            if constexpr (SIDE) {
+              U.causal = sq.causal;
+              U.part = b >= p.B ? 1 : 0;
+            }
             U.whole = kt0 == 0 && uend <= end ? 1 : 0;
             U.second = first ? 0 : 1;
             U.more = kt0 == 0 ? (uend - 1) / step_run : -1;   // cut: the CTAs behind this one that go on with it
@@ -580,7 +604,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             rt = 0;
             if (++h == p.Hkv) {
               h = 0;
-              do sq = TileSeq(p, ++b, qu);   // steps are left: there is another unit
+              do sq = TileSeq<SIDE>(p, ++b, qu);   // steps are left: there is another unit
               while (sq.units == 0);
             }
           }
@@ -603,9 +627,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int n_t = U.nt[t], kt0 = U.kt0 + (SPLIT ? t : 0), len = U.len, h = U.h, q0 = U.q0;
       const int n_other = SPLIT ? U.nt[1] : 0;
       const bool more = U.nmax >= 0, live = r < U.rows;
-      const int* table = p.table + (long long)U.b * p.max_pages;
-      const int lim = (p.causal && live ? U.lim0 + qi : len) - kt0 * 128;                       // visible keys of this row,
-      const int min_lim = (p.causal ? U.lim0 + row0 / p.g : len) - kt0 * 128;                // of the tile's first row
+      const int* table = table_of(U);
+      const bool causal = SIDE ? U.causal != 0 : p.causal != 0;
+      const int lim = (causal && live ? U.lim0 + qi : len) - kt0 * 128;                       // visible keys of this row,
+      const int min_lim = (causal ? U.lim0 + row0 / p.g : len) - kt0 * 128;                // of the tile's first row
       __syncwarp();
       if (lane == 0) unit_done(nu);
       if (!more) break;
@@ -804,7 +829,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (!__all_sync(0xffffffffu, unit_ready(nu))) { ok = false; break; }
       const UnitDesc& U = desc[nu % kUnitSlots];
       const int nmax = U.nmax, nt0 = U.nt[0], nt1 = U.nt[1], kt0 = U.kt0, len = U.len, h = U.h;
-      const int* table = p.table + (long long)U.b * p.max_pages;
+      const int* table = table_of(U);
+      const int part_of_keys = SIDE ? U.part : 0;
       if (nmax < 0) break;                   // the last descriptor is not reused
       float rref = kMinScale;                // largest V scale so far
       float rref_other = kMinScale;          // SPLIT: of the other tile's blocks (they take turns)
@@ -904,7 +930,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // Epilogue per tile: O / l to its rows, or O and the statistics to the workspace.
       const bool whole = U.whole != 0;
       const int part = 2 * blockIdx.x + U.second, rows = U.rows, q0 = U.q0;
-      if (U.more > 0 && !whole && ct == 0) *rec = make_int4(h, q0, rows / p.g, 2 * U.more + U.second);
+      if (U.more > 0 && !whole && ct == 0) *rec = make_int4(h | part_of_keys << 30, q0, rows / p.g, 2 * U.more + U.second);
       // Every product of both tiles is complete: O is final and V16 is free.
       if (nt0 > 0 && !warp_wait(BAR(T_OFULL), nof0++ & 1, wc)) { ok = false; break; }
       if (nt1 > 0 && !warp_wait(BAR(T_OFULL + 1), nof1++ & 1, wc)) { ok = false; break; }
@@ -950,7 +976,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const long long prow = (long long)part * kTRows + r;
         float inv = whole ? (l == 0.f ? 0.f : ref / l) : 1.f, lse2 = m - kPShift + __log2f(l), w_side = 0.f;
         const long long pieces = (long long)p.total_q * p.g;       // from one piece of 4 columns to the next
-        float4* side = side_piece<D>(p, h, q0, r, 0);              // (used where the row is live)
+        float4* side = side_piece<D>(p, part_of_keys, h, q0, r, 0);              // (used where the row is live)
         if (whole && live && SIDE && p.side == SIDE_IN) {
           const float2 w = join_side(p, side_row(p, h, q0, r), lse2, lse2);
           inv *= w.x;
@@ -985,7 +1011,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               for (int i = 0; i < 4; ++i) {
                 float4 y = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
                                        __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
-                if (p.side == SIDE_OUT) {
+                if (p.side != SIDE_IN) {
                   if (live) at[i * pieces] = y;
                   continue;
                 }
@@ -1025,7 +1051,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           __syncwarp();
         }
-        if (whole && !(SIDE && p.side == SIDE_OUT)) {
+        if (whole && !(SIDE && p.side != SIDE_IN)) {
           constexpr int LPR = D / 8, RPS = 32 / LPR;
           const long long mine = live ? orow : -1;
 #pragma unroll 4
@@ -1045,13 +1071,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < D; ++i) {
             if (nan_keys[(nu & 1) * D + i] >= U.lim0 + qi) continue;
-            if (whole && SIDE && p.side == SIDE_OUT) reinterpret_cast<float*>(side + (i / 4) * pieces)[i % 4] = __int_as_float(0x7fffffff);
+            if (whole && SIDE && p.side != SIDE_IN) reinterpret_cast<float*>(side + (i / 4) * pieces)[i % 4] = __int_as_float(0x7fffffff);
             else if (whole) static_cast<uint16_t*>(p.o)[orow * D + i] = 0x7fff;
             else reinterpret_cast<uint32_t*>(ws + W.part)[(((long long)part * (D / 4) + i / 4) * kTRows + r) * 4 + i % 4] = 0x7fffffffu;
           }
         }
         if (live) {
-          if (whole && SIDE && p.side == SIDE_OUT) p.side_lse[side_row(p, h, q0, r)] = lse2;
+          if (whole && SIDE && p.side != SIDE_IN) p.side_lse[part_of_keys][side_row(p, h, q0, r)] = lse2;
           else if (whole) p.lse[orow] = lse2 * kLn2;
           else reinterpret_cast<float4*>(ws + W.stat)[prow] = make_float4(m - kPShift, l, ref, 0.f);
         }
@@ -1100,7 +1126,8 @@ cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, i
   if (p.side != SIDE_NONE) return launch_fwd_cache_tile_side(maps, p, d, sms, s);
 #endif
   // 16 sequences of 16000 keys, 128 rows per K/V head: 145 us against 203; 32 rows 141 against 198.
-  const bool split = (long long)p.max_q * p.g <= 128;
+  const int max_q = p.side == SIDE_BOTH && p.two.max_q > p.max_q ? p.two.max_q : p.max_q;
+  const bool split = (long long)max_q * p.g <= 128;
   auto go = [&](auto dim, auto groups) {
     constexpr bool side = CACHE_TILE_SIDE;
     return split ? launch_tile<dim, groups, true, side>(maps, p, sms, s) : launch_tile<dim, groups, false, side>(maps, p, sms, s);

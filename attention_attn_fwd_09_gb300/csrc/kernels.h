@@ -263,14 +263,20 @@ struct CacheParams {
   // [list_count], negative ones left out; g, Hkv count virtual heads, rep of which share a K/V head.
   const int* list;
   int list_count, rep;
-  // Keys in two parts (a shared prefix, then a sequence's own): the first part's result goes to side_o
+  // Keys in two parts (a shared prefix, then a sequence's own).  A part's result goes to its side_o
   // [Hkv][d / 4][total_q g] (pieces of 4 columns; a K/V head's rows are query by query, its heads side by side) and
-  // side_lse [Hkv][total_q g] (log2) instead of o and lse, the second part's is joined with it.
-  int side;                  // SIDE_NONE, SIDE_OUT (first part) or SIDE_IN (second)
-  float *side_o, *side_lse;
-  int* side_bad;             // the first part's offsets were invalid: the second writes nothing
+  // side_lse [Hkv][total_q g] (log2) instead of o and lse.  One launch may do both parts (SIDE_BOTH: `two` is the second
+  // one, launch_fwd_cache_join joins them), or one the first part (SIDE_OUT) and another the second, joining it with
+  // the first's results (SIDE_IN).
+  int side;
+  float *side_o[2], *side_lse[2];
+  int* side_bad;             // some offsets were invalid: what comes after writes nothing
+  struct {
+    const int *table, *cu_q, *kv_lens;
+    int B, max_q, max_pages, max_len, causal;
+  } two;
 };
-enum : int { SIDE_NONE = 0, SIDE_OUT = 1, SIDE_IN = 2 };
+enum : int { SIDE_NONE = 0, SIDE_OUT = 1, SIDE_IN = 2, SIDE_BOTH = 3 };
 // Tensor maps over the codes as 128-byte lines, [num_pages * Hkv][page * d / 128][128], boxes of
 // 32 keys (a page of 16: 16 keys), 128-byte swizzle.
 struct CacheMaps {
@@ -290,5 +296,7 @@ cudaError_t launch_fwd_cache_pages(const CacheMaps& maps, const CacheParams& p, 
 size_t cache_tile_workspace_bytes(int d, int sms);
 cudaError_t launch_fwd_cache_tile(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
 cudaError_t launch_fwd_cache_tile_side(const CacheMaps& maps, const CacheParams& p, int d, int sms, cudaStream_t s);
+// Both parts' results into o and lse, a dependent launch.
+cudaError_t launch_fwd_cache_join(const CacheParams& p, int d, cudaStream_t s);
 
 }  // namespace attn
