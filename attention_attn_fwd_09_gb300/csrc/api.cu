@@ -1279,9 +1279,13 @@ int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cac
   }
   CacheMaps maps[2];
   if ((rc = cache_maps(mine, few_rows(p[0]), &maps[0])) != ATTN_OK) return rc;
-  if (few_rows(p[0]) == few_rows(p[1])) {
-    // The same kernel for both parts: one launch of it and one that joins them (a prefix of 5000 and one of 16001 keys
-    // before 24 pieces of up to 60 queries, 16 heads on 2, d = 64: XX us against 85 one after the other).
+  // One kernel for both parts, then one that joins them, where the same one suits both (prefixes of 5000 and 16001 keys
+  // before 24 pieces of up to 60 queries, 16 heads on 2, d = 64: 67 us against 85 one after the other); and where the
+  // sequences' own part has few rows but no more units than there are SMs: their starts cost less in the tiles' launch than
+  // two launches do (8 sequences x 8 K/V heads: 33 us against 36; 10 x 4 24 against 42; 64 x 2 with 260 keys each 45
+  // against 43; 38 x 8 59 against 49, so no further).
+  const bool tiles = !few_rows(p[0]) && (!few_rows(p[1]) || (long long)B * Hkv <= sms);
+  if (tiles || (few_rows(p[0]) && few_rows(p[1]))) {
     p[0].side = SIDE_BOTH;
     p[0].two = {page_table, cu_seqlens_q, kv_lens, B, max_q, max_pages, max_pages * page_size, causal ? 1 : 0};
     if ((rc = launch_cache(maps[0], p[0], d, sms, st)) != ATTN_OK) return rc;
