@@ -204,6 +204,8 @@ SHAPES = [  # prefix lengths, own lengths, queries, queries per prefix
     ([513, 129], [60, 250, 131], [31, 40, 1], [50, 22]),                   # tiles everywhere; borders inside a sequence
     ([64], [300], [100], [100]),
     ([1], [1], [1], [1]),
+    ([30, 0, 77, 400, 5], [64], [20], [4] * 5),                            # few rows behind each prefix, tiles of one sequence
+    ([700], [1 + 7 * (i % 9) for i in range(160)], [1] * 160, [160]),      # tiles, then more units of few rows than SMs
 ]
 
 
@@ -267,6 +269,23 @@ def test_prefix_device_checks_write_nothing(A):
     assert A.attn_device_status(True) == INVALID
 
 
+@pytest.mark.parametrize("ns,members,lens", [([1] * 80, [80], [9] * 80), ([20], [4] * 5, [30])])
+def test_prefix_by_two_kernels_device_checks_write_nothing(A, ns, members, lens):
+    """Tiles then few rows (more units than SMs), and few rows then tiles: a launch for each part."""
+    G, B, T = len(members), len(ns), sum(ns)
+    c, pre = prefixed([50] * G, lens, ns, members, 8, 2, 32, 64, seed=6)
+    check_prefix(A, c, pre)
+    o = torch.full((8, T, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((8, T), 7.0, device=DEV)
+    cu, mine = pre["cu"].copy(), c["cu"].copy()
+    cu[-1] -= 1
+    mine[-1] += 1
+    for p, q in ((dict(cu=cu), {}), (dict(lens=np.full(G, -1)), {}), ({}, dict(cu=mine)), ({}, dict(lens=np.full(B, 1 << 20)))):
+        as32 = lambda d: {n: np.asarray(x, np.int32) for n, x in d.items()}
+        run_prefix(A, {**c, **as32(q)}, {**pre, **as32(p)}, o=o, lse=lse, max_prefix_q=max(members), max_q=max(ns))
+        assert A.attn_device_status(True) == INVALID and (o == 7).all() and (lse == 7).all()
+
+
 def test_prefix_tiles_device_checks_write_nothing(A):
     ns = [20, 30]
     c, pre = prefixed([100], [20, 33], ns, [50], 4, 2, 32, 64, seed=5)
@@ -279,7 +298,7 @@ def test_prefix_tiles_device_checks_write_nothing(A):
 
 
 # ------------------------------------------------------------------ how they are called
-@pytest.mark.parametrize("which", ["pages", "prefix", "prefix_tiles"])
+@pytest.mark.parametrize("which", ["pages", "prefix", "prefix_tiles", "prefix_two"])
 def test_captured_replayed_and_on_another_stream(A, which):
     if which == "pages":
         c = filled([500, 90], [1, 2], 8, 2, 32, 128, seed=31)
@@ -287,14 +306,11 @@ def test_captured_replayed_and_on_another_stream(A, which):
         args = [dev(c["q"]), *cache_args(c), dev(c["table"]), dev(c["cu"]), dev(c["lens"]), dev(pages)]
         call, size = A.attn_fwd_kv_fp8_pages, A.attn_fwd_kv_fp8_pages_workspace_size(8, 2, 3, 128)
     else:
-        n = 1 if which == "prefix" else 30
-        c, pre = prefixed([400], [50, 20], [n, n], [2 * n], 8, 2, 32, 128, seed=32)
-        if n > 1:
-            c["lens"][:] = [50, 30]
-            c, pre = prefixed([400], [50, 30], [n, n], [2 * n], 8, 2, 32, 128, seed=32)
-        args = [dev(c["q"]), *cache_args(c), dev(pre["table"]), dev(pre["cu"]), dev(pre["lens"]), 2 * n, dev(c["table"]),
+        n, B = {"prefix": (1, 2), "prefix_tiles": (30, 2), "prefix_two": (1, 90)}[which]
+        c, pre = prefixed([400], [30 + i % 2 * 20 for i in range(B)], [n] * B, [B * n], 8, 2, 32, 128, seed=32)
+        args = [dev(c["q"]), *cache_args(c), dev(pre["table"]), dev(pre["cu"]), dev(pre["lens"]), B * n, dev(c["table"]),
                 dev(c["cu"]), dev(c["lens"]), n]
-        call, size = A.attn_fwd_kv_fp8_prefix, A.attn_fwd_kv_fp8_prefix_workspace_size(8, 2, 2 * n, 2 * n, n, 128)
+        call, size = A.attn_fwd_kv_fp8_prefix, A.attn_fwd_kv_fp8_prefix_workspace_size(8, 2, B * n, B * n, n, 128)
     want = call(*args)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -328,15 +344,15 @@ def test_captured_replayed_and_on_another_stream(A, which):
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
-@pytest.mark.parametrize("which", ["pages", "prefix", "prefix_tiles"])
+@pytest.mark.parametrize("which", ["pages", "prefix", "prefix_tiles", "prefix_two"])
 def test_a_wait_that_runs_out(A, which):
-    n = 20 if which == "prefix_tiles" else 1
-    c, pre = prefixed([400], [50], [n], [n], 8, 2, 32, 128, seed=33)
+    n, B = {"prefix_tiles": (20, 1), "prefix_two": (1, 90)}.get(which, (1, 1))
+    c, pre = prefixed([400], [50] * B, [n] * B, [n * B], 8, 2, 32, 128, seed=33)
     A.attn_set_debug_knobs(wait_limit_ns=2_000_000)
     A.attn_set_test_hooks(skip_first_kv_load=True)
     try:
         if which == "pages":
-            run_pages(A, c, np.zeros((2, 1, 1), np.int32))
+            run_pages(A, c, np.zeros((2, n * B, 1), np.int32))
         else:
             run_prefix(A, c, pre)
         assert A.attn_device_status(True) == TIMEOUT
