@@ -1136,6 +1136,7 @@ int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_sc
     return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 1, first=%d and last=%d >= 0 and together within it", count, first,
                 last);
   if (B == 0 || total_q == 0) return ATTN_OK;
+  if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
   if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
   if (!q || !k_bounds || !k_scale || !page_table || !cu_seqlens_q || !kv_lens || !pages)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");

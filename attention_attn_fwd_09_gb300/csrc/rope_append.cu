@@ -492,12 +492,10 @@ template <int D>
 cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
   const int vecs = p.a.page * D / 8;                   // 16-byte pieces of a page
   const size_t smem = (size_t)p.a.page * turn_row(p.rot) * sizeof(float2);
-  if (vecs == 128) rope_append_kernel<D, 1, 128, 8><<<grid, 128, smem, s>>>(p);
-  else if (vecs == 256) rope_append_kernel<D, 1, 256, 4><<<grid, 256, smem, s>>>(p);
-  else if (vecs == 512) rope_append_kernel<D, 2, 256, 4><<<grid, 256, smem, s>>>(p);
-  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 2><<<grid, 256, smem, s>>>(p);
-  else if (vecs == 2048) {
-    // The only table of more than 40 KB (d = 128, a page of 128: 64 KB).
+  if constexpr (D == 64) {
+    if (vecs == 128) rope_append_kernel<D, 1, 128, 8><<<grid, 128, smem, s>>>(p);
+  } else if (vecs == 2048) {
+    // The only table of more than 40 KB (a page of 128: 64 KB).
     static std::once_flag flags[64];
     static cudaError_t attr_err[64];
     int dev = 0;
@@ -508,7 +506,10 @@ cudaError_t launch_d(const RopeAppendParams& p, dim3 grid, cudaStream_t s) {
     });
     if (attr_err[dev & 63] != cudaSuccess) return attr_err[dev & 63];
     rope_append_kernel<D, 8, 256, 2><<<grid, 256, smem, s>>>(p);
-  } else return cudaErrorInvalidValue;
+  }
+  if (vecs == 256) rope_append_kernel<D, 1, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 512) rope_append_kernel<D, 2, 256, 4><<<grid, 256, smem, s>>>(p);
+  else if (vecs == 1024) rope_append_kernel<D, 4, 256, 2><<<grid, 256, smem, s>>>(p);
   return cudaGetLastError();
 }
 

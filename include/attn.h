@@ -326,8 +326,8 @@ size_t attn_fwd_kv_fp8_pages_workspace_size(int Hq, int Hkv, int total_q, int d)
  *       (kv_lens counts these only), as attn_fwd_kv_fp8; causal concerns these only.
  *   max_prefix_q: an upper bound on the queries that share one prefix, from 1 to total_q; max_q as
  *       attn_fwd_kv_fp8.  Each chooses the kernel of its part as there.
- *   workspace: attn_fwd_kv_fp8_prefix_workspace_size(...) bytes, which holds the prefix part's results
- *       in fp32; other arguments and ownership as attn_fwd_kv_fp8.
+ *   workspace: attn_fwd_kv_fp8_prefix_workspace_size(...) bytes, which holds both parts' results in fp32 (8 Hq total_q d
+ *       bytes and more); other arguments and ownership as attn_fwd_kv_fp8.
  * Errors as attn_fwd_kv_fp8, of both parts; if either part's offsets or lengths break a rule nothing is
  *   written to o and lse.
  */
@@ -521,7 +521,7 @@ int attn_set_debug_knobs(float tau, int poly_per_16, long long wait_limit_ns, in
 int attn_get_debug_knobs(float* tau, int* poly_per_16, long long* wait_limit_ns, int* sync_check);
 
 /*
- * Test hook (off by default): skip_first_kv_load = 1 makes the forward (attn_fwd_kv_fp8 too) never
+ * Test hook (off by default): skip_first_kv_load = 1 makes the forward (attn_fwd_kv_fp8, _pages and _prefix too) never
  * issue the first K tile of each CTA, so the consumer's bounded wait runs out, the CTA
  * gives up cleanly and the device status word reads ATTN_ERR_TIMEOUT.  Used to test the
  * timeout path without faulting anything.  No counterpart on the pages.

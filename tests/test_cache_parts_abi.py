@@ -69,7 +69,7 @@ def test_append_refusals(A):
 
 def test_select_refusals(A):
     for bad in (dict(count=0), dict(first=-1), dict(last=-1), dict(first=3, last=2), dict(first=1 << 30, last=1 << 30, count=4),
-                dict(mq=0), dict(mq=4), dict(Hq=3), dict(out=None)):
+                dict(mq=0), dict(mq=4), dict(Hq=3), dict(out=None), dict(pages=0)):
         assert select(A, **bad) == -1, bad
     assert select(A, Hq=514) == -2 and select(A, Hq=65536) == -2
     assert select(A, q=EIGHT) == -3 and select(A, out=ODD) == -3

@@ -217,6 +217,31 @@ def test_prefix(A, shape, Hq, H, P, d):
     check_prefix(A, c, pre)
 
 
+@pytest.mark.parametrize("ns,members,Hq,lens", [([2, 1], [3], 4, [70, 5]), ([20, 9], [29], 4, [70, 40]), ([1] * 100, [100], 4, [70] + [5] * 99),
+                                                ([20], [4] * 5, 2, [70])])
+def test_prefix_nan_values_reach_the_queries_that_see_them(A, ns, members, Hq, lens):
+    """A NaN among a sequence's own values reaches its queries from there on; one in a prefix all behind it."""
+    H, P, d = 2, 32, 64
+    G = len(members)
+    c, pre = prefixed([90] * G, lens, ns, members, Hq, H, P, d, seed=17)
+    ref = lambda cc: osp.attend_prefix(cc["q"].float().numpy(), cc, pre["table"], pre["cu"], pre["lens"], True, d ** -0.5)[0]
+    clean = ref(c)
+    at = lens[0] - 1                                       # the first sequence's last key: its last query's alone
+    own = {**c, "v_cache": c["v_cache"].copy()}
+    own["v_cache"][c["table"][0, at // P], 1, at % P, 7:9] = 0x7F
+    o = run_prefix(A, own, pre)[0].float().cpu().numpy()
+    want = np.zeros(o.shape, bool)
+    want[Hq // 2:, ns[0] - 1, 7:9] = True
+    assert (np.isnan(o) == want).all()
+    front = {**c, "v_cache": c["v_cache"].copy()}
+    front["v_cache"][pre["table"][G - 1, 1], 0, 3, 60] = 0xFF
+    o = run_prefix(A, front, pre)[0].float().cpu().numpy()
+    want = np.zeros(o.shape, bool)
+    want[:Hq // 2, pre["cu"][G - 1]:, 60] = True
+    assert (np.isnan(o) == want).all()
+    assert np.abs(o - clean)[~want].max() < 0.1
+
+
 def test_prefix_bounds_larger_than_needed_and_not_causal(A):
     c, pre = prefixed([700, 130], [40, 0, 9], [2, 1, 3], [3, 3], 8, 2, 32, 128, seed=11)
     check_prefix(A, c, pre, causal=False)
