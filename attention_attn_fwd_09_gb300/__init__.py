@@ -9,7 +9,9 @@ Names match the C ABI in include/attn.h: ``attn_fwd``, ``attn_fwd_kv``,
 ``attn_bwd_noalloc``, ``attn_quantize_fp8`` and ``attn_fwd_fp8`` (e4m3 inputs with
 per-block scales), ``attn_rope`` and ``attn_rope_bwd`` (rotary positions),
 ``attn_kv_append_fp8`` and ``attn_fwd_kv_fp8`` (a paged e4m3 key/value cache and the attention
-over it), the ``*_workspace_size`` queries, ``attn_last_error`` and the
+over it), ``attn_rope_kv_append_fp8`` (rotation and append at once), ``attn_select_pages_fp8`` and
+``attn_fwd_kv_fp8_pages`` (the pages each query is to read, attention over them),
+``attn_fwd_kv_fp8_prefix`` (sequences behind shared prefixes), the ``*_workspace_size`` queries, ``attn_last_error`` and the
 test/tuning knobs.
 """
 from __future__ import annotations

@@ -23,6 +23,10 @@
 // cache, 91 % of a copy's rate; 8 of 8192 keys 32.9 us in a graph, 4.1 TB/s (15 us of it are the
 // start, the first pieces' way from memory and the merge); one of 1000 keys 8.6 us in a graph.
 // With d = 64 (half the bytes, as many scores) the same take 0.78, 0.76 and 0.98 of these times.
+// Lists (a unit is a query and its pages): 128 pages of 32 keys for each of 64 sequences 113 us in a graph,
+// 4.7 TB/s; 64 pages for one 13 us, of the kernel's 12300 cycles 3300 the start, 2700 look-ups, 2300 the join.
+// Behind shared prefixes: a unit's result is joined with the other part's, in the epilogue or by
+// fwd_cache_join_kernel; 64 sequences' keys behind 32768 92 us in all, by tiles and then here.
 //
 // Numbers: q is scaled by a power of two per row (largest |q| in [2^14, 2^15)) and held in f16: exact
 // down to 2^-31 of the row's largest component, off by at most 2^-39 of it below.  exp2(s - m + 14)
@@ -45,7 +49,7 @@ constexpr int kPiece = 32;                   // keys per piece
 constexpr int kSMs = 152;                  // blocks of the merge kernel are a multiple of these
 constexpr float kShift = 14.f;               // weights are held times 2^14
 // What starting and ending a unit counts for when work is cut, in pieces (shared prefixes before 64 sequences of up
-// to 1024 keys: 90 us, without it 114, as one CTA had all the short ones; 6 and 20 alike).  attn_fwd_kv_fp8 counts
+// to 1024 keys: 90 us, without it 114; 6 and 20 alike).  attn_fwd_kv_fp8 counts
 // pieces alone.
 constexpr int kUnitCost = 12;
 
