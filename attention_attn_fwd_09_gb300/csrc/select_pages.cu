@@ -371,7 +371,7 @@ __device__ __forceinline__ float unordered32(int b) { return __int_as_float(b < 
 // The exact score of page pg for packed query q and heads r0 .. r0 + 3 of the group of K/V head h, as ordered()
 // bits; by a warp.  Codes are m 2^x with 4 bits of m and q's components with 8, so that their products, as whole
 // numbers times one power of two, add up exactly in 64 bits where q's components lie within 2^29 of each other;
-// elsewhere doubles do it (ten times as long: an SM has two 64-bit multiply-adds a cycle).
+// elsewhere doubles do it (all by doubles, two pages took 11000 cycles).
 constexpr int kExactHeads = 4;
 template <int D>
 __device__ unsigned long long exact_score(const SelectParams& p, int q, int h, int r0, int pg) {
