@@ -1115,6 +1115,9 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
   return post_launch(s, st);
 }
 
+// Entries of a list: kernels step up to 1024 past its end, in 32 bits.
+constexpr int kMaxListed = 0x7fff0000;
+
 size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages) {
   if (Hkv <= 0 || total_q < 0 || max_pages < 0) {
     set_last_error("attn_select_pages_fp8_workspace_size: invalid sizes");
@@ -1135,6 +1138,7 @@ int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_sc
   if (count < 1 || first < 0 || last < 0 || first > count || last > count - first)
     return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 1, first=%d and last=%d >= 0 and together within it", count, first,
                 last);
+  if (count > kMaxListed) return fail(ATTN_ERR_INVALID_ARG, "count=%d must be at most 2^31 - 65536", count);
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
   if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
@@ -1195,7 +1199,8 @@ int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cach
                     B, Hq, Hkv, total_q, d, num_pages, page_size, max_pages, causal, scale};
   int rc = check_cache_call(c);
   if (rc != ATTN_OK) return rc;
-  if (count < 0) return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 0", count);
+  if (count < 0 || count > kMaxListed)
+    return fail(ATTN_ERR_INVALID_ARG, "count=%d must be between 0 and 2^31 - 65536", count);
   if (B == 0 || total_q == 0) return ATTN_OK;
   if ((rc = check_cache_pointers(c)) != ATTN_OK) return rc;
   if (count > 0 && !pages) return fail(ATTN_ERR_INVALID_ARG, "null pointer");

@@ -262,8 +262,8 @@ size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int m
  *       page_table, cu_seqlens_q, kv_lens, max_q, causal as attn_fwd_kv_fp8.
  *   pages: DEVICE int32 [Hkv, total_q, count] out: numbers of pages within the query's sequence, ascending, -1
  *       behind the last one.  A query that sees up to count pages lists them all.  Otherwise its list
- *       holds the first `first` and the last `last` of them (together at most count; the last one holds the
- *       query's own key) and, of the others, the count - first - last with the largest scores.
+ *       holds the first `first` and the last `last` of them (together at most count, itself at most
+ *       2^31 - 65536; the last one holds the query's own key) and, of the others, the count - first - last with the largest scores.
  *   The choice is that of exact scores: equal ones by number, NaN (of the query or the bounds) above
  *       all.  Scores come in fp32 first, and pages whose order that cannot tell are scored again in 64 bits, which
  *       takes long when a great many are alike.
@@ -291,7 +291,7 @@ size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages)
  *       holds its rows j * page_size ..; attn_select_pages_fp8 writes such lists).  The numbers of a list
  *       are distinct and of pages that the query sees a key of; negative entries are left out, and where
  *       the list is longer than the pages the query sees, what lies behind as many entries is negative
- *       (so it is in lists that are filled from the front).  count may be 0.
+ *       (so it is in lists that are filled from the front).  count: 0 .. 2^31 - 65536.
  *   Keys of a listed page that the query does not see (causal, or behind kv_lens[b]) are masked.  A
  *       query without a visible listed key gets O = 0 and LSE = -inf.
  *   Groups: Hq / Hkv heads share a list and its pages; up to 16 (or their largest divisor up to 16)

@@ -1,0 +1,15 @@
+"""Sizes at the ends of their ranges for the calls over parts of the 8-bit cache: counts near 2^31, tables without
+entries.  Each call ends in a refusal before anything is launched."""
+import pytest
+
+from test_cache_parts_abi import A, ODD, listed, prefix, select  # noqa: F401  (A: the fixture)
+
+TOP = 0x7fffffff
+
+
+def test_counts_near_the_int_range_are_refused(A):  # noqa: F811
+    """The kernels step past the end of a list by up to 1024 entries: that has to stay below 2^31."""
+    for count in (TOP, TOP - 127, 0x7fff0001):
+        assert select(A, count=count, ws=None) == -1 and listed(A, count=count, ws=None) == -1
+        assert select(A, count=count, first=count, last=0, ws=None) == -1
+    assert select(A, count=0x7fff0000, ws=None) == -4 and listed(A, count=0x7fff0000, ws=None) == -4
