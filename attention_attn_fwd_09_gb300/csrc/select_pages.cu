@@ -36,7 +36,7 @@ namespace {
 constexpr int kScoreThreads = 128, kScoreWarps = kScoreThreads / 32, kScoreCtas = 4;   // CTAs per SM
 constexpr int kStep = 16;                    // pages that a warp scores at once
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr float kBig = 3.0e38f;
+constexpr float kBig = 3.0e38f, kTiny = 1.17549435e-38f;          // 2^-126
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -333,7 +333,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) select_score_kernel
           }
         }
         const float s0 = got[0] ? (scale[0] <= kBig ? scale[0] : INFINITY) : 0.f, s1 = got[1] ? (scale[1] <= kBig ? scale[1] : INFINITY) : 0.f;
-        const float error = norm * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s0, s1))));
+        const float top_scale = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s0, s1))));
+        // 0 only where q or the scales are: what underflows here or in a score stays below the smallest normal number.
+        const float error = norm > 0.f && top_scale > 0.f ? fmaxf(norm * top_scale, kTiny) : 0.f;
         if (lane < nq) {
           float* out = p.errors + (out_row + lane) * p.groups + p.first / kStep + step + s;
           *out = rt > 0 ? fmaxf(*out, error) : error;
