@@ -7,9 +7,10 @@
 // much attention falls on whatever the query) and the last ones (the nearest keys) are always
 // listed, the best of the others fill the list, ascending; a sequence with few enough pages lists all.
 //
-// What is chosen is what exact scores choose (equal ones by number), whatever order a sum is taken
-// in: the kernels score in fp32 with a bound on their error, and only pages too near the border to
-// tell are scored again in 64 bits.  So the list depends on nothing but the query and the bounds.
+// What is chosen is what scores in 64-bit floating point choose, each head's sum rounded once (equal ones go by
+// number), whatever order a sum is taken in: the kernels score in fp32 with a bound on their error, and only pages
+// too near the border to tell are scored again, by exact sums.  So the list depends on nothing but the query and
+// the bounds.
 //
 // Two dependent launches:
 //   * scores, bound by the bounds' bytes (2 d per page and K/V head): a warp takes 16 pages as the rows
@@ -370,10 +371,63 @@ __device__ __forceinline__ int ordered32(float x) {
 }
 __device__ __forceinline__ float unordered32(int b) { return __int_as_float(b < 0 ? b ^ 0x7fffffff : b); }
 
+// The sum over a warp of products m n 2^(s - 142) (signed; m n below 2^12, s up to 267) that lie too far apart for
+// 64 bits, rounded once: nine digits of 32 bits, each added up by itself (128 products stay below 2^50).  A lane
+// brings up to four, as 512 m n + s.
+__device__ __noinline__ double far_sum(int4 terms) {
+  constexpr int DIGITS = 9;
+  const int t[4] = {terms.x, terms.y, terms.z, terms.w};
+  uint32_t digit[DIGITS];
+  long long carry = 0;
+#pragma unroll
+  for (int i = 0; i < DIGITS; ++i) {
+    long long sum = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if ((t[x] >> 5 & 15) == i) sum += (long long)(t[x] >> 9) * (1ll << (t[x] & 31));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum += carry;
+    digit[i] = (uint32_t)sum;
+    carry = sum >> 32;                       // (rounds down)
+  }
+  const bool negative = carry < 0;           // the sum is below 2^288: 0 or -1
+  if (negative) {
+    uint32_t one = 1;
+#pragma unroll
+    for (int i = 0; i < DIGITS; ++i) {
+      digit[i] = ~digit[i] + one;
+      one = one != 0 && digit[i] == 0 ? 1 : 0;
+    }
+  }
+  // The leading 64 bits, the last of them set if any behind is: the conversion then rounds as the whole sum would.
+  uint32_t a = 0, b = 0, c = 0, rest = 0;
+  int top = 0;
+#pragma unroll
+  for (int i = DIGITS - 1; i >= 0; --i) {
+    if (a == 0) {
+      a = digit[i];
+      b = i > 0 ? digit[i > 0 ? i - 1 : 0] : 0u;
+      c = i > 1 ? digit[i > 1 ? i - 2 : 0] : 0u;
+      rest = 0;
+      top = i;
+    } else if (i < top - 2) {
+      rest |= digit[i];
+    }
+  }
+  if (a == 0) return 0.0;
+  const int z = __clz(a);
+  const unsigned long long lead = (((unsigned long long)a << 32 | b) << z) | (z > 0 ? c >> (32 - z) : 0u);
+  const double x = __ull2double_rn(lead | ((c << z | rest) != 0 ? 1u : 0u)) *
+                   __longlong_as_double((long long)(32 * (top - 1) - z - 142 + 1023) << 52);
+  return negative ? -x : x;
+}
+
 // The exact score of page pg for packed query q and heads r0 .. r0 + 3 of the group of K/V head h, as ordered()
-// bits; by a warp.  Codes are m 2^x with 4 bits of m and q's components with 8, so that their products, as whole
-// numbers times one power of two, add up exactly in 64 bits where q's components lie within 2^29 of each other;
-// elsewhere doubles do it (all by doubles, two pages took 11000 cycles).
+// bits: each head's sum rounded once to 64-bit floating point, times the scale; by a warp.  Codes are m 2^x with 4
+// bits of m and q's components with 8, so that their products, as whole numbers times one power of two, add up
+// exactly in 64 bits where q's components lie within 2^29 of each other, elsewhere in more (far_sum).  Sums with
+// infinities and NaN, where no rounding counts, are taken in doubles (all by doubles, two pages took 11000 cycles).
 constexpr int kExactHeads = 4;
 template <int D>
 __device__ unsigned long long exact_score(const SelectParams& p, int q, int h, int r0, int pg) {
@@ -407,8 +461,10 @@ __device__ unsigned long long exact_score(const SelectParams& p, int q, int h, i
 #pragma unroll
     for (int x = 0; x < COLS; ++x) top = max(top, (int)(w[r][x >> 1] >> (x & 1) * 16 + 7 & 0xff));
     top = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
-    bool far = top == 255;                   // an infinity or NaN
+    const bool strange = top == 255;         // an infinity or NaN
+    bool far = false;
     long long sum = 0;
+    int terms[4] = {0, 0, 0, 0};             // for far_sum
 #pragma unroll
     for (int x = 0; x < COLS; ++x) {
       const uint32_t y = w[r][x >> 1] >> (x & 1) * 16 & 0xffffu, e = y >> 7 & 0xff;
@@ -416,11 +472,14 @@ __device__ unsigned long long exact_score(const SelectParams& p, int q, int h, i
       far |= m != 0 && below > 29;
       const uint32_t code = ((y >> 15 ? lo : hi) >> 8 * x) & 0xff, ce = code >> 3 & 15;
       const int n = (int)((code & 7) | (ce ? 8 : 0));
-      const long long product = (long long)(m * n) << (max(29 - below, 0) + max((int)ce, 1) - 1);
-      sum += (y >> 15) != (code >> 7) ? -product : product;
+      const int product = (y >> 15) != (code >> 7) ? -m * n : m * n;
+      terms[x] = product * 512 + max((int)e, 1) - 1 + max((int)ce, 1) - 1;
+      sum += (long long)product * (1ll << (max(29 - below, 0) + max((int)ce, 1) - 1));
     }
     double s;
-    if (!__any_sync(0xffffffffu, far)) {
+    if (!strange && __any_sync(0xffffffffu, far)) {
+      s = far_sum(make_int4(terms[0], terms[1], terms[2], terms[3]));
+    } else if (!strange) {
       const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffffu);
       const unsigned b = __reduce_add_sync(0xffffffffu, (unsigned)(sum >> 24) & 0xffffffu);
       const int d = __reduce_add_sync(0xffffffffu, (int)(sum >> 48));

@@ -264,9 +264,9 @@ size_t attn_fwd_kv_fp8_workspace_size(int B, int Hq, int Hkv, int total_q, int m
  *       behind the last one.  A query that sees up to count pages lists them all.  Otherwise its list
  *       holds the first `first` and the last `last` of them (together at most count, itself at most
  *       2^31 - 65536; the last one holds the query's own key) and, of the others, the count - first - last with the largest scores.
- *   The choice is that of exact scores: equal ones by number, NaN (of the query or the bounds) above
- *       all.  Scores come in fp32 first, and pages whose order that cannot tell are scored again in 64 bits, which
- *       takes long when a great many are alike.
+ *   The choice is that of scores in 64-bit floating point, each head's sum rounded once: equal ones by
+ *       number, NaN (of the query or the bounds) above all.  Scores come in fp32 first, and pages whose order that
+ *       cannot tell are scored again by exact sums, which takes long when a great many are alike.
  *   workspace: attn_select_pages_fp8_workspace_size(...) bytes, 16-byte aligned, owned by the caller,
  *       contents on entry irrelevant; calls (graphs) that may run at once need one each.
  * Errors as attn_fwd_kv_fp8: invalid offsets or lengths write nothing; with a page table entry outside the
