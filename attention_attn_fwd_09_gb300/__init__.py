@@ -840,8 +840,11 @@ def attn_fwd_kv_fp8_pages(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_
     """O, LSE of packed queries over listed pages only: ``pages`` int32 [Hkv, total_q, count] holds
     for each K/V head and query distinct page numbers within the query's sequence (0 is its first
     page, as ``attn_select_pages_fp8`` returns them), negative ones being left out.  Keys the query
-    does not see (causal) are masked; other arguments as ``attn_fwd_kv_fp8``.  ``workspace``: a uint8 CUDA
-    tensor of at least attn_fwd_kv_fp8_pages_workspace_size(...) bytes (allocated when None)."""
+    does not see (causal) are masked.  A page that the query sees has to be among the list's first n entries,
+    n being the pages it sees (so it is in ascending lists without gaps, and in gapless lists of seen pages);
+    otherwise, and where a number lies behind the sequence, ``attn_device_status`` reads INVALID_ARG.  Other arguments as
+    ``attn_fwd_kv_fp8``.  ``workspace``: a uint8 CUDA tensor of at least
+    attn_fwd_kv_fp8_pages_workspace_size(...) bytes (allocated when None)."""
     if not q.is_cuda or q.dim() != 3:
         raise ValueError(f"q: expected a CUDA tensor [Hq, total_q, d], got {tuple(q.shape)} on {q.device}")
     dev = q.device

@@ -78,7 +78,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 
 // What the kernel works on: sequences; queries with lists of pages (p.list); sequences whose keys come in two parts
 // (p.side).  The latter two count what starting and ending a unit costs when they cut the work.
-enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };
+enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };   // LIST: a unit is one query and K/V head, its pages end to end
 
 template <int KIND>
 __device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {
@@ -94,7 +94,6 @@ __device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {
   return n > 0 ? max(1, (len + kPiece - 1) / kPiece) : 0;
 }
 
-// LIST: a unit is one query and K/V head with a list of pages of its own, laid end to end in pieces.
 // The sequence of packed query t: the last one that starts at or before it (decoding: its own number).
 __device__ __forceinline__ int seq_of(const CacheParams& p, int t) {
   if (p.B == p.total_q && __ldg(p.cu_q + t) == t && __ldg(p.cu_q + t + 1) == t + 1) return t;
@@ -114,6 +113,10 @@ __device__ __forceinline__ int keys_seen(const CacheParams& p, int b, int t) {
 // Pages it sees; as many entries of its list are read at most (they are distinct).
 __device__ __forceinline__ int pages_seen(const CacheParams& p, int b, int t) {
   return (int)(((unsigned)max(keys_seen(p, b, t), 0) + p.page - 1) / p.page);
+}
+// Pages of its sequence.
+__device__ __forceinline__ int pages_of(const CacheParams& p, int b) {
+  return (int)(((unsigned)__ldg(p.kv_lens + b) + p.page - 1) / p.page);
 }
 __device__ __forceinline__ int list_pieces(const CacheParams& p, int seen) {
   return max(1, (min(seen, p.list_count) * p.page + kPiece - 1) / kPiece);
@@ -324,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (e >= min(ahead.seen, p.list_count)) return -1;
       const int lp = __ldg(p.list + ((long long)kv_head(ahead.h) * p.total_q + ahead.t) * p.list_count + e);
       if (lp < 0) return -1;
-      if (lp >= ahead.seen) {                // a page that the query does not see
+      if (lp >= ahead.seen) {                // a page that the query does not see (later ones of its sequence may)
+        if (lp < pages_of(p, ahead.b)) return -1;
         atomicExch(p.status, DEV_BAD_PAGE);
         return -2;
       }
@@ -423,10 +427,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       len = LIST ? keys_seen(p, seg.b, seg.t) : __ldg(p.kv_lens + seg.b);
     }
     const int part_of_keys = SIDE && seg.b >= p.B ? 1 : 0;
-    if (LIST && seg.f == seg.ubeg) {         // entries behind as many as the query sees pages are not read: none counts
+    if (LIST && seg.f == seg.ubeg) {         // entries behind as many as the query sees pages are not read: none may count
       const int* entries = p.list + ((long long)kv_head(seg.h) * p.total_q + seg.t) * p.list_count;
-      for (int e = seg.seen + tid; e < p.list_count; e += kThreads)
-        if (__ldg(entries + e) >= 0) atomicExch(p.status, DEV_BAD_PAGE);
+      for (int e = seg.seen + tid; e < p.list_count; e += kThreads) {
+        const int lp = __ldg(entries + e);
+        if (lp >= 0 && (lp < seg.seen || lp >= pages_of(p, seg.b))) atomicExch(p.status, DEV_BAD_PAGE);
+      }
     }
     const long long send = min(seg.uend, re);
     const int rows = n * g;

@@ -289,18 +289,19 @@ size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages)
  *
  *   pages: DEVICE int32 [Hkv, total_q, count]: page numbers within the query's sequence (page j
  *       holds its rows j * page_size ..; attn_select_pages_fp8 writes such lists).  The numbers of a list
- *       are distinct and of pages that the query sees a key of; negative entries are left out, and where
- *       the list is longer than the pages the query sees, what lies behind as many entries is negative
- *       (so it is in lists that are filled from the front).  count: 0 .. 2^31 - 65536.
+ *       are distinct and of pages of the sequence; negative entries are left out, and pages that the query
+ *       does not see yet (drafts that share a list) count for nothing.  Where the list is longer than the pages
+ *       the query sees, what lies behind as many entries is negative or not seen (so it is in ascending lists
+ *       without gaps and in gapless lists of seen pages).  count: 0 .. 2^31 - 65536.
  *   Keys of a listed page that the query does not see (causal, or behind kv_lens[b]) are masked.  A
  *       query without a visible listed key gets O = 0 and LSE = -inf.
  *   Groups: Hq / Hkv heads share a list and its pages; up to 16 (or their largest divisor up to 16)
  *       read them together, so 17 or 19 heads would read them once each.
  *   workspace: attn_fwd_kv_fp8_pages_workspace_size(...) bytes; other arguments, ownership and
  *       limits as attn_fwd_kv_fp8 (there is no bound on a sequence's queries).
- * Errors as attn_fwd_kv_fp8.  A listed page that the query does not see, or a number behind as many
- *   entries as it sees pages, is found on the device: the device status word reads ATTN_ERR_INVALID_ARG and the results of
- *   that query and head are undefined; a page listed twice counts twice.
+ * Errors as attn_fwd_kv_fp8.  A listed page behind the sequence's last one, or a page that the query sees
+ *   listed behind as many entries as it sees pages, is found on the device: the device status word reads
+ *   ATTN_ERR_INVALID_ARG and the results of that query and head are undefined; a page listed twice counts twice.
  */
 int attn_fwd_kv_fp8_pages(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                           const float* v_scale, const int* page_table, const int* cu_seqlens_q, const int* kv_lens,
