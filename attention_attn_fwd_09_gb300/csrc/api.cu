@@ -1045,8 +1045,9 @@ static int check_max_q(const char* name, int max_q, int total_q) {
   return ATTN_OK;
 }
 static int check_cache_pointers(const CacheCall& c) {
-  if (!c.q || !c.k_cache || !c.v_cache || !c.k_scale || !c.v_scale || !c.page_table || !c.cu_seqlens_q || !c.kv_lens ||
-      !c.o || !c.lse)
+  // (A table without columns, whose lengths are all 0, is never read.)
+  if (!c.q || !c.k_cache || !c.v_cache || !c.k_scale || !c.v_scale || (!c.page_table && c.max_pages > 0) ||
+      !c.cu_seqlens_q || !c.kv_lens || !c.o || !c.lse)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(c.q) || !aligned16(c.o) || !aligned16(c.k_cache) || !aligned16(c.v_cache))
     return fail(ATTN_ERR_MISALIGNED, "q, o and the cache must be 16-byte aligned");
@@ -1142,7 +1143,7 @@ int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_sc
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);
   if ((rc = check_max_q("max_q", max_q, total_q)) != ATTN_OK) return rc;
-  if (!q || !k_bounds || !k_scale || !page_table || !cu_seqlens_q || !kv_lens || !pages)
+  if (!q || !k_bounds || !k_scale || (!page_table && max_pages > 0) || !cu_seqlens_q || !kv_lens || !pages)
     return fail(ATTN_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(k_bounds)) return fail(ATTN_ERR_MISALIGNED, "q and k_bounds must be 16-byte aligned");
   if (!aligned4(k_scale) || !aligned4(page_table) || !aligned4(cu_seqlens_q) || !aligned4(kv_lens) || !aligned4(pages))

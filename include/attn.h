@@ -166,9 +166,9 @@ int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, co
  * codes (one byte each), k_scale and v_scale [num_pages, Hkv] fp32: the value of an element is
  * decode(code) * scale of its page and head.  Row t of sequence b is row t % page_size of page
  * page_table[b][t / page_size]; page_table is a DEVICE int32 array [B, max_pages], of which only
- * the entries that a sequence's length reaches are read.  kv_lens, DEVICE int32 [B]: the rows of
- * each sequence AFTER the call (appending) or at the call (attention).  d: 64 or 128;
- * page_size: 16, 32, 64 or 128.
+ * the entries that a sequence's length reaches are read (max_pages = 0, all lengths 0: may be NULL).
+ * kv_lens, DEVICE int32 [B]: the rows of each sequence AFTER the call (appending) or at the call
+ * (attention).  d: 64 or 128; page_size: 16, 32, 64 or 128.
  *
  * attn_kv_append_fp8: appends the packed rows k, v [Hkv, total, d] bf16: rows cu_seqlens[b] ..
  *   cu_seqlens[b+1]-1 (n of them; DEVICE int32, B + 1 offsets) become rows kv_lens[b] - n ..

@@ -54,3 +54,24 @@ def test_a_page_behind_the_sequence_and_one_too_far_back_in_the_list(A):
         pages[where] = entry
         run_pages(A, c, pages)
         assert A.attn_device_status(True) == INVALID, (where, entry)
+
+
+def test_tables_without_entries(A):
+    """Lengths of 0 need no pages: tables of no columns are as good as any."""
+    c, pre = prefixed([0, 0], [40, 7, 90], [1, 1, 2], [1, 3], 8, 2, 32, 64, seed=1)
+    none = np.zeros((2, 0), np.int32)
+    want = run_prefix(A, c, pre)
+    check_prefix(A, c, {**pre, "table": none})
+    got = run_prefix(A, c, {**pre, "table": none})
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    c, pre = prefixed([300], [0] * 20, [2] * 20, [40], 8, 2, 32, 64, seed=2)            # by tiles
+    check_prefix(A, {**c, "table": np.zeros((20, 0), np.int32)}, pre, causal=False)
+    empty = filled([0, 0], [1, 2], 8, 2, 32, 64, seed=3)
+    empty["table"] = none
+    args = [dev(empty["q"]), *cache_args(empty), dev(none), dev(empty["cu"]), dev(empty["lens"])]
+    for o, lse in (A.attn_fwd_kv_fp8(*args, 2, causal=False), A.attn_fwd_kv_fp8(*[bf16(np.ones((32, 3, 64))).to(DEV), *args[1:]], 2, causal=False),
+                   A.attn_fwd_kv_fp8_pages(*args, dev(np.full((2, 3, 4), -1, np.int32)), causal=False)):
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    bounds = torch.zeros(empty["k_cache"].shape[0], 2, 2, 64, dtype=torch.uint8, device=DEV)
+    lists = A.attn_select_pages_fp8(args[0], bounds, args[3], dev(none), args[6], args[7], 32, 4, 2, causal=False)
+    assert (lists == -1).all()

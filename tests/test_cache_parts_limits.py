@@ -2,6 +2,7 @@
 entries.  Each call ends in a refusal before anything is launched."""
 import pytest
 
+from test_cache_abi import attend
 from test_cache_parts_abi import A, ODD, listed, prefix, select  # noqa: F401  (A: the fixture)
 
 TOP = 0x7fffffff
@@ -13,3 +14,12 @@ def test_counts_near_the_int_range_are_refused(A):  # noqa: F811
         assert select(A, count=count, ws=None) == -1 and listed(A, count=count, ws=None) == -1
         assert select(A, count=count, first=count, last=0, ws=None) == -1
     assert select(A, count=0x7fff0000, ws=None) == -4 and listed(A, count=0x7fff0000, ws=None) == -4
+
+
+def test_a_table_without_columns_may_be_null(A):  # noqa: F811
+    """An empty tensor has no address.  (The refusals that follow show that the pointer was let through.)"""
+    assert attend(A, t=None, width=0, ws=None) == -4 and attend(A, t=None, width=1, ws=None) == -1
+    assert listed(A, t=None, width=0, ws=None) == -4 and listed(A, t=None, width=1, ws=None) == -1
+    assert prefix(A, pt=None, pwidth=0, ws=None) == -4 and prefix(A, pt=None, pwidth=1, ws=None) == -1
+    assert prefix(A, t=None, width=0, ws=None) == -4 and prefix(A, t=None, width=1, ws=None) == -1
+    assert select(A, t=None, width=0, out=ODD) == -3 and select(A, t=None, width=1, out=ODD) == -1
