@@ -1118,9 +1118,11 @@ int attn_fwd_kv_fp8(const void* q, const void* k_cache, const void* v_cache, con
 
 // Entries of a list: kernels step up to 1024 past its end, in 32 bits.
 constexpr int kMaxListed = 0x7fff0000;
+// A block chooses a list (and the workspace's size stays within 64 bits).
+static bool few_lists(int Hkv, int total_q) { return (long long)Hkv * total_q <= 0x7fffffffLL; }
 
 size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages) {
-  if (Hkv <= 0 || total_q < 0 || max_pages < 0) {
+  if (Hkv <= 0 || total_q < 0 || max_pages < 0 || !few_lists(Hkv, total_q) || max_pages > kMaxListed / 16) {
     set_last_error("attn_select_pages_fp8_workspace_size: invalid sizes");
     return (size_t)-1;
   }
@@ -1139,6 +1141,8 @@ int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_sc
   if (count < 1 || first < 0 || last < 0 || first > count || last > count - first)
     return fail(ATTN_ERR_INVALID_ARG, "count=%d must be >= 1, first=%d and last=%d >= 0 and together within it", count, first,
                 last);
+  if (!few_lists(Hkv, total_q))
+    return fail(ATTN_ERR_UNSUPPORTED, "Hkv * total_q = %lld lists (supported: below 2^31)", (long long)Hkv * total_q);
   if (count > kMaxListed) return fail(ATTN_ERR_INVALID_ARG, "count=%d must be at most 2^31 - 65536", count);
   if (B == 0 || total_q == 0) return ATTN_OK;
   if (num_pages == 0) return fail(ATTN_ERR_INVALID_ARG, "%d queries, but no pages", total_q);

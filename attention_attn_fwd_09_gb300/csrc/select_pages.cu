@@ -791,8 +791,7 @@ cudaError_t launch_select_pages(SelectParams p, int d, int sms, cudaStream_t s) 
   const bool small = (long long)p.max_q * p.g <= 8;
   p.qn = p.g >= 16 ? 1 : (p.max_q < 16 / p.g ? p.max_q : 16 / p.g);
   p.groups = (p.max_pages + kStep - 1) / kStep;
-  const long long lists = (long long)p.total_q * p.Hkv;
-  if (lists > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long lists = (long long)p.total_q * p.Hkv;            // below 2^31
   cudaError_t e = cudaSuccess;
   const dim3 grid((unsigned)(kScoreCtas * sms));
   auto score = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kScoreThreads), 0, s, p); };

@@ -279,7 +279,7 @@ int attn_select_pages_fp8(const void* q, const void* k_bounds, const float* k_sc
 
 /*
  * Bytes of workspace attn_select_pages_fp8 needs: about 16 per query, K/V head and entry of a page table's row;
- * (size_t)-1 for invalid sizes.
+ * (size_t)-1 for invalid sizes (2^31 lists, Hkv total_q, and more among them).
  */
 size_t attn_select_pages_fp8_workspace_size(int Hkv, int total_q, int max_pages);
 
