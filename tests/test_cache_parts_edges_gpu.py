@@ -75,3 +75,22 @@ def test_tables_without_entries(A):
     bounds = torch.zeros(empty["k_cache"].shape[0], 2, 2, 64, dtype=torch.uint8, device=DEV)
     lists = A.attn_select_pages_fp8(args[0], bounds, args[3], dev(none), args[6], args[7], 32, 4, 2, causal=False)
     assert (lists == -1).all()
+
+
+@pytest.mark.parametrize("Hq,H,P,d", [(4, 2, 32, 64), (16, 1, 128, 128)])
+def test_tiles_of_both_parts_write_nothing_when_the_second_is_wrong(A, Hq, H, P, d):
+    """One launch of tiles for both parts: offsets and lengths of either part that break a rule."""
+    ns = [20, 30]
+    c, pre = prefixed([100, 70], [20, 33], ns, [15, 35], Hq, H, P, d, seed=5)
+    check_prefix(A, c, pre)
+    o = torch.full((Hq, 50, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Hq, 50), 7.0, device=DEV)
+    big = 1 << 20
+    for mine, front in ((dict(cu=[0, 20, 49]), {}), (dict(cu=[1, 20, 50]), {}), (dict(cu=[0, 51, 50]), {}), (dict(lens=[20, 29]), {}),
+                        (dict(lens=[-1, 33]), {}), (dict(lens=[20, big]), {}), ({}, dict(cu=[0, 15, 51])), ({}, dict(lens=[100, -1])),
+                        ({}, dict(lens=[big, 70]))):
+        as32 = lambda x: {n: np.asarray(v, np.int32) for n, v in x.items()}
+        run_prefix(A, {**c, **as32(mine)}, {**pre, **as32(front)}, o=o, lse=lse, max_prefix_q=35, max_q=30)
+        assert A.attn_device_status(True) == INVALID and (o == 7).all() and (lse == 7).all(), (mine, front)
+    run_prefix(A, c, pre, o=o, lse=lse, max_prefix_q=35, max_q=29)          # a bound that is too small
+    assert A.attn_device_status(True) == INVALID and (o == 7).all()
