@@ -652,7 +652,7 @@ def attn_rope_kv_append_fp8(q, k, v, inv_freq, k_cache, v_cache, k_scale, v_scal
     ``mscale``: as ``attn_rope``; ``positions`` int32 [total], by default each row's place in its
     sequence.  ``k_bounds`` uint8 [num_pages, Hkv, 2, d], if given, is kept up to date: the smallest and
     the largest e4m3 code of each column over the page's rows, which ``attn_select_pages_fp8`` goes by
-    (a page's bounds must have been kept since its first row).  ``q_out``: a new contiguous tensor unless given;
+    (a page's bounds must have been kept since its first row; rows given up since still count).  ``q_out``: a new contiguous tensor unless given;
     it may be q (in place).  Cache tensors, offsets and lengths as ``attn_kv_append_fp8``."""
     if not k.is_cuda or k.dim() != 3:
         raise ValueError(f"k: expected a CUDA tensor [Hkv, total, d], got {tuple(k.shape)} on {k.device}")

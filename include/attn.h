@@ -202,7 +202,8 @@ int attn_kv_append_fp8(const void* k, const void* v, void* k_cache, void* v_cach
  *   k_bounds: uint8 [num_pages, Hkv, 2, d] e4m3 codes in and out, 16-byte aligned, or NULL: per page, K/V
  *       head and column the smallest [0] and the largest [1] code of the page's rows (NaN if one is), before
  *       the page's scale.  Bounds of a page that receives rows are updated from what they were, so every
- *       call that writes to the page since its first row must have kept them.
+ *       call that writes to the page since its first row must have kept them; rows given up and written
+ *       over (drafts that were not taken) still count, until a call writes the page's first row again.
  *   strides: NULL for contiguous tensors, or a HOST array {q head, q token, k head, k token, v head, v
  *       token, q_out head, q_out token} of element strides: k's and v's multiples of 8, q's and
  *       q_out's as attn_rope.  q_out overlaps neither k nor v.
