@@ -1292,9 +1292,15 @@ int attn_fwd_kv_fp8_prefix(const void* q, const void* k_cache, const void* v_cac
   if ((rc = cache_maps(mine, few_rows(p[0]), &maps[0])) != ATTN_OK) return rc;
   // One kernel for both parts, then one that joins them, where the same one suits both (prefixes of 5000 and 16001 keys
   // before 24 pieces of up to 60 queries, 16 heads on 2, d = 64: 67 us against 85 one after the other); and where the
-  // sequences' own part has few rows but no more units than there are SMs: their starts cost less in the tiles' launch than
-  // two launches do (8 sequences x 8 K/V heads: 33 us against 36; 10 x 4 24 against 42; 64 x 2 with 260 keys each 45
-  // against 43; 38 x 8 59 against 49, so no further).
+  // sequences' own part has few rows and no more units than there are SMs, so that two main launches' starts count.  One
+  // token of each sequence behind 8192 keys, 4 heads to a K/V head, in a graph, by tiles against two launches:
+  //   own keys                16        260       2000      16000
+  //   10 x 4 K/V heads        31, 41    30, 36    33, 38     65, 69
+  //    8 x 8                  39, 41    33, 36    37, 39     90, 85
+  //   16 x 8                  34, 42    38, 38    47, 48    151, 128
+  //   64 x 2                  38, 47    41, 42    54, 51    218, 133
+  // (38 x 8, beyond the rule: 59 against 49.)  So long own keys behind a short prefix lose by it where units are many; the
+  // lengths that decide it are on the device.
   const bool tiles = !few_rows(p[0]) && (!few_rows(p[1]) || (long long)B * Hkv <= sms);
   if (tiles || (few_rows(p[0]) && few_rows(p[1]))) {
     p[0].side = SIDE_BOTH;

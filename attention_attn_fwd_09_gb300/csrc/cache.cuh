@@ -81,10 +81,9 @@ constexpr int kNoKey = 0x7fffffff;
 // A sequence of either part: sequences of the second are counted behind those of the first.
 struct PartSeq {
   const int *cu, *lens, *table;              // of its part
-  int b, B, max_q, max_pages, max_len, causal, part;
+  int b, B, max_q, max_pages, max_len, causal;
   __device__ __forceinline__ PartSeq(const CacheParams& p, int i) {
-    part = i >= p.B ? 1 : 0;
-    if (part) {
+    if (i >= p.B) {
       cu = p.two.cu_q; lens = p.two.kv_lens; table = p.two.table;
       b = i - p.B; B = p.two.B; max_q = p.two.max_q; max_pages = p.two.max_pages; max_len = p.two.max_len; causal = p.two.causal;
     } else {

@@ -48,9 +48,8 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kPiece = 32;                   // keys per piece
 constexpr int kSMs = 152;                  // blocks of the merge kernel are a multiple of these
 constexpr float kShift = 14.f;               // weights are held times 2^14
-// What starting and ending a unit counts for when work is cut, in pieces (shared prefixes before 64 sequences of up
-// to 1024 keys: 90 us, without it 114; 6 and 20 alike).  attn_fwd_kv_fp8 counts
-// pieces alone.
+// What starting and ending a unit counts for when work is cut, in pieces (a shared prefix before 64 sequences of up
+// to 1024 keys: 90 us, without it 114; 6 and 20 alike).  attn_fwd_kv_fp8 counts pieces alone.
 constexpr int kUnitCost = 12;
 
 template <int D>
@@ -78,7 +77,8 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 
 // What the kernel works on: sequences; queries with lists of pages (p.list); sequences whose keys come in two parts
 // (p.side).  The latter two count what starting and ending a unit costs when they cut the work.
-enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };   // LIST: a unit is one query and K/V head, its pages end to end
+// KIND_LIST: a unit is one query and K/V head, its list's pages end to end in pieces.
+enum : int { KIND_PLAIN = 0, KIND_LIST = 1, KIND_SIDE = 2 };
 
 template <int KIND>
 __device__ __forceinline__ int pieces_of(const CacheParams& p, int b) {

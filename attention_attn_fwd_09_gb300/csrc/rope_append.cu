@@ -15,9 +15,13 @@
 //     fills a table of 16 rows' sines and cosines, so each is made once for 8 heads.  One row of 64
 //     sequences, 32 + 8 heads: 5.7 us in a graph, queries included;
 //   * prompts: a CTA per slot, up to 8 heads and K or V.  The page's table is made while the first
-//     head's rows are on their way from memory; a head's rows stay in registers between the rotation,
-//     the maximum and the rounding, and the next head's are under way meanwhile.  Two prompts of 8192,
-//     32 + 8 heads, d = 128: 74 us with the queries' 42 (5.0 TB/s); K and V alone 36.
+//     head's rows are on their way from memory; a head's rotated rows are kept in fp32 between the
+//     maximum and the rounding, and the next head's are under way meanwhile.  That is more than the registers
+//     hold: of a thread's 364 bytes are stored and 420 loaded in local memory with pages of 128 and d = 128 (128
+//     registers), about 230 and 310 with 16 elements a thread at 64 registers, 36 to 96 elsewhere.  V goes through the
+//     same kernel, whose registers and table it does not need.  Two prompts of 8192, 32 + 8 heads, d = 128: 74 us with
+//     the queries' 42 (5.0 TB/s), K and V alone 36; attn_rope and attn_kv_append_fp8 one after the other take
+//     72, so with prompts the call saves a rounding of K and keeps bounds, but no time.
 // The queries rotate in the same launch where there are few of them, else in rope.cu's kernel, beside this one where
 // it leaves room.
 #include <cstdint>
@@ -415,7 +419,7 @@ __device__ __forceinline__ void append_page(const RopeAppendParams& p, const Slo
   for (int head = h_begin; head < h_end; ++head) {
     const Target t(p.a, s, head, is_v, D);
     const float s_old = s.kept > 0 ? *t.scale : 0.f;
-    // The rotated rows stay in registers until the page's scale is known.
+    // The rotated rows are kept until the page's scale is known.
     float y[NV][8], amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {                     // (threads without a row: any one, as 0)

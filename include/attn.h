@@ -327,7 +327,9 @@ size_t attn_fwd_kv_fp8_pages_workspace_size(int Hq, int Hkv, int total_q, int d)
  *   page_table, cu_seqlens_q, kv_lens: each sequence's own keys, which start on a page of their own
  *       (kv_lens counts these only), as attn_fwd_kv_fp8; causal concerns these only.
  *   max_prefix_q: an upper bound on the queries that share one prefix, from 1 to total_q; max_q as
- *       attn_fwd_kv_fp8.  Each chooses the kernel of its part as there.
+ *       attn_fwd_kv_fp8.  Each chooses the kernel of its part as there; where a prefix goes to the kernel for
+ *       many rows, few sequences' own keys may go along, so what attn_fwd_kv_fp8 says of small components of q
+ *       holds where either bound times Hq / Hkv is above 16.
  *   workspace: attn_fwd_kv_fp8_prefix_workspace_size(...) bytes, which holds both parts' results in fp32 (8 Hq total_q d
  *       bytes and more); other arguments and ownership as attn_fwd_kv_fp8.
  * Errors as attn_fwd_kv_fp8, of both parts; if either part's offsets or lengths break a rule nothing is
